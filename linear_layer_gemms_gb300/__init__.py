@@ -11,8 +11,11 @@ first use instead of falling back to anything else.
     dbias   (OC)      = sum over (b,t) of dout        (NULL / None skips it)
 
 and the layer's forward, out = inp . weight^T + bias (mmbwd_forward); plus the
-LayerNorm backward of a GPT-2 block (lnbwd_run, include/layernorm_backward.h)
-and the encoder backward (encbwd_run, include/encoder_backward.h).
+LayerNorm forward and backward of a GPT-2 block (lnbwd_forward,
+include/layernorm_forward.h; lnbwd_run, include/layernorm_backward.h), the
+encoder backward (encbwd_run, include/encoder_backward.h), and the linear layer
+in 8-bit floats with a scale per block of 128 (mmbwd_q8_quantize,
+mmbwd_q8_forward, mmbwd_q8_backward, include/q8_linear.h).
 
 Pointers may be given as integers or as objects with ``data_ptr()`` (for
 example torch tensors on the current CUDA device); ``stream`` is a raw
@@ -31,15 +34,18 @@ OK = 0
 ERR_NULL, ERR_DTYPE, ERR_SHAPE, ERR_ALIGN, ERR_ALIAS = -1, -2, -3, -4, -5
 ERR_ALLOC, ERR_CUDA, ERR_DEVICE_TIMEOUT, ERR_ARCH, ERR_CAPTURE = -6, -7, -8, -9, -10
 ERR_SCRATCH, ERR_MEMORY = -11, -12
+E4M3 = 0  # MMBWD_E4M3, MMBWD_E5M2: 8-bit formats
+E5M2 = 1
+Q8_BLOCK = 128
+Q8_ADD_DINP, Q8_ADD_DWEIGHT = 1, 2  # MMBWD_Q8_ADD_*: mmbwd_q8_backward's accumulate bits
 STATIC_SCRATCH_BYTES = 32 << 20  # MMBWD_STATIC_SCRATCH_BYTES
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_build", "libmmbwd.so")
 
-# Names and C signatures of every entry point declared in include/mmbwd.h,
-# include/layernorm_backward.h and include/encoder_backward.h.
-_vp, _i64, _ci, _u64, _sz = (ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_uint64,
-                             ctypes.c_size_t)
+# Names and C signatures of every entry point declared in include/*.h.
+_vp, _i64, _ci, _u64, _sz, _f32 = (ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_uint64,
+                                   ctypes.c_size_t, ctypes.c_float)
 SIGNATURES = {
     "mmbwd_run": ([_vp] * 6 + [_i64] * 4 + [_ci, _vp], _ci),
     "mmbwd_run_sr": ([_vp] * 6 + [_i64] * 4 + [_ci, _u64, _vp], _ci),
@@ -63,6 +69,14 @@ SIGNATURES = {
     "encbwd_run_planned": ([_vp] * 4 + [_i64] * 4 + [_ci, ctypes.POINTER(_u64), _vp], _ci),
     "encbwd_workspace_bytes": ([_i64] * 4 + [_ci], _sz),
     "lnbwd_workspace_bytes": ([_i64] * 3 + [_ci], _sz),
+    "lnbwd_forward": ([_vp] * 6 + [_i64] * 3 + [_f32, _ci, _vp], _ci),
+    "mmbwd_q8_data_bytes": ([_i64] * 2, _sz),
+    "mmbwd_q8_scale_bytes": ([_i64] * 2, _sz),
+    "mmbwd_q8_quantize": ([_vp] * 7 + [_sz] + [_i64] * 2 + [_ci] * 2 + [_vp], _ci),
+    "mmbwd_q8_quantize_workspace_bytes": ([_i64] * 2, _sz),
+    "mmbwd_q8_forward": ([_vp] * 6 + [_i64] * 4 + [_ci] * 3 + [_vp], _ci),
+    "mmbwd_q8_backward": ([_vp] * 11 + [_sz] + [_i64] * 4 + [_ci] * 6 + [_vp], _ci),
+    "mmbwd_q8_backward_workspace_bytes": ([_i64] * 4, _sz),
 }
 LNBWD_MAX_C = {F32: 1 << 20, BF16: 1 << 20}  # LNBWD_MAX_C_F32, LNBWD_MAX_C_BF16
 ENCBWD_MAX_POSITIONS, ENCBWD_MAX_VOCAB, ENCBWD_MAX_CHANNELS = 1 << 24, 131071, 65536
@@ -151,6 +165,63 @@ def lnbwd_run(dinp, dweight, dbias, dout, inp, weight, mean, rstd, B: int, T: in
     and rstd are fp32 row statistics; returns the C status code."""
     return load().lnbwd_run(_ptr(dinp), _ptr(dweight), _ptr(dbias), _ptr(dout), _ptr(inp), _ptr(weight),
                             _ptr(mean), _ptr(rstd), B, T, C, dtype, _stream(stream))
+
+
+def lnbwd_forward(out, mean, rstd, inp, weight, bias, B: int, T: int, C: int, eps: float, dtype: int,
+                  stream=None) -> int:
+    """Enqueue the LayerNorm forward; mean and rstd (fp32, one per row; None: not
+    wanted) are the statistics lnbwd_run reads. out may be inp itself; bias may
+    be None. Returns the C status code."""
+    return load().lnbwd_forward(_ptr(out), _ptr(mean), _ptr(rstd), _ptr(inp), _ptr(weight), _ptr(bias), B, T, C,
+                                eps, dtype, _stream(stream))
+
+
+def mmbwd_q8_data_bytes(rows: int, K: int) -> int:
+    """Bytes of the values of a rows x K matrix in 8-bit form (rows of K rounded up to 16)."""
+    return int(load().mmbwd_q8_data_bytes(rows, K))
+
+
+def mmbwd_q8_scale_bytes(rows: int, K: int) -> int:
+    """Bytes of the scales of a rows x K matrix in 8-bit form."""
+    return int(load().mmbwd_q8_scale_bytes(rows, K))
+
+
+def mmbwd_q8_quantize(q, scale, qt, scale_t, colsum, x, workspace, workspace_bytes: int, rows: int, cols: int,
+                      dtype: int, format: int, stream=None) -> int:
+    """Enqueue x (rows x cols) into its row form (q, scale) and / or column form
+    (qt, scale_t; either pair may be None), with the column sums in colsum
+    (None: not wanted; they need a workspace). Returns the C status code."""
+    return load().mmbwd_q8_quantize(_ptr(q), _ptr(scale), _ptr(qt), _ptr(scale_t), _ptr(colsum), _ptr(x),
+                                    _ptr(workspace), workspace_bytes, rows, cols, dtype, format, _stream(stream))
+
+
+def mmbwd_q8_quantize_workspace_bytes(rows: int, cols: int) -> int:
+    return int(load().mmbwd_q8_quantize_workspace_bytes(rows, cols))
+
+
+def mmbwd_q8_forward(out, inp_q, inp_scale, weight_q, weight_scale, bias, B: int, T: int, C: int, OC: int,
+                     inp_format: int, weight_format: int, dtype: int, stream=None) -> int:
+    """Enqueue out = inp . weight^T + bias from the row forms of inp and weight
+    (bias may be None); returns the C status code."""
+    return load().mmbwd_q8_forward(_ptr(out), _ptr(inp_q), _ptr(inp_scale), _ptr(weight_q), _ptr(weight_scale),
+                                   _ptr(bias), B, T, C, OC, inp_format, weight_format, dtype, _stream(stream))
+
+
+def mmbwd_q8_backward(dinp, dweight, dout_q, dout_scale, dout_qt, dout_scale_t, inp_qt, inp_scale_t, weight_qt,
+                      weight_scale_t, workspace, workspace_bytes: int, B: int, T: int, C: int, OC: int,
+                      dout_format: int, inp_format: int, weight_format: int, dinp_dtype: int, dweight_dtype: int,
+                      accumulate: int = 0, stream=None) -> int:
+    """Enqueue dinp = dout . weight and dweight = dout^T . inp from 8-bit operands
+    (either output may be None); accumulate: Q8_ADD_DINP | Q8_ADD_DWEIGHT add to
+    the old contents. Returns the C status code."""
+    return load().mmbwd_q8_backward(_ptr(dinp), _ptr(dweight), _ptr(dout_q), _ptr(dout_scale), _ptr(dout_qt),
+                                    _ptr(dout_scale_t), _ptr(inp_qt), _ptr(inp_scale_t), _ptr(weight_qt),
+                                    _ptr(weight_scale_t), _ptr(workspace), workspace_bytes, B, T, C, OC, dout_format,
+                                    inp_format, weight_format, dinp_dtype, dweight_dtype, accumulate, _stream(stream))
+
+
+def mmbwd_q8_backward_workspace_bytes(B: int, T: int, C: int, OC: int) -> int:
+    return int(load().mmbwd_q8_backward_workspace_bytes(B, T, C, OC))
 
 
 def encbwd_run(dwte, dwpe, dout, inp, B: int, T: int, C: int, V: int, dtype: int, stream=None) -> int:

@@ -4,8 +4,11 @@
 #include "../../include/mmbwd.h"
 #include "../../include/layernorm_backward.h"
 #include "../../include/encoder_backward.h"
+#include "../../include/layernorm_forward.h"
+#include "../../include/q8_linear.h"
 #include "internal.h"
 #include "ops.h"
+#include "q8.h"
 
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -13,6 +16,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <cstdint>
 #include <cstdio>
 #include <cstdlib>
@@ -779,6 +783,270 @@ int lnbwd_run(void* dinp, void* dweight, void* dbias, const void* dout, const vo
     if (rc != MMBWD_OK) return rc;
     const cudaError_t e = ln_launch(plan, dinp, dweight, dbias, dout, inp, weight, mean, rstd, s.BT,
                                     static_cast<int>(C), dtype, d->ws, stream);
+    return e == cudaSuccess ? MMBWD_OK : MMBWD_ERR_CUDA;
+}
+
+// ---------------------------------------------------------------------------
+// LayerNorm forward (layernorm_forward.h)
+
+namespace {
+
+// A tensor argument of a call: where it is, its bytes, whether the call writes it.
+struct Arg {
+    const void* p;
+    size_t n;
+    bool out;
+};
+
+// 16-byte alignment of every pointer given, and no written tensor over another tensor.
+int check_args(const Arg* a, int n) {
+    for (int i = 0; i < n; ++i)
+        if (a[i].p && !aligned16(a[i].p)) return MMBWD_ERR_ALIGN;
+    for (int i = 0; i < n; ++i)
+        for (int j = i + 1; j < n; ++j)
+            if ((a[i].out || a[j].out) && overlaps(a[i].p, a[i].n, a[j].p, a[j].n)) return MMBWD_ERR_ALIAS;
+    return MMBWD_OK;
+}
+
+// The current device's state, and every tensor in its memory. Caller holds g_mutex.
+int check_device(const Arg* a, int n, DeviceState** d) {
+    int dev = 0;
+    const int rc = device_state(d, &dev);
+    if (rc != MMBWD_OK) return rc;
+    Span spans[16];
+    for (int i = 0; i < n; ++i) spans[i] = {a[i].p, a[i].n};
+    return check_local(spans, n, dev);
+}
+
+}  // namespace
+
+int lnbwd_forward(void* out, float* mean, float* rstd, const void* inp, const void* weight, const void* bias,
+                  int64_t B, int64_t T, int64_t C, float eps, int dtype, cudaStream_t stream) {
+    NvtxRange nvtx("lnbwd_forward");
+    LnShape s;
+    int rc = ln_check_shape(B, T, C, dtype, &s);
+    if (rc != MMBWD_OK) return rc;
+    if (!(eps >= 0.f) || std::isinf(eps)) return MMBWD_ERR_SHAPE;
+    const size_t b_rows = static_cast<size_t>(s.n) * s.es, b_col = static_cast<size_t>(C) * s.es,
+                 b_stat = C > 0 ? static_cast<size_t>(s.BT) * 4 : 0;
+    if ((b_rows && (!out || !inp)) || (b_col && !weight)) return MMBWD_ERR_NULL;
+    if ((reinterpret_cast<uintptr_t>(mean) | reinterpret_cast<uintptr_t>(rstd)) & 3u) return MMBWD_ERR_ALIGN;
+    if (b_col % 16 != 0) return MMBWD_ERR_ALIGN;
+    // in place: a row is read whole before any of it is written
+    const Arg args[4] = {{out, b_rows, true}, {inp == out ? nullptr : inp, b_rows, false}, {weight, b_col, false},
+                         {bias, b_col, false}};
+    rc = check_args(args, 4);
+    if (rc != MMBWD_OK) return rc;
+    const Arg stats[2] = {{mean, b_stat, true}, {rstd, b_stat, true}};
+    for (const Arg& t : stats)
+        for (const Arg& a : args)
+            if (overlaps(t.p, t.n, a.p, a.n)) return MMBWD_ERR_ALIAS;
+    if (overlaps(mean, b_stat, rstd, b_stat)) return MMBWD_ERR_ALIAS;
+
+    std::lock_guard<std::mutex> g(g_mutex);
+    DeviceState* d = nullptr;
+    const Arg all[6] = {args[0], {inp, b_rows, false}, args[2], args[3], stats[0], stats[1]};
+    rc = check_device(all, 6, &d);
+    if (rc != MMBWD_OK) return rc;
+    if (s.BT == 0 || C == 0) return MMBWD_OK;
+    int sms = 0;
+    rc = ln_num_sms(&sms);
+    if (rc != MMBWD_OK) return rc;
+    const cudaError_t e = ln_forward_launch(out, mean, rstd, inp, weight, bias, s.BT, static_cast<int>(C), eps, dtype,
+                                            sms, stream);
+    return e == cudaSuccess ? MMBWD_OK : MMBWD_ERR_CUDA;
+}
+
+// ---------------------------------------------------------------------------
+// 8-bit linear layer (q8_linear.h)
+
+namespace {
+
+constexpr int64_t Q8_MAX = (int64_t(1) << 31) - 1;  // rows, columns and tiles
+
+bool q8_format_ok(int format) { return format == MMBWD_E4M3 || format == MMBWD_E5M2; }
+
+bool q8_shape_ok(int64_t rows, int64_t K) {
+    return rows >= 0 && K >= 0 && rows <= Q8_MAX - 256 && K <= Q8_MAX - 256;
+}
+
+size_t q8_scale_size(int64_t rows, int64_t K) {
+    return static_cast<size_t>((rows + 127) / 128) * static_cast<size_t>(q8_groups(K)) * 512;
+}
+
+size_t q8_data_size(int64_t rows, int64_t K) { return static_cast<size_t>(rows) * static_cast<size_t>(q8_ld(K)); }
+
+}  // namespace
+
+size_t mmbwd_q8_data_bytes(int64_t rows, int64_t K) { return q8_shape_ok(rows, K) ? q8_data_size(rows, K) : 0; }
+
+size_t mmbwd_q8_scale_bytes(int64_t rows, int64_t K) { return q8_shape_ok(rows, K) ? q8_scale_size(rows, K) : 0; }
+
+size_t mmbwd_q8_quantize_workspace_bytes(int64_t rows, int64_t cols) {
+    if (!q8_shape_ok(rows, cols)) return 0;
+    return (static_cast<size_t>(q8_blocks(rows)) * static_cast<size_t>(cols) * 4 + 255) & ~size_t(255);
+}
+
+int mmbwd_q8_quantize(void* q, void* scale, void* qt, void* scale_t, void* colsum, const void* x, void* workspace,
+                      size_t workspace_bytes, int64_t rows, int64_t cols, int dtype, int format,
+                      cudaStream_t stream) {
+    NvtxRange nvtx("mmbwd_q8_quantize");
+    if ((dtype != MMBWD_F32 && dtype != MMBWD_BF16) || !q8_format_ok(format)) return MMBWD_ERR_DTYPE;
+    if (!q8_shape_ok(rows, cols)) return MMBWD_ERR_SHAPE;
+    if (q8_blocks(rows) * q8_blocks(cols) > Q8_MAX) return MMBWD_ERR_SHAPE;
+    const size_t es = dtype == MMBWD_F32 ? 4 : 2;
+    const bool empty = rows == 0 || cols == 0;
+    if ((q == nullptr) != (scale == nullptr) || (qt == nullptr) != (scale_t == nullptr)) return MMBWD_ERR_NULL;
+    if (!empty && (!x || (!q && !qt))) return MMBWD_ERR_NULL;
+    const size_t need = colsum ? mmbwd_q8_quantize_workspace_bytes(rows, cols) : 0;
+    if (need && !workspace) return MMBWD_ERR_NULL;
+    if (need > workspace_bytes) return MMBWD_ERR_SHAPE;
+    if (need && (reinterpret_cast<uintptr_t>(workspace) & 255u)) return MMBWD_ERR_ALIGN;
+    if (static_cast<size_t>(cols) * es % 16 != 0) return MMBWD_ERR_ALIGN;
+    const Arg args[7] = {{q, q8_data_size(rows, cols), true},
+                         {scale, q8_scale_size(rows, cols), true},
+                         {qt, q8_data_size(cols, rows), true},
+                         {scale_t, q8_scale_size(cols, rows), true},
+                         {colsum, static_cast<size_t>(cols) * es, true},
+                         {need ? workspace : nullptr, need, true},
+                         {x, static_cast<size_t>(rows) * static_cast<size_t>(cols) * es, false}};
+    int rc = check_args(args, 7);
+    if (rc != MMBWD_OK) return rc;
+    std::lock_guard<std::mutex> g(g_mutex);
+    DeviceState* d = nullptr;
+    rc = check_device(args, 7, &d);
+    if (rc != MMBWD_OK) return rc;
+    cudaError_t e = cudaSuccess;
+    if (empty) {
+        if (colsum && cols > 0) e = cudaMemsetAsync(colsum, 0, static_cast<size_t>(cols) * es, stream);
+    } else {
+        e = q8_quantize_launch(static_cast<uint8_t*>(q), static_cast<uint8_t*>(scale), static_cast<uint8_t*>(qt),
+                               static_cast<uint8_t*>(scale_t), colsum, x, static_cast<float*>(workspace), rows, cols,
+                               dtype, format, stream);
+    }
+    return e == cudaSuccess ? MMBWD_OK : MMBWD_ERR_CUDA;
+}
+
+int mmbwd_q8_forward(void* out, const void* inp_q, const void* inp_scale, const void* weight_q,
+                     const void* weight_scale, const void* bias, int64_t B, int64_t T, int64_t C, int64_t OC,
+                     int inp_format, int weight_format, int dtype, cudaStream_t stream) {
+    NvtxRange nvtx("mmbwd_q8_forward");
+    if (!q8_format_ok(inp_format) || !q8_format_ok(weight_format)) return MMBWD_ERR_DTYPE;
+    Shape s;
+    int rc = check_shape(B, T, C, OC, dtype, &s);
+    if (rc != MMBWD_OK) return rc;
+    if (!q8_shape_ok(s.BT, C) || !q8_shape_ok(OC, C)) return MMBWD_ERR_SHAPE;
+    const size_t b_out = static_cast<size_t>(s.n_dout) * s.es;
+    if ((b_out && !out) || (s.n_dinp && (!inp_q || !inp_scale)) || (s.n_dw && (!weight_q || !weight_scale)))
+        return MMBWD_ERR_NULL;
+    if (static_cast<size_t>(OC) * s.es % 16 != 0) return MMBWD_ERR_ALIGN;
+    const Arg args[6] = {{out, b_out, true},
+                         {inp_q, q8_data_size(s.BT, C), false},
+                         {inp_scale, q8_scale_size(s.BT, C), false},
+                         {weight_q, q8_data_size(OC, C), false},
+                         {weight_scale, q8_scale_size(OC, C), false},
+                         {bias, static_cast<size_t>(OC) * s.es, false}};
+    rc = check_args(args, 6);
+    if (rc != MMBWD_OK) return rc;
+    std::lock_guard<std::mutex> g(g_mutex);
+    DeviceState* d = nullptr;
+    rc = check_device(args, 6, &d);
+    if (rc != MMBWD_OK) return rc;
+    if (s.BT == 0 || OC == 0) return MMBWD_OK;
+    cudaError_t e;
+    if (C == 0) {
+        e = fill_rows_launch(out, bias, s.BT, OC, dtype, stream);
+    } else {
+        Q8Product p;
+        p.D = out, p.bias = bias;
+        p.A = static_cast<const uint8_t*>(inp_q), p.a_scale = static_cast<const uint8_t*>(inp_scale);
+        p.B = static_cast<const uint8_t*>(weight_q), p.b_scale = static_cast<const uint8_t*>(weight_scale);
+        p.M = s.BT, p.N = OC, p.K = C;
+        p.a_format = inp_format, p.b_format = weight_format, p.dtype = dtype;
+        e = q8_product_launch(&p, 1, stream);
+    }
+    return e == cudaSuccess ? MMBWD_OK : MMBWD_ERR_CUDA;
+}
+
+size_t mmbwd_q8_backward_workspace_bytes(int64_t B, int64_t T, int64_t C, int64_t OC) {
+    Shape s;
+    if (check_shape(B, T, C, OC, MMBWD_F32, &s) != MMBWD_OK) return 0;
+    return 0;
+}
+
+int mmbwd_q8_backward(void* dinp, void* dweight, const void* dout_q, const void* dout_scale, const void* dout_qt,
+                      const void* dout_scale_t, const void* inp_qt, const void* inp_scale_t, const void* weight_qt,
+                      const void* weight_scale_t, void* workspace, size_t workspace_bytes, int64_t B, int64_t T,
+                      int64_t C, int64_t OC, int dout_format, int inp_format, int weight_format, int dinp_dtype,
+                      int dweight_dtype, int accumulate, cudaStream_t stream) {
+    NvtxRange nvtx("mmbwd_q8_backward");
+    if (!q8_format_ok(dout_format) || !q8_format_ok(inp_format) || !q8_format_ok(weight_format))
+        return MMBWD_ERR_DTYPE;
+    Shape s, sw;
+    int rc = check_shape(B, T, C, OC, dinp_dtype, &s);
+    if (rc == MMBWD_OK) rc = check_shape(B, T, C, OC, dweight_dtype, &sw);
+    if (rc != MMBWD_OK) return rc;
+    if (!q8_shape_ok(s.BT, C) || !q8_shape_ok(OC, C) || !q8_shape_ok(s.BT, OC)) return MMBWD_ERR_SHAPE;
+    if (accumulate & ~(MMBWD_Q8_ADD_DINP | MMBWD_Q8_ADD_DWEIGHT)) return MMBWD_ERR_SHAPE;
+    const size_t b_dinp = static_cast<size_t>(s.n_dinp) * s.es, b_dw = static_cast<size_t>(s.n_dw) * sw.es;
+    if (!dinp && !dweight && (b_dinp || b_dw)) return MMBWD_ERR_NULL;
+    if (dinp && b_dinp && OC > 0 && (!dout_q || !dout_scale || !weight_qt || !weight_scale_t)) return MMBWD_ERR_NULL;
+    if (dweight && b_dw && s.BT > 0 && (!dout_qt || !dout_scale_t || !inp_qt || !inp_scale_t)) return MMBWD_ERR_NULL;
+    if ((dinp && static_cast<size_t>(C) * s.es % 16 != 0) || (dweight && static_cast<size_t>(C) * sw.es % 16 != 0))
+        return MMBWD_ERR_ALIGN;
+    const size_t need = mmbwd_q8_backward_workspace_bytes(B, T, C, OC);
+    if (need && !workspace) return MMBWD_ERR_NULL;
+    if (need > workspace_bytes) return MMBWD_ERR_SHAPE;
+    if (need && (reinterpret_cast<uintptr_t>(workspace) & 255u)) return MMBWD_ERR_ALIGN;
+    // operands of a product that is not wanted are not looked at
+    const Arg args[11] = {{dinp, b_dinp, true},
+                          {dweight, b_dw, true},
+                          {need ? workspace : nullptr, need, true},
+                          {dinp ? dout_q : nullptr, q8_data_size(s.BT, OC), false},
+                          {dinp ? dout_scale : nullptr, q8_scale_size(s.BT, OC), false},
+                          {dweight ? dout_qt : nullptr, q8_data_size(OC, s.BT), false},
+                          {dweight ? dout_scale_t : nullptr, q8_scale_size(OC, s.BT), false},
+                          {dweight ? inp_qt : nullptr, q8_data_size(C, s.BT), false},
+                          {dweight ? inp_scale_t : nullptr, q8_scale_size(C, s.BT), false},
+                          {dinp ? weight_qt : nullptr, q8_data_size(C, OC), false},
+                          {dinp ? weight_scale_t : nullptr, q8_scale_size(C, OC), false}};
+    rc = check_args(args, 11);
+    if (rc != MMBWD_OK) return rc;
+    std::lock_guard<std::mutex> g(g_mutex);
+    DeviceState* d = nullptr;
+    rc = check_device(args, 11, &d);
+    if (rc != MMBWD_OK) return rc;
+
+    Q8Product prod[2];
+    int n = 0;
+    cudaError_t e = cudaSuccess;
+    if (dinp && b_dinp) {
+        if (OC == 0) {
+            if (!(accumulate & MMBWD_Q8_ADD_DINP)) e = cudaMemsetAsync(dinp, 0, b_dinp, stream);
+        } else {
+            Q8Product& p = prod[n++];
+            p.D = dinp;
+            p.A = static_cast<const uint8_t*>(dout_q), p.a_scale = static_cast<const uint8_t*>(dout_scale);
+            p.B = static_cast<const uint8_t*>(weight_qt), p.b_scale = static_cast<const uint8_t*>(weight_scale_t);
+            p.M = s.BT, p.N = C, p.K = OC;
+            p.a_format = dout_format, p.b_format = weight_format, p.dtype = dinp_dtype;
+            p.add = (accumulate & MMBWD_Q8_ADD_DINP) ? 1 : 0;
+        }
+    }
+    if (dweight && b_dw) {
+        if (s.BT == 0) {
+            if (!(accumulate & MMBWD_Q8_ADD_DWEIGHT)) e = cudaMemsetAsync(dweight, 0, b_dw, stream);
+        } else {
+            Q8Product& p = prod[n++];
+            p.D = dweight;
+            p.A = static_cast<const uint8_t*>(dout_qt), p.a_scale = static_cast<const uint8_t*>(dout_scale_t);
+            p.B = static_cast<const uint8_t*>(inp_qt), p.b_scale = static_cast<const uint8_t*>(inp_scale_t);
+            p.M = OC, p.N = C, p.K = s.BT;
+            p.a_format = dout_format, p.b_format = inp_format, p.dtype = dweight_dtype;
+            p.add = (accumulate & MMBWD_Q8_ADD_DWEIGHT) ? 1 : 0;
+        }
+    }
+    if (e == cudaSuccess && n > 0) e = q8_product_launch(prod, n, stream);
     return e == cudaSuccess ? MMBWD_OK : MMBWD_ERR_CUDA;
 }
 

@@ -1,0 +1,237 @@
+// LayerNorm forward (llm.c dev/cuda/layernorm_backward.cu, layernorm_forward_cpu):
+// per row mean, variance, rstd, and out = (x - mean) * rstd * weight + bias.
+//
+// Bound by HBM: each row read once and written once. A team of P warps owns a
+// row and keeps it in registers (VPT 16-byte vectors per thread), so the
+// variance is the mean of the squared differences, formed after the mean
+// without a second read, and no cancellation is paid for it. Sums: in the
+// thread, an xor butterfly over the warp, the warps in order. Rows wider than
+// the largest team holds are read three times (mean, variance, output), the
+// second and third time from L2.
+#include "../../include/layernorm_forward.h"
+#include "ops.h"
+#include "ptx.cuh"
+#include "q8.h"
+
+#include <cuda_bf16.h>
+
+#include <algorithm>
+
+namespace mmbwd {
+namespace {
+
+template <typename T>
+struct Vec;
+template <>
+struct Vec<float> {
+    static constexpr int N = 4;
+    __device__ static void get(const uint4& v, float (&f)[4]) {
+        f[0] = __uint_as_float(v.x), f[1] = __uint_as_float(v.y), f[2] = __uint_as_float(v.z), f[3] = __uint_as_float(v.w);
+    }
+    __device__ static uint4 put(const float (&f)[4]) {
+        return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+    }
+};
+template <>
+struct Vec<__nv_bfloat16> {
+    static constexpr int N = 8;
+    __device__ static void get(const uint4& v, float (&f)[8]) {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            f[2 * i] = __uint_as_float(w[i] << 16);
+            f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+        }
+    }
+    __device__ static uint4 put(const float (&f)[8]) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+            w[i] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+};
+
+__device__ __forceinline__ float warp_sum(float s) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    return s;
+}
+
+// The sum of the team's P warp sums, in warp order, in every thread. `slot`:
+// 2 P floats of the team's; `which` alternates, so that one barrier per sum is enough.
+template <int P>
+__device__ __forceinline__ float team_sum(float s, float* slot, int which, int warp_in_team, int team) {
+    s = warp_sum(s);
+    if constexpr (P == 1) {
+        return s;
+    } else {
+        float* at = slot + which * P;
+        if ((threadIdx.x & 31) == 0) at[warp_in_team] = s;
+        ptx::named_bar_sync(static_cast<uint32_t>(1 + team), 32 * P);
+        float t = at[0];
+#pragma unroll
+        for (int w = 1; w < P; ++w) t += at[w];
+        return t;
+    }
+}
+
+constexpr int LNF_WARPS = 8;  // per block, where a team is no larger
+
+template <typename T, int P, int VPT>
+__global__ void __launch_bounds__(32 * (P > LNF_WARPS ? P : LNF_WARPS))
+    ln_fwd_kernel(T* out, float* mean_out, float* rstd_out, const T* inp, const T* __restrict__ weight,
+                  const T* __restrict__ bias, int64_t rows, int C, float eps) {
+    using V = Vec<T>;
+    constexpr int N = V::N;
+    constexpr int TEAMS = (P > LNF_WARPS ? P : LNF_WARPS) / P;
+    __shared__ float slots[TEAMS][2 * P];
+    const int warp = static_cast<int>(threadIdx.x >> 5), lane = static_cast<int>(threadIdx.x & 31);
+    const int team = warp / P, wt = warp % P, t = wt * 32 + lane;
+    const int nvec = C / N;
+    const float inv_c = 1.f / static_cast<float>(C);
+    ptx::grid_launch_dependents();
+    ptx::grid_dependency_wait();
+    for (int64_t r = static_cast<int64_t>(blockIdx.x) * TEAMS + team; r < rows; r += static_cast<int64_t>(gridDim.x) * TEAMS) {
+        const uint4* xr = reinterpret_cast<const uint4*>(inp + r * C);
+        uint4 x[VPT];
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            const int v = t + 32 * P * j;
+            x[j] = v < nvec ? xr[v] : make_uint4(0u, 0u, 0u, 0u);
+        }
+        float s = 0.f;
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            float f[N];
+            V::get(x[j], f);
+#pragma unroll
+            for (int e = 0; e < N; ++e) s += f[e];
+        }
+        const float mean = team_sum<P>(s, slots[team], 0, wt, team) * inv_c;
+        s = 0.f;
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            if (t + 32 * P * j < nvec) {
+                float f[N];
+                V::get(x[j], f);
+#pragma unroll
+                for (int e = 0; e < N; ++e) s += (f[e] - mean) * (f[e] - mean);
+            }
+        }
+        const float var = team_sum<P>(s, slots[team], 1, wt, team) * inv_c;
+        const float rstd = 1.f / sqrtf(var + eps);
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            const int v = t + 32 * P * j;
+            if (v < nvec) {
+                float f[N], w[N], b[N];
+                V::get(x[j], f);
+                V::get(__ldg(reinterpret_cast<const uint4*>(weight) + v), w);
+                V::get(bias ? __ldg(reinterpret_cast<const uint4*>(bias) + v) : make_uint4(0u, 0u, 0u, 0u), b);
+#pragma unroll
+                for (int e = 0; e < N; ++e) f[e] = (f[e] - mean) * rstd * w[e] + b[e];
+                reinterpret_cast<uint4*>(out + r * C)[v] = V::put(f);
+            }
+        }
+        if (t == 0) {
+            if (mean_out) mean_out[r] = mean;
+            if (rstd_out) rstd_out[r] = rstd;
+        }
+    }
+}
+
+// Rows wider than a team of 32 warps holds: a block of 32 warps per row, read
+// three times.
+template <typename T>
+__global__ void __launch_bounds__(1024) ln_fwd_wide_kernel(T* out, float* mean_out, float* rstd_out, const T* inp,
+                                                           const T* __restrict__ weight, const T* __restrict__ bias,
+                                                           int64_t rows, int C, float eps) {
+    using V = Vec<T>;
+    constexpr int N = V::N;
+    __shared__ float slots[2 * 32];
+    const int t = static_cast<int>(threadIdx.x), wt = t >> 5;
+    const int nvec = C / N;
+    const float inv_c = 1.f / static_cast<float>(C);
+    ptx::grid_launch_dependents();
+    ptx::grid_dependency_wait();
+    for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
+        const uint4* xr = reinterpret_cast<const uint4*>(inp + r * C);
+        float s = 0.f;
+        for (int v = t; v < nvec; v += 1024) {
+            float f[N];
+            V::get(xr[v], f);
+#pragma unroll
+            for (int e = 0; e < N; ++e) s += f[e];
+        }
+        const float mean = team_sum<32>(s, slots, 0, wt, 0) * inv_c;
+        s = 0.f;
+        for (int v = t; v < nvec; v += 1024) {
+            float f[N];
+            V::get(xr[v], f);
+#pragma unroll
+            for (int e = 0; e < N; ++e) s += (f[e] - mean) * (f[e] - mean);
+        }
+        const float var = team_sum<32>(s, slots, 1, wt, 0) * inv_c;
+        const float rstd = 1.f / sqrtf(var + eps);
+        for (int v = t; v < nvec; v += 1024) {
+            float f[N], w[N], b[N];
+            V::get(xr[v], f);
+            V::get(__ldg(reinterpret_cast<const uint4*>(weight) + v), w);
+            V::get(bias ? __ldg(reinterpret_cast<const uint4*>(bias) + v) : make_uint4(0u, 0u, 0u, 0u), b);
+#pragma unroll
+            for (int e = 0; e < N; ++e) f[e] = (f[e] - mean) * rstd * w[e] + b[e];
+            reinterpret_cast<uint4*>(out + r * C)[v] = V::put(f);
+        }
+        if (t == 0) {
+            if (mean_out) mean_out[r] = mean;
+            if (rstd_out) rstd_out[r] = rstd;
+        }
+    }
+}
+
+template <typename T>
+using LnFwdKernel = void (*)(T*, float*, float*, const T*, const T*, const T*, int64_t, int, float);
+
+template <typename T>
+cudaError_t launch(T* out, float* mean, float* rstd, const T* inp, const T* weight, const T* bias, int64_t BT, int C,
+                   float eps, int num_sms, cudaStream_t stream) {
+    const int nvec = C / Vec<T>::N;
+    LnFwdKernel<T> k;
+    int warps, rows_per_block;
+    if (nvec <= 32 * 4) k = ln_fwd_kernel<T, 1, 4>, warps = 8, rows_per_block = 8;
+    else if (nvec <= 64 * 4) k = ln_fwd_kernel<T, 2, 4>, warps = 8, rows_per_block = 4;
+    else if (nvec <= 128 * 4) k = ln_fwd_kernel<T, 4, 4>, warps = 8, rows_per_block = 2;
+    else if (nvec <= 256 * 4) k = ln_fwd_kernel<T, 8, 4>, warps = 8, rows_per_block = 1;
+    else if (nvec <= 1024 * 4) k = ln_fwd_kernel<T, 32, 4>, warps = 32, rows_per_block = 1;
+    else k = ln_fwd_wide_kernel<T>, warps = 32, rows_per_block = 1;
+    const int64_t blocks = (BT + rows_per_block - 1) / rows_per_block;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(blocks, static_cast<int64_t>(num_sms) * (64 / warps))), 1, 1);
+    cfg.blockDim = dim3(static_cast<unsigned>(32 * warps), 1, 1);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, k, out, mean, rstd, inp, weight, bias, BT, C, eps);
+}
+
+}  // namespace
+
+cudaError_t ln_forward_launch(void* out, float* mean, float* rstd, const void* inp, const void* weight,
+                              const void* bias, int64_t BT, int C, float eps, int dtype, int num_sms,
+                              cudaStream_t stream) {
+    if (take_injected_launch_failure()) return cudaErrorLaunchFailure;
+    if (dtype == MMBWD_F32)
+        return launch(static_cast<float*>(out), mean, rstd, static_cast<const float*>(inp),
+                      static_cast<const float*>(weight), static_cast<const float*>(bias), BT, C, eps, num_sms, stream);
+    return launch(static_cast<__nv_bfloat16*>(out), mean, rstd, static_cast<const __nv_bfloat16*>(inp),
+                  static_cast<const __nv_bfloat16*>(weight), static_cast<const __nv_bfloat16*>(bias), BT, C, eps,
+                  num_sms, stream);
+}
+
+}  // namespace mmbwd

@@ -1,0 +1,44 @@
+// Internal declarations of the 8-bit linear layer (quantisation, products) and
+// of the LayerNorm forward, shared with the C-ABI layer. Not part of the
+// public ABI.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <cstddef>
+#include <cstdint>
+
+namespace mmbwd {
+
+constexpr int Q8_BLOCK = 128;  // values per scale
+
+// Blocks of a row of K values, groups of four blocks, bytes between rows.
+inline int64_t q8_blocks(int64_t K) { return (K + Q8_BLOCK - 1) / Q8_BLOCK; }
+inline int64_t q8_groups(int64_t K) { return (q8_blocks(K) + 3) / 4; }
+inline int64_t q8_ld(int64_t K) { return (K + 15) & ~int64_t(15); }
+
+// q/scale and qt/scale_t: either pair may be null. `partials` holds
+// ceil(rows / 128) * cols floats when colsum is wanted.
+cudaError_t q8_quantize_launch(uint8_t* q, uint8_t* scale, uint8_t* qt, uint8_t* scale_t, void* colsum, const void* x,
+                               float* partials, int64_t rows, int64_t cols, int dtype, int format,
+                               cudaStream_t stream);
+
+// One product D (M x N, row-major, leading dimension N) = A (M x K) . B (N x K)^T
+// (+ bias per column, + the old D), A and B in 8-bit form.
+struct Q8Product {
+    void* D = nullptr;
+    const void* bias = nullptr;  // per column of D, type of D; null: none
+    const uint8_t *A = nullptr, *a_scale = nullptr, *B = nullptr, *b_scale = nullptr;
+    int64_t M = 0, N = 0, K = 0;
+    int a_format = 0, b_format = 0;
+    int dtype = 0;  // of D and bias
+    int add = 0;    // add to the old D
+};
+
+cudaError_t q8_product_launch(const Q8Product* products, int n, cudaStream_t stream);
+
+cudaError_t ln_forward_launch(void* out, float* mean, float* rstd, const void* inp, const void* weight,
+                              const void* bias, int64_t BT, int C, float eps, int dtype, int num_sms,
+                              cudaStream_t stream);
+
+}  // namespace mmbwd
