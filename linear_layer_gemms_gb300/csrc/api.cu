@@ -475,6 +475,13 @@ int mmbwd_device_status(int reset, int* info) {
         if (info)
             for (int i = 0; i < 3; ++i) info[i] = enc_info[i];
     }
+    int q8_code = MMBWD_OK, q8_info[3] = {0, 0, 0};
+    if (q8_read_status(&q8_code, q8_info, reset != 0) != cudaSuccess) return MMBWD_ERR_CUDA;
+    if (code == MMBWD_OK && q8_code != MMBWD_OK) {
+        code = q8_code;
+        if (info)
+            for (int i = 0; i < 3; ++i) info[i] = q8_info[i];
+    }
     return code;
 }
 
@@ -963,7 +970,7 @@ int mmbwd_q8_forward(void* out, const void* inp_q, const void* inp_scale, const 
         p.B = static_cast<const uint8_t*>(weight_q), p.b_scale = static_cast<const uint8_t*>(weight_scale);
         p.M = s.BT, p.N = OC, p.K = C;
         p.a_format = inp_format, p.b_format = weight_format, p.dtype = dtype;
-        e = q8_product_launch(&p, 1, stream);
+        e = q8_products_launch(&p, 1, false, nullptr, 0, d->num_sms, stream);
     }
     return e == cudaSuccess ? MMBWD_OK : MMBWD_ERR_CUDA;
 }
@@ -971,7 +978,23 @@ int mmbwd_q8_forward(void* out, const void* inp_q, const void* inp_scale, const 
 size_t mmbwd_q8_backward_workspace_bytes(int64_t B, int64_t T, int64_t C, int64_t OC) {
     Shape s;
     if (check_shape(B, T, C, OC, MMBWD_F32, &s) != MMBWD_OK) return 0;
-    return 0;
+    if (!q8_shape_ok(s.BT, C) || !q8_shape_ok(OC, C) || !q8_shape_ok(s.BT, OC)) return 0;
+    if (s.BT == 0 || C == 0 || OC == 0) return 0;
+    int sms = 0;
+    {
+        std::lock_guard<std::mutex> g(g_mutex);
+        DeviceState* d = nullptr;
+        int dev = 0;
+        if (device_state(&d, &dev) == MMBWD_OK) sms = d->num_sms;
+    }
+    if (sms <= 0) sms = 152;  // no usable device: size for a full GB300
+    Q8Product p[2];
+    p[0].M = s.BT, p[0].N = C, p[0].K = OC;
+    p[1].M = OC, p[1].N = C, p[1].K = s.BT;
+    // both products, or one of them alone: whichever plan needs most
+    const size_t most = std::max(q8_products_workspace(p, 2, sms),
+                                 std::max(q8_products_workspace(p, 1, sms), q8_products_workspace(p + 1, 1, sms)));
+    return (most + 255) & ~size_t(255);
 }
 
 int mmbwd_q8_backward(void* dinp, void* dweight, const void* dout_q, const void* dout_scale, const void* dout_qt,
@@ -1046,7 +1069,8 @@ int mmbwd_q8_backward(void* dinp, void* dweight, const void* dout_q, const void*
             p.add = (accumulate & MMBWD_Q8_ADD_DWEIGHT) ? 1 : 0;
         }
     }
-    if (e == cudaSuccess && n > 0) e = q8_product_launch(prod, n, stream);
+    if (e == cudaSuccess && n > 0)
+        e = q8_products_launch(prod, n, true, workspace, workspace_bytes, d->num_sms, stream);
     return e == cudaSuccess ? MMBWD_OK : MMBWD_ERR_CUDA;
 }
 

@@ -35,7 +35,13 @@ struct Q8Product {
     int add = 0;    // add to the old D
 };
 
-cudaError_t q8_product_launch(const Q8Product* products, int n, cudaStream_t stream);
+// One or two products in one launch (their K ranges split where that fills the
+// device and `may_split`; the split sums then need the workspace). The
+// workspace depends on the shapes only.
+size_t q8_products_workspace(const Q8Product* products, int n, int num_sms);
+cudaError_t q8_products_launch(const Q8Product* products, int n, bool may_split, void* ws, size_t ws_bytes, int num_sms,
+                               cudaStream_t stream);
+cudaError_t q8_read_status(int* code, int* info3, bool reset);
 
 cudaError_t ln_forward_launch(void* out, float* mean, float* rstd, const void* inp, const void* weight,
                               const void* bias, int64_t BT, int C, float eps, int dtype, int num_sms,

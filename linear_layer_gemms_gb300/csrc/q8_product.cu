@@ -1,112 +1,841 @@
-// Products of matrices in 8-bit form: D (M x N) = A (M x K) . B (N x K)^T with a
-// power-of-two scale per block of 128 along K (include/q8_linear.h).
+// Products of matrices in 8-bit form (include/q8_linear.h) on the sm_103a tensor
+// cores: D (M x N) = A (M x K) . B (N x K)^T, with one power-of-two scale per row
+// and block of 128 along K.
 //
-// One block of 256 threads forms a 64 x 64 tile of D: 32 values of K at a time
-// are decoded to fp32 with their scale into shared memory, and each thread
-// accumulates 4 x 4 elements.
+// The block scales go through the tensor core itself: tcgen05.mma of
+// kind::mxf8f6f4 multiplies each step of 32 products by both rows' ue8m0 scales
+// on its way into the fp32 accumulator, so a block scale costs no pass over the
+// accumulator. An MMA takes one byte per row out of a 32-bit scale word in tensor
+// memory, and the scales are stored as those words (tiles of 128 rows x 4
+// blocks): one tcgen05.cp per 128 rows serves 512 values of K, and the
+// instruction descriptor picks the block's byte.
+//
+// CTA pairs, as in the bf16 kernel: a cluster of two CTAs computes a 256 x bn tile
+// (bn 256 or 128) with pair MMAs (M = 256, K = 32); CTA r stages rows
+// [128 r, 128 r + 128) of A, its half of the columns of B, the scales of its 128
+// rows of A, and the scales of all bn columns. Both operands are K-major; a stage
+// is 128 bytes of K per row (128-byte swizzle), which moves as many bytes per
+// tensor-core cycle as a bf16 stage (half the bytes, twice the rate).
+//
+// Tensor memory (512 columns): two accumulators of 256 columns overlap in 64,
+// [0, 256) and [192, 448), and leave 64 columns for the scales. The epilogue
+// reads the shared columns first and then lets the next tile's MMAs start, so only
+// the first chunk of each epilogue is exposed.
+//
+// Warp roles (10 warps per CTA): 0 TMA producer; 1 MMA issuer (even CTA) or
+// forwarder of "stage full" to the even CTA (odd CTA); 2-9 epilogue, two warps per
+// tensor-memory lane quadrant, each taking every other 32-column chunk of its 32
+// rows: accumulator (+ bias, + old values fetched by TMA) rounded once into a
+// swizzled chunk buffer and out with one bulk store.
+//
+// Work list: the tiles of one or two products (dinp and dweight), each product's
+// reduction cut into `splits` ranges of blocks where its tiles alone do not
+// fill the pairs; items go to pairs longest first on the host. Partial tiles of
+// a cut product are fp32, in the caller's workspace, and a second kernel adds
+// them in split order, so no result depends on timing.
+//
+// Every wait is bounded (2 s): one that gives up records the failure in the
+// device status word and all roles unwind.
 #include "../../include/q8_linear.h"
+#include "internal.h"
 #include "ops.h"
-#include "ptx.cuh"
+#include "q8.cuh"
 #include "q8.h"
 
+#include <cuda.h>
 #include <cuda_bf16.h>
-#include <cuda_fp16.h>
+
+#include <algorithm>
+#include <climits>
+#include <cstdio>
+#include <cstdlib>
+#include <cstring>
+#include <mutex>
 
 namespace mmbwd {
+
+__device__ unsigned int g_q8_status[4];
+
 namespace {
 
-constexpr int SP_TILE = 64, SP_K = 32;
+constexpr int BM = 128, PAIR_M = 256;
+constexpr int STAGES = 5;
+constexpr int A_BYTES = BM * 128, B_BYTES = 128 * 128;
+constexpr int SF_BYTES = 3 * 512;  // scales of 128 rows of A and up to 256 of B, four blocks of K
+constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
+constexpr int EPI_WARPS = 8, FIRST_EPI = 2;
+constexpr int THREADS = 32 * (FIRST_EPI + EPI_WARPS);
+constexpr int CHUNK_BYTES = 4096;  // per epilogue warp: one fp32 chunk (32 x 32), or two bf16 chunks
+constexpr int OLD_SLOTS = 2;
+constexpr uint32_t TMEM_COLS = 512, ACC1 = 192, SF_COL = 448, SF_STRIDE = 12;
+// Scale buffers in tensor memory: a copy into buffer i may only be issued once the
+// MMAs of the group that used it are done. The copy of group g + SF_BUFS follows
+// the wait for a stage whose refill waited for the MMAs up to block
+// 4 (g + SF_BUFS) - STAGES, which covers group g while STAGES <= 4 SF_BUFS - 3.
+constexpr int SF_BUFS = 4;
+static_assert(STAGES <= 4 * SF_BUFS - 3 && SF_BUFS * SF_STRIDE <= 64, "scale buffers");
 
-__device__ __forceinline__ float q8_value(uint8_t b, int format) {
-    uint32_t h;
-    const uint16_t two = b;
-    if (format == MMBWD_E4M3)
-        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(two));
-    else
-        asm("cvt.rn.f16x2.e5m2x2 %0, %1;" : "=r"(h) : "h"(two));
-    return __half2float(__ushort_as_half(static_cast<unsigned short>(h & 0xFFFFu)));
-}
+constexpr int BAR_FULL = 0, BAR_EMPTY = STAGES, BAR_ACC_FULL = 2 * STAGES, BAR_ACC_FREE = 2 * STAGES + 1,
+              BAR_TEARDOWN = 2 * STAGES + 2, BAR_OLD = 2 * STAGES + 3, N_BARS = BAR_OLD + EPI_WARPS * OLD_SLOTS;
+constexpr int OFF_SF = STAGES * STAGE_BYTES;
+constexpr int OFF_CHUNKS = (OFF_SF + STAGES * SF_BYTES + 1023) & ~1023;
+constexpr int OFF_BARS = OFF_CHUNKS + EPI_WARPS * CHUNK_BYTES;
+constexpr int OFF_MISC = OFF_BARS + N_BARS * 8;  // [0] tensor-memory base, [1] abort flag
+constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;
+static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
 
-__device__ __forceinline__ float scale_value(uint8_t b) {
-    return b == 0 ? __uint_as_float(1u << 22) : __uint_as_float(static_cast<uint32_t>(b) << 23);
-}
+constexpr int MAX_PAIRS = 128, MAX_ITEMS = 3072;
 
-struct Operand {
-    const uint8_t *q, *scale;
-    int64_t rows, ld, groups;
-    int format;
+struct Schedule {
+    uint16_t start[MAX_PAIRS + 1];
+    uint16_t items[MAX_ITEMS];
 };
 
-__device__ __forceinline__ float load_value(const Operand& o, int64_t r, int64_t k, int64_t K) {
-    if (r >= o.rows || k >= K) return 0.f;
-    const int64_t kb = k / Q8_BLOCK;
-    const uint8_t s = o.scale[(r / 128 * o.groups + kb / 4) * 512 + (r % 32) * 16 + (r % 128) / 32 * 4 + kb % 4];
-    return q8_value(o.q[r * o.ld + k], o.format) * scale_value(s);
+struct Prod {
+    const uint8_t *a_scale, *b_scale;
+    const void* bias;
+    int64_t M, N;
+    int groups;  // of four blocks, per row of the scales
+    int bn, tiles_m, tiles_n, kb, splits, kb_per_split, item0;
+    int f32, add;
+    uint32_t idesc;
+};
+
+struct Params {
+    Prod prod[2];
+    int n_items, n_prod, table;
+};
+
+struct Maps {
+    CUtensorMap a[2], b[2], d[2], part[2];
+};
+
+struct Item {
+    int which, pm, n_tile, split, kb0, kb1;
+};
+
+__device__ __forceinline__ Item decode(const Params& p, int w) {
+    Item it;
+    it.which = p.n_prod == 2 && w >= p.prod[1].item0 ? 1 : 0;
+    const Prod& d = p.prod[it.which];
+    const int local = w - d.item0, rest = local / d.tiles_n;
+    it.n_tile = local % d.tiles_n;
+    it.pm = rest % d.tiles_m;
+    it.split = rest / d.tiles_m;
+    it.kb0 = it.split * d.kb_per_split;
+    it.kb1 = min(it.kb0 + d.kb_per_split, d.kb);
+    return it;
 }
 
+__device__ __forceinline__ int item_at(const Params& p, const Schedule& s, int round) {
+    const int c = static_cast<int>(blockIdx.x) / 2;
+    if (p.table) {
+        const int i = s.start[c] + round;
+        return i < s.start[c + 1] ? static_cast<int>(s.items[i]) : p.n_items;
+    }
+    return round * (static_cast<int>(gridDim.x) / 2) + c;
+}
+
+__device__ __forceinline__ float lo_bf16(uint32_t x) { return __uint_as_float(x << 16); }
+__device__ __forceinline__ float hi_bf16(uint32_t x) { return __uint_as_float(x & 0xFFFF0000u); }
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+__global__ void __launch_bounds__(THREADS, 1)
+    q8_pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params p,
+                   const __grid_constant__ Schedule sch) {
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = ptx::smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
+    volatile uint32_t* misc = reinterpret_cast<volatile uint32_t*>(smem_raw + (base - raw) + OFF_MISC);
+    const uint32_t bars = base + OFF_BARS;
+    const int warp = static_cast<int>(threadIdx.x >> 5), lane = static_cast<int>(threadIdx.x & 31);
+    const uint32_t rank = ptx::cluster_ctarank();
+    const bool leader = rank == 0;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < STAGES; ++s) {
+            ptx::mbar_init(bars + 8u * (BAR_FULL + s), leader ? 2u : 1u);  // own producer, even CTA: and the forwarder
+            ptx::mbar_init(bars + 8u * (BAR_EMPTY + s), 1u);
+        }
+        ptx::mbar_init(bars + 8u * BAR_ACC_FULL, 1u);
+        ptx::mbar_init(bars + 8u * BAR_ACC_FREE, 2u * EPI_WARPS);
+        ptx::mbar_init(bars + 8u * BAR_TEARDOWN, 1u);
+        for (int b = 0; b < EPI_WARPS * OLD_SLOTS; ++b) ptx::mbar_init(bars + 8u * (BAR_OLD + b), 1u);
+        misc[1] = 0u;
+        ptx::fence_mbar_init();
+    }
+    if (warp == 1) {
+        ptx::tmem_alloc_pair(base + OFF_MISC, TMEM_COLS);
+        ptx::tmem_relinquish_pair();
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::cluster_sync();
+    ptx::tc_fence_after();
+    if (warp >= FIRST_EPI) ptx::grid_dependency_wait();
+    const uint32_t tmem = misc[0];
+    const q8::Waiter wt{misc + 1, g_q8_status};
+
+    if (warp == 0) {
+        // ------------------------------------------------------------ producer
+        if (lane == 0) {
+            for (int i = 0; i < p.n_prod; ++i) {
+                ptx::prefetch_tmap(&maps.a[i]);
+                ptx::prefetch_tmap(&maps.b[i]);
+                ptx::prefetch_tmap(&maps.d[i]);
+            }
+            uint32_t stage = 0, phase = 0, issued = 0, last_parity = 0;
+            bool ok = true, waited = false;
+            for (int r = 0; ok; ++r) {
+                const int w = item_at(p, sch, r);
+                if (w >= p.n_items) break;
+                const Item it = decode(p, w);
+                const Prod& d = p.prod[it.which];
+                const int row0 = it.pm * PAIR_M + static_cast<int>(rank) * BM;
+                const int half = d.bn / 2;
+                const int n0 = it.n_tile * d.bn, col0 = n0 + static_cast<int>(rank) * half;
+                // boxes and scale tiles wholly outside the matrix are not loaded: they
+                // would only reach rows and columns of D that are not stored
+                const bool has_a = row0 < d.M, has_b = col0 < d.N;
+                const int sf_b = d.bn > 128 && n0 + 128 < d.N ? 2 : 1;
+                const uint32_t bytes = (has_a ? A_BYTES : 0u) + (has_b ? static_cast<uint32_t>(half) * 128u : 0u);
+                const uint32_t sf_bytes = (has_a ? 512u : 0u) + 512u * sf_b;
+                const int64_t gstride = static_cast<int64_t>(d.groups) * 512;
+                const uint8_t* sa = d.a_scale + (row0 / 128) * gstride;
+                const uint8_t* sb = d.b_scale + (n0 / 128) * gstride;
+                for (int kb = it.kb0; kb < it.kb1; ++kb) {
+                    if (!wt.wait(bars + 8u * (BAR_EMPTY + stage), phase ^ 1u, q8::SITE_EMPTY, w)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t at = base + stage * STAGE_BYTES, fb = bars + 8u * (BAR_FULL + stage);
+                    const bool sf = kb == it.kb0 || (kb & 3) == 0;
+                    ptx::mbar_arrive_expect_tx(fb, bytes + (sf ? sf_bytes : 0u));
+                    if (!waited) {
+                        ptx::grid_dependency_wait();
+                        waited = true;
+                    }
+                    if (sf) {
+                        const uint32_t st = base + OFF_SF + stage * SF_BYTES;
+                        const int64_t g = static_cast<int64_t>(kb >> 2) * 512;
+                        if (has_a) q8::bulk_load(st, sa + g, 512u, fb);
+                        for (int j = 0; j < sf_b; ++j) q8::bulk_load(st + 512u * (1 + j), sb + j * gstride + g, 512u, fb);
+                    }
+                    if (has_a) ptx::tma_load_2d(at, &maps.a[it.which], fb, kb * 128, row0);
+                    if (has_b) ptx::tma_load_2d(at + A_BYTES, &maps.b[it.which], fb, kb * 128, col0);
+                    issued |= 1u << stage;
+                    last_parity = (last_parity & ~(1u << stage)) | (phase << stage);
+                    if (++stage == STAGES) stage = 0, phase ^= 1u;
+                }
+            }
+            for (int s = 0; s < STAGES; ++s)
+                if ((issued >> s) & 1u)
+                    wt.wait(bars + 8u * (BAR_FULL + s), (last_parity >> s) & 1u, q8::SITE_TEARDOWN, -1, true);
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        if (leader && lane == 0) {
+            // -------------------------------------------------------- MMA issuer
+            uint32_t stage = 0, phase = 0, tile = 0, sf_buf = 0;
+            bool ok = true;
+            for (int r = 0; ok; ++r, ++tile) {
+                const int w = item_at(p, sch, r);
+                if (w >= p.n_items) break;
+                const Item it = decode(p, w);
+                const Prod& d = p.prod[it.which];
+                // both CTAs' epilogues have read the columns this tile shares with
+                // the one before (and, before that, all of this accumulator)
+                if (tile > 0 && !wt.wait(bars + 8u * BAR_ACC_FREE, (tile - 1) & 1u, q8::SITE_ACC_FREE, w)) break;
+                ptx::tc_fence_after();
+                const uint32_t acc = tmem + (tile & 1u) * ACC1;
+                uint32_t sfa = 0;
+                for (int kb = it.kb0; kb < it.kb1; ++kb) {
+                    if (!wt.wait(bars + 8u * (BAR_FULL + stage), phase, q8::SITE_FULL, w)) {
+                        ok = false;
+                        break;
+                    }
+                    ptx::tc_fence_after();
+                    if (kb == it.kb0 || (kb & 3) == 0) {
+                        const uint64_t sd = q8::scale_desc(base + OFF_SF + stage * SF_BYTES);
+                        sfa = tmem + SF_COL + sf_buf * SF_STRIDE;
+                        if (++sf_buf == SF_BUFS) sf_buf = 0;
+                        q8::copy_scales_pair(sfa, sd);
+                        q8::copy_scales_pair(sfa + 4, sd + 32);
+                        if (d.bn > 128) q8::copy_scales_pair(sfa + 8, sd + 64);
+                    }
+                    const uint32_t at = base + stage * STAGE_BYTES;
+                    const uint64_t a0 = ptx::smem_desc_sw128(at, 16, 1024);
+                    const uint64_t b0 = ptx::smem_desc_sw128(at + A_BYTES, 16, 1024);
+                    const uint32_t idesc = d.idesc | q8::scale_id(static_cast<uint32_t>(kb) & 3u);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)  // 32 values of K: 32 bytes further into each swizzled row
+                        q8::mma_mxf8_pair(acc, a0 + 2u * k, b0 + 2u * k, idesc, sfa, sfa + 4, (kb > it.kb0 || k > 0) ? 1u : 0u);
+                    ptx::mma_commit_pair_multicast(bars + 8u * (BAR_EMPTY + stage), 0x3u);
+                    if (++stage == STAGES) stage = 0, phase ^= 1u;
+                }
+                if (!ok) break;
+                ptx::mma_commit_pair_multicast(bars + 8u * BAR_ACC_FULL, 0x3u);
+            }
+            ptx::mma_commit_pair(bars + 8u * BAR_TEARDOWN);
+            wt.wait(bars + 8u * BAR_TEARDOWN, 0u, q8::SITE_TEARDOWN, -1, true);
+        } else if (!leader && lane == 0) {
+            // ---------------------------------------------- forwarder (odd CTA)
+            const uint32_t full0 = ptx::mapa(bars + 8u * BAR_FULL, 0);
+            uint32_t stage = 0, phase = 0;
+            bool ok = true;
+            for (int r = 0; ok; ++r) {
+                const int w = item_at(p, sch, r);
+                if (w >= p.n_items) break;
+                const Item it = decode(p, w);
+                for (int kb = it.kb0; kb < it.kb1; ++kb) {
+                    if (!wt.wait(bars + 8u * (BAR_FULL + stage), phase, q8::SITE_FORWARD, w)) {
+                        ok = false;
+                        break;
+                    }
+                    ptx::mbar_arrive_cluster_relaxed(full0 + 8u * stage);
+                    if (++stage == STAGES) stage = 0, phase ^= 1u;
+                }
+            }
+        }
+        __syncwarp();
+    } else {
+        // ------------------------------------------------------------ epilogue
+        const int ew = warp - FIRST_EPI;
+        const int q = warp & 3;   // tensor-memory lane quadrant this warp may read
+        const int h = ew >> 2;    // which of the quadrant's two warps
+        const uint32_t buf = base + OFF_CHUNKS + ew * CHUNK_BYTES;
+        const uint32_t old0 = bars + 8u * (BAR_OLD + ew * OLD_SLOTS);
+        const uint32_t free_bar = ptx::mapa(bars + 8u * BAR_ACC_FREE, 0);
+        uint32_t tile = 0, oldpar = 0, oldpend = 0;
+        for (int r = 0;; ++r, ++tile) {
+            const int w = item_at(p, sch, r);
+            if (w >= p.n_items) break;
+            const Item it = decode(p, w);
+            const Prod& d = p.prod[it.which];
+            const int64_t row0 = static_cast<int64_t>(it.pm) * PAIR_M + static_cast<int>(rank) * BM + q * 32;
+            const int col0 = it.n_tile * d.bn;
+            const int ncols = static_cast<int>(min(static_cast<int64_t>(d.bn), d.N - col0));
+            const int nk = d.bn / 64;  // this warp's chunks of a whole tile
+            const bool part = d.splits > 1;
+            const bool wide = part || d.f32;       // fp32 chunks: 128-byte rows, one buffer
+            const bool add = d.add && !part;
+            const int slots = wide ? 1 : OLD_SLOTS;
+            const uint32_t slot_bytes = wide ? 4096u : 2048u;
+            const bool in_rows = row0 < d.M;
+            // chunk of step k: the shared columns (the last 64 of the even
+            // accumulator, the first 64 of the odd one) come first
+            auto chunk = [&](int k) {
+                return (d.bn == 256 && (tile & 1u) == 0) ? (k == 0 ? 6 + h : 2 * (k - 1) + h) : 2 * k + h;
+            };
+            auto next = [&](int k) {
+                while (k < nk && chunk(k) * 32 >= ncols) ++k;
+                return k;
+            };
+            if (lane == 0) ptx::bulk_wait_read_all();  // the buffers are free
+            __syncwarp();
+            const CUtensorMap* dm = part ? &maps.part[it.which] : &maps.d[it.which];
+            int k = in_rows ? next(0) : nk;
+            int ahead = k;
+            if (add) {
+                for (int s = 0; s < slots && ahead < nk; ++s, ahead = next(ahead + 1))
+                    if (lane == 0) {
+                        ptx::mbar_arrive_expect_tx(old0 + 8u * s, slot_bytes);
+                        ptx::tma_load_2d(buf + s * slot_bytes, dm, old0 + 8u * s, col0 + chunk(ahead) * 32,
+                                         static_cast<int32_t>(row0));
+                        oldpend |= 1u << s;
+                    }
+            }
+            if (!wt.wait_warp(bars + 8u * BAR_ACC_FULL, tile & 1u, q8::SITE_ACC_FULL, w)) break;
+            ptx::tc_fence_after();
+            const uint32_t acc = tmem + (static_cast<uint32_t>(q * 32) << 16) + (tile & 1u) * ACC1;
+            bool released = false, ok = true;
+            auto release = [&]() {
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive_cluster_relaxed(free_bar);
+                released = true;
+            };
+            int x0 = 0;
+            int64_t y0 = row0;
+            if (part)  // [128-row tile x column tile][split][128][bn]
+                y0 = ((static_cast<int64_t>(it.pm * 2 + static_cast<int>(rank)) * d.tiles_n + it.n_tile) * d.splits + it.split) * BM +
+                     q * 32;
+            else
+                x0 = col0;
+            int slot = 0;
+            uint32_t used = 0;
+#pragma unroll 1
+            while (k < nk) {
+                const int c = chunk(k);
+                uint32_t v[32];
+                ptx::tmem_ld32(acc + c * 32, v);
+                if (!released) release();
+                const uint32_t at = buf + slot * slot_bytes;
+                if (add) {
+                    if (!wt.wait_warp(old0 + 8u * slot, (oldpar >> slot) & 1u, q8::SITE_OLD, w)) {
+                        ok = false;
+                        break;
+                    }
+                    oldpar ^= 1u << slot;
+                    oldpend &= ~(1u << slot);
+                } else {
+                    if (used >= static_cast<uint32_t>(slots) && lane == 0) {
+                        if (wide) ptx::bulk_wait_read_all();
+                        else ptx::bulk_wait_read_but_last();
+                    }
+                    __syncwarp();
+                }
+                ++used;
+                const int cc = col0 + c * 32;
+                if (wide) {  // row `lane`: 16-byte granule g at g ^ (lane & 7)
+                    const uint32_t row = at + lane * 128, swz = static_cast<uint32_t>(lane & 7);
+#pragma unroll
+                    for (int g = 0; g < 8; ++g) {
+                        const uint32_t a = row + ((static_cast<uint32_t>(g) ^ swz) << 4);
+                        float4 f = make_float4(__uint_as_float(v[4 * g]), __uint_as_float(v[4 * g + 1]),
+                                               __uint_as_float(v[4 * g + 2]), __uint_as_float(v[4 * g + 3]));
+                        if (!part) {
+                            if (d.bias && cc + 4 * g < d.N) {
+                                const float4 b = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(d.bias) + cc) + g);
+                                f.x += b.x, f.y += b.y, f.z += b.z, f.w += b.w;
+                            }
+                            if (add) {
+                                const float4 o = ptx::lds128f(a);
+                                f.x += o.x, f.y += o.y, f.z += o.z, f.w += o.w;
+                            }
+                        }
+                        ptx::sts128(a, f.x, f.y, f.z, f.w);
+                    }
+                } else {  // row `lane`: 16-byte granule g at g ^ ((lane >> 1) & 3)
+                    const uint32_t row = at + lane * 64, swz = static_cast<uint32_t>((lane >> 1) & 3);
+#pragma unroll
+                    for (int g = 0; g < 4; ++g) {
+                        const uint32_t a = row + ((static_cast<uint32_t>(g) ^ swz) << 4);
+                        uint4 o = make_uint4(0u, 0u, 0u, 0u);
+                        if (add)
+                            o = ptx::lds128(a);
+                        else if (d.bias && cc + 8 * g < d.N)
+                            o = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(d.bias) + cc) + g);
+                        const uint32_t ow[4] = {o.x, o.y, o.z, o.w};
+                        uint32_t rw[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            rw[e] = pack_bf16(__uint_as_float(v[8 * g + 2 * e]) + lo_bf16(ow[e]),
+                                              __uint_as_float(v[8 * g + 2 * e + 1]) + hi_bf16(ow[e]));
+                        ptx::sts128u(a, make_uint4(rw[0], rw[1], rw[2], rw[3]));
+                    }
+                }
+                ptx::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    ptx::tma_store_2d(dm, at, x0 + c * 32, static_cast<int32_t>(y0));
+                    ptx::bulk_commit_group();
+                }
+                if (add && ahead < nk) {  // refill this buffer once its store has read it
+                    if (lane == 0) {
+                        ptx::bulk_wait_read_all();
+                        ptx::mbar_arrive_expect_tx(old0 + 8u * slot, slot_bytes);
+                        ptx::tma_load_2d(at, dm, old0 + 8u * slot, col0 + chunk(ahead) * 32, static_cast<int32_t>(row0));
+                        oldpend |= 1u << slot;
+                    }
+                    ahead = next(ahead + 1);
+                }
+                __syncwarp();
+                if (++slot == slots) slot = 0;
+                k = next(k + 1);
+            }
+            if (!released) release();
+            if (!ok) break;
+        }
+        if (lane == 0) {
+            for (int s = 0; s < OLD_SLOTS; ++s)
+                if ((oldpend >> s) & 1u) wt.wait(old0 + 8u * s, (oldpar >> s) & 1u, q8::SITE_TEARDOWN, -1, true);
+            ptx::bulk_wait_all();
+        }
+        __syncwarp();
+    }
+
+    ptx::grid_launch_dependents();
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::cluster_sync();  // the even CTA's MMAs use both CTAs' memory
+    if (warp == 1) {
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc_pair(tmem, TMEM_COLS);
+    }
+}
+
+// D = (old D +) partial_0 + partial_1 + ... in split order, rounded once; four
+// columns per thread.
 template <typename T>
-__global__ void __launch_bounds__(256) q8_product_kernel(T* D, const T* bias, Operand A, Operand B, int64_t K, int add) {
-    __shared__ float sa[SP_K][SP_TILE + 1], sb[SP_K][SP_TILE + 1];
-    const int tid = static_cast<int>(threadIdx.x);
-    const int64_t tiles_n = (B.rows + SP_TILE - 1) / SP_TILE;
-    const int64_t m0 = blockIdx.x / tiles_n * SP_TILE, n0 = blockIdx.x % tiles_n * SP_TILE;
-    const int ty = tid / 16, tx = tid % 16;
+__global__ void __launch_bounds__(256) q8_join_kernel(T* D, const float* __restrict__ partials, int64_t M, int64_t N,
+                                                      int bn, int tiles_n, int splits, int add) {
     ptx::grid_launch_dependents();
     ptx::grid_dependency_wait();
-    float acc[4][4] = {};
-    for (int64_t k0 = 0; k0 < K; k0 += SP_K) {
-        for (int i = tid; i < SP_TILE * SP_K; i += 256) {
-            const int r = i / SP_K, k = i % SP_K;
-            sa[k][r] = load_value(A, m0 + r, k0 + k, K);
-            sb[k][r] = load_value(B, n0 + r, k0 + k, K);
+    const int64_t per_row = N / 4, n = M * per_row, stride = static_cast<int64_t>(gridDim.x) * blockDim.x;
+    const int64_t tile = static_cast<int64_t>(BM) * bn;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < n; i += stride) {
+        const int64_t row = i / per_row, col = (i - row * per_row) * 4;
+        const float* src = partials + ((row / BM) * tiles_n + col / bn) * splits * tile + (row % BM) * bn + col % bn;
+        float4 old = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (add) {
+            if constexpr (sizeof(T) == 4) {
+                old = *reinterpret_cast<const float4*>(D + row * N + col);
+            } else {
+                const uint2 o = *reinterpret_cast<const uint2*>(D + row * N + col);
+                old = make_float4(lo_bf16(o.x), hi_bf16(o.x), lo_bf16(o.y), hi_bf16(o.y));
+            }
         }
-        __syncthreads();
+        float4 s = __ldcg(reinterpret_cast<const float4*>(src));
 #pragma unroll 4
-        for (int k = 0; k < SP_K; ++k)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) acc[i][j] += sa[k][ty + 16 * i] * sb[k][tx + 16 * j];
-        __syncthreads();
-    }
-    for (int i = 0; i < 4; ++i)
-        for (int j = 0; j < 4; ++j) {
-            const int64_t m = m0 + ty + 16 * i, n = n0 + tx + 16 * j;
-            if (m >= A.rows || n >= B.rows) continue;
-            float v = acc[i][j];
-            if (bias) v += static_cast<float>(bias[n]);
-            if (add) v += static_cast<float>(D[m * B.rows + n]);
-            D[m * B.rows + n] = static_cast<T>(v);
+        for (int k = 1; k < splits; ++k) {
+            const float4 f = __ldcg(reinterpret_cast<const float4*>(src + k * tile));
+            s.x += f.x, s.y += f.y, s.z += f.z, s.w += f.w;
         }
+        if (add) s.x += old.x, s.y += old.y, s.z += old.z, s.w += old.w;
+        if constexpr (sizeof(T) == 4)
+            *reinterpret_cast<float4*>(D + row * N + col) = s;
+        else
+            *reinterpret_cast<uint2*>(D + row * N + col) = make_uint2(pack_bf16(s.x, s.y), pack_bf16(s.z, s.w));
+    }
+}
+
+// ------------------------------------------------------------------ planning
+
+struct ProductPlan {
+    int bn, tiles_m, tiles_n, kb, splits, kb_per_split, item0, items;
+    size_t ws_off, ws_bytes;
+};
+
+struct Plan {
+    ProductPlan p[2];
+    int n, n_items, table, grid;
+    size_t ws_bytes;
+    Schedule sched;
+};
+
+int ceil_div(int64_t a, int64_t b) { return static_cast<int>((a + b - 1) / b); }
+
+// Time model (us): a block of K costs t_kb, an item a handoff (the first chunk of
+// its epilogue) and, at the end, an epilogue that nothing overlaps; a split
+// product the pass that joins its partials.
+double kb_us(int bn) { return bn == 256 ? 0.30 : 0.22; }
+constexpr double ITEM_US = 0.6;
+double epi_us(const ProductPlan& p) { return (p.splits > 1 ? 3.0 : 2.0) * p.bn / 256.0; }
+
+double item_us(const ProductPlan& p, int split) {
+    const int k0 = split * p.kb_per_split, k1 = std::min(k0 + p.kb_per_split, p.kb);
+    return std::max((k1 - k0) * kb_us(p.bn), epi_us(p)) + ITEM_US;
+}
+
+double join_us(const ProductPlan& p, int64_t M, int64_t N) {
+    return p.splits == 1 ? 0.0 : 2.5 + static_cast<double>(M) * N * 4.0 * (p.splits + 1) / 8e6;
+}
+
+// Longest item first, each to the pair with the least work (ties to the lower
+// pair, items in order): a pure function of the plan. Returns the makespan.
+double assign(Plan& pl, int pairs) {
+    static thread_local double load[MAX_PAIRS];
+    static thread_local int cnt[MAX_PAIRS], order[MAX_ITEMS];
+    static thread_local float cost[MAX_ITEMS];
+    static thread_local uint8_t owner[MAX_ITEMS];
+    for (int i = 0; i < pl.n; ++i) {
+        const ProductPlan& p = pl.p[i];
+        const int tiles = p.tiles_m * p.tiles_n;
+        for (int k = 0; k < p.items; ++k) cost[p.item0 + k] = static_cast<float>(item_us(p, k / tiles));
+    }
+    for (int w = 0; w < pl.n_items; ++w) order[w] = w;
+    std::stable_sort(order, order + pl.n_items, [&](int a, int b) { return cost[a] > cost[b]; });
+    for (int c = 0; c < pairs; ++c) load[c] = 0.0, cnt[c] = 0;
+    for (int k = 0; k < pl.n_items; ++k) {
+        int best = 0;
+        for (int c = 1; c < pairs; ++c)
+            if (load[c] < load[best] - 1e-9) best = c;
+        load[best] += cost[order[k]];
+        owner[k] = static_cast<uint8_t>(best);
+        ++cnt[best];
+    }
+    pl.sched.start[0] = 0;
+    for (int c = 0; c < MAX_PAIRS; ++c)
+        pl.sched.start[c + 1] = static_cast<uint16_t>(pl.sched.start[c] + (c < pairs ? cnt[c] : 0));
+    int fill[MAX_PAIRS];
+    for (int c = 0; c < pairs; ++c) fill[c] = pl.sched.start[c];
+    for (int k = 0; k < pl.n_items; ++k) pl.sched.items[fill[owner[k]]++] = static_cast<uint16_t>(order[k]);
+    double m = 0.0;
+    for (int c = 0; c < pairs; ++c) m = std::max(m, load[c]);
+    return m;
+}
+
+struct Shape3 {
+    int64_t M, N, K;
+};
+
+// Overrides for tuning and tests: MMBWD_Q8_TILE_N and MMBWD_Q8_SPLITS = "<first
+// product>,<second product>" (dinp, dweight; 0: the planner's choice).
+struct Forced {
+    int bn[2], splits[2];
+    bool operator==(const Forced& o) const { return std::memcmp(this, &o, sizeof(o)) == 0; }
+};
+
+Forced forced_from_env() {
+    Forced f{};
+    if (const char* t = std::getenv("MMBWD_Q8_TILE_N")) {
+        int a = 0, b = 0;
+        if (std::sscanf(t, "%d,%d", &a, &b) == 2) {
+            f.bn[0] = a == 128 || a == 256 ? a : 0;
+            f.bn[1] = b == 128 || b == 256 ? b : 0;
+        }
+    }
+    if (const char* t = std::getenv("MMBWD_Q8_SPLITS")) {
+        int a = 0, b = 0;
+        if (std::sscanf(t, "%d,%d", &a, &b) == 2) f.splits[0] = std::max(0, std::min(a, 16)), f.splits[1] = std::max(0, std::min(b, 16));
+    }
+    return f;
+}
+
+// The best plan by the time model over tile widths and, where allowed, splits.
+void make_plan(const Shape3* s, int n, bool may_split, const Forced& force, int num_sms, Plan* out) {
+    static thread_local Plan c;
+    const int max_pairs = std::max(1, std::min(num_sms / 2, MAX_PAIRS));
+    double best = 1e300;
+    static const int kSplits[] = {1, 2, 3, 4, 6, 8, 12, 16};
+    for (int widths = 0; widths < (n == 2 ? 4 : 2); ++widths)
+        for (int s0 : kSplits)
+            for (int s1 : kSplits) {
+                if ((n == 1 && s1 > 1) || (!may_split && (s0 > 1 || s1 > 1))) continue;
+                bool skip = false;
+                for (int i = 0; i < n; ++i) {
+                    const int bn = (widths >> i) & 1 ? 128 : 256, want = i == 0 ? s0 : s1;
+                    if (force.bn[i] && force.bn[i] != bn) skip = true;
+                    // a forced count above the number of blocks, or one that would leave
+                    // an empty range, is lowered to the nearest that does not
+                    if (may_split && force.splits[i]) {
+                        const int kb = ceil_div(s[i].K, 128), per = ceil_div(kb, std::min(force.splits[i], kb));
+                        const int count = ceil_div(kb, per);
+                        int usable = 1;
+                        for (int o : kSplits)
+                            if (o <= count && ceil_div(kb, ceil_div(kb, o)) == o) usable = o;
+                        if (want != usable) skip = true;
+                    }
+                }
+                if (skip) continue;
+                c.n = n;
+                c.n_items = 0;
+                c.ws_bytes = 0;
+                bool ok = true;
+                double work = 0.0, longest = 0.0, tail = 0.0;
+                int64_t total = 0;
+                for (int i = 0; i < n; ++i) {
+                    ProductPlan& p = c.p[i];
+                    p.bn = (widths >> i) & 1 ? 128 : 256;
+                    p.tiles_m = ceil_div(s[i].M, PAIR_M);
+                    p.tiles_n = ceil_div(s[i].N, p.bn);
+                    p.kb = ceil_div(s[i].K, 128);
+                    const int want = i == 0 ? s0 : s1;
+                    p.kb_per_split = ceil_div(p.kb, std::min(want, p.kb));
+                    p.splits = ceil_div(p.kb, p.kb_per_split);
+                    if (want > 1 && p.splits != want) ok = false;
+                    const int64_t tiles = static_cast<int64_t>(p.tiles_m) * p.tiles_n;
+                    p.item0 = static_cast<int>(total);
+                    total += tiles * p.splits;
+                    if (total > INT32_MAX) {
+                        ok = false;
+                        break;
+                    }
+                    p.items = static_cast<int>(tiles * p.splits);
+                    p.ws_off = c.ws_bytes;
+                    const int64_t part_rows = 2 * tiles * p.splits * BM;
+                    if (p.splits > 1 && (part_rows > INT32_MAX || total > MAX_ITEMS)) ok = false;
+                    p.ws_bytes = p.splits > 1 ? static_cast<size_t>(part_rows) * p.bn * 4 : 0;
+                    c.ws_bytes += p.ws_bytes;
+                    for (int k = 0; k < p.splits; ++k) {
+                        work += item_us(p, k) * tiles;
+                        longest = std::max(longest, item_us(p, k));
+                    }
+                    tail += join_us(p, s[i].M, s[i].N);
+                }
+                if (!ok) continue;
+                c.n_items = static_cast<int>(total);
+                c.table = c.n_items <= MAX_ITEMS ? 1 : 0;
+                const int pairs = static_cast<int>(std::min<int64_t>(total, max_pairs));
+                c.grid = 2 * pairs;
+                if (std::max(work / pairs, longest) + tail >= best) continue;
+                double t = tail;
+                if (c.table)
+                    t += assign(c, pairs);
+                else
+                    t += std::ceil(static_cast<double>(total) / pairs) * longest;
+                if (t < best) {
+                    best = t;
+                    *out = c;
+                }
+            }
+}
+
+// Plans are pure functions of the shape and the device's resident pairs; the
+// search is remembered for the last shapes seen.
+struct Key {
+    Shape3 s[2];
+    int n, split, sms;
+    Forced force;
+};
+constexpr int CACHE = 32;
+std::mutex g_plan_mutex;
+Key g_keys[CACHE];
+Plan g_plans[CACHE];
+int g_plan_count = 0, g_plan_next = 0;
+
+bool same_key(const Key& a, const Key& b) {
+    if (a.n != b.n || a.split != b.split || a.sms != b.sms || !(a.force == b.force)) return false;
+    for (int i = 0; i < a.n; ++i)
+        if (a.s[i].M != b.s[i].M || a.s[i].N != b.s[i].N || a.s[i].K != b.s[i].K) return false;
+    return true;
+}
+
+// Caller holds g_plan_mutex while it uses the result.
+const Plan& plan_for(const Shape3* s, int n, bool may_split, int num_sms) {
+    Key k{};
+    k.n = n;
+    k.split = may_split ? 1 : 0;
+    k.sms = num_sms;
+    k.force = forced_from_env();
+    for (int i = 0; i < n; ++i) k.s[i] = s[i];
+    for (int i = 0; i < g_plan_count; ++i)
+        if (same_key(g_keys[i], k)) return g_plans[i];
+    const int slot = g_plan_next;
+    g_plan_next = (g_plan_next + 1) % CACHE;
+    if (g_plan_count < CACHE) ++g_plan_count;
+    g_keys[slot] = k;
+    make_plan(s, n, may_split, k.force, num_sms, &g_plans[slot]);
+    return g_plans[slot];
+}
+
+// ------------------------------------------------------------------ launch
+
+bool encode_2d(CUtensorMap* m, CUtensorMapDataType type, const void* base, uint64_t inner, uint64_t rows, uint64_t pitch,
+               uint32_t box_inner, uint32_t box_rows, CUtensorMapSwizzle swz) {
+    EncodeTiledFn encode = get_encode_tiled();
+    if (!encode) return false;
+    const cuuint64_t dims[2] = {inner, rows}, strides[1] = {pitch};
+    const cuuint32_t box[2] = {box_inner, box_rows}, estr[2] = {1, 1};
+    return encode(m, type, 2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swz,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+cudaError_t set_smem_once() {
+    static std::mutex m;
+    static bool done[64];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    std::lock_guard<std::mutex> g(m);
+    if (dev >= 0 && dev < 64 && done[dev]) return cudaSuccess;
+    e = cudaFuncSetAttribute(q8_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
+    if (e == cudaSuccess && dev >= 0 && dev < 64) done[dev] = true;
+    return e;
+}
+
+cudaError_t launch_pair(const Plan& pl, const Q8Product* prod, uint8_t* ws, cudaStream_t stream) {
+    cudaError_t e = set_smem_once();
+    if (e != cudaSuccess) return e;
+    static thread_local Maps maps;
+    Params par{};
+    par.n_prod = pl.n;
+    par.n_items = pl.n_items;
+    par.table = pl.table;
+    for (int i = 0; i < pl.n; ++i) {
+        const Q8Product& q = prod[i];
+        const ProductPlan& pp = pl.p[i];
+        const uint64_t ld = static_cast<uint64_t>(q8_ld(q.K)), m = static_cast<uint64_t>(q.M), n = static_cast<uint64_t>(q.N);
+        const bool f32 = q.dtype == MMBWD_F32;
+        const CUtensorMapDataType dt = f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+        bool ok = encode_2d(&maps.a[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, q.A, ld, m, ld, 128, BM, CU_TENSOR_MAP_SWIZZLE_128B) &&
+                  encode_2d(&maps.b[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, q.B, ld, n, ld, 128,
+                            static_cast<uint32_t>(pp.bn / 2), CU_TENSOR_MAP_SWIZZLE_128B) &&
+                  encode_2d(&maps.d[i], dt, q.D, n, m, n * (f32 ? 4 : 2), 32, 32,
+                            f32 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
+        if (ok && pp.splits > 1)
+            ok = encode_2d(&maps.part[i], CU_TENSOR_MAP_DATA_TYPE_FLOAT32, ws + pp.ws_off, static_cast<uint64_t>(pp.bn),
+                           pp.ws_bytes / (static_cast<uint64_t>(pp.bn) * 4), static_cast<uint64_t>(pp.bn) * 4, 32, 32,
+                           CU_TENSOR_MAP_SWIZZLE_128B);
+        if (!ok) return cudaErrorInvalidValue;
+        Prod& d = par.prod[i];
+        d.a_scale = q.a_scale, d.b_scale = q.b_scale, d.bias = q.bias;
+        d.M = q.M, d.N = q.N;
+        d.groups = static_cast<int>(q8_groups(q.K));
+        d.bn = pp.bn, d.tiles_m = pp.tiles_m, d.tiles_n = pp.tiles_n, d.kb = pp.kb;
+        d.splits = pp.splits, d.kb_per_split = pp.kb_per_split, d.item0 = pp.item0;
+        d.f32 = f32 ? 1 : 0, d.add = q.add;
+        d.idesc = q8::idesc_mxf8(PAIR_M, pp.bn, q.a_format, q.b_format);
+    }
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 2;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(pl.grid), 1, 1);
+    cfg.blockDim = dim3(THREADS, 1, 1);
+    cfg.dynamicSmemBytes = SMEM_BYTES;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    e = cudaLaunchKernelEx(&cfg, q8_pair_kernel, maps, par, pl.sched);
+    for (int i = 0; i < pl.n && e == cudaSuccess; ++i) {
+        const ProductPlan& pp = pl.p[i];
+        if (pp.splits == 1) continue;
+        const Q8Product& q = prod[i];
+        cudaLaunchConfig_t jc{};
+        jc.gridDim = dim3(static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>((q.M * (q.N / 4) + 255) / 256, 1216))), 1, 1);
+        jc.blockDim = dim3(256, 1, 1);
+        jc.stream = stream;
+        jc.attrs = attr;
+        jc.numAttrs = 1;
+        const float* part = reinterpret_cast<const float*>(ws + pp.ws_off);
+        e = q.dtype == MMBWD_F32
+                ? cudaLaunchKernelEx(&jc, q8_join_kernel<float>, static_cast<float*>(q.D), part, q.M, q.N, pp.bn,
+                                     pp.tiles_n, pp.splits, q.add)
+                : cudaLaunchKernelEx(&jc, q8_join_kernel<__nv_bfloat16>, static_cast<__nv_bfloat16*>(q.D), part, q.M, q.N,
+                                     pp.bn, pp.tiles_n, pp.splits, q.add);
+    }
+    return e;
 }
 
 }  // namespace
 
-cudaError_t q8_product_launch(const Q8Product* products, int n, cudaStream_t stream) {
+size_t q8_products_workspace(const Q8Product* products, int n, int num_sms) {
+    Shape3 s[2];
+    for (int i = 0; i < n; ++i) s[i] = {products[i].M, products[i].N, products[i].K};
+    std::lock_guard<std::mutex> g(g_plan_mutex);
+    return plan_for(s, n, true, num_sms).ws_bytes;
+}
+
+cudaError_t q8_products_launch(const Q8Product* products, int n, bool may_split, void* ws, size_t ws_bytes, int num_sms,
+                               cudaStream_t stream) {
     if (take_injected_launch_failure()) return cudaErrorLaunchFailure;
-    for (int i = 0; i < n; ++i) {
-        const Q8Product& p = products[i];
-        const Operand A{p.A, p.a_scale, p.M, q8_ld(p.K), q8_groups(p.K), p.a_format};
-        const Operand B{p.B, p.b_scale, p.N, q8_ld(p.K), q8_groups(p.K), p.b_format};
-        const int64_t tiles = ((p.M + SP_TILE - 1) / SP_TILE) * ((p.N + SP_TILE - 1) / SP_TILE);
-        cudaLaunchConfig_t cfg{};
-        cfg.gridDim = dim3(static_cast<unsigned>(tiles), 1, 1);
-        cfg.blockDim = dim3(256, 1, 1);
-        cfg.stream = stream;
-        cudaLaunchAttribute attr[1];
-        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[0].val.programmaticStreamSerializationAllowed = 1;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
-        const cudaError_t e =
-            p.dtype == MMBWD_F32
-                ? cudaLaunchKernelEx(&cfg, q8_product_kernel<float>, static_cast<float*>(p.D),
-                                     static_cast<const float*>(p.bias), A, B, p.K, p.add)
-                : cudaLaunchKernelEx(&cfg, q8_product_kernel<__nv_bfloat16>, static_cast<__nv_bfloat16*>(p.D),
-                                     static_cast<const __nv_bfloat16*>(p.bias), A, B, p.K, p.add);
-        if (e != cudaSuccess) return e;
+    Shape3 s[2];
+    for (int i = 0; i < n; ++i) s[i] = {products[i].M, products[i].N, products[i].K};
+    std::lock_guard<std::mutex> g(g_plan_mutex);
+    const Plan& pl = plan_for(s, n, may_split, num_sms);
+    if (pl.ws_bytes > ws_bytes) return cudaErrorInvalidValue;
+    return launch_pair(pl, products, static_cast<uint8_t*>(ws), stream);
+}
+
+cudaError_t q8_read_status(int* code, int* info3, bool reset) {
+    unsigned int h[4] = {0, 0, 0, 0};
+    cudaError_t e = cudaMemcpyFromSymbol(h, g_q8_status, sizeof(h));
+    if (e != cudaSuccess) return e;
+    *code = h[0] ? -static_cast<int>(h[0]) : MMBWD_OK;
+    for (int i = 0; i < 3; ++i) info3[i] = static_cast<int>(h[1 + i]);
+    if (reset) {
+        const unsigned int z[4] = {0, 0, 0, 0};
+        e = cudaMemcpyToSymbol(g_q8_status, z, sizeof(z));
     }
-    return cudaSuccess;
+    return e;
 }
 
 }  // namespace mmbwd

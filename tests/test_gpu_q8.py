@@ -248,6 +248,40 @@ def test_backward(shape, types):
         assert np.all(np.abs(host(dw) - want) <= tol)
 
 
+@pytest.mark.parametrize("tiles", ["256,256", "128,128", "128,256"])
+@pytest.mark.parametrize("splits", ["1,1", "2,3", "4,1", "1,8"])
+def test_backward_splits_and_tile_widths(monkeypatch, splits, tiles):
+    """Every tile width and split count the planner may take gives the result,
+    in one order of additions."""
+    import torch
+
+    monkeypatch.setenv("MMBWD_Q8_SPLITS", splits)
+    monkeypatch.setenv("MMBWD_Q8_TILE_N", tiles)
+    T, C, OC = 1400, 392, 1096
+    d, inp, w = normal((T, OC), "bf16", 4, 1e-2), normal((T, C), "bf16", 5), normal((OC, C), "bf16", 6, 0.02)
+    dq, ds, dv = q8(d, mm.E4M3)
+    dqt, dst, dvt = q8(d.T, mm.E4M3)
+    iqt, ist, ivt = q8(inp.T, mm.E4M3)
+    wqt, wst, wvt = q8(w.T, mm.E4M3)
+    n = mm.mmbwd_q8_backward_workspace_bytes(1, T, C, OC)
+    assert (n > 0) == (splits != "1,1")
+    ws = torch.full((max(n, 1),), 0xFF, dtype=torch.uint8, device="cuda")
+    old = [normal((T, C), "bf16", 7), normal((OC, C), "f32", 8)]
+    for add in (0, 3):
+        got = []
+        for _ in range(2):
+            dinp, dw = dev(old[0], "bf16"), dev(old[1], "f32")
+            assert mm.mmbwd_q8_backward(dinp, dw, dq, ds, dqt, dst, iqt, ist, wqt, wst, ws, n, 1, T, C, OC, 0, 0, 0,
+                                        mm.BF16, mm.F32, add) == mm.OK
+            torch.cuda.synchronize()
+            got.append((dinp, dw))
+        assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+        want, tol = ref.product_bound(dv, wvt, "bf16", old[0] if add else 0.0)
+        assert np.all(np.abs(host(got[0][0]) - want) <= tol)
+        want, tol = ref.product_bound(dvt, ivt, "f32", old[1] if add else 0.0)
+        assert np.all(np.abs(host(got[0][1]) - want) <= tol)
+
+
 def test_backward_one_output_only():
     import torch
 
