@@ -121,6 +121,8 @@ def _stream(stream) -> int:
         return int(stream)
     import torch  # only for the current stream handle
 
+    if torch.cuda.is_initialized():  # the handle alone: 0.1 us, building a Stream object 2.9 us
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     return torch.cuda.current_stream().cuda_stream
 
 

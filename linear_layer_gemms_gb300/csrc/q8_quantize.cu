@@ -3,16 +3,26 @@
 // (column form: the 8-bit form of the transposed matrix), or both from one
 // read of x, with the column sums of x on request.
 //
-// Bound by HBM: es bytes read and one byte written per element and form. A
-// block of 256 threads takes a 128 x 128 tile, so that one tile holds whole
-// blocks of both directions. Thread (g, u) = (tid / 16, tid % 16) keeps rows
-// 8g .. 8g+7 of columns 8u .. 8u+7 in registers: a row's maximum is then four
-// shuffles over the 16 lanes that share the row; a column's maximum goes over
-// the eight rows in registers, one shuffle, and a shared-memory atomic maximum
-// across the eight warps (exact, so its order does not matter). The column
-// form's bytes are turned through shared memory (16 KB; the 8-byte granule g
-// of column c at g ^ (c / 8), free of bank conflicts in both directions) and
-// written as 128 contiguous bytes per column.
+// Bound by HBM: es bytes read and one byte written per element and form (31 us
+// for 8192 x 6400 bf16 into both forms at the measured copy rate). A block of 256
+// threads takes a 128 x 128 tile, so that one tile holds whole blocks of both
+// directions. Thread (g, u) = (tid / 16, tid % 16) keeps rows 8g .. 8g+7 of
+// columns 8u .. 8u+7 in registers as they are stored: a row's maximum is then four
+// shuffles over the 16 lanes that share the row (two rows to a word in bf16); a
+// column's maximum goes over the eight rows in registers, one shuffle, and a
+// shared-memory atomic maximum across the eight warps (exact, so its order does
+// not matter). The column form's bytes are turned through shared memory (16 KB; the
+// 8-byte granule g of column c at g ^ (c / 8), free of bank conflicts in both
+// directions) and written as 128 contiguous bytes per column.
+//
+// Next to the bytes the integer pipe is the limit (64 % busy at 8192 x 6400), so
+// the inner steps are chosen for few instructions: maxima by max.xorsign.abs
+// (no sign masks; a NaN wins, which is how a tile with a non-finite value is
+// found and sent down a path of its own), scales by one carrying addition, bf16
+// halves multiplied and summed into fp32 without unpacking them. 8192 x 6400 bf16:
+// row form 24.3 us (6.5 TB/s), column form 22.7, both 36.4 (5.8 TB/s), both with
+// the column sums 40.3; the first version, with a finiteness test per value,
+// took 110. Four blocks an SM against three: 36.4 against 40.
 #include "../../include/q8_linear.h"
 #include "ops.h"
 #include "ptx.cuh"
@@ -46,190 +56,356 @@ struct Fmt<MMBWD_E5M2> {
     }
 };
 
-// Scale byte (s + 127) of a block whose largest finite magnitude is amax >= 0:
-// both formats' largest value is 1.75 * 2^EMAX, so amax = m * 2^p (m in [1, 2))
-// needs s = p - EMAX, one more when m > 1.75.
+// Scale byte (s + 127) of a block whose largest finite magnitude has the fp32
+// bits b: both formats' largest value is 1.75 * 2^EMAX, so amax = m * 2^p (m in
+// [1, 2)) needs s = p - EMAX, one more when m > 1.75: adding 0x1FFFFF to the
+// bits carries into the exponent exactly then.
 template <int FMT>
-__device__ __forceinline__ int scale_byte(float amax) {
-    const uint32_t b = __float_as_uint(amax);
+__device__ __forceinline__ int scale_byte(uint32_t b) {
     if (b == 0u) return 127;
-    const int s = static_cast<int>(b >> 23) - 127 - Fmt<FMT>::EMAX + ((b & 0x7FFFFFu) > 0x600000u ? 1 : 0);
-    return s < -127 ? 0 : s + 127;
+    const int e = static_cast<int>((b + 0x1FFFFFu) >> 23) - Fmt<FMT>::EMAX;
+    return e < 0 ? 0 : e;
 }
 
-// 2^-s of a scale byte (s in -127 .. 120, so the result is a normal number).
-__device__ __forceinline__ float inv_scale(int byte) { return __uint_as_float(static_cast<uint32_t>(254 - byte) << 23); }
+// 2^-s of the same block, as fp32 bits (s in -127 .. 120: a normal number). A
+// block of zeros gets the largest, which leaves them zeros.
+template <int FMT>
+__device__ __forceinline__ uint32_t inv_scale(uint32_t b) {
+    constexpr uint32_t LOW = static_cast<uint32_t>(Fmt<FMT>::EMAX) << 23, TOP = static_cast<uint32_t>(254 + Fmt<FMT>::EMAX) << 23;
+    const uint32_t t = b + 0x1FFFFFu;
+    return TOP - ((t > LOW ? t : LOW) & 0xFF800000u);
+}
+// The same for two bf16 magnitudes in one word, as a bf16 pair.
+template <int FMT>
+__device__ __forceinline__ uint32_t inv_scale2(uint32_t p) {
+    constexpr uint32_t LOW = (Fmt<FMT>::EMAX << 7) * 0x00010001u, TOP = ((254 + Fmt<FMT>::EMAX) << 7) * 0x00010001u;
+    return TOP - (__vmaxu2(p + 0x001F001Fu, LOW) & 0xFF80FF80u);
+}
 
-// Eight consecutive values of a row, as they are stored.
+__device__ __forceinline__ uint32_t lo_bf16(uint32_t w) { return w << 16; }
+__device__ __forceinline__ uint32_t hi_bf16(uint32_t w) { return w & 0xFFFF0000u; }
+
+// Eight consecutive values of a row as they are stored: W words. larger():
+// per value the larger magnitude of two, a NaN if either is one; its sign
+// means nothing (max.NaN.xorsign.abs takes magnitudes without extra instructions).
 template <typename T>
-struct Raw8;
+struct Eight;
+
 template <>
-struct Raw8<__nv_bfloat16> {
-    uint4 a;
-    __device__ void zero() { a = make_uint4(0u, 0u, 0u, 0u); }
-    __device__ void load(const __nv_bfloat16* p, int64_t left) {  // left >= 1: whole vectors remain
-        a = left >= 8 ? __ldcs(reinterpret_cast<const uint4*>(p)) : make_uint4(0u, 0u, 0u, 0u);
+struct Eight<__nv_bfloat16> {
+    static constexpr int W = 4;  // two values a word
+    static constexpr uint32_t MAG = 0x7FFF7FFFu;
+    uint32_t w[4];
+    __device__ void load(const __nv_bfloat16* p, int64_t left) {  // left: values up to the row's end, <= 0: none
+        const uint4 a = left >= 8 ? __ldcs(reinterpret_cast<const uint4*>(p)) : make_uint4(0u, 0u, 0u, 0u);
+        w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
     }
+    __device__ static uint32_t larger(uint32_t a, uint32_t b) {
+        uint32_t r;
+        asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+        return r;
+    }
+    // whether a maximum (sign cleared) is an infinity or a NaN
+    __device__ static bool bad(uint32_t m) { return (m & 0xFFFFu) >= 0x7F80u || (m >> 16) >= 0x7F80u; }
+    // value e of eight maxima, as fp32 bits
+    __device__ static uint32_t bits(const uint32_t (&m)[4], int e) { return e & 1 ? hi_bf16(m[e >> 1]) : lo_bf16(m[e >> 1]); }
     __device__ void get(float (&f)[8]) const {
-        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            f[2 * i] = __uint_as_float(w[i] << 16);
-            f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-        }
+        for (int i = 0; i < 4; ++i) f[2 * i] = __uint_as_float(lo_bf16(w[i])), f[2 * i + 1] = __uint_as_float(hi_bf16(w[i]));
     }
 };
+
 template <>
-struct Raw8<float> {
-    float4 a, b;
-    __device__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+struct Eight<float> {
+    static constexpr int W = 8;
+    static constexpr uint32_t MAG = 0x7FFFFFFFu;
+    uint32_t w[8];
     __device__ void load(const float* p, int64_t left) {
-        a = left >= 4 ? __ldcs(reinterpret_cast<const float4*>(p)) : make_float4(0.f, 0.f, 0.f, 0.f);
-        b = left >= 8 ? __ldcs(reinterpret_cast<const float4*>(p) + 1) : make_float4(0.f, 0.f, 0.f, 0.f);
+        const uint4 z = make_uint4(0u, 0u, 0u, 0u);
+        const uint4 a = left >= 4 ? __ldcs(reinterpret_cast<const uint4*>(p)) : z;
+        const uint4 b = left >= 8 ? __ldcs(reinterpret_cast<const uint4*>(p) + 1) : z;
+        w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
     }
+    __device__ static uint32_t larger(uint32_t a, uint32_t b) {
+        float r;
+        asm("max.NaN.xorsign.abs.f32 %0, %1, %2;" : "=f"(r) : "f"(__uint_as_float(a)), "f"(__uint_as_float(b)));
+        return __float_as_uint(r);
+    }
+    __device__ static bool bad(uint32_t m) { return m >= 0x7F800000u; }
+    __device__ static uint32_t bits(const uint32_t (&m)[8], int e) { return m[e]; }
     __device__ void get(float (&f)[8]) const {
-        f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w;
-        f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(w[i]);
     }
 };
 
 __device__ __forceinline__ bool finite(float x) { return (__float_as_uint(x) & 0x7F800000u) != 0x7F800000u; }
 
+// A tile's shared memory.
+struct TileMem {
+    uint32_t col_max[128];
+    uint32_t col_inv[128];  // 2^-s as fp32 bits
+    float sums[8][128];
+    alignas(16) uint8_t turned[128 * 128];
+};
+
+// Products and sums of a bf16 half of a word in fp32, one instruction each
+// without unpacking it (x * s - 0: exact, and keeps the sign of a zero).
+template <int HALF>
+__device__ __forceinline__ float mul_half(uint32_t w, uint32_t s) {
+    float r;
+    if constexpr (HALF == 0)
+        asm("{.reg .b16 a, b, c, d;\n\tmov.b32 {a, b}, %1;\n\tmov.b32 {c, d}, %2;\n\tfma.rn.f32.bf16 %0, a, c, %3;}"
+            : "=f"(r) : "r"(w), "r"(s), "f"(-0.0f));
+    else
+        asm("{.reg .b16 a, b, c, d;\n\tmov.b32 {a, b}, %1;\n\tmov.b32 {c, d}, %2;\n\tfma.rn.f32.bf16 %0, b, d, %3;}"
+            : "=f"(r) : "r"(w), "r"(s), "f"(-0.0f));
+    return r;
+}
+template <int HALF>
+__device__ __forceinline__ float add_half(uint32_t w, float acc) {
+    float r;
+    if constexpr (HALF == 0)
+        asm("{.reg .b16 a, b;\n\tmov.b32 {a, b}, %1;\n\tadd.rn.f32.bf16 %0, a, %2;}" : "=f"(r) : "r"(w), "f"(acc));
+    else
+        asm("{.reg .b16 a, b;\n\tmov.b32 {a, b}, %1;\n\tadd.rn.f32.bf16 %0, b, %2;}" : "=f"(r) : "r"(w), "f"(acc));
+    return r;
+}
+
+// Values 2i, 2i+1 of `v` times two scales given as fp32 bits (bf16: as a bf16
+// pair in s0): exact, the scales being powers of two. RARE: a product that is
+// not finite becomes a NaN.
+template <typename T, bool RARE>
+__device__ __forceinline__ void two(const Eight<T>& v, int i, uint32_t s0, uint32_t s1, float& a, float& b) {
+    if constexpr (sizeof(T) == 2) {
+        a = mul_half<0>(v.w[i], s0), b = mul_half<1>(v.w[i], s0);
+    } else {
+        a = __uint_as_float(v.w[2 * i]) * __uint_as_float(s0), b = __uint_as_float(v.w[2 * i + 1]) * __uint_as_float(s1);
+    }
+    if constexpr (RARE) {
+        const float n = __uint_as_float(0x7FFFFFFFu);
+        a = finite(a) ? a : n, b = finite(b) ? b : n;
+    }
+}
+
+// The row form of a tile, from registers.
+template <typename T, int FMT, bool RARE>
+__device__ __forceinline__ void row_form(const Eight<T> (&v)[8], uint8_t* __restrict__ q, uint8_t* __restrict__ scale,
+                                         int64_t tr, int64_t tc, int64_t rows, int64_t ld, int64_t kb) {
+    using E = Eight<T>;
+    const int tid = static_cast<int>(threadIdx.x), g = tid >> 4, u = tid & 15;
+    const int64_t c = tc * 128 + 8 * u, r0 = tr * 128 + 8 * g;
+    uint32_t mine = 0;  // maximum of row 8g + u, as fp32 bits
+    uint8_t* dst = q + r0 * ld + c;
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+        uint32_t t[2];  // the two rows' maxima over this thread's values
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const E& x = v[i + e];
+            if constexpr (RARE) {
+                float f[8], best = 0.f;
+                x.get(f);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) best = finite(f[j]) ? fmaxf(best, fabsf(f[j])) : best;
+                t[e] = __float_as_uint(best);
+                if constexpr (sizeof(T) == 2) t[e] |= t[e] >> 16;
+            } else {
+                t[e] = E::larger(x.w[0], x.w[1]);
+#pragma unroll
+                for (int k = 2; k < E::W; ++k) t[e] = E::larger(t[e], x.w[k]);
+            }
+        }
+        uint32_t s0[2];
+        if constexpr (sizeof(T) == 2) {  // both rows' maxima in one word through the shuffles
+            uint32_t p = E::larger(__byte_perm(t[0], t[1], 0x5410), __byte_perm(t[0], t[1], 0x7632));
+#pragma unroll
+            for (int o = 1; o < 16; o <<= 1) p = E::larger(p, __shfl_xor_sync(0xffffffffu, p, o));
+            p &= E::MAG;
+            if (u == i) mine = lo_bf16(p);
+            if (u == i + 1) mine = hi_bf16(p);
+            const uint32_t inv = inv_scale2<FMT>(p);
+            s0[0] = __byte_perm(inv, 0u, 0x1010), s0[1] = __byte_perm(inv, 0u, 0x3232);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                for (int o = 1; o < 16; o <<= 1) t[e] = E::larger(t[e], __shfl_xor_sync(0xffffffffu, t[e], o));
+                t[e] &= E::MAG;
+                if (u == i + e) mine = t[e];
+                s0[e] = inv_scale<FMT>(t[e]);
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            uint32_t w[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                float a, b;
+                two<T, RARE>(v[i + e], j, s0[e], s0[e], a, b);
+                w[j] = Fmt<FMT>::pack2(a, b);
+            }
+            if (r0 + i + e < rows && c < ld)
+                *reinterpret_cast<uint2*>(dst + (i + e) * ld) = make_uint2(__byte_perm(w[0], w[1], 0x5410), __byte_perm(w[2], w[3], 0x5410));
+        }
+    }
+    if (u < 8) {  // lane u of the sixteen holds row 8g + u
+        const int rl = 8 * g + u;
+        uint8_t* at = scale + (tr * ((kb + 3) / 4) + tc / 4) * 512 + (rl % 32) * 16 + (rl / 32) * 4;
+        at[tc % 4] = static_cast<uint8_t>(scale_byte<FMT>(mine));
+        if (tc == kb - 1)
+            for (int64_t k = tc % 4 + 1; k < 4; ++k) at[k] = 127;
+    }
+}
+
+// The column form's bytes of a tile into `turned`, from registers.
+template <typename T, int FMT, bool RARE>
+__device__ __forceinline__ void turn_columns(const Eight<T> (&v)[8], TileMem& sm) {
+    const int tid = static_cast<int>(threadIdx.x), g = tid >> 4, u = tid & 15;
+    uint32_t inv[8];  // as fp32 bits; bf16: words 0 .. 3 hold pairs
+    *reinterpret_cast<uint4*>(inv) = *reinterpret_cast<const uint4*>(&sm.col_inv[8 * u]);
+    *reinterpret_cast<uint4*>(inv + 4) = *reinterpret_cast<const uint4*>(&sm.col_inv[8 * u + 4]);
+    if constexpr (sizeof(T) == 2) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) inv[j] = __byte_perm(inv[2 * j], inv[2 * j + 1], 0x7632);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {  // columns 2j and 2j + 1, byte i of each is row i
+        const uint32_t i0 = sizeof(T) == 2 ? inv[j] : inv[2 * j], i1 = sizeof(T) == 2 ? 0u : inv[2 * j + 1];
+        uint32_t lo[4], hi[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float a0, b0, a1, b1;
+            two<T, RARE>(v[2 * i], j, i0, i1, a0, b0);
+            two<T, RARE>(v[2 * i + 1], j, i0, i1, a1, b1);
+            lo[i] = Fmt<FMT>::pack2(a0, a1), hi[i] = Fmt<FMT>::pack2(b0, b1);
+        }
+        uint8_t* at = sm.turned + (8 * u + 2 * j) * 128 + ((g ^ u) << 3);
+        *reinterpret_cast<uint2*>(at) = make_uint2(__byte_perm(lo[0], lo[1], 0x5410), __byte_perm(lo[2], lo[3], 0x5410));
+        *reinterpret_cast<uint2*>(at + 128) = make_uint2(__byte_perm(hi[0], hi[1], 0x5410), __byte_perm(hi[2], hi[3], 0x5410));
+    }
+}
+
 template <typename T, int FMT, bool ROW, bool COL>
-__global__ void __launch_bounds__(QT_THREADS) q8_quantize_kernel(uint8_t* __restrict__ q, uint8_t* __restrict__ scale,
-                                                                 uint8_t* __restrict__ qt, uint8_t* __restrict__ scale_t,
-                                                                 float* __restrict__ partials, const T* __restrict__ x,
-                                                                 int64_t rows, int64_t cols, int64_t ld, int64_t ldt,
-                                                                 int64_t kb_row, int64_t kb_col, int64_t tiles_c) {
-    using F = Fmt<FMT>;
-    __shared__ uint32_t col_max[128];
-    __shared__ float col_inv[128];
-    __shared__ __align__(16) uint8_t turned[COL ? 128 * 128 : 16];
-    __shared__ float sums[8][128];
-    const int tid = static_cast<int>(threadIdx.x), warp = tid >> 5;
+__global__ void __launch_bounds__(QT_THREADS, sizeof(T) == 2 ? 4 : 2)
+    q8_quantize_kernel(uint8_t* __restrict__ q, uint8_t* __restrict__ scale, uint8_t* __restrict__ qt,
+                       uint8_t* __restrict__ scale_t, float* __restrict__ partials, const T* __restrict__ x, int64_t rows,
+                       int64_t cols, int64_t ld, int64_t ldt, int64_t kb_row, int64_t kb_col, int64_t tiles_c) {
+    using E = Eight<T>;
+    __shared__ TileMem sm;
+    const int tid = static_cast<int>(threadIdx.x), warp = tid >> 5, lane = tid & 31;
     const int g = tid >> 4, u = tid & 15;
     const int64_t tr = blockIdx.x / tiles_c, tc = blockIdx.x % tiles_c;  // the tile: row block, column block
     const int64_t r0 = tr * 128, c0 = tc * 128;
-    if (COL && tid < 128) col_max[tid] = 0u;
+    if (COL && tid < 128) sm.col_max[tid] = 0u;
     ptx::grid_launch_dependents();
     ptx::grid_dependency_wait();
 
-    Raw8<T> raw[8];
-    const int64_t c = c0 + 8 * u;
+    E v[8];
+    {
+        const int64_t c = c0 + 8 * u, r = r0 + 8 * g;
+        const T* src = x + r * cols + c;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int64_t r = r0 + 8 * g + i;
-        raw[i].zero();
-        if (r < rows && c < cols) raw[i].load(x + r * cols + c, cols - c);
+        for (int i = 0; i < 8; ++i) v[i].load(src + i * cols, r + i < rows ? cols - c : 0);
     }
-
-    float cmax[8], csum[8];
+    // column maxima of the thread's eight rows; one non-finite value in the tile
+    // sends the whole block down the path that looks at every value
+    uint32_t cm[E::W];
+    bool bad = false;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) cmax[j] = csum[j] = 0.f;
-    int my_scale = 127;
+    for (int k = 0; k < E::W; ++k) {
+        uint32_t m = E::larger(v[0].w[k], v[1].w[k]);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        float f[8];
-        raw[i].get(f);
-        float m = 0.f;
-        if (partials) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) csum[j] += f[j];
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float a = finite(f[j]) ? fabsf(f[j]) : 0.f;
-            m = fmaxf(m, a);
-            if (COL) cmax[j] = fmaxf(cmax[j], a);
-        }
-        if constexpr (ROW) {
-#pragma unroll
-            for (int o = 1; o < 16; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-            const int sb = scale_byte<FMT>(m);
-            if (u == i) my_scale = sb;
-            const float inv = inv_scale(sb);
-            uint32_t w[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {  // (inf * 2^-s stays inf: stored as the format's NaN)
-                const float a = finite(f[2 * j]) ? f[2 * j] * inv : __uint_as_float(0x7FFFFFFFu);
-                const float b = finite(f[2 * j + 1]) ? f[2 * j + 1] * inv : __uint_as_float(0x7FFFFFFFu);
-                w[j] = F::pack2(a, b);
-            }
-            const int64_t r = r0 + 8 * g + i;
-            if (r < rows && c < ld)
-                *reinterpret_cast<uint2*>(q + r * ld + c) = make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
-        }
-    }
-    if constexpr (ROW) {
-        const int64_t groups = (kb_row + 3) / 4;
-        const int rl = 8 * g + u;  // lanes u < 8 hold one row's scale each
-        uint8_t* at = scale + (tr * groups + tc / 4) * 512 + (rl % 32) * 16 + (rl / 32) * 4;
-        if (u < 8) {
-            at[tc % 4] = static_cast<uint8_t>(my_scale);
-            if (tc == kb_row - 1)
-                for (int64_t k = tc % 4 + 1; k < 4; ++k) at[k] = 127;
-        }
+        for (int i = 2; i < 8; ++i) m = E::larger(m, v[i].w[k]);
+        cm[k] = m & E::MAG;
+        bad |= E::bad(cm[k]);
     }
     if (partials) {
+        float s[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float s = csum[j] + __shfl_down_sync(0xffffffffu, csum[j], 16);
-            if ((tid & 31) < 16) sums[warp][8 * u + j] = s;
-        }
-    }
-    if (COL || partials) __syncthreads();
-    if (partials && tid < 128 && c0 + tid < cols) {
-        float s = sums[0][tid];
+        for (int j = 0; j < 8; ++j) s[j] = 0.f;
 #pragma unroll
-        for (int w = 1; w < 8; ++w) s += sums[w][tid];
-        partials[tr * cols + c0 + tid] = s;
-    }
-    if constexpr (COL) {
+        for (int i = 0; i < 8; ++i) {
+            if constexpr (sizeof(T) == 2) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float m = fmaxf(cmax[j], __shfl_xor_sync(0xffffffffu, cmax[j], 16));
-            if ((tid & 31) < 16) atomicMax(&col_max[8 * u + j], __float_as_uint(m));
-        }
-        __syncthreads();
-        if (tid < 128) {
-            const int sb = scale_byte<FMT>(__uint_as_float(col_max[tid]));
-            col_inv[tid] = inv_scale(sb);
-            const int64_t groups = (kb_col + 3) / 4;
-            uint8_t* at = scale_t + (tc * groups + tr / 4) * 512 + (tid % 32) * 16 + (tid / 32) * 4;
-            at[tr % 4] = static_cast<uint8_t>(sb);
-            if (tr == kb_col - 1)
-                for (int64_t k = tr % 4 + 1; k < 4; ++k) at[k] = 127;
-        }
-        __syncthreads();
-        uint32_t w[8][2];
+                for (int k = 0; k < 4; ++k) {
+                    s[2 * k] = add_half<0>(v[i].w[k], s[2 * k]);
+                    s[2 * k + 1] = add_half<1>(v[i].w[k], s[2 * k + 1]);
+                }
+            } else {
 #pragma unroll
-        for (int i = 0; i < 8; i += 2) {
-            float f0[8], f1[8];
-            raw[i].get(f0);
-            raw[i + 1].get(f1);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float inv = col_inv[8 * u + j];
-                const float a = finite(f0[j]) ? f0[j] * inv : __uint_as_float(0x7FFFFFFFu);
-                const float b = finite(f1[j]) ? f1[j] * inv : __uint_as_float(0x7FFFFFFFu);
-                const uint32_t p = F::pack2(a, b);
-                w[j][i / 4] = (i % 4) ? w[j][i / 4] | (p << 16) : p;
+                for (int j = 0; j < 8; ++j) s[j] += __uint_as_float(v[i].w[j]);
             }
         }
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            *reinterpret_cast<uint2*>(turned + (8 * u + j) * 128 + ((g ^ u) << 3)) = make_uint2(w[j][0], w[j][1]);
+        for (int j = 0; j < 8; ++j) s[j] += __shfl_down_sync(0xffffffffu, s[j], 16);
+        if (lane < 16) {
+            *reinterpret_cast<float4*>(&sm.sums[warp][8 * u]) = make_float4(s[0], s[1], s[2], s[3]);
+            *reinterpret_cast<float4*>(&sm.sums[warp][8 * u + 4]) = make_float4(s[4], s[5], s[6], s[7]);
+        }
+    }
+    if (COL) __syncthreads();  // col_max is zero
+    if (COL) {
+#pragma unroll
+        for (int k = 0; k < E::W; ++k) cm[k] = E::larger(cm[k], __shfl_xor_sync(0xffffffffu, cm[k], 16)) & E::MAG;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {  // each half warp takes four of the eight columns
+            const uint32_t lo = E::bits(cm, e), hi = E::bits(cm, e + 4);
+            atomicMax(&sm.col_max[8 * u + e + (lane < 16 ? 0 : 4)], lane < 16 ? lo : hi);
+        }
+    }
+    const bool rare = __syncthreads_or(bad);
+    if (COL && rare) {  // the maxima again, over finite values
+        if (tid < 128) sm.col_max[tid] = 0u;
+        __syncthreads();
+#pragma unroll 1
+        for (int i = 0; i < 8; ++i) {
+            float f[8];
+            E t;
+#pragma unroll
+            for (int n = 0; n < 8; ++n)
+                if (n == i) t = v[n];
+            t.get(f);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (finite(f[j])) atomicMax(&sm.col_max[8 * u + j], __float_as_uint(fabsf(f[j])));
+        }
+        __syncthreads();
+    }
+    if (partials && tid < 128 && c0 + tid < cols) {
+        float s = sm.sums[0][tid];
+#pragma unroll
+        for (int w = 1; w < 8; ++w) s += sm.sums[w][tid];
+        partials[tr * cols + c0 + tid] = s;
+    }
+    if (COL && tid < 128) {
+        const uint32_t m = sm.col_max[tid];
+        sm.col_inv[tid] = inv_scale<FMT>(m);
+        uint8_t* at = scale_t + (tc * ((kb_col + 3) / 4) + tr / 4) * 512 + (tid % 32) * 16 + (tid / 32) * 4;
+        at[tr % 4] = static_cast<uint8_t>(scale_byte<FMT>(m));
+        if (tr == kb_col - 1)
+            for (int64_t k = tr % 4 + 1; k < 4; ++k) at[k] = 127;
+    }
+    if constexpr (ROW) {
+        if (rare) row_form<T, FMT, true>(v, q, scale, tr, tc, rows, ld, kb_row);
+        else row_form<T, FMT, false>(v, q, scale, tr, tc, rows, ld, kb_row);
+    }
+    if constexpr (COL) {
+        __syncthreads();
+        if (rare) turn_columns<T, FMT, true>(v, sm);
+        else turn_columns<T, FMT, false>(v, sm);
         __syncthreads();
         const int h = tid & 7;
         const int64_t rr = r0 + 16 * h;
+        uint8_t* dst = qt + (c0 + (tid >> 3)) * ldt + rr;
 #pragma unroll
         for (int it = 0; it < 4; ++it) {
             const int cl = 32 * it + (tid >> 3);
-            const uint8_t* row = turned + cl * 128;
+            const uint8_t* row = sm.turned + cl * 128;
             const uint2 a = *reinterpret_cast<const uint2*>(row + (((2 * h) ^ (cl >> 3)) << 3));
             const uint2 b = *reinterpret_cast<const uint2*>(row + (((2 * h + 1) ^ (cl >> 3)) << 3));
             if (c0 + cl < cols && rr < ldt)
-                *reinterpret_cast<uint4*>(qt + (c0 + cl) * ldt + rr) = make_uint4(a.x, a.y, b.x, b.y);
+                *reinterpret_cast<uint4*>(dst + 32 * it * ldt) = make_uint4(a.x, a.y, b.x, b.y);
         }
     }
 }
