@@ -61,10 +61,47 @@ __device__ __forceinline__ void mma_mxf8(uint32_t d, uint64_t a, uint64_t b, uin
         : "memory");
 }
 
+// 32 contiguous bytes between registers and global memory. `left`: elements up to
+// the row's end (none is touched beyond it; a multiple of 16 bytes), `per16`: elements in 16
+// bytes, `wide`: the address is a multiple of 32 (else two accesses of 16).
+__device__ __forceinline__ void st256(void* p, const uint32_t* v) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]),
+                 "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+__device__ __forceinline__ void st256(void* p, const uint32_t* v, int64_t left, int per16, int wide) {
+    if (wide) {
+        if (left > 0) st256(p, v);
+    } else {
+        uint4* q = static_cast<uint4*>(p);
+        if (left > 0) q[0] = make_uint4(v[0], v[1], v[2], v[3]);
+        if (left > per16) q[1] = make_uint4(v[4], v[5], v[6], v[7]);
+    }
+}
+__device__ __forceinline__ void ld256(const void* p, uint32_t* v, int64_t left, int per16, int wide) {
+    if (wide) {
+        if (left > 0)
+            asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                         : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+                         : "l"(p)
+                         : "memory");
+    } else {
+        const uint4* q = static_cast<const uint4*>(p);
+        if (left > 0) {
+            const uint4 a = q[0];
+            v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+        }
+        if (left > per16) {
+            const uint4 a = q[1];
+            v[4] = a.x, v[5] = a.y, v[6] = a.z, v[7] = a.w;
+        }
+    }
+}
+
 constexpr unsigned long long TIMEOUT_NS = 2000000000ull;  // 2 s per wait
 
 // Where a wait gave up (device status word of the 8-bit products).
-enum Site : int { SITE_EMPTY = 1, SITE_ACC_FREE = 2, SITE_FULL = 3, SITE_ACC_FULL = 4, SITE_TEARDOWN = 8, SITE_FORWARD = 10, SITE_OLD = 11, SITE_DONE = 12 };
+enum Site : int { SITE_EMPTY = 1, SITE_ACC_FREE = 2, SITE_FULL = 3, SITE_ACC_FULL = 4, SITE_TEARDOWN = 8, SITE_FORWARD = 10, SITE_DONE = 12 };
 
 // Bounded mbarrier wait: false after TIMEOUT_NS (recorded in `status`) or once
 // another warp of the CTA has given up; a teardown wait ignores the latter.

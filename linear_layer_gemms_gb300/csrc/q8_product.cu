@@ -25,8 +25,8 @@
 // Warp roles (10 warps per CTA): 0 TMA producer; 1 MMA issuer (even CTA) or
 // forwarder of "stage full" to the even CTA (odd CTA); 2-9 epilogue, two warps per
 // tensor-memory lane quadrant, each taking every other 32-column chunk of its 32
-// rows: accumulator (+ bias, + old values fetched by TMA) rounded once into a
-// swizzled chunk buffer and out with one bulk store.
+// rows: accumulator (+ bias, + old values, requested a chunk ahead) rounded once
+// and stored from registers, 32 bytes of a row per thread and store.
 //
 // Work list: the tiles of one or two products (dinp and dweight), each product's
 // reduction cut into `splits` ranges of blocks where its tiles alone do not
@@ -59,14 +59,12 @@ __device__ unsigned int g_q8_status[4];
 namespace {
 
 constexpr int BM = 128, PAIR_M = 256;
-constexpr int STAGES = 5;
+constexpr int STAGES = 6;
 constexpr int A_BYTES = BM * 128, B_BYTES = 128 * 128;
 constexpr int SF_BYTES = 3 * 512;  // scales of 128 rows of A and up to 256 of B, four blocks of K
 constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
 constexpr int EPI_WARPS = 8, FIRST_EPI = 2;
 constexpr int THREADS = 32 * (FIRST_EPI + EPI_WARPS);
-constexpr int CHUNK_BYTES = 4096;  // per epilogue warp: one fp32 chunk (32 x 32), or two bf16 chunks
-constexpr int OLD_SLOTS = 2;
 constexpr uint32_t TMEM_COLS = 512, ACC1 = 192, SF_COL = 448, SF_STRIDE = 12;
 // Scale buffers in tensor memory: a copy into buffer i may only be issued once the
 // MMAs of the group that used it are done. The copy of group g + SF_BUFS follows
@@ -76,10 +74,9 @@ constexpr int SF_BUFS = 4;
 static_assert(STAGES <= 4 * SF_BUFS - 3 && SF_BUFS * SF_STRIDE <= 64, "scale buffers");
 
 constexpr int BAR_FULL = 0, BAR_EMPTY = STAGES, BAR_ACC_FULL = 2 * STAGES, BAR_ACC_FREE = 2 * STAGES + 1,
-              BAR_TEARDOWN = 2 * STAGES + 2, BAR_OLD = 2 * STAGES + 3, N_BARS = BAR_OLD + EPI_WARPS * OLD_SLOTS;
+              BAR_TEARDOWN = 2 * STAGES + 2, N_BARS = 2 * STAGES + 3;
 constexpr int OFF_SF = STAGES * STAGE_BYTES;
-constexpr int OFF_CHUNKS = (OFF_SF + STAGES * SF_BYTES + 1023) & ~1023;
-constexpr int OFF_BARS = OFF_CHUNKS + EPI_WARPS * CHUNK_BYTES;
+constexpr int OFF_BARS = OFF_SF + STAGES * SF_BYTES;
 constexpr int OFF_MISC = OFF_BARS + N_BARS * 8;  // [0] tensor-memory base, [1] abort flag
 constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;
 static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
@@ -94,10 +91,13 @@ struct Schedule {
 struct Prod {
     const uint8_t *a_scale, *b_scale;
     const void* bias;
+    void* D;
+    float* partials;
     int64_t M, N;
     int groups;  // of four blocks, per row of the scales
     int bn, tiles_m, tiles_n, kb, splits, kb_per_split, item0;
     int f32, add;
+    int wide;  // rows of D start on 32-byte boundaries
     uint32_t idesc;
 };
 
@@ -107,7 +107,7 @@ struct Params {
 };
 
 struct Maps {
-    CUtensorMap a[2], b[2], d[2], part[2];
+    CUtensorMap a[2], b[2];
 };
 
 struct Item {
@@ -162,7 +162,6 @@ __global__ void __launch_bounds__(THREADS, 1)
         ptx::mbar_init(bars + 8u * BAR_ACC_FULL, 1u);
         ptx::mbar_init(bars + 8u * BAR_ACC_FREE, 2u * EPI_WARPS);
         ptx::mbar_init(bars + 8u * BAR_TEARDOWN, 1u);
-        for (int b = 0; b < EPI_WARPS * OLD_SLOTS; ++b) ptx::mbar_init(bars + 8u * (BAR_OLD + b), 1u);
         misc[1] = 0u;
         ptx::fence_mbar_init();
     }
@@ -184,7 +183,6 @@ __global__ void __launch_bounds__(THREADS, 1)
             for (int i = 0; i < p.n_prod; ++i) {
                 ptx::prefetch_tmap(&maps.a[i]);
                 ptx::prefetch_tmap(&maps.b[i]);
-                ptx::prefetch_tmap(&maps.d[i]);
             }
             uint32_t stage = 0, phase = 0, issued = 0, last_parity = 0;
             bool ok = true, waited = false;
@@ -302,159 +300,127 @@ __global__ void __launch_bounds__(THREADS, 1)
         __syncwarp();
     } else {
         // ------------------------------------------------------------ epilogue
-        const int ew = warp - FIRST_EPI;
-        const int q = warp & 3;   // tensor-memory lane quadrant this warp may read
-        const int h = ew >> 2;    // which of the quadrant's two warps
-        const uint32_t buf = base + OFF_CHUNKS + ew * CHUNK_BYTES;
-        const uint32_t old0 = bars + 8u * (BAR_OLD + ew * OLD_SLOTS);
+        const int q = warp & 3;                  // tensor-memory lane quadrant this warp may read
+        const int h = (warp - FIRST_EPI) >> 2;   // which of the quadrant's two warps
         const uint32_t free_bar = ptx::mapa(bars + 8u * BAR_ACC_FREE, 0);
-        uint32_t tile = 0, oldpar = 0, oldpend = 0;
+        uint32_t tile = 0;
         for (int r = 0;; ++r, ++tile) {
             const int w = item_at(p, sch, r);
             if (w >= p.n_items) break;
             const Item it = decode(p, w);
             const Prod& d = p.prod[it.which];
-            const int64_t row0 = static_cast<int64_t>(it.pm) * PAIR_M + static_cast<int>(rank) * BM + q * 32;
+            const int64_t row = static_cast<int64_t>(it.pm) * PAIR_M + static_cast<int>(rank) * BM + q * 32 + lane;
             const int col0 = it.n_tile * d.bn;
-            const int ncols = static_cast<int>(min(static_cast<int64_t>(d.bn), d.N - col0));
-            const int nk = d.bn / 64;  // this warp's chunks of a whole tile
-            const bool part = d.splits > 1;
-            const bool wide = part || d.f32;       // fp32 chunks: 128-byte rows, one buffer
-            const bool add = d.add && !part;
-            const int slots = wide ? 1 : OLD_SLOTS;
-            const uint32_t slot_bytes = wide ? 4096u : 2048u;
-            const bool in_rows = row0 < d.M;
+            const int nk = d.bn / 64;  // this warp's 32-column chunks of the tile
+            const bool in_row = row < d.M;
             // chunk of step k: the shared columns (the last 64 of the even
             // accumulator, the first 64 of the odd one) come first
             auto chunk = [&](int k) {
                 return (d.bn == 256 && (tile & 1u) == 0) ? (k == 0 ? 6 + h : 2 * (k - 1) + h) : 2 * k + h;
             };
-            auto next = [&](int k) {
-                while (k < nk && chunk(k) * 32 >= ncols) ++k;
-                return k;
-            };
-            if (lane == 0) ptx::bulk_wait_read_all();  // the buffers are free
-            __syncwarp();
-            const CUtensorMap* dm = part ? &maps.part[it.which] : &maps.d[it.which];
-            int k = in_rows ? next(0) : nk;
-            int ahead = k;
-            if (add) {
-                for (int s = 0; s < slots && ahead < nk; ++s, ahead = next(ahead + 1))
-                    if (lane == 0) {
-                        ptx::mbar_arrive_expect_tx(old0 + 8u * s, slot_bytes);
-                        ptx::tma_load_2d(buf + s * slot_bytes, dm, old0 + 8u * s, col0 + chunk(ahead) * 32,
-                                         static_cast<int32_t>(row0));
-                        oldpend |= 1u << s;
-                    }
-            }
-            if (!wt.wait_warp(bars + 8u * BAR_ACC_FULL, tile & 1u, q8::SITE_ACC_FULL, w)) break;
-            ptx::tc_fence_after();
             const uint32_t acc = tmem + (static_cast<uint32_t>(q * 32) << 16) + (tile & 1u) * ACC1;
-            bool released = false, ok = true;
-            auto release = [&]() {
+            auto release = [&](int k) {  // after the first chunk has been read
+                if (k > 0) return;
                 ptx::tc_fence_before();
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive_cluster_relaxed(free_bar);
-                released = true;
             };
-            int x0 = 0;
-            int64_t y0 = row0;
-            if (part)  // [128-row tile x column tile][split][128][bn]
-                y0 = ((static_cast<int64_t>(it.pm * 2 + static_cast<int>(rank)) * d.tiles_n + it.n_tile) * d.splits + it.split) * BM +
-                     q * 32;
-            else
-                x0 = col0;
-            int slot = 0;
-            uint32_t used = 0;
+            if (d.splits > 1) {  // partial sums: [128-row tile x column tile][split][128][bn]
+                if (!wt.wait_warp(bars + 8u * BAR_ACC_FULL, tile & 1u, q8::SITE_ACC_FULL, w)) break;
+                ptx::tc_fence_after();
+                float* dst = d.partials +
+                             (((static_cast<int64_t>(it.pm * 2 + static_cast<int>(rank)) * d.tiles_n + it.n_tile) * d.splits + it.split) * BM +
+                              q * 32 + lane) * d.bn;
 #pragma unroll 1
-            while (k < nk) {
-                const int c = chunk(k);
-                uint32_t v[32];
-                ptx::tmem_ld32(acc + c * 32, v);
-                if (!released) release();
-                const uint32_t at = buf + slot * slot_bytes;
-                if (add) {
-                    if (!wt.wait_warp(old0 + 8u * slot, (oldpar >> slot) & 1u, q8::SITE_OLD, w)) {
-                        ok = false;
-                        break;
-                    }
-                    oldpar ^= 1u << slot;
-                    oldpend &= ~(1u << slot);
-                } else {
-                    if (used >= static_cast<uint32_t>(slots) && lane == 0) {
-                        if (wide) ptx::bulk_wait_read_all();
-                        else ptx::bulk_wait_read_but_last();
-                    }
-                    __syncwarp();
-                }
-                ++used;
-                const int cc = col0 + c * 32;
-                if (wide) {  // row `lane`: 16-byte granule g at g ^ (lane & 7)
-                    const uint32_t row = at + lane * 128, swz = static_cast<uint32_t>(lane & 7);
+                for (int k = 0; k < nk; ++k) {
+                    uint32_t v[32];
+                    const int c = chunk(k) * 32;
+                    ptx::tmem_ld32(acc + c, v);
+                    release(k);
+                    if (in_row) {
 #pragma unroll
-                    for (int g = 0; g < 8; ++g) {
-                        const uint32_t a = row + ((static_cast<uint32_t>(g) ^ swz) << 4);
-                        float4 f = make_float4(__uint_as_float(v[4 * g]), __uint_as_float(v[4 * g + 1]),
-                                               __uint_as_float(v[4 * g + 2]), __uint_as_float(v[4 * g + 3]));
-                        if (!part) {
-                            if (d.bias && cc + 4 * g < d.N) {
-                                const float4 b = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(d.bias) + cc) + g);
-                                f.x += b.x, f.y += b.y, f.z += b.z, f.w += b.w;
+                        for (int g = 0; g < 4; ++g) q8::st256(dst + c + 8 * g, v + 8 * g);
+                    }
+                }
+            } else if (d.f32) {
+                float* D = static_cast<float*>(d.D) + row * d.N + col0;
+                uint32_t old[32];
+                auto fetch = [&](int k) {
+                    const int c = chunk(k) * 32;
+#pragma unroll
+                    for (int g = 0; g < 4; ++g) q8::ld256(D + c + 8 * g, old + 8 * g, in_row ? d.N - col0 - c - 8 * g : 0, 4, d.wide);
+                };
+                if (d.add) fetch(0);
+                if (!wt.wait_warp(bars + 8u * BAR_ACC_FULL, tile & 1u, q8::SITE_ACC_FULL, w)) break;
+                ptx::tc_fence_after();
+#pragma unroll 1
+                for (int k = 0; k < nk; ++k) {
+                    uint32_t v[32];
+                    const int c = chunk(k) * 32;
+                    ptx::tmem_ld32(acc + c, v);
+                    release(k);
+                    if (d.bias) {
+                        const float* b = static_cast<const float*>(d.bias) + col0 + c;
+#pragma unroll
+                        for (int g = 0; g < 8; ++g)
+                            if (col0 + c + 4 * g < d.N) {
+                                const float4 f = __ldg(reinterpret_cast<const float4*>(b) + g);
+                                v[4 * g] = __float_as_uint(__uint_as_float(v[4 * g]) + f.x);
+                                v[4 * g + 1] = __float_as_uint(__uint_as_float(v[4 * g + 1]) + f.y);
+                                v[4 * g + 2] = __float_as_uint(__uint_as_float(v[4 * g + 2]) + f.z);
+                                v[4 * g + 3] = __float_as_uint(__uint_as_float(v[4 * g + 3]) + f.w);
                             }
-                            if (add) {
-                                const float4 o = ptx::lds128f(a);
-                                f.x += o.x, f.y += o.y, f.z += o.z, f.w += o.w;
-                            }
+                    }
+                    if (d.add) {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) + __uint_as_float(old[e]));
+                        if (k + 1 < nk) fetch(k + 1);
+                    }
+#pragma unroll
+                    for (int g = 0; g < 4; ++g) q8::st256(D + c + 8 * g, v + 8 * g, in_row ? d.N - col0 - c - 8 * g : 0, 4, d.wide);
+                }
+            } else {
+                __nv_bfloat16* D = static_cast<__nv_bfloat16*>(d.D) + row * d.N + col0;
+                uint32_t old[16];
+                auto fetch = [&](int k) {
+                    const int c = chunk(k) * 32;
+#pragma unroll
+                    for (int g = 0; g < 2; ++g) q8::ld256(D + c + 16 * g, old + 8 * g, in_row ? d.N - col0 - c - 16 * g : 0, 8, d.wide);
+                };
+                if (d.add) fetch(0);
+                if (!wt.wait_warp(bars + 8u * BAR_ACC_FULL, tile & 1u, q8::SITE_ACC_FULL, w)) break;
+                ptx::tc_fence_after();
+#pragma unroll 1
+                for (int k = 0; k < nk; ++k) {
+                    uint32_t v[32], o[16];
+                    const int c = chunk(k) * 32;
+                    ptx::tmem_ld32(acc + c, v);
+                    release(k);
+                    if (d.add) {
+#pragma unroll
+                        for (int e = 0; e < 16; ++e)
+                            o[e] = pack_bf16(__uint_as_float(v[2 * e]) + lo_bf16(old[e]), __uint_as_float(v[2 * e + 1]) + hi_bf16(old[e]));
+                        if (k + 1 < nk) fetch(k + 1);
+                    } else if (d.bias) {
+                        const __nv_bfloat16* b = static_cast<const __nv_bfloat16*>(d.bias) + col0 + c;
+#pragma unroll
+                        for (int g = 0; g < 4; ++g) {
+                            const uint4 f = col0 + c + 8 * g < d.N ? __ldg(reinterpret_cast<const uint4*>(b) + g) : make_uint4(0u, 0u, 0u, 0u);
+                            const uint32_t fw[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                o[4 * g + e] = pack_bf16(__uint_as_float(v[8 * g + 2 * e]) + lo_bf16(fw[e]),
+                                                         __uint_as_float(v[8 * g + 2 * e + 1]) + hi_bf16(fw[e]));
                         }
-                        ptx::sts128(a, f.x, f.y, f.z, f.w);
-                    }
-                } else {  // row `lane`: 16-byte granule g at g ^ ((lane >> 1) & 3)
-                    const uint32_t row = at + lane * 64, swz = static_cast<uint32_t>((lane >> 1) & 3);
+                    } else {
 #pragma unroll
-                    for (int g = 0; g < 4; ++g) {
-                        const uint32_t a = row + ((static_cast<uint32_t>(g) ^ swz) << 4);
-                        uint4 o = make_uint4(0u, 0u, 0u, 0u);
-                        if (add)
-                            o = ptx::lds128(a);
-                        else if (d.bias && cc + 8 * g < d.N)
-                            o = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(d.bias) + cc) + g);
-                        const uint32_t ow[4] = {o.x, o.y, o.z, o.w};
-                        uint32_t rw[4];
+                        for (int e = 0; e < 16; ++e) o[e] = pack_bf16(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1]));
+                    }
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            rw[e] = pack_bf16(__uint_as_float(v[8 * g + 2 * e]) + lo_bf16(ow[e]),
-                                              __uint_as_float(v[8 * g + 2 * e + 1]) + hi_bf16(ow[e]));
-                        ptx::sts128u(a, make_uint4(rw[0], rw[1], rw[2], rw[3]));
-                    }
+                    for (int g = 0; g < 2; ++g) q8::st256(D + c + 16 * g, o + 8 * g, in_row ? d.N - col0 - c - 16 * g : 0, 8, d.wide);
                 }
-                ptx::fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) {
-                    ptx::tma_store_2d(dm, at, x0 + c * 32, static_cast<int32_t>(y0));
-                    ptx::bulk_commit_group();
-                }
-                if (add && ahead < nk) {  // refill this buffer once its store has read it
-                    if (lane == 0) {
-                        ptx::bulk_wait_read_all();
-                        ptx::mbar_arrive_expect_tx(old0 + 8u * slot, slot_bytes);
-                        ptx::tma_load_2d(at, dm, old0 + 8u * slot, col0 + chunk(ahead) * 32, static_cast<int32_t>(row0));
-                        oldpend |= 1u << slot;
-                    }
-                    ahead = next(ahead + 1);
-                }
-                __syncwarp();
-                if (++slot == slots) slot = 0;
-                k = next(k + 1);
             }
-            if (!released) release();
-            if (!ok) break;
         }
-        if (lane == 0) {
-            for (int s = 0; s < OLD_SLOTS; ++s)
-                if ((oldpend >> s) & 1u) wt.wait(old0 + 8u * s, (oldpar >> s) & 1u, q8::SITE_TEARDOWN, -1, true);
-            ptx::bulk_wait_all();
-        }
-        __syncwarp();
     }
 
     ptx::grid_launch_dependents();
@@ -714,14 +680,15 @@ const Plan& plan_for(const Shape3* s, int n, bool may_split, int num_sms) {
 
 // ------------------------------------------------------------------ launch
 
-bool encode_2d(CUtensorMap* m, CUtensorMapDataType type, const void* base, uint64_t inner, uint64_t rows, uint64_t pitch,
-               uint32_t box_inner, uint32_t box_rows, CUtensorMapSwizzle swz) {
+// An operand's 8-bit values: boxes of 128 bytes of K by `box_rows` rows.
+bool encode_2d(CUtensorMap* m, const void* base, uint64_t ld, uint64_t rows, uint32_t box_rows) {
     EncodeTiledFn encode = get_encode_tiled();
     if (!encode) return false;
-    const cuuint64_t dims[2] = {inner, rows}, strides[1] = {pitch};
-    const cuuint32_t box[2] = {box_inner, box_rows}, estr[2] = {1, 1};
-    return encode(m, type, 2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swz,
-                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    const cuuint64_t dims[2] = {ld, rows}, strides[1] = {ld};
+    const cuuint32_t box[2] = {128, box_rows}, estr[2] = {1, 1};
+    return encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 cudaError_t set_smem_once() {
@@ -750,19 +717,12 @@ cudaError_t launch_pair(const Plan& pl, const Q8Product* prod, uint8_t* ws, cuda
         const ProductPlan& pp = pl.p[i];
         const uint64_t ld = static_cast<uint64_t>(q8_ld(q.K)), m = static_cast<uint64_t>(q.M), n = static_cast<uint64_t>(q.N);
         const bool f32 = q.dtype == MMBWD_F32;
-        const CUtensorMapDataType dt = f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-        bool ok = encode_2d(&maps.a[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, q.A, ld, m, ld, 128, BM, CU_TENSOR_MAP_SWIZZLE_128B) &&
-                  encode_2d(&maps.b[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, q.B, ld, n, ld, 128,
-                            static_cast<uint32_t>(pp.bn / 2), CU_TENSOR_MAP_SWIZZLE_128B) &&
-                  encode_2d(&maps.d[i], dt, q.D, n, m, n * (f32 ? 4 : 2), 32, 32,
-                            f32 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
-        if (ok && pp.splits > 1)
-            ok = encode_2d(&maps.part[i], CU_TENSOR_MAP_DATA_TYPE_FLOAT32, ws + pp.ws_off, static_cast<uint64_t>(pp.bn),
-                           pp.ws_bytes / (static_cast<uint64_t>(pp.bn) * 4), static_cast<uint64_t>(pp.bn) * 4, 32, 32,
-                           CU_TENSOR_MAP_SWIZZLE_128B);
+        const bool ok = encode_2d(&maps.a[i], q.A, ld, m, BM) && encode_2d(&maps.b[i], q.B, ld, n, static_cast<uint32_t>(pp.bn / 2));
         if (!ok) return cudaErrorInvalidValue;
         Prod& d = par.prod[i];
         d.a_scale = q.a_scale, d.b_scale = q.b_scale, d.bias = q.bias;
+        d.D = q.D, d.partials = reinterpret_cast<float*>(ws + pp.ws_off);
+        d.wide = reinterpret_cast<uintptr_t>(q.D) % 32 == 0 && n * (f32 ? 4 : 2) % 32 == 0 ? 1 : 0;
         d.M = q.M, d.N = q.N;
         d.groups = static_cast<int>(q8_groups(q.K));
         d.bn = pp.bn, d.tiles_m = pp.tiles_m, d.tiles_n = pp.tiles_n, d.kb = pp.kb;
