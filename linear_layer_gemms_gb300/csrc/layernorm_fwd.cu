@@ -16,6 +16,7 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <cstdint>
 
 namespace mmbwd {
 namespace {
@@ -78,68 +79,70 @@ __device__ __forceinline__ float team_sum(float s, float* slot, int which, int w
     }
 }
 
-constexpr int LNF_WARPS = 8;  // per block, where a team is no larger
+// Teams of one warp share a block of four rows; larger teams are a block.
+template <int P>
+constexpr int TEAMS_PER_BLOCK = P == 1 ? 4 : 1;
 
 template <typename T, int P, int VPT>
-__global__ void __launch_bounds__(32 * (P > LNF_WARPS ? P : LNF_WARPS))
+__global__ void __launch_bounds__(32 * P * TEAMS_PER_BLOCK<P>)
     ln_fwd_kernel(T* out, float* mean_out, float* rstd_out, const T* inp, const T* __restrict__ weight,
                   const T* __restrict__ bias, int64_t rows, int C, float eps) {
     using V = Vec<T>;
     constexpr int N = V::N;
-    constexpr int TEAMS = (P > LNF_WARPS ? P : LNF_WARPS) / P;
+    constexpr int TEAMS = TEAMS_PER_BLOCK<P>;
     __shared__ float slots[TEAMS][2 * P];
     const int warp = static_cast<int>(threadIdx.x >> 5), lane = static_cast<int>(threadIdx.x & 31);
     const int team = warp / P, wt = warp % P, t = wt * 32 + lane;
     const int nvec = C / N;
     const float inv_c = 1.f / static_cast<float>(C);
+    const int64_t r = static_cast<int64_t>(blockIdx.x) * TEAMS + team;
     ptx::grid_launch_dependents();
     ptx::grid_dependency_wait();
-    for (int64_t r = static_cast<int64_t>(blockIdx.x) * TEAMS + team; r < rows; r += static_cast<int64_t>(gridDim.x) * TEAMS) {
-        const uint4* xr = reinterpret_cast<const uint4*>(inp + r * C);
-        uint4 x[VPT];
+    if (r >= rows) return;  // (a whole team)
+    const uint4* xr = reinterpret_cast<const uint4*>(inp + r * C);
+    uint4 raw[VPT];
 #pragma unroll
-        for (int j = 0; j < VPT; ++j) {
-            const int v = t + 32 * P * j;
-            x[j] = v < nvec ? xr[v] : make_uint4(0u, 0u, 0u, 0u);
+    for (int j = 0; j < VPT; ++j) {
+        const int v = t + 32 * P * j;
+        raw[j] = v < nvec ? xr[v] : make_uint4(0u, 0u, 0u, 0u);
+    }
+    float x[VPT][N];
+    float s = 0.f;
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+        V::get(raw[j], x[j]);
+#pragma unroll
+        for (int e = 0; e < N; ++e) s += x[j][e];
+    }
+    const float mean = team_sum<P>(s, slots[team], 0, wt, team) * inv_c;
+    s = 0.f;
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+        const bool on = j + 1 < VPT || t + 32 * P * j < nvec;  // only the last vector may be missing
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+            x[j][e] = on ? x[j][e] - mean : 0.f;
+            s += x[j][e] * x[j][e];
         }
-        float s = 0.f;
+    }
+    const float var = team_sum<P>(s, slots[team], 1, wt, team) * inv_c;
+    const float rstd = 1.f / sqrtf(var + eps);
+    uint4* dst = reinterpret_cast<uint4*>(out + r * C);
 #pragma unroll
-        for (int j = 0; j < VPT; ++j) {
-            float f[N];
-            V::get(x[j], f);
+    for (int j = 0; j < VPT; ++j) {
+        const int v = t + 32 * P * j;
+        if (j + 1 < VPT || v < nvec) {
+            float w[N], b[N];
+            V::get(__ldg(reinterpret_cast<const uint4*>(weight) + v), w);
+            V::get(bias ? __ldg(reinterpret_cast<const uint4*>(bias) + v) : make_uint4(0u, 0u, 0u, 0u), b);
 #pragma unroll
-            for (int e = 0; e < N; ++e) s += f[e];
+            for (int e = 0; e < N; ++e) x[j][e] = x[j][e] * rstd * w[e] + b[e];
+            __stcs(dst + v, V::put(x[j]));
         }
-        const float mean = team_sum<P>(s, slots[team], 0, wt, team) * inv_c;
-        s = 0.f;
-#pragma unroll
-        for (int j = 0; j < VPT; ++j) {
-            if (t + 32 * P * j < nvec) {
-                float f[N];
-                V::get(x[j], f);
-#pragma unroll
-                for (int e = 0; e < N; ++e) s += (f[e] - mean) * (f[e] - mean);
-            }
-        }
-        const float var = team_sum<P>(s, slots[team], 1, wt, team) * inv_c;
-        const float rstd = 1.f / sqrtf(var + eps);
-#pragma unroll
-        for (int j = 0; j < VPT; ++j) {
-            const int v = t + 32 * P * j;
-            if (v < nvec) {
-                float f[N], w[N], b[N];
-                V::get(x[j], f);
-                V::get(__ldg(reinterpret_cast<const uint4*>(weight) + v), w);
-                V::get(bias ? __ldg(reinterpret_cast<const uint4*>(bias) + v) : make_uint4(0u, 0u, 0u, 0u), b);
-#pragma unroll
-                for (int e = 0; e < N; ++e) f[e] = (f[e] - mean) * rstd * w[e] + b[e];
-                reinterpret_cast<uint4*>(out + r * C)[v] = V::put(f);
-            }
-        }
-        if (t == 0) {
-            if (mean_out) mean_out[r] = mean;
-            if (rstd_out) rstd_out[r] = rstd;
-        }
+    }
+    if (t == 0) {
+        if (mean_out) mean_out[r] = mean;
+        if (rstd_out) rstd_out[r] = rstd;
     }
 }
 
@@ -195,22 +198,34 @@ __global__ void __launch_bounds__(1024) ln_fwd_wide_kernel(T* out, float* mean_o
 template <typename T>
 using LnFwdKernel = void (*)(T*, float*, float*, const T*, const T*, const T*, int64_t, int, float);
 
+// The kernel whose team of P warps holds a row in exactly `need` vectors a thread.
+template <typename T, int P, int VPT>
+LnFwdKernel<T> pick(int need) {
+    if constexpr (VPT > 8) {
+        return ln_fwd_wide_kernel<T>;
+    } else {
+        if (need <= VPT) return ln_fwd_kernel<T, P, VPT>;
+        return pick<T, P, VPT + 1>(need);
+    }
+}
+
 template <typename T>
 cudaError_t launch(T* out, float* mean, float* rstd, const T* inp, const T* weight, const T* bias, int64_t BT, int C,
                    float eps, int num_sms, cudaStream_t stream) {
+    // Up to eight vectors a thread: a warp per row while that is enough (no
+    // barrier), then a block of 8 or 32 warps.
     const int nvec = C / Vec<T>::N;
     LnFwdKernel<T> k;
-    int warps, rows_per_block;
-    if (nvec <= 32 * 4) k = ln_fwd_kernel<T, 1, 4>, warps = 8, rows_per_block = 8;
-    else if (nvec <= 64 * 4) k = ln_fwd_kernel<T, 2, 4>, warps = 8, rows_per_block = 4;
-    else if (nvec <= 128 * 4) k = ln_fwd_kernel<T, 4, 4>, warps = 8, rows_per_block = 2;
-    else if (nvec <= 256 * 4) k = ln_fwd_kernel<T, 8, 4>, warps = 8, rows_per_block = 1;
-    else if (nvec <= 1024 * 4) k = ln_fwd_kernel<T, 32, 4>, warps = 32, rows_per_block = 1;
-    else k = ln_fwd_wide_kernel<T>, warps = 32, rows_per_block = 1;
-    const int64_t blocks = (BT + rows_per_block - 1) / rows_per_block;
+    int threads;
+    int64_t blocks = BT;
+    if (nvec <= 32 * 8) k = pick<T, 1, 1>((nvec + 31) / 32), threads = 128, blocks = (BT + 3) / 4;
+    else if (nvec <= 256 * 8) k = pick<T, 8, 2>((nvec + 255) / 256), threads = 256;
+    else if (nvec <= 1024 * 8) k = pick<T, 32, 3>((nvec + 1023) / 1024), threads = 1024;
+    else k = ln_fwd_wide_kernel<T>, threads = 1024, blocks = std::min<int64_t>(BT, 2 * num_sms);
+    if (blocks > INT32_MAX) return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(blocks, static_cast<int64_t>(num_sms) * (64 / warps))), 1, 1);
-    cfg.blockDim = dim3(static_cast<unsigned>(32 * warps), 1, 1);
+    cfg.gridDim = dim3(static_cast<unsigned>(blocks), 1, 1);
+    cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
