@@ -94,6 +94,8 @@ class MmbwdError(RuntimeError):
 def load(path: str | None = None):
     """Load libmmbwd.so (built by ``__graft_entry__.build()``)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             p = path or LIB_PATH
@@ -109,9 +111,7 @@ def load(path: str | None = None):
 
 
 def _ptr(x) -> int | None:
-    if x is None:
-        return None
-    if isinstance(x, int):
+    if x is None or isinstance(x, int):
         return x
     return x.data_ptr()
 

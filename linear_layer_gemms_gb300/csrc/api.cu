@@ -815,14 +815,59 @@ int check_args(const Arg* a, int n) {
     return MMBWD_OK;
 }
 
-// The current device's state, and every tensor in its memory. Caller holds g_mutex.
+using PointerAttributesFn = CUresult (*)(unsigned int, CUpointer_attribute*, void**, CUdeviceptr);
+
+PointerAttributesFn pointer_attributes() {
+    static std::once_flag once;
+    static PointerAttributesFn fn = nullptr;
+    std::call_once(once, [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q{};
+        if (cudaGetDriverEntryPointByVersion("cuPointerGetAttributes", &p, 7000, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<PointerAttributesFn>(p);
+    });
+    return fn;
+}
+
+// The current device's state, and every tensor in its memory (check_local's
+// rule). Tensors of one allocation share a query: an allocation found to be
+// device memory of this device is remembered for the rest of this call, and a
+// tensor that lies wholly in one needs no query of its own. Caller holds g_mutex.
 int check_device(const Arg* a, int n, DeviceState** d) {
     int dev = 0;
     const int rc = device_state(d, &dev);
     if (rc != MMBWD_OK) return rc;
-    Span spans[16];
-    for (int i = 0; i < n; ++i) spans[i] = {a[i].p, a[i].n};
-    return check_local(spans, n, dev);
+    const PointerAttributesFn query = pointer_attributes();
+    uintptr_t lo[16], hi[16];
+    int known = 0;
+    for (int i = 0; i < n; ++i) {
+        if (!a[i].p || a[i].n == 0) continue;
+        const uintptr_t p = reinterpret_cast<uintptr_t>(a[i].p);
+        bool inside = false;
+        for (int k = 0; k < known && !inside; ++k) inside = p >= lo[k] && p < hi[k] && a[i].n <= hi[k] - p;
+        if (inside) continue;
+        if (query) {
+            unsigned int type = 0;
+            int ordinal = -1;
+            CUdeviceptr start = 0;
+            size_t size = 0;
+            unsigned int managed = 0;
+            CUpointer_attribute what[5] = {CU_POINTER_ATTRIBUTE_MEMORY_TYPE, CU_POINTER_ATTRIBUTE_DEVICE_ORDINAL,
+                                           CU_POINTER_ATTRIBUTE_RANGE_START_ADDR, CU_POINTER_ATTRIBUTE_RANGE_SIZE,
+                                           CU_POINTER_ATTRIBUTE_IS_MANAGED};
+            void* into[5] = {&type, &ordinal, &start, &size, &managed};
+            if (query(5, what, into, static_cast<CUdeviceptr>(p)) == CUDA_SUCCESS && type == CU_MEMORYTYPE_DEVICE &&
+                !managed && ordinal == dev && start <= p && p - start < size && a[i].n <= size - (p - start)) {
+                if (known < 16) lo[known] = start, hi[known] = start + size, ++known;
+                continue;
+            }
+        }
+        const Span one{a[i].p, a[i].n};  // not in one allocation, or not plain device memory
+        const int bad = check_local(&one, 1, dev);
+        if (bad != MMBWD_OK) return bad;
+    }
+    return MMBWD_OK;
 }
 
 }  // namespace
