@@ -41,6 +41,9 @@ struct Q8Product {
 size_t q8_products_workspace(const Q8Product* products, int n, int num_sms);
 cudaError_t q8_products_launch(const Q8Product* products, int n, bool may_split, void* ws, size_t ws_bytes, int num_sms,
                                cudaStream_t stream);
+// The forward (D overwritten) for few tokens (rows of A).
+cudaError_t q8_tokens_launch(const Q8Product& product, int num_sms, cudaStream_t stream);
+cudaError_t q8_tokens_read_status(int* code, int* info3, bool reset);
 cudaError_t q8_read_status(int* code, int* info3, bool reset);
 
 cudaError_t ln_forward_launch(void* out, float* mean, float* rstd, const void* inp, const void* weight,

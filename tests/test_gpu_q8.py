@@ -215,6 +215,43 @@ def test_forward(shape, dtype):
         assert torch.all(out[T] == 7.0)
 
 
+@pytest.mark.parametrize("splits", ["1", "2", "4", "8"])
+@pytest.mark.parametrize("shape", [(1, 1032, 264), (7, 2056, 520), (16, 1160, 132), (31, 1800, 260), (33, 1096, 392),
+                                   (64, 1032, 1000)], ids=lambda s: "x".join(map(str, s)))
+def test_forward_few_tokens_every_split(monkeypatch, shape, splits):
+    """Few tokens: K shared by 1 to 8 CTAs, partial tiles of tokens and rows."""
+    import torch
+
+    monkeypatch.setenv("MMBWD_Q8_TOKEN_SPLITS", splits)
+    T, C, OC = shape
+    iq, isc, iv = q8(normal((T, C), "bf16", 1), mm.E4M3)
+    wq, wsc, wv = q8(normal((OC, C), "bf16", 2, 0.02), mm.E4M3)
+    for dtype in ("f32", "bf16") if OC % 8 == 0 else ("f32",):
+        bias = normal((OC,), dtype, 3)
+        out = torch.full((T + 1, OC), 7.0, dtype=tdt(dtype), device="cuda")
+        for _ in range(2):
+            assert mm.mmbwd_q8_forward(out, iq, isc, wq, wsc, dev(bias, dtype), 1, T, C, OC, 0, 0, DT[dtype]) == mm.OK
+        torch.cuda.synchronize()
+        want, tol = ref.product_bound(iv, wv, dtype, bias)
+        assert np.all(np.abs(host(out[:T]) - want) <= tol)
+        assert torch.all(out[T] == 7.0)
+
+
+@pytest.mark.parametrize("T", [1, 20, 50])
+def test_forward_few_tokens_many_tiles(T):
+    """More tiles than CTAs: each CTA walks several."""
+    import torch
+
+    C, OC = 264, 80_040
+    iq, isc, iv = q8(normal((T, C), "bf16", 1), mm.E4M3)
+    wq, wsc, wv = q8(normal((OC, C), "bf16", 2, 0.02), mm.E4M3)
+    out = torch.empty(T, OC, dtype=torch.bfloat16, device="cuda")
+    assert mm.mmbwd_q8_forward(out, iq, isc, wq, wsc, None, 1, T, C, OC, 0, 0, mm.BF16) == mm.OK
+    torch.cuda.synchronize()
+    want, tol = ref.product_bound(iv, wv, "bf16")
+    assert np.all(np.abs(host(out) - want) <= tol)
+
+
 BACKWARD = [(1, 8, 8), (3, 264, 136), (128, 128, 128), (200, 328, 520), (500, 136, 264), (300, 1032, 24),
             (1000, 264, 392), (130, 520, 2304)]
 
