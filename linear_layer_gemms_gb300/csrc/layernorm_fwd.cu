@@ -83,7 +83,9 @@ __device__ __forceinline__ float team_sum(float s, float* slot, int which, int w
 template <int P>
 constexpr int TEAMS_PER_BLOCK = P == 1 ? 4 : 1;
 
-template <typename T, int P, int VPT>
+// AHEAD: the blocks are as many as are resident and each thread has its next
+// row's vectors in flight while it works on one; otherwise a team per row.
+template <typename T, int P, int VPT, bool AHEAD>
 __global__ void __launch_bounds__(32 * P * TEAMS_PER_BLOCK<P>)
     ln_fwd_kernel(T* out, float* mean_out, float* rstd_out, const T* inp, const T* __restrict__ weight,
                   const T* __restrict__ bias, int64_t rows, int C, float eps) {
@@ -95,54 +97,61 @@ __global__ void __launch_bounds__(32 * P * TEAMS_PER_BLOCK<P>)
     const int team = warp / P, wt = warp % P, t = wt * 32 + lane;
     const int nvec = C / N;
     const float inv_c = 1.f / static_cast<float>(C);
-    const int64_t r = static_cast<int64_t>(blockIdx.x) * TEAMS + team;
+    const int64_t stride = static_cast<int64_t>(gridDim.x) * TEAMS;
     ptx::grid_launch_dependents();
     ptx::grid_dependency_wait();
-    if (r >= rows) return;  // (a whole team)
-    const uint4* xr = reinterpret_cast<const uint4*>(inp + r * C);
     uint4 raw[VPT];
+    auto fetch = [&](int64_t r) {
+        const uint4* xr = reinterpret_cast<const uint4*>(inp + r * C);
 #pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-        const int v = t + 32 * P * j;
-        raw[j] = v < nvec ? xr[v] : make_uint4(0u, 0u, 0u, 0u);
-    }
-    float x[VPT][N];
-    float s = 0.f;
-#pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-        V::get(raw[j], x[j]);
-#pragma unroll
-        for (int e = 0; e < N; ++e) s += x[j][e];
-    }
-    const float mean = team_sum<P>(s, slots[team], 0, wt, team) * inv_c;
-    s = 0.f;
-#pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-        const bool on = j + 1 < VPT || t + 32 * P * j < nvec;  // only the last vector may be missing
-#pragma unroll
-        for (int e = 0; e < N; ++e) {
-            x[j][e] = on ? x[j][e] - mean : 0.f;
-            s += x[j][e] * x[j][e];
+        for (int j = 0; j < VPT; ++j) {
+            const int v = t + 32 * P * j;
+            raw[j] = j + 1 < VPT || v < nvec ? xr[v] : make_uint4(0u, 0u, 0u, 0u);  // only the last vector may be missing
         }
-    }
-    const float var = team_sum<P>(s, slots[team], 1, wt, team) * inv_c;
-    const float rstd = 1.f / sqrtf(var + eps);
-    uint4* dst = reinterpret_cast<uint4*>(out + r * C);
+    };
+    int64_t r = static_cast<int64_t>(blockIdx.x) * TEAMS + team;
+    if (r < rows) fetch(r);
+    for (; r < rows; r += stride) {
+        float x[VPT][N];
+        float s = 0.f;
 #pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-        const int v = t + 32 * P * j;
-        if (j + 1 < VPT || v < nvec) {
-            float w[N], b[N];
-            V::get(__ldg(reinterpret_cast<const uint4*>(weight) + v), w);
-            V::get(bias ? __ldg(reinterpret_cast<const uint4*>(bias) + v) : make_uint4(0u, 0u, 0u, 0u), b);
+        for (int j = 0; j < VPT; ++j) {
+            V::get(raw[j], x[j]);
 #pragma unroll
-            for (int e = 0; e < N; ++e) x[j][e] = x[j][e] * rstd * w[e] + b[e];
-            __stcs(dst + v, V::put(x[j]));
+            for (int e = 0; e < N; ++e) s += x[j][e];
         }
-    }
-    if (t == 0) {
-        if (mean_out) mean_out[r] = mean;
-        if (rstd_out) rstd_out[r] = rstd;
+        if (AHEAD && r + stride < rows) fetch(r + stride);
+        const float mean = team_sum<P>(s, slots[team], 0, wt, team) * inv_c;
+        s = 0.f;
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            const bool on = j + 1 < VPT || t + 32 * P * j < nvec;
+#pragma unroll
+            for (int e = 0; e < N; ++e) {
+                x[j][e] = on ? x[j][e] - mean : 0.f;
+                s += x[j][e] * x[j][e];
+            }
+        }
+        const float var = team_sum<P>(s, slots[team], 1, wt, team) * inv_c;
+        const float rstd = 1.f / sqrtf(var + eps);
+        uint4* dst = reinterpret_cast<uint4*>(out + r * C);
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            const int v = t + 32 * P * j;
+            if (j + 1 < VPT || v < nvec) {
+                float w[N], b[N];
+                V::get(__ldg(reinterpret_cast<const uint4*>(weight) + v), w);
+                V::get(bias ? __ldg(reinterpret_cast<const uint4*>(bias) + v) : make_uint4(0u, 0u, 0u, 0u), b);
+#pragma unroll
+                for (int e = 0; e < N; ++e) x[j][e] = x[j][e] * rstd * w[e] + b[e];
+                __stcs(dst + v, V::put(x[j]));
+            }
+        }
+        if (t == 0) {
+            if (mean_out) mean_out[r] = mean;
+            if (rstd_out) rstd_out[r] = rstd;
+        }
+        if (!AHEAD) break;
     }
 }
 
@@ -198,14 +207,26 @@ __global__ void __launch_bounds__(1024) ln_fwd_wide_kernel(T* out, float* mean_o
 template <typename T>
 using LnFwdKernel = void (*)(T*, float*, float*, const T*, const T*, const T*, int64_t, int, float);
 
-// The kernel whose team of P warps holds a row in exactly `need` vectors a thread.
+template <typename T>
+struct Choice {
+    LnFwdKernel<T> kernel;
+    bool ahead;
+};
+
+// The kernel whose team of P warps holds a row in exactly `need` vectors a
+// thread. `ahead` where it was measured faster: teams of one warp, and of eight
+// with at most two vectors (more of them no longer fit beside the next row's:
+// 8192 x 4096 bf16 26.5 -> 22.2 us with it, 4096 x 8192 fp32 41.5 -> 46.7).
 template <typename T, int P, int VPT>
-LnFwdKernel<T> pick(int need) {
+Choice<T> pick(int need, bool ahead) {
     if constexpr (VPT > 8) {
-        return ln_fwd_wide_kernel<T>;
+        return {ln_fwd_wide_kernel<T>, true};
     } else {
-        if (need <= VPT) return ln_fwd_kernel<T, P, VPT>;
-        return pick<T, P, VPT + 1>(need);
+        if (need > VPT) return pick<T, P, VPT + 1>(need, ahead);
+        if constexpr (P == 1 || (P == 8 && VPT <= 2)) {
+            if (ahead) return {ln_fwd_kernel<T, P, VPT, true>, true};
+        }
+        return {ln_fwd_kernel<T, P, VPT, false>, false};
     }
 }
 
@@ -213,15 +234,23 @@ template <typename T>
 cudaError_t launch(T* out, float* mean, float* rstd, const T* inp, const T* weight, const T* bias, int64_t BT, int C,
                    float eps, int num_sms, cudaStream_t stream) {
     // Up to eight vectors a thread: a warp per row while that is enough (no
-    // barrier), then a block of 8 or 32 warps.
+    // barrier), then a block of 8 or 32 warps. A next row to fetch ahead only
+    // where every resident team has several.
     const int nvec = C / Vec<T>::N;
-    LnFwdKernel<T> k;
+    const bool many = BT >= 4096;
+    Choice<T> c;
     int threads;
     int64_t blocks = BT;
-    if (nvec <= 32 * 8) k = pick<T, 1, 1>((nvec + 31) / 32), threads = 128, blocks = (BT + 3) / 4;
-    else if (nvec <= 256 * 8) k = pick<T, 8, 2>((nvec + 255) / 256), threads = 256;
-    else if (nvec <= 1024 * 8) k = pick<T, 32, 3>((nvec + 1023) / 1024), threads = 1024;
-    else k = ln_fwd_wide_kernel<T>, threads = 1024, blocks = std::min<int64_t>(BT, 2 * num_sms);
+    if (nvec <= 32 * 8) c = pick<T, 1, 1>((nvec + 31) / 32, many), threads = 128, blocks = (BT + 3) / 4;
+    else if (nvec <= 256 * 8) c = pick<T, 8, 2>((nvec + 255) / 256, many), threads = 256;
+    else if (nvec <= 1024 * 8) c = pick<T, 32, 3>((nvec + 1023) / 1024, many), threads = 1024;
+    else c = {ln_fwd_wide_kernel<T>, true}, threads = 1024;
+    if (c.ahead) {
+        int per_sm = 0;
+        const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, c.kernel, threads, 0);
+        if (e != cudaSuccess) return e;
+        blocks = std::min<int64_t>(blocks, static_cast<int64_t>(num_sms) * std::max(per_sm, 1));
+    }
     if (blocks > INT32_MAX) return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>(blocks), 1, 1);
@@ -232,7 +261,7 @@ cudaError_t launch(T* out, float* mean, float* rstd, const T* inp, const T* weig
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, k, out, mean, rstd, inp, weight, bias, BT, C, eps);
+    return cudaLaunchKernelEx(&cfg, c.kernel, out, mean, rstd, inp, weight, bias, BT, C, eps);
 }
 
 }  // namespace
