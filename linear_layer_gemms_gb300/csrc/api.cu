@@ -1017,12 +1017,8 @@ int mmbwd_q8_forward(void* out, const void* inp_q, const void* inp_scale, const 
         p.B = static_cast<const uint8_t*>(weight_q), p.b_scale = static_cast<const uint8_t*>(weight_scale);
         p.M = s.BT, p.N = OC, p.K = C;
         p.a_format = inp_format, p.b_format = weight_format, p.dtype = dtype;
-        // Few tokens: the weight's bytes are the work, and a tile with the weight on its
-        // 128-row side wastes less. Measured (us, tokens kernel against pair kernel):
-        // 1 token 1600 -> 4800 5.2 / 7.3, 64 tokens 6.9 / 7.4, 64 x 768 -> 768 4.5 / 4.5,
-        // 64 x 12800 -> 4096 15.0 / 32.4; at 128 tokens its forerunner took 11.8 / 9.3.
-        e = s.BT <= 64 ? q8_tokens_launch(p, d->num_sms, stream)
-                       : q8_products_launch(&p, 1, false, nullptr, 0, d->num_sms, stream);
+        e = q8_few_tokens(s.BT, OC, d->num_sms) ? q8_tokens_launch(p, d->num_sms, stream)
+                                                : q8_products_launch(&p, 1, false, nullptr, 0, d->num_sms, stream);
     }
     return e == cudaSuccess ? MMBWD_OK : MMBWD_ERR_CUDA;
 }

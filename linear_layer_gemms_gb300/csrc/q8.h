@@ -41,6 +41,16 @@ struct Q8Product {
 size_t q8_products_workspace(const Q8Product* products, int n, int num_sms);
 cudaError_t q8_products_launch(const Q8Product* products, int n, bool may_split, void* ws, size_t ws_bytes, int num_sms,
                                cudaStream_t stream);
+// Whether the forward takes the few-tokens kernel: always up to 64 tokens, and
+// up to 256 while its 128 x 64 tiles are at most half the SMs, so that several
+// CTAs share each tile's K. Measured (us, this kernel against the pair kernel): 1 token
+// 1600 -> 4800 5.2 / 7.3; 64 tokens 6.9 / 7.4; 64 x 768 -> 768 4.5 / 4.5; 128 x 6400 ->
+// 1600 9.1 / 18.1; 128 x 12800 -> 4096 22.8 / 32.8; 256 x 6400 -> 1600 12.8 / 18.2;
+// beyond the rule 192 x 12800 -> 4096 36.8 / 32.8, 192 x 1600 -> 4800 8.0 / 7.7.
+inline bool q8_few_tokens(int64_t tokens, int64_t N, int num_sms) {
+    return tokens <= 64 || (tokens <= 256 && (tokens + 63) / 64 * ((N + 127) / 128) <= num_sms / 2);
+}
+
 // The forward (D overwritten) for few tokens (rows of A).
 cudaError_t q8_tokens_launch(const Q8Product& product, int num_sms, cudaStream_t stream);
 cudaError_t q8_tokens_read_status(int* code, int* info3, bool reset);

@@ -4,7 +4,7 @@
 //
 // The product is turned around: 128 rows of the weight are the MMA's M side and
 // NT tokens (16, 32 or 64) its N side, so a small T does not fill most of a
-// 256-row tile with nothing. Block scales enter the MMA as in the pair kernel
+// 256-row tile with nothing; more tokens are more tiles. Block scales enter the MMA as in the pair kernel
 // (q8_product.cu). Two CTAs per SM, each with a ring of up to 100 KB.
 //
 // Tiles alone fill the device when there are many (a vocabulary): CTAs then
@@ -66,9 +66,9 @@ struct Params {
     void* out;
     const void* bias;
     const uint8_t *w_scale, *x_scale;
-    int64_t N;
+    int64_t T, N;
     int64_t groups;
-    int T, kb, tiles, splits, f32;
+    int kb, tiles, tiles_n, splits, f32;
     uint32_t idesc;
 };
 
@@ -121,7 +121,10 @@ __global__ void __launch_bounds__(THREADS, 2)
         if (lane == 0) {
             uint32_t stage = 0, phase = 0, issued = 0, last_parity = 0;
             for (int tile = first; tile < p.tiles && ok; tile += step) {
-                const uint8_t* sw = p.w_scale + tile * p.groups * 512;
+                const int n0 = tile % p.tiles_n * ROWS;
+                const int64_t t0 = static_cast<int64_t>(tile / p.tiles_n) * NT;
+                const uint8_t* sw = p.w_scale + (n0 / 128) * p.groups * 512;
+                const uint8_t* sx = p.x_scale + (t0 / 128) * p.groups * 512;
                 for (int kb = kb0; kb < kb1; ++kb) {
                     if (!wt.wait(empty + 8u * stage, phase ^ 1u, q8::SITE_EMPTY, tile)) {
                         ok = false;
@@ -130,14 +133,14 @@ __global__ void __launch_bounds__(THREADS, 2)
                     const uint32_t at = base + stage * L::STAGE, bar = full + 8u * stage;
                     const bool sf = kb == kb0 || (kb & 3) == 0;
                     ptx::mbar_arrive_expect_tx(bar, L::STAGE + (sf ? 1024u : 0u));
-                    ptx::tma_load_2d(at, &tm_w, bar, kb * 128, tile * ROWS);
+                    ptx::tma_load_2d(at, &tm_w, bar, kb * 128, n0);
                     if (sf) {
                         const uint32_t st = base + L::OFF_SF + stage * 1024;
                         const int64_t g = static_cast<int64_t>(kb >> 2) * 512;
                         q8::bulk_load(st, sw + g, 512u, bar);
-                        q8::bulk_load(st + 512u, p.x_scale + g, 512u, bar);
+                        q8::bulk_load(st + 512u, sx + g, 512u, bar);
                     }
-                    ptx::tma_load_2d(at + ROWS * 128, &tm_x, bar, kb * 128, 0);
+                    ptx::tma_load_2d(at + ROWS * 128, &tm_x, bar, kb * 128, static_cast<int32_t>(t0));
                     issued |= 1u << stage;
                     last_parity = (last_parity & ~(1u << stage)) | (phase << stage);
                     if (++stage == L::STAGES) stage = 0, phase ^= 1u;
@@ -152,6 +155,9 @@ __global__ void __launch_bounds__(THREADS, 2)
             uint32_t stage = 0, phase = 0, sf_buf = 0, sfa = 0, n = 0;
             for (int tile = first; tile < p.tiles && ok; tile += step, ++n) {
                 const uint32_t acc = n & 1u;
+                // the tokens' scales are a tile of 128 rows, 32 to a column: the second
+                // 64 tokens of it start two columns in
+                const uint32_t sfb_at = 4u + (NT == 64 ? static_cast<uint32_t>(tile / p.tiles_n & 1) * 2u : 0u);
                 if (n >= 2 && !wt.wait(acc_free + 8u * acc, ((n >> 1) - 1u) & 1u, q8::SITE_ACC_FREE, tile)) break;
                 ptx::tc_fence_after();
                 for (int kb = kb0; kb < kb1; ++kb) {
@@ -173,7 +179,8 @@ __global__ void __launch_bounds__(THREADS, 2)
                     const uint32_t idesc = p.idesc | q8::scale_id(static_cast<uint32_t>(kb) & 3u);
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        q8::mma_mxf8(tmem + acc * L::ACC, a0 + 2u * k, b0 + 2u * k, idesc, sfa, sfa + 4u, (kb > kb0 || k > 0) ? 1u : 0u);
+                        q8::mma_mxf8(tmem + acc * L::ACC, a0 + 2u * k, b0 + 2u * k, idesc, sfa, sfa + sfb_at,
+                                     (kb > kb0 || k > 0) ? 1u : 0u);
                     ptx::mma_commit(empty + 8u * stage);
                     if (++stage == L::STAGES) stage = 0, phase ^= 1u;
                 }
@@ -197,7 +204,9 @@ __global__ void __launch_bounds__(THREADS, 2)
         const int shift = __ffs(p.splits) - 1;
         uint32_t n = 0;
         for (int tile = first; tile < p.tiles; tile += step, ++n) {
-            const int64_t o = static_cast<int64_t>(tile) * ROWS + row;
+            const int64_t o = static_cast<int64_t>(tile % p.tiles_n) * ROWS + row;
+            const int64_t t0 = static_cast<int64_t>(tile / p.tiles_n) * NT;
+            const int tokens = static_cast<int>(min(static_cast<int64_t>(NT), p.T - t0));
             const bool in = o < p.N;
             float b = 0.f;
             if (p.bias && in && p.splits == 1)
@@ -207,29 +216,29 @@ __global__ void __launch_bounds__(THREADS, 2)
             ptx::tc_fence_after();
             const uint32_t src = tmem + (static_cast<uint32_t>(32 * q) << 16) + acc * L::ACC;
 #pragma unroll 1
-            for (int c = 0; c < p.T; c += 16) {
+            for (int c = 0; c < tokens; c += 16) {
                 uint32_t v[16];
                 q8::tmem_ld16(src + c, v);
                 if (p.splits > 1) {
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
                         const int t = c + e;
-                        if (t < p.T)
+                        if (t < tokens)
                             ptx::st_dsmem_u32(ptx::mapa(part + static_cast<uint32_t>(t >> shift) * (ROWS * 4u),
                                                         static_cast<uint32_t>(t & (p.splits - 1))),
                                               v[e]);
                     }
                 } else if (in) {
                     if (p.f32) {
-                        float* dst = static_cast<float*>(p.out) + c * p.N + o;
+                        float* dst = static_cast<float*>(p.out) + (t0 + c) * p.N + o;
 #pragma unroll
                         for (int e = 0; e < 16; ++e, dst += p.N)
-                            if (c + e < p.T) *dst = __uint_as_float(v[e]) + b;
+                            if (c + e < tokens) *dst = __uint_as_float(v[e]) + b;
                     } else {
-                        __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + c * p.N + o;
+                        __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + (t0 + c) * p.N + o;
 #pragma unroll
                         for (int e = 0; e < 16; ++e, dst += p.N)
-                            if (c + e < p.T) *dst = __float2bfloat16_rn(__uint_as_float(v[e]) + b);
+                            if (c + e < tokens) *dst = __float2bfloat16_rn(__uint_as_float(v[e]) + b);
                     }
                 }
             }
@@ -240,7 +249,9 @@ __global__ void __launch_bounds__(THREADS, 2)
     }
     if (p.splits > 1) {
         ptx::cluster_sync();  // this rank's tokens have every rank's partial sums
-        const int64_t o = static_cast<int64_t>(first) * ROWS + 4 * lane;  // (N is a multiple of 4)
+        const int64_t o = static_cast<int64_t>(first % p.tiles_n) * ROWS + 4 * lane;  // (N is a multiple of 4)
+        const int64_t t0 = static_cast<int64_t>(first / p.tiles_n) * NT;
+        const int tokens = static_cast<int>(min(static_cast<int64_t>(NT), p.T - t0));
         const int owned = (NT + p.splits - 1) / p.splits;
         if (o < p.N) {
             float b[4] = {0.f, 0.f, 0.f, 0.f};
@@ -249,7 +260,7 @@ __global__ void __launch_bounds__(THREADS, 2)
                 for (int e = 0; e < 4; ++e)
                     b[e] = p.f32 ? static_cast<const float*>(p.bias)[o + e] : __bfloat162float(static_cast<const __nv_bfloat16*>(p.bias)[o + e]);
             }
-            for (int i = warp; rank + i * p.splits < p.T; i += THREADS / 32) {
+            for (int i = warp; rank + i * p.splits < tokens; i += THREADS / 32) {
                 const uint32_t at = base + L::OFF_PART + static_cast<uint32_t>((i * ROWS + 4 * lane) * 4);
                 float4 f[8];
 #pragma unroll
@@ -259,7 +270,7 @@ __global__ void __launch_bounds__(THREADS, 2)
 #pragma unroll
                 for (int s = 1; s < 8; ++s)
                     if (s < p.splits) v.x += f[s].x, v.y += f[s].y, v.z += f[s].z, v.w += f[s].w;
-                const int64_t to = static_cast<int64_t>(rank + i * p.splits) * p.N + o;
+                const int64_t to = (t0 + rank + i * p.splits) * p.N + o;
                 v.x += b[0], v.y += b[1], v.z += b[2], v.w += b[3];
                 if (p.f32) {
                     *reinterpret_cast<float4*>(static_cast<float*>(p.out) + to) = v;
@@ -352,13 +363,15 @@ cudaError_t launch(const Q8Product& q, Params p, int num_sms, cudaStream_t strea
 
 cudaError_t q8_tokens_launch(const Q8Product& q, int num_sms, cudaStream_t stream) {
     if (take_injected_launch_failure()) return cudaErrorLaunchFailure;
-    if (q.M > 64) return cudaErrorInvalidValue;
     Params p{};
     p.out = q.D, p.bias = q.bias, p.w_scale = q.b_scale, p.x_scale = q.a_scale;
-    p.T = static_cast<int>(q.M), p.N = q.N, p.groups = q8_groups(q.K);
+    p.T = q.M, p.N = q.N, p.groups = q8_groups(q.K);
     p.kb = static_cast<int>(q8_blocks(q.K));
     p.f32 = q.dtype == MMBWD_F32 ? 1 : 0;
-    p.tiles = static_cast<int>((q.N + ROWS - 1) / ROWS);
+    p.tiles_n = static_cast<int>((q.N + ROWS - 1) / ROWS);
+    const int64_t tiles = p.tiles_n * (q.M <= 64 ? 1 : (q.M + 63) / 64);
+    if (tiles > INT32_MAX / 8) return cudaErrorInvalidValue;
+    p.tiles = static_cast<int>(tiles);
     if (q.M <= 16) return launch<16>(q, p, num_sms, stream);
     if (q.M <= 32) return launch<32>(q, p, num_sms, stream);
     return launch<64>(q, p, num_sms, stream);

@@ -192,7 +192,7 @@ def test_quantize_offsets_beyond_32_bits():
 # (tokens, C, OC): single tokens, short and odd prompts, ragged in every direction
 SHAPES = [(1, 8, 8), (1, 1600, 520), (2, 264, 136), (5, 24, 1000), (16, 768, 2304), (17, 1000, 264), (48, 640, 328),
           (64, 136, 4104), (100, 520, 392), (129, 128, 128), (130, 1160, 136), (255, 392, 776), (300, 2056, 264),
-          (777, 264, 1032)]
+          (777, 264, 1032), (100, 264, 10_008), (200, 392, 5000), (257, 1032, 24)]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
@@ -217,7 +217,7 @@ def test_forward(shape, dtype):
 
 @pytest.mark.parametrize("splits", ["1", "2", "4", "8"])
 @pytest.mark.parametrize("shape", [(1, 1032, 264), (7, 2056, 520), (16, 1160, 132), (31, 1800, 260), (33, 1096, 392),
-                                   (64, 1032, 1000)], ids=lambda s: "x".join(map(str, s)))
+                                   (64, 1032, 1000), (65, 1032, 264), (130, 1160, 392), (256, 1096, 136)], ids=lambda s: "x".join(map(str, s)))
 def test_forward_few_tokens_every_split(monkeypatch, shape, splits):
     """Few tokens: K shared by 1 to 8 CTAs, partial tiles of tokens and rows."""
     import torch
