@@ -86,8 +86,8 @@ size_t mmbwd_q8_scale_bytes(int64_t rows, int64_t K);
  *                  rows (of the unquantised values, fp32): dbias when x is dout
  *   x              device, (rows, cols), read only
  *   workspace      device, mmbwd_q8_quantize_workspace_bytes() bytes, 256-byte
- *                  aligned, contents ignored and overwritten; only read with colsum
- *                  (may be NULL without)
+ *                  aligned, contents ignored and overwritten; used with colsum of more
+ *                  than 1024 rows (may be NULL where 0 bytes are needed)
  *   rows, cols     >= 0; cols times the element size a multiple of 16 bytes
  *   dtype          MMBWD_F32 or MMBWD_BF16 (x and colsum)
  *   format         MMBWD_E4M3 or MMBWD_E5M2 (both forms)

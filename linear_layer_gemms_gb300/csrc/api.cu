@@ -937,7 +937,7 @@ size_t mmbwd_q8_data_bytes(int64_t rows, int64_t K) { return q8_shape_ok(rows, K
 size_t mmbwd_q8_scale_bytes(int64_t rows, int64_t K) { return q8_shape_ok(rows, K) ? q8_scale_size(rows, K) : 0; }
 
 size_t mmbwd_q8_quantize_workspace_bytes(int64_t rows, int64_t cols) {
-    if (!q8_shape_ok(rows, cols)) return 0;
+    if (!q8_shape_ok(rows, cols) || q8_blocks(rows) <= Q8_SUM_CLUSTER) return 0;
     return (static_cast<size_t>(q8_blocks(rows)) * static_cast<size_t>(cols) * 4 + 255) & ~size_t(255);
 }
 

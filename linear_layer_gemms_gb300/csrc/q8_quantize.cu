@@ -293,13 +293,17 @@ __device__ __forceinline__ void turn_columns(const Eight<T> (&v)[8], TileMem& sm
 template <typename T, int FMT, bool ROW, bool COL>
 __global__ void __launch_bounds__(QT_THREADS, sizeof(T) == 2 ? 4 : 2)
     q8_quantize_kernel(uint8_t* __restrict__ q, uint8_t* __restrict__ scale, uint8_t* __restrict__ qt,
-                       uint8_t* __restrict__ scale_t, float* __restrict__ partials, const T* __restrict__ x, int64_t rows,
-                       int64_t cols, int64_t ld, int64_t ldt, int64_t kb_row, int64_t kb_col, uint32_t tiles_c) {
+                       uint8_t* __restrict__ scale_t, float* __restrict__ partials, T* __restrict__ colsum,
+                       const T* __restrict__ x, int64_t rows, int64_t cols, int64_t ld, int64_t ldt, int64_t kb_row,
+                       int64_t kb_col, uint32_t tiles_c) {
     using E = Eight<T>;
     __shared__ TileMem sm;
     const int tid = static_cast<int>(threadIdx.x), warp = tid >> 5, lane = tid & 31;
     const int g = tid >> 4, u = tid & 15;
-    const int64_t tr = blockIdx.x / tiles_c, tc = blockIdx.x % tiles_c;  // the tile: row block, column block
+    // the tile: row block, column block (colsum: the row blocks of a column are a cluster)
+    const uint32_t kbc = static_cast<uint32_t>(kb_col);
+    const int64_t tr = colsum ? blockIdx.x % kbc : blockIdx.x / tiles_c, tc = colsum ? blockIdx.x / kbc : blockIdx.x % tiles_c;
+    const bool sums = partials || colsum;
     const int64_t r0 = tr * 128, c0 = tc * 128;
     if (COL && tid < 128) sm.col_max[tid] = 0u;
     ptx::grid_launch_dependents();
@@ -331,7 +335,7 @@ __global__ void __launch_bounds__(QT_THREADS, sizeof(T) == 2 ? 4 : 2)
         cm[k] = m & E::MAG;
         bad |= E::bad(cm[k]);
     }
-    if (partials) {
+    if (sums) {
         float s[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) s[j] = 0.f;
@@ -383,11 +387,12 @@ __global__ void __launch_bounds__(QT_THREADS, sizeof(T) == 2 ? 4 : 2)
         }
         __syncthreads();
     }
-    if (partials && tid < 128 && c0 + tid < cols) {
+    if (sums && tid < 128) {
         float s = sm.sums[0][tid];
 #pragma unroll
         for (int w = 1; w < 8; ++w) s += sm.sums[w][tid];
-        partials[tr * cols + c0 + tid] = s;
+        if (colsum) sm.sums[0][tid] = s;
+        else if (c0 + tid < cols) partials[tr * cols + c0 + tid] = s;
     }
     if (COL && tid < 128) {
         const uint32_t m = sm.col_max[tid];
@@ -420,9 +425,22 @@ __global__ void __launch_bounds__(QT_THREADS, sizeof(T) == 2 ? 4 : 2)
             if (cl < cols_here) *reinterpret_cast<uint4*>(dst) = make_uint4(a.x, a.y, b.x, b.y);
         }
     }
+    if (colsum) {  // the row blocks' sums, in order, by the first CTA of the cluster
+        ptx::cluster_sync();
+        if (tr == 0 && tid < 128 && c0 + tid < cols) {
+            const uint32_t at = ptx::smem_u32(&sm.sums[0][tid]);
+            float t = sm.sums[0][tid];
+            for (uint32_t k = 1; k < kbc; ++k) t += __uint_as_float(ptx::ld_dsmem_u32(ptx::mapa(at, k)));
+            if constexpr (sizeof(T) == 4)
+                colsum[c0 + tid] = t;
+            else
+                colsum[c0 + tid] = __float2bfloat16_rn(t);
+        }
+        ptx::cluster_sync();
+    }
 }
 
-// colsum[c] = the row blocks' sums added in order: eight warps of a block each
+// More than Q8_SUM_CLUSTER row blocks: colsum[c] = their sums added in order, eight warps of a block each
 // take a contiguous eighth of the row blocks for 32 columns, then the eighths
 // are added in order and rounded once.
 template <typename T>
@@ -453,19 +471,22 @@ __global__ void __launch_bounds__(256) q8_colsum_kernel(T* __restrict__ colsum, 
 }
 
 template <typename T, int FMT, bool ROW, bool COL>
-cudaError_t launch_tiles(uint8_t* q, uint8_t* scale, uint8_t* qt, uint8_t* scale_t, float* partials, const T* x,
+cudaError_t launch_tiles(uint8_t* q, uint8_t* scale, uint8_t* qt, uint8_t* scale_t, float* partials, T* colsum, const T* x,
                          int64_t rows, int64_t cols, cudaStream_t stream) {
     const int64_t tiles_r = q8_blocks(rows), tiles_c = q8_blocks(cols);
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>(tiles_r * tiles_c), 1, 1);
     cfg.blockDim = dim3(QT_THREADS, 1, 1);
     cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(colsum ? tiles_r : 1);
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, q8_quantize_kernel<T, FMT, ROW, COL>, q, scale, qt, scale_t, partials, x, rows,
+    cfg.numAttrs = colsum ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, q8_quantize_kernel<T, FMT, ROW, COL>, q, scale, qt, scale_t, partials, colsum, x, rows,
                               cols, q8_ld(cols), q8_ld(rows), q8_blocks(cols), q8_blocks(rows),
                               static_cast<uint32_t>(tiles_c));
 }
@@ -473,15 +494,17 @@ cudaError_t launch_tiles(uint8_t* q, uint8_t* scale, uint8_t* qt, uint8_t* scale
 template <typename T, int FMT>
 cudaError_t launch_forms(uint8_t* q, uint8_t* scale, uint8_t* qt, uint8_t* scale_t, void* colsum, const T* x,
                          float* partials, int64_t rows, int64_t cols, cudaStream_t stream) {
-    float* part = colsum ? partials : nullptr;
+    // few row blocks: their sums meet in a cluster; more: in the workspace
+    T* direct = q8_blocks(rows) <= Q8_SUM_CLUSTER ? static_cast<T*>(colsum) : nullptr;
+    float* part = colsum && !direct ? partials : nullptr;
     cudaError_t e;
     if (q && qt)
-        e = launch_tiles<T, FMT, true, true>(q, scale, qt, scale_t, part, x, rows, cols, stream);
+        e = launch_tiles<T, FMT, true, true>(q, scale, qt, scale_t, part, direct, x, rows, cols, stream);
     else if (qt)
-        e = launch_tiles<T, FMT, false, true>(q, scale, qt, scale_t, part, x, rows, cols, stream);
+        e = launch_tiles<T, FMT, false, true>(q, scale, qt, scale_t, part, direct, x, rows, cols, stream);
     else
-        e = launch_tiles<T, FMT, true, false>(q, scale, qt, scale_t, part, x, rows, cols, stream);
-    if (e != cudaSuccess || !colsum) return e;
+        e = launch_tiles<T, FMT, true, false>(q, scale, qt, scale_t, part, direct, x, rows, cols, stream);
+    if (e != cudaSuccess || !part) return e;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>((cols + 31) / 32), 1, 1);
     cfg.blockDim = dim3(256, 1, 1);

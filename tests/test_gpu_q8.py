@@ -84,7 +84,8 @@ def q8(x, fmt):
     return torch.from_numpy(bits).cuda(), torch.from_numpy(scales).cuda(), value
 
 
-SIZES = [(1, 8), (1, 1600), (7, 128), (33, 136), (127, 120), (128, 512), (129, 264), (300, 1000), (777, 520)]
+SIZES = [(1, 8), (1, 1600), (7, 128), (33, 136), (127, 120), (128, 512), (129, 264), (300, 1000), (777, 520), (1024, 136),
+         (1025, 264), (2500, 72)]
 
 
 @pytest.mark.parametrize("fmt", [mm.E4M3, mm.E5M2], ids=["e4m3", "e5m2"])

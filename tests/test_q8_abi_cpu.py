@@ -24,7 +24,7 @@ def test_sizes():
     assert mm.mmbwd_q8_data_bytes(0, 100) == 0 and mm.mmbwd_q8_scale_bytes(5, 0) == 0
     assert mm.mmbwd_q8_data_bytes(-1, 100) == 0 and mm.mmbwd_q8_scale_bytes(5, 1 << 31) == 0
     assert mm.mmbwd_q8_data_bytes(1 << 22, 2048) == 1 << 33
-    assert mm.mmbwd_q8_quantize_workspace_bytes(129, 64) == 512
+    assert mm.mmbwd_q8_quantize_workspace_bytes(1025, 64) == 9 * 64 * 4 and mm.mmbwd_q8_quantize_workspace_bytes(1024, 64) == 0
     assert mm.mmbwd_q8_quantize_workspace_bytes(-1, 64) == 0
     assert mm.mmbwd_q8_backward_workspace_bytes(-1, 8, 64, 64) == 0
 
@@ -46,14 +46,15 @@ def test_quantize_refusals():
     assert quantize(scale=None) == mm.ERR_NULL
     assert quantize(qt=None) == mm.ERR_NULL
     assert quantize(q=None, scale=None, qt=None, scale_t=None) == mm.ERR_NULL
-    assert quantize(workspace=None) == mm.ERR_NULL
-    assert quantize(workspace_bytes=8) == mm.ERR_SHAPE
-    assert quantize(workspace=7 * A + 16) == mm.ERR_ALIGN
+    assert quantize(workspace=None, rows=2000) == mm.ERR_NULL
+    assert quantize(workspace_bytes=8, rows=2000) == mm.ERR_SHAPE
+    assert quantize(workspace=7 * A + 16, rows=2000) == mm.ERR_ALIGN
     assert quantize(x=6 * A + 8) == mm.ERR_ALIGN
     assert quantize(cols=60) == mm.ERR_ALIGN
     assert quantize(q=6 * A + 64) == mm.ERR_ALIAS
     assert quantize(scale=A + 6400 - 16) == mm.ERR_ALIAS
-    assert quantize(colsum=7 * A) == mm.ERR_ALIAS
+    assert quantize(colsum=7 * A, rows=2000) == mm.ERR_ALIAS
+    assert quantize(colsum=6 * A) == mm.ERR_ALIAS
 
 
 def forward(**kw):
