@@ -561,11 +561,14 @@ Forced forced_from_env() {
     return f;
 }
 
-// The best plan by the time model over tile widths and, where allowed, splits.
+// The best plan by the time model over tile widths and, where allowed, splits;
+// n_items == 0 where no candidate is possible (an override that asks for more items
+// than the schedule holds).
 void make_plan(const Shape3* s, int n, bool may_split, const Forced& force, int num_sms, Plan* out) {
     static thread_local Plan c;
     const int max_pairs = std::max(1, std::min(num_sms / 2, MAX_PAIRS));
     double best = 1e300;
+    *out = Plan{};
     static const int kSplits[] = {1, 2, 3, 4, 6, 8, 12, 16};
     for (int widths = 0; widths < (n == 2 ? 4 : 2); ++widths)
         for (int s0 : kSplits)
@@ -675,6 +678,7 @@ const Plan& plan_for(const Shape3* s, int n, bool may_split, int num_sms) {
     if (g_plan_count < CACHE) ++g_plan_count;
     g_keys[slot] = k;
     make_plan(s, n, may_split, k.force, num_sms, &g_plans[slot]);
+    if (g_plans[slot].n_items == 0) make_plan(s, n, may_split, Forced{}, num_sms, &g_plans[slot]);
     return g_plans[slot];
 }
 
@@ -781,7 +785,7 @@ cudaError_t q8_products_launch(const Q8Product* products, int n, bool may_split,
     for (int i = 0; i < n; ++i) s[i] = {products[i].M, products[i].N, products[i].K};
     std::lock_guard<std::mutex> g(g_plan_mutex);
     const Plan& pl = plan_for(s, n, may_split, num_sms);
-    if (pl.ws_bytes > ws_bytes) return cudaErrorInvalidValue;
+    if (pl.n_items == 0 || pl.ws_bytes > ws_bytes) return cudaErrorInvalidValue;
     return launch_pair(pl, products, static_cast<uint8_t*>(ws), stream);
 }
 

@@ -106,6 +106,19 @@ def test_backward_refusals():
         assert backward(workspace=None) == mm.ERR_NULL
 
 
+def test_an_impossible_override_falls_back_to_the_planner(monkeypatch):
+    """A forced split that needs more items than the schedule holds is dropped:
+    the plan is the unforced one, never one left over from another shape."""
+    shape = (8, 1024, 1600, 6400)
+    want = mm.mmbwd_q8_backward_workspace_bytes(*shape)
+    for T in range(1, 40):  # plans of other shapes, with workspaces of their own
+        monkeypatch.setenv("MMBWD_Q8_SPLITS", "1,2")
+        assert mm.mmbwd_q8_backward_workspace_bytes(T, 1024, 264, 392) > 0
+    monkeypatch.setenv("MMBWD_Q8_SPLITS", "16,16")
+    monkeypatch.setenv("MMBWD_Q8_TILE_N", "128,128")
+    assert mm.mmbwd_q8_backward_workspace_bytes(*shape) == want
+
+
 def layernorm(**kw):
     a = dict(out=A, mean=2 * A, rstd=3 * A, inp=4 * A, weight=5 * A, bias=6 * A, B=2, T=8, C=64, eps=1e-5, dtype=mm.BF16,
              stream=0)
