@@ -210,51 +210,53 @@ using LnFwdKernel = void (*)(T*, float*, float*, const T*, const T*, const T*, i
 template <typename T>
 struct Choice {
     LnFwdKernel<T> kernel;
+    int threads;
     bool ahead;
 };
 
 // The kernel whose team of P warps holds a row in exactly `need` vectors a
-// thread. `ahead` where it was measured faster: teams of one warp, and of eight
-// with at most two vectors (more of them no longer fit beside the next row's:
-// 8192 x 4096 bf16 26.5 -> 22.2 us with it, 4096 x 8192 fp32 41.5 -> 46.7).
-template <typename T, int P, int VPT>
-Choice<T> pick(int need, bool ahead) {
-    if constexpr (VPT > 8) {
-        return {ln_fwd_wide_kernel<T>, true};
-    } else {
-        if (need > VPT) return pick<T, P, VPT + 1>(need, ahead);
-        if constexpr (P == 1 || (P == 8 && VPT <= 2)) {
-            if (ahead) return {ln_fwd_kernel<T, P, VPT, true>, true};
-        }
-        return {ln_fwd_kernel<T, P, VPT, false>, false};
+// thread, VPT at least and eight at most.
+template <typename T, int P, int VPT, bool AHEAD>
+Choice<T> pick(int need) {
+    if constexpr (VPT < 8) {
+        if (need > VPT) return pick<T, P, VPT + 1, AHEAD>(need);
     }
+    return {ln_fwd_kernel<T, P, VPT, AHEAD>, 32 * P * TEAMS_PER_BLOCK<P>, AHEAD};
+}
+
+// By the row's 16-byte vectors: a warp per row up to eight vectors a lane (no
+// barrier), then teams that fill most of their lanes. The next row is fetched ahead
+// where its registers fit beside the current row's. Measured (us), AHEAD / not:
+// 8192 x 1600 bf16 (one warp) 10.5 / 11.4; 4000 x 2400 bf16 (4 warps, 3 vectors) 8.4 /
+// 9.5, with 8 warps 12.5; 2000 x 6400 bf16 (4 warps, 7) 10.6 / 12.8, fp32 8192 x 3200
+// 34.9 / 32.4; 4096 x 8192 fp32 (8 warps, 8) 46.7 / 41.4.
+template <typename T>
+Choice<T> choose(int nvec) {
+    if (nvec <= 32 * 8) return pick<T, 1, 1, true>((nvec + 31) / 32);
+    if (nvec <= 128 * 4) return pick<T, 4, 3, true>((nvec + 127) / 128);
+    if (nvec <= 128 * 8) return pick<T, 4, 5, sizeof(T) == 2>((nvec + 127) / 128);
+    if (nvec <= 256 * 8) return pick<T, 8, 5, false>((nvec + 255) / 256);
+    if (nvec <= 512 * 8) return pick<T, 16, 5, false>((nvec + 511) / 512);
+    if (nvec <= 1024 * 8) return pick<T, 32, 5, false>((nvec + 1023) / 1024);
+    return {ln_fwd_wide_kernel<T>, 1024, true};
 }
 
 template <typename T>
 cudaError_t launch(T* out, float* mean, float* rstd, const T* inp, const T* weight, const T* bias, int64_t BT, int C,
                    float eps, int num_sms, cudaStream_t stream) {
-    // Up to eight vectors a thread: a warp per row while that is enough (no
-    // barrier), then a block of 8 or 32 warps. A next row to fetch ahead only
-    // where every resident team has several.
-    const int nvec = C / Vec<T>::N;
-    const bool many = BT >= 4096;
-    Choice<T> c;
-    int threads;
-    int64_t blocks = BT;
-    if (nvec <= 32 * 8) c = pick<T, 1, 1>((nvec + 31) / 32, many), threads = 128, blocks = (BT + 3) / 4;
-    else if (nvec <= 256 * 8) c = pick<T, 8, 2>((nvec + 255) / 256, many), threads = 256;
-    else if (nvec <= 1024 * 8) c = pick<T, 32, 3>((nvec + 1023) / 1024, many), threads = 1024;
-    else c = {ln_fwd_wide_kernel<T>, true}, threads = 1024;
+    const Choice<T> c = choose<T>(C / Vec<T>::N);
+    const int teams = C / Vec<T>::N <= 32 * 8 ? TEAMS_PER_BLOCK<1> : 1;
+    int64_t blocks = (BT + teams - 1) / teams;
     if (c.ahead) {
         int per_sm = 0;
-        const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, c.kernel, threads, 0);
+        const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, c.kernel, c.threads, 0);
         if (e != cudaSuccess) return e;
         blocks = std::min<int64_t>(blocks, static_cast<int64_t>(num_sms) * std::max(per_sm, 1));
     }
     if (blocks > INT32_MAX) return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>(blocks), 1, 1);
-    cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
+    cfg.blockDim = dim3(static_cast<unsigned>(c.threads), 1, 1);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

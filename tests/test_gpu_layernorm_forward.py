@@ -72,7 +72,8 @@ def call(x, w, b, eps, dtype, stats=True, in_place=False):
 
 
 # widths of every kernel variant, their borders, and ragged ones
-WIDTHS = [8, 64, 264, 768, 1024, 1032, 1600, 2048, 2056, 4096, 4104, 6400, 8192, 8200, 32768, 32776, 65544]
+WIDTHS = [8, 64, 264, 768, 1024, 1032, 1600, 2048, 2056, 4096, 4104, 6400, 8192, 8200, 16384, 16392, 32768, 32776,
+          65544]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
@@ -89,13 +90,15 @@ def test_against_64_bits(C, dtype):
         assert np.all(np.abs(host(got) - want) <= tol)
 
 
-@pytest.mark.parametrize("T", [1, 2, 7, 4099])
-def test_rows(T):
-    x, w, b = normal((T, 520), "bf16", T), normal((520,), "bf16", 1), normal((520,), "bf16", 2)
-    for C in (520,):
-        out, mean, rstd = call(x, w, b, 1e-5, "bf16")
-        for got, (want, tol) in zip((mean, rstd, out), expected(x, w, b, 1e-5, "bf16")):
-            assert np.all(np.abs(host(got) - want) <= tol)
+@pytest.mark.parametrize("size", [(1, 520), (2, 520), (7, 520), (4099, 520), (4099, 2400), (2500, 6400)],
+                         ids=lambda s: "x".join(map(str, s)))
+def test_rows(size):
+    """One row, less than a block of rows, and many to each team."""
+    T, C = size
+    x, w, b = normal((T, C), "bf16", T), normal((C,), "bf16", 1), normal((C,), "bf16", 2)
+    out, mean, rstd = call(x, w, b, 1e-5, "bf16")
+    for got, (want, tol) in zip((mean, rstd, out), expected(x, w, b, 1e-5, "bf16")):
+        assert np.all(np.abs(host(got) - want) <= tol)
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
