@@ -111,7 +111,7 @@ size_t mmbwd_q8_quantize_workspace_bytes(int64_t rows, int64_t cols);
  *   weight_q, weight_scale  device, row form of weight (OC x C), format weight_format
  *   bias_or_null            device, (OC), type `dtype`
  *
- * OC times the element size a multiple of 16 bytes; C and B*T any size. No
+ * OC a multiple of 4; C and B*T any size. No
  * workspace. C == 0 gives out = bias (or 0); B*T == 0 or OC == 0 enqueue nothing.
  * Errors as mmbwd_q8_quantize.
  */
@@ -139,7 +139,7 @@ int mmbwd_q8_forward(void* out, const void* inp_q, const void* inp_scale, const 
  *                     contents (one rounding after the addition); a clear bit overwrites
  *
  * dbias is the column sum that mmbwd_q8_quantize forms while it quantises dout.
- * C times each output's element size is a multiple of 16 bytes. An empty sum
+ * C is a multiple of 4, OC and B*T any size. An empty sum
  * (OC == 0 for dinp, B*T == 0 for dweight) overwrites with zeros, or adds
  * nothing. Errors as mmbwd_q8_quantize; ERR_SHAPE also for unknown accumulate bits.
  */

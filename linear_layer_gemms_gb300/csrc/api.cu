@@ -993,7 +993,7 @@ int mmbwd_q8_forward(void* out, const void* inp_q, const void* inp_scale, const 
     const size_t b_out = static_cast<size_t>(s.n_dout) * s.es;
     if ((b_out && !out) || (s.n_dinp && (!inp_q || !inp_scale)) || (s.n_dw && (!weight_q || !weight_scale)))
         return MMBWD_ERR_NULL;
-    if (static_cast<size_t>(OC) * s.es % 16 != 0) return MMBWD_ERR_ALIGN;
+    if (OC % 4 != 0) return MMBWD_ERR_ALIGN;
     const Arg args[6] = {{out, b_out, true},
                          {inp_q, q8_data_size(s.BT, C), false},
                          {inp_scale, q8_scale_size(s.BT, C), false},
@@ -1063,8 +1063,7 @@ int mmbwd_q8_backward(void* dinp, void* dweight, const void* dout_q, const void*
     if (!dinp && !dweight && (b_dinp || b_dw)) return MMBWD_ERR_NULL;
     if (dinp && b_dinp && OC > 0 && (!dout_q || !dout_scale || !weight_qt || !weight_scale_t)) return MMBWD_ERR_NULL;
     if (dweight && b_dw && s.BT > 0 && (!dout_qt || !dout_scale_t || !inp_qt || !inp_scale_t)) return MMBWD_ERR_NULL;
-    if ((dinp && static_cast<size_t>(C) * s.es % 16 != 0) || (dweight && static_cast<size_t>(C) * sw.es % 16 != 0))
-        return MMBWD_ERR_ALIGN;
+    if (C % 4 != 0) return MMBWD_ERR_ALIGN;
     const size_t need = mmbwd_q8_backward_workspace_bytes(B, T, C, OC);
     if (need && !workspace) return MMBWD_ERR_NULL;
     if (need > workspace_bytes) return MMBWD_ERR_SHAPE;

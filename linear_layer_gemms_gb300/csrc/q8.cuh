@@ -74,30 +74,36 @@ __device__ __forceinline__ void mma_mxf8(uint32_t d, uint64_t a, uint64_t b, uin
 }
 
 // 32 contiguous bytes between registers and global memory. `left`: elements up to
-// the row's end (none is touched beyond it; a multiple of 16 bytes), `per16`: elements in 16
-// bytes, `wide`: the address is a multiple of 32 (else two accesses of 16).
+// the row's end (none is touched beyond it), `per16`: elements in 16 bytes, `wide`:
+// what every row's start is a multiple of, and with it the rows' length: 32 bytes
+// (2), 16 (1) or 8 (0).
 __device__ __forceinline__ void st256(void* p, const uint32_t* v) {
     asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]),
                  "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
                  : "memory");
 }
 __device__ __forceinline__ void st256(void* p, const uint32_t* v, int64_t left, int per16, int wide) {
-    if (wide) {
+    if (wide == 2) {
         if (left > 0) st256(p, v);
-    } else {
+    } else if (wide == 1) {
         uint4* q = static_cast<uint4*>(p);
         if (left > 0) q[0] = make_uint4(v[0], v[1], v[2], v[3]);
         if (left > per16) q[1] = make_uint4(v[4], v[5], v[6], v[7]);
+    } else {
+        uint2* q = static_cast<uint2*>(p);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (left > i * per16 / 2) q[i] = make_uint2(v[2 * i], v[2 * i + 1]);
     }
 }
 __device__ __forceinline__ void ld256(const void* p, uint32_t* v, int64_t left, int per16, int wide) {
-    if (wide) {
+    if (wide == 2) {
         if (left > 0)
             asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                          : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
                          : "l"(p)
                          : "memory");
-    } else {
+    } else if (wide == 1) {
         const uint4* q = static_cast<const uint4*>(p);
         if (left > 0) {
             const uint4 a = q[0];
@@ -107,6 +113,14 @@ __device__ __forceinline__ void ld256(const void* p, uint32_t* v, int64_t left, 
             const uint4 a = q[1];
             v[4] = a.x, v[5] = a.y, v[6] = a.z, v[7] = a.w;
         }
+    } else {
+        const uint2* q = static_cast<const uint2*>(p);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (left > i * per16 / 2) {
+                const uint2 a = q[i];
+                v[2 * i] = a.x, v[2 * i + 1] = a.y;
+            }
     }
 }
 

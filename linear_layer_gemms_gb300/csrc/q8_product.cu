@@ -97,7 +97,7 @@ struct Prod {
     int groups;  // of four blocks, per row of the scales
     int bn, tiles_m, tiles_n, kb, splits, kb_per_split, item0;
     int f32, add;
-    int wide;  // rows of D start on 32-byte boundaries
+    int wide;  // rows of D start on multiples of 32 bytes (2), 16 (1), 8 (0)
     uint32_t idesc;
 };
 
@@ -405,8 +405,10 @@ __global__ void __launch_bounds__(THREADS, 1)
                         const __nv_bfloat16* b = static_cast<const __nv_bfloat16*>(d.bias) + col0 + c;
 #pragma unroll
                         for (int g = 0; g < 4; ++g) {
-                            const uint4 f = col0 + c + 8 * g < d.N ? __ldg(reinterpret_cast<const uint4*>(b) + g) : make_uint4(0u, 0u, 0u, 0u);
-                            const uint32_t fw[4] = {f.x, f.y, f.z, f.w};
+                            const uint2 none = make_uint2(0u, 0u);
+                            const uint2 f0 = col0 + c + 8 * g < d.N ? __ldg(reinterpret_cast<const uint2*>(b) + 2 * g) : none;
+                            const uint2 f1 = col0 + c + 8 * g + 4 < d.N ? __ldg(reinterpret_cast<const uint2*>(b) + 2 * g + 1) : none;
+                            const uint32_t fw[4] = {f0.x, f0.y, f1.x, f1.y};
 #pragma unroll
                             for (int e = 0; e < 4; ++e)
                                 o[4 * g + e] = pack_bf16(__uint_as_float(v[8 * g + 2 * e]) + lo_bf16(fw[e]),
@@ -726,7 +728,8 @@ cudaError_t launch_pair(const Plan& pl, const Q8Product* prod, uint8_t* ws, cuda
         Prod& d = par.prod[i];
         d.a_scale = q.a_scale, d.b_scale = q.b_scale, d.bias = q.bias;
         d.D = q.D, d.partials = reinterpret_cast<float*>(ws + pp.ws_off);
-        d.wide = reinterpret_cast<uintptr_t>(q.D) % 32 == 0 && n * (f32 ? 4 : 2) % 32 == 0 ? 1 : 0;
+        const uint64_t at = reinterpret_cast<uintptr_t>(q.D) | n * (f32 ? 4 : 2);  // (N is a multiple of 4)
+        d.wide = at % 32 == 0 ? 2 : at % 16 == 0 ? 1 : 0;
         d.M = q.M, d.N = q.N;
         d.groups = static_cast<int>(q8_groups(q.K));
         d.bn = pp.bn, d.tiles_m = pp.tiles_m, d.tiles_n = pp.tiles_n, d.kb = pp.kb;

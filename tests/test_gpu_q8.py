@@ -193,7 +193,8 @@ def test_quantize_offsets_beyond_32_bits():
 # (tokens, C, OC): single tokens, short and odd prompts, ragged in every direction
 SHAPES = [(1, 8, 8), (1, 1600, 520), (2, 264, 136), (5, 24, 1000), (16, 768, 2304), (17, 1000, 264), (48, 640, 328),
           (64, 136, 4104), (100, 520, 392), (129, 128, 128), (130, 1160, 136), (255, 392, 776), (300, 2056, 264),
-          (777, 264, 1032), (100, 264, 10_008), (200, 392, 5000), (257, 1032, 24)]
+          (777, 264, 1032), (100, 264, 10_008), (200, 392, 5000), (257, 1032, 24), (300, 140, 1004),
+          (3, 77, 12), (400, 1001, 4)]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
@@ -227,7 +228,7 @@ def test_forward_few_tokens_every_split(monkeypatch, shape, splits):
     T, C, OC = shape
     iq, isc, iv = q8(normal((T, C), "bf16", 1), mm.E4M3)
     wq, wsc, wv = q8(normal((OC, C), "bf16", 2, 0.02), mm.E4M3)
-    for dtype in ("f32", "bf16") if OC % 8 == 0 else ("f32",):
+    for dtype in ("f32", "bf16"):
         bias = normal((OC,), dtype, 3)
         out = torch.full((T + 1, OC), 7.0, dtype=tdt(dtype), device="cuda")
         for _ in range(2):
@@ -254,7 +255,8 @@ def test_forward_few_tokens_many_tiles(T):
 
 
 BACKWARD = [(1, 8, 8), (3, 264, 136), (128, 128, 128), (200, 328, 520), (500, 136, 264), (300, 1032, 24),
-            (1000, 264, 392), (130, 520, 2304)]
+  (1000, 264, 392),
+            (130, 520, 2304), (300, 260, 131), (77, 1044, 25), (600, 4, 1001)]
 
 
 @pytest.mark.parametrize("types", [("bf16", "bf16"), ("bf16", "f32"), ("f32", "bf16")], ids="-".join)

@@ -72,7 +72,7 @@ def test_forward_refusals():
     assert forward(B=1 << 20, T=1 << 20) == mm.ERR_SHAPE
     assert forward(out=None) == mm.ERR_NULL
     assert forward(weight_scale=None) == mm.ERR_NULL
-    assert forward(OC=36) == mm.ERR_ALIGN
+    assert forward(OC=34) == mm.ERR_ALIGN
     assert forward(inp_scale=3 * A + 4) == mm.ERR_ALIGN
     assert forward(out=4 * A + 16) == mm.ERR_ALIAS
     assert forward(bias=A + 32) == mm.ERR_ALIAS
@@ -96,7 +96,7 @@ def test_backward_refusals():
     assert backward(dinp=None, dweight=None) == mm.ERR_NULL
     assert backward(weight_qt=None) == mm.ERR_NULL
     assert backward(inp_scale_t=None) == mm.ERR_NULL
-    assert backward(C=60) == mm.ERR_ALIGN
+    assert backward(C=62) == mm.ERR_ALIGN
     assert backward(dinp=A + 8) == mm.ERR_ALIGN
     assert backward(dweight=A + 64) == mm.ERR_ALIAS
     assert backward(dinp=9 * A) == mm.ERR_ALIAS
