@@ -116,14 +116,21 @@ def _ptr(x) -> int | None:
     return x.data_ptr()
 
 
+_raw_stream = _device = None  # torch's handle-only queries, once CUDA is initialised
+
+
 def _stream(stream) -> int:
+    global _raw_stream, _device
     if stream is not None:
         return int(stream)
-    import torch  # only for the current stream handle
+    if _raw_stream is None:
+        import torch  # only for the current stream handle
 
-    if torch.cuda.is_initialized():  # the handle alone: 0.1 us, building a Stream object 2.9 us
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
-    return torch.cuda.current_stream().cuda_stream
+        if not torch.cuda.is_initialized():
+            return torch.cuda.current_stream().cuda_stream
+        # the handle alone takes 0.1 us; building a Stream object takes 2.9
+        _device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+    return _raw_stream(_device())
 
 
 def mmbwd_run(dinp, dweight, dbias, dout, inp, weight, B: int, T: int, C: int, OC: int, dtype: int,

@@ -127,7 +127,7 @@ __device__ __forceinline__ void ld256(const void* p, uint32_t* v, int64_t left, 
 constexpr unsigned long long TIMEOUT_NS = 2000000000ull;  // 2 s per wait
 
 // Where a wait gave up (device status word of the 8-bit products).
-enum Site : int { SITE_EMPTY = 1, SITE_ACC_FREE = 2, SITE_FULL = 3, SITE_ACC_FULL = 4, SITE_TEARDOWN = 8, SITE_FORWARD = 10, SITE_DONE = 12 };
+enum Site : int { SITE_EMPTY = 1, SITE_ACC_FREE = 2, SITE_FULL = 3, SITE_ACC_FULL = 4, SITE_TEARDOWN = 8, SITE_FORWARD = 10 };
 
 // Bounded mbarrier wait: false after TIMEOUT_NS (recorded in `status`) or once
 // another warp of the CTA has given up; a teardown wait ignores the latter.

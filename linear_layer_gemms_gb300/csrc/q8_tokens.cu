@@ -50,7 +50,7 @@ struct Cfg {
     static constexpr int OFF_PART = STAGES * STAGE;  // partial sums [rank][owned token][128], fp32
     static constexpr int OFF_SF = OFF_PART + NT * ROWS * 4;  // per stage: 512 bytes of the weight's scales, 512 of the tokens'
     static constexpr int OFF_BARS = OFF_SF + STAGES * 1024;
-    static constexpr int N_BARS = 2 * STAGES + 4;
+    static constexpr int N_BARS = 2 * STAGES + 5;
     static constexpr int OFF_MISC = OFF_BARS + N_BARS * 8;
     static constexpr int SMEM = OFF_MISC + 16 + 1024;
     static constexpr int SF_BUFS = 4;  // scale buffers in tensor memory (8 columns each)
@@ -82,6 +82,7 @@ __global__ void __launch_bounds__(THREADS, 2)
     volatile uint32_t* misc = reinterpret_cast<volatile uint32_t*>(smem_raw + (base - raw) + L::OFF_MISC);
     const uint32_t full = base + L::OFF_BARS, empty = full + 8u * L::STAGES;
     const uint32_t acc_full = empty + 8u * L::STAGES, acc_free = acc_full + 16u;  // two of each
+    const uint32_t teardown = acc_free + 16u;
     const int warp = static_cast<int>(threadIdx.x >> 5), lane = static_cast<int>(threadIdx.x & 31);
     // splits > 1: one tile per cluster; else the CTA's tiles are first, first + step, ...
     const int rank = static_cast<int>(blockIdx.x) % p.splits, first = static_cast<int>(blockIdx.x) / p.splits;
@@ -100,6 +101,7 @@ __global__ void __launch_bounds__(THREADS, 2)
             ptx::mbar_init(acc_full + 8u * i, 1u);
             ptx::mbar_init(acc_free + 8u * i, 4u);
         }
+        ptx::mbar_init(teardown, 1u);
         misc[1] = 0u;
         ptx::fence_mbar_init();
     }
@@ -187,13 +189,9 @@ __global__ void __launch_bounds__(THREADS, 2)
                 if (!ok) break;
                 ptx::mma_commit(acc_full + 8u * acc);
             }
-            // (every MMA has completed when the last accumulator is full, which
-            // the epilogue waits for; after a wait that gave up, the last commit
-            // to `empty` is waited for by no one, so commit and wait here)
-            if (!ok) {
-                ptx::mma_commit(acc_full);
-                wt.wait(acc_full, 0u, q8::SITE_TEARDOWN, -1, true);
-            }
+            // every MMA has completed before shared and tensor memory go
+            ptx::mma_commit(teardown);
+            wt.wait(teardown, 0u, q8::SITE_TEARDOWN, -1, true);
         }
         __syncwarp();
     } else {
