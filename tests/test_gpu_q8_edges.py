@@ -189,3 +189,44 @@ def test_few_tokens_in_a_graph():
     torch.cuda.synchronize()
     want, tol = ref.product_bound(ref.quantize(y, mm.E4M3)[2], w8[2], "bf16")
     assert np.all(np.abs(host(out) - want) <= tol)
+
+
+def test_gradients_against_differences():
+    """L = sum of dout * out is linear in each coordinate of inp and weight, so
+    L(x + e_k) - L(x) is the gradient exactly. Whole numbers up to 8 are exact in
+    either format and direction, and every sum is exact in fp32."""
+    import torch
+
+    T, C, OC = 70, 136, 72
+    g = np.random.default_rng(5)
+    inp, w, d = (g.integers(-4, 5, s).astype(float) for s in ((T, C), (OC, C), (T, OC)))
+
+    def forms(x):
+        R, K = x.shape
+        a, b = room(R, K), room(K, R)
+        assert mm.mmbwd_q8_quantize(*a, *b, None, dev(x, "f32"), None, 0, R, K, mm.F32, mm.E4M3) == mm.OK
+        return a, b
+
+    def loss(x, v):
+        out = torch.empty(T, OC, device="cuda")
+        assert mm.mmbwd_q8_forward(out, *forms(x)[0], *forms(v)[0], None, 1, T, C, OC, 0, 0, mm.F32) == mm.OK
+        return float((host(out) * d).sum())
+
+    dinp, dw, db = torch.empty(T, C, device="cuda"), torch.empty(OC, C, device="cuda"), torch.empty(OC, device="cuda")
+    a, b = room(T, OC), room(OC, T)
+    assert mm.mmbwd_q8_quantize(*a, *b, db, dev(d, "f32"), None, 0, T, OC, mm.F32, mm.E4M3) == mm.OK
+    n = mm.mmbwd_q8_backward_workspace_bytes(1, T, C, OC)
+    ws = torch.empty(max(n, 1), dtype=torch.uint8, device="cuda")
+    assert mm.mmbwd_q8_backward(dinp, dw, *a, *b, *forms(inp)[1], *forms(w)[1], ws, n, 1, T, C, OC, 0, 0, 0, mm.F32,
+                                mm.F32, 0) == mm.OK
+    torch.cuda.synchronize()
+    at = loss(inp, w)
+    for r, c in ((0, 0), (69, 135), (3, 127), (40, 128), (17, 64)):
+        x = inp.copy()
+        x[r, c] += 1
+        assert loss(x, w) - at == host(dinp)[r, c]
+    for r, c in ((0, 0), (71, 135), (5, 127), (64, 128), (31, 9)):
+        v = w.copy()
+        v[r, c] += 1
+        assert loss(inp, v) - at == host(dw)[r, c]
+    np.testing.assert_array_equal(host(db), d.sum(0))  # L is affine in a bias with slope sum of dout
