@@ -26,6 +26,11 @@ struct Vec;
 template <>
 struct Vec<float> {
     static constexpr int N = 4;
+    // value e of a vector, plus c
+    __device__ static float plus(const uint4& v, int e, float c) {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        return __uint_as_float(w[e]) + c;
+    }
     __device__ static void get(const uint4& v, float (&f)[4]) {
         f[0] = __uint_as_float(v.x), f[1] = __uint_as_float(v.y), f[2] = __uint_as_float(v.z), f[3] = __uint_as_float(v.w);
     }
@@ -36,6 +41,15 @@ struct Vec<float> {
 template <>
 struct Vec<__nv_bfloat16> {
     static constexpr int N = 8;
+    __device__ static float plus(const uint4& v, int e, float c) {  // one instruction, without unpacking
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        float r;
+        if (e & 1)
+            asm("{.reg .b16 a, b;\n\tmov.b32 {a, b}, %1;\n\tadd.rn.f32.bf16 %0, b, %2;}" : "=f"(r) : "r"(w[e >> 1]), "f"(c));
+        else
+            asm("{.reg .b16 a, b;\n\tmov.b32 {a, b}, %1;\n\tadd.rn.f32.bf16 %0, a, %2;}" : "=f"(r) : "r"(w[e >> 1]), "f"(c));
+        return r;
+    }
     __device__ static void get(const uint4& v, float (&f)[8]) {
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -100,27 +114,26 @@ __global__ void __launch_bounds__(32 * P * TEAMS_PER_BLOCK<P>)
     const int64_t stride = static_cast<int64_t>(gridDim.x) * TEAMS;
     ptx::grid_launch_dependents();
     ptx::grid_dependency_wait();
-    uint4 raw[VPT];
-    auto fetch = [&](int64_t r) {
+    // A row's vectors as they are stored: 16 bytes of registers each, so that the
+    // next row fits beside it; the differences from the mean are formed twice.
+    uint4 x[VPT], next[VPT];
+    auto fetch = [&](uint4 (&to)[VPT], int64_t r) {
         const uint4* xr = reinterpret_cast<const uint4*>(inp + r * C);
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
             const int v = t + 32 * P * j;
-            raw[j] = j + 1 < VPT || v < nvec ? xr[v] : make_uint4(0u, 0u, 0u, 0u);  // only the last vector may be missing
+            to[j] = j + 1 < VPT || v < nvec ? xr[v] : make_uint4(0u, 0u, 0u, 0u);  // only the last vector may be missing
         }
     };
     int64_t r = static_cast<int64_t>(blockIdx.x) * TEAMS + team;
-    if (r < rows) fetch(r);
+    if (r < rows) fetch(x, r);
     for (; r < rows; r += stride) {
-        float x[VPT][N];
+        if (AHEAD && r + stride < rows) fetch(next, r + stride);
         float s = 0.f;
 #pragma unroll
-        for (int j = 0; j < VPT; ++j) {
-            V::get(raw[j], x[j]);
+        for (int j = 0; j < VPT; ++j)
 #pragma unroll
-            for (int e = 0; e < N; ++e) s += x[j][e];
-        }
-        if (AHEAD && r + stride < rows) fetch(r + stride);
+            for (int e = 0; e < N; ++e) s = V::plus(x[j], e, s);
         const float mean = team_sum<P>(s, slots[team], 0, wt, team) * inv_c;
         s = 0.f;
 #pragma unroll
@@ -128,8 +141,8 @@ __global__ void __launch_bounds__(32 * P * TEAMS_PER_BLOCK<P>)
             const bool on = j + 1 < VPT || t + 32 * P * j < nvec;
 #pragma unroll
             for (int e = 0; e < N; ++e) {
-                x[j][e] = on ? x[j][e] - mean : 0.f;
-                s += x[j][e] * x[j][e];
+                const float d = on ? V::plus(x[j], e, -mean) : 0.f;
+                s += d * d;
             }
         }
         const float var = team_sum<P>(s, slots[team], 1, wt, team) * inv_c;
@@ -139,13 +152,14 @@ __global__ void __launch_bounds__(32 * P * TEAMS_PER_BLOCK<P>)
         for (int j = 0; j < VPT; ++j) {
             const int v = t + 32 * P * j;
             if (j + 1 < VPT || v < nvec) {
-                float w[N], b[N];
+                float y[N], w[N], b[N];
                 V::get(__ldg(reinterpret_cast<const uint4*>(weight) + v), w);
                 V::get(bias ? __ldg(reinterpret_cast<const uint4*>(bias) + v) : make_uint4(0u, 0u, 0u, 0u), b);
 #pragma unroll
-                for (int e = 0; e < N; ++e) x[j][e] = x[j][e] * rstd * w[e] + b[e];
-                __stcs(dst + v, V::put(x[j]));
+                for (int e = 0; e < N; ++e) y[e] = V::plus(x[j], e, -mean) * rstd * w[e] + b[e];
+                __stcs(dst + v, V::put(y));
             }
+            if (AHEAD) x[j] = next[j];
         }
         if (t == 0) {
             if (mean_out) mean_out[r] = mean;
@@ -228,7 +242,7 @@ Choice<T> pick(int need) {
 // barrier), then teams that fill most of their lanes. The next row is fetched ahead
 // where its registers fit beside the current row's. Measured (us), AHEAD / not:
 // 8192 x 1600 bf16 (one warp) 10.5 / 11.4; 4000 x 2400 bf16 (4 warps, 3 vectors) 8.4 /
-// 9.5, with 8 warps 12.5; 2000 x 6400 bf16 (4 warps, 7) 10.6 / 12.8, fp32 8192 x 3200
+// 9.5, with 8 warps 12.5; with two warps a row 8192 x 1600 takes 11.3; 2000 x 6400 bf16 (4 warps, 7) 10.6 / 12.8, fp32 8192 x 3200
 // 34.9 / 32.4; 4096 x 8192 fp32 (8 warps, 8) 46.7 / 41.4.
 template <typename T>
 Choice<T> choose(int nvec) {
