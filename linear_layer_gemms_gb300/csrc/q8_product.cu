@@ -25,7 +25,7 @@
 // Warp roles (10 warps per CTA): 0 TMA producer; 1 MMA issuer (even CTA) or
 // forwarder of "stage full" to the even CTA (odd CTA); 2-9 epilogue, two warps per
 // tensor-memory lane quadrant, each taking every other 32-column chunk of its 32
-// rows: accumulator (+ bias, + old values, requested a chunk ahead) rounded once
+// rows: accumulator (+ bias, + old values, requested two chunks ahead) rounded once
 // and stored from registers, 32 bytes of a row per thread and store.
 //
 // Work list: the tiles of one or two products (dinp and dweight), each product's
@@ -344,17 +344,18 @@ __global__ void __launch_bounds__(THREADS, 1)
                 }
             } else if (d.f32) {
                 float* D = static_cast<float*>(d.D) + row * d.N + col0;
-                uint32_t old[32];
+                uint32_t old[2][32];
                 auto fetch = [&](int k) {
                     const int c = chunk(k) * 32;
 #pragma unroll
-                    for (int g = 0; g < 4; ++g) q8::ld256(D + c + 8 * g, old + 8 * g, in_row ? d.N - col0 - c - 8 * g : 0, 4, d.wide);
+                    for (int g = 0; g < 4; ++g) q8::ld256(D + c + 8 * g, old[k & 1] + 8 * g, in_row ? d.N - col0 - c - 8 * g : 0, 4, d.wide);
                 };
-                if (d.add) fetch(0);
+                if (d.add) fetch(0), fetch(1);
                 if (!wt.wait_warp(bars + 8u * BAR_ACC_FULL, tile & 1u, q8::SITE_ACC_FULL, w)) break;
                 ptx::tc_fence_after();
-#pragma unroll 1
-                for (int k = 0; k < nk; ++k) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    if (k >= nk) break;
                     uint32_t v[32];
                     const int c = chunk(k) * 32;
                     ptx::tmem_ld32(acc + c, v);
@@ -373,25 +374,26 @@ __global__ void __launch_bounds__(THREADS, 1)
                     }
                     if (d.add) {
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) + __uint_as_float(old[e]));
-                        if (k + 1 < nk) fetch(k + 1);
+                        for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) + __uint_as_float(old[k & 1][e]));
+                        if (k + 2 < nk) fetch(k + 2);
                     }
 #pragma unroll
                     for (int g = 0; g < 4; ++g) q8::st256(D + c + 8 * g, v + 8 * g, in_row ? d.N - col0 - c - 8 * g : 0, 4, d.wide);
                 }
             } else {
                 __nv_bfloat16* D = static_cast<__nv_bfloat16*>(d.D) + row * d.N + col0;
-                uint32_t old[16];
+                uint32_t old[2][16];
                 auto fetch = [&](int k) {
                     const int c = chunk(k) * 32;
 #pragma unroll
-                    for (int g = 0; g < 2; ++g) q8::ld256(D + c + 16 * g, old + 8 * g, in_row ? d.N - col0 - c - 16 * g : 0, 8, d.wide);
+                    for (int g = 0; g < 2; ++g) q8::ld256(D + c + 16 * g, old[k & 1] + 8 * g, in_row ? d.N - col0 - c - 16 * g : 0, 8, d.wide);
                 };
-                if (d.add) fetch(0);
+                if (d.add) fetch(0), fetch(1);
                 if (!wt.wait_warp(bars + 8u * BAR_ACC_FULL, tile & 1u, q8::SITE_ACC_FULL, w)) break;
                 ptx::tc_fence_after();
-#pragma unroll 1
-                for (int k = 0; k < nk; ++k) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    if (k >= nk) break;
                     uint32_t v[32], o[16];
                     const int c = chunk(k) * 32;
                     ptx::tmem_ld32(acc + c, v);
@@ -399,8 +401,9 @@ __global__ void __launch_bounds__(THREADS, 1)
                     if (d.add) {
 #pragma unroll
                         for (int e = 0; e < 16; ++e)
-                            o[e] = pack_bf16(__uint_as_float(v[2 * e]) + lo_bf16(old[e]), __uint_as_float(v[2 * e + 1]) + hi_bf16(old[e]));
-                        if (k + 1 < nk) fetch(k + 1);
+                            o[e] = pack_bf16(__uint_as_float(v[2 * e]) + lo_bf16(old[k & 1][e]),
+                                             __uint_as_float(v[2 * e + 1]) + hi_bf16(old[k & 1][e]));
+                        if (k + 2 < nk) fetch(k + 2);
                     } else if (d.bias) {
                         const __nv_bfloat16* b = static_cast<const __nv_bfloat16*>(d.bias) + col0 + c;
 #pragma unroll
@@ -474,6 +477,7 @@ __global__ void __launch_bounds__(256) q8_join_kernel(T* D, const float* __restr
 
 struct ProductPlan {
     int bn, tiles_m, tiles_n, kb, splits, kb_per_split, item0, items;
+    double epi;  // us of a 256-column epilogue
     size_t ws_off, ws_bytes;
 };
 
@@ -491,7 +495,16 @@ int ceil_div(int64_t a, int64_t b) { return static_cast<int>((a + b - 1) / b); }
 // product the pass that joins its partials.
 double kb_us(int bn) { return bn == 256 ? 0.30 : 0.22; }
 constexpr double ITEM_US = 0.6;
-double epi_us(const ProductPlan& p) { return (p.splits > 1 ? 3.0 : 2.0) * p.bn / 256.0; }
+double epi_us(const ProductPlan& p) { return (p.splits > 1 ? 3.0 : p.epi) * p.bn / 256.0; }
+
+// A 256-column epilogue: plain stores are not waited for, adding to the old values is
+// (a dweight of 9728 x 2048 from 8 tokens, four rounds of tiles: fp32 22.1 us, added to
+// 38.4; bf16 14.4 and 20.1). Widths and splits are searched with the first cost, so
+// that the workspace depends on the shapes alone; items are then assigned to pairs
+// by their own (512 tokens, C = 1600, OC = 6400, fp32 dweight added to: 34.2 -> 27.5 us;
+// with dearer plain stores too, 2200 x 8680 without adding got slower, 28.7 -> 31.6).
+constexpr double EPI_SEARCH = 2.0;
+double epi_of(bool f32, bool add) { return !add ? EPI_SEARCH : f32 ? 8.5 : 4.0; }
 
 double item_us(const ProductPlan& p, int split) {
     const int k0 = split * p.kb_per_split, k1 = std::min(k0 + p.kb_per_split, p.kb);
@@ -538,6 +551,7 @@ double assign(Plan& pl, int pairs) {
 
 struct Shape3 {
     int64_t M, N, K;
+    int f32, add;  // what its epilogue stores
 };
 
 // Overrides for tuning and tests: MMBWD_Q8_TILE_N and MMBWD_Q8_SPLITS = "<first
@@ -601,6 +615,7 @@ void make_plan(const Shape3* s, int n, bool may_split, const Forced& force, int 
                 for (int i = 0; i < n; ++i) {
                     ProductPlan& p = c.p[i];
                     p.bn = (widths >> i) & 1 ? 128 : 256;
+                    p.epi = EPI_SEARCH;
                     p.tiles_m = ceil_div(s[i].M, PAIR_M);
                     p.tiles_n = ceil_div(s[i].N, p.bn);
                     p.kb = ceil_div(s[i].K, 128);
@@ -661,7 +676,9 @@ int g_plan_count = 0, g_plan_next = 0;
 bool same_key(const Key& a, const Key& b) {
     if (a.n != b.n || a.split != b.split || a.sms != b.sms || !(a.force == b.force)) return false;
     for (int i = 0; i < a.n; ++i)
-        if (a.s[i].M != b.s[i].M || a.s[i].N != b.s[i].N || a.s[i].K != b.s[i].K) return false;
+        if (a.s[i].M != b.s[i].M || a.s[i].N != b.s[i].N || a.s[i].K != b.s[i].K || a.s[i].f32 != b.s[i].f32 ||
+            a.s[i].add != b.s[i].add)
+            return false;
     return true;
 }
 
@@ -680,8 +697,11 @@ const Plan& plan_for(const Shape3* s, int n, bool may_split, int num_sms) {
     if (g_plan_count < CACHE) ++g_plan_count;
     g_keys[slot] = k;
     make_plan(s, n, may_split, k.force, num_sms, &g_plans[slot]);
-    if (g_plans[slot].n_items == 0) make_plan(s, n, may_split, Forced{}, num_sms, &g_plans[slot]);
-    return g_plans[slot];
+    Plan& pl = g_plans[slot];
+    if (pl.n_items == 0) make_plan(s, n, may_split, Forced{}, num_sms, &pl);
+    for (int i = 0; i < pl.n; ++i) pl.p[i].epi = epi_of(s[i].f32 != 0, s[i].add != 0);
+    if (pl.n_items > 0 && pl.table) assign(pl, pl.grid / 2);
+    return pl;
 }
 
 // ------------------------------------------------------------------ launch
@@ -776,7 +796,7 @@ cudaError_t launch_pair(const Plan& pl, const Q8Product* prod, uint8_t* ws, cuda
 
 size_t q8_products_workspace(const Q8Product* products, int n, int num_sms) {
     Shape3 s[2];
-    for (int i = 0; i < n; ++i) s[i] = {products[i].M, products[i].N, products[i].K};
+    for (int i = 0; i < n; ++i) s[i] = {products[i].M, products[i].N, products[i].K, products[i].dtype == MMBWD_F32 ? 1 : 0, products[i].add};
     std::lock_guard<std::mutex> g(g_plan_mutex);
     return plan_for(s, n, true, num_sms).ws_bytes;
 }
@@ -785,7 +805,7 @@ cudaError_t q8_products_launch(const Q8Product* products, int n, bool may_split,
                                cudaStream_t stream) {
     if (take_injected_launch_failure()) return cudaErrorLaunchFailure;
     Shape3 s[2];
-    for (int i = 0; i < n; ++i) s[i] = {products[i].M, products[i].N, products[i].K};
+    for (int i = 0; i < n; ++i) s[i] = {products[i].M, products[i].N, products[i].K, products[i].dtype == MMBWD_F32 ? 1 : 0, products[i].add};
     std::lock_guard<std::mutex> g(g_plan_mutex);
     const Plan& pl = plan_for(s, n, may_split, num_sms);
     if (pl.n_items == 0 || pl.ws_bytes > ws_bytes) return cudaErrorInvalidValue;
