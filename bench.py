@@ -551,14 +551,19 @@ def time_back_to_back(torch, stream, calls, per_batch, batches=5):
     per_batch, CUDA events on `stream`; the calls cycle through `calls` (one
     per resident input set) so that consecutive calls touch different memory.
     Each batch is queued behind a device spin (`hold_stream`), lengthened and
-    the batch taken again if the spin ended before the batch was queued."""
+    the batch taken again if the spin ended before the batch was queued. The
+    first calls are not part of the host time that sets the spin: loading a
+    library can take them seconds, and the spin would take minutes."""
     with torch.cuda.stream(stream):
-        t0 = time.perf_counter()
-        for c in calls * 2:
+        for c in calls:
             c()
-        host_us = (time.perf_counter() - t0) * 1e6 / (2 * len(calls))
+        torch.cuda.synchronize()
+        t0 = time.perf_counter()
+        for c in calls:
+            c()
+        host_us = (time.perf_counter() - t0) * 1e6 / len(calls)
     torch.cuda.synchronize()
-    hold_us = 50.0 + 2.0 * host_us * per_batch
+    hold_us = min(2e5, 50.0 + 2.0 * host_us * per_batch)
     times = []
     for _ in range(batches):
         while True:
