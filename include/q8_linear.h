@@ -48,7 +48,13 @@
  * MMBWD_ERR_* code with nothing enqueued. The library keeps no state between
  * calls: what a call needs beyond its tensors is a workspace of the caller's,
  * so calls with their own workspaces may overlap on different streams or in
- * different captured graphs.
+ * different captured graphs, from one thread or several.
+ *
+ * For tuning and tests the environment overrides the work split:
+ * MMBWD_Q8_SPLITS = "<dinp>,<dweight>" (pieces of each product's reduction, 0: the
+ * planner's choice) and MMBWD_Q8_TILE_N = "<dinp>,<dweight>" (tile widths, 128 or
+ * 256) of the backward, MMBWD_Q8_TOKEN_SPLITS (1, 2, 4 or 8 CTAs to a tile) of the
+ * forward for few tokens. The workspace size follows the first two.
  */
 #ifndef Q8_LINEAR_H
 #define Q8_LINEAR_H

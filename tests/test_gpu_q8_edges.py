@@ -230,3 +230,37 @@ def test_gradients_against_differences():
         v[r, c] += 1
         assert loss(inp, v) - at == host(dw)[r, c]
     np.testing.assert_array_equal(host(db), d.sum(0))  # L is affine in a bias with slope sum of dout
+
+
+def test_calls_from_several_threads_at_once():
+    """Threads with a stream and buffers each, calling at the same time: every
+    result is the one a single call gives."""
+    import threading
+
+    import torch
+
+    from test_gpu_q8 import _Buffers, _layer
+
+    T, C, OC = 600, 520, 392
+    g = torch.Generator(device="cuda")
+    g.manual_seed(3)
+    made = []
+    for _ in range(3):
+        x = [torch.randn(s, generator=g, device="cuda").bfloat16() for s in ((T, C), (OC, C), (T, OC))]
+        made.append((x, _Buffers(T, C, OC), torch.cuda.Stream(), [t.clone() for t in _layer(*x)]))
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work(x, b, stream, want):
+        with torch.cuda.stream(stream):
+            for _ in range(20):
+                got = _layer(*x, b)
+                stream.synchronize()
+                wrong.extend(i for i, (p, q) in enumerate(zip(got, want)) if not torch.equal(p, q))
+
+    threads = [threading.Thread(target=work, args=m) for m in made]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
