@@ -41,7 +41,10 @@
  * Element types: MMBWD_F32 / MMBWD_BF16 codes of mmbwd.h for the unquantised
  * tensors. Products of 8-bit values are exact; sums are formed in fp32 on the
  * tensor cores, each block's products times both blocks' scales; each output
- * element is rounded once. Repeated calls give bitwise identical results (no
+ * element is rounded once. The tensor core cuts each accumulation of 32 products
+ * toward zero: sums whose terms all have one sign come out low by a share that
+ * grows with their length (measured 1e-7 at 1024 terms, 3e-6 at 8192, 4e-5 at
+ * 51200); where signs mix it stays near 1e-7. Repeated calls give bitwise identical results (no
  * float atomics; every sum in an order fixed by shape and device).
  *
  * Every call enqueues on `stream` and returns MMBWD_OK or a negative
