@@ -25,7 +25,7 @@
 // Warp roles (10 warps per CTA): 0 TMA producer; 1 MMA issuer (even CTA) or
 // forwarder of "stage full" to the even CTA (odd CTA); 2-9 epilogue, two warps per
 // tensor-memory lane quadrant, each taking every other 32-column chunk of its 32
-// rows: accumulator (+ bias, + old values, requested two chunks ahead) rounded once
+// rows: accumulator (+ bias or old values, requested two chunks ahead) rounded once
 // and stored from registers, 32 bytes of a row per thread and store.
 //
 // Work list: the tiles of one or two products (dinp and dweight), each product's
@@ -105,6 +105,7 @@ struct Prod {
     int bn, tiles_m, tiles_n, kb, splits, kb_per_split, item0;
     int f32, add;
     int wide;  // rows of D start on multiples of 32 bytes (2), 16 (1), 8 (0)
+    int bias_wide;  // the same of the bias and its length
     uint32_t idesc;
 };
 
@@ -351,85 +352,91 @@ __global__ void __launch_bounds__(THREADS, 1)
                 }
             } else if (d.f32) {
                 float* D = static_cast<float*>(d.D) + row * d.N + col0;
-                uint32_t old[2][32];
-                auto fetch = [&](int k) {
-                    const int c = chunk(k) * 32;
+                auto store = [&](int c, const uint32_t (&v)[32]) {
 #pragma unroll
-                    for (int g = 0; g < 4; ++g) q8::ld256(D + c + 8 * g, old[k & 1] + 8 * g, in_row ? d.N - col0 - c - 8 * g : 0, 4, d.wide);
+                    for (int g = 0; g < 4; ++g) q8::st256(D + c + 8 * g, v + 8 * g, in_row ? d.N - col0 - c - 8 * g : 0, 4, d.wide);
                 };
-                if (d.add) fetch(0), fetch(1);
-                if (!wt.wait_warp(bars + 8u * BAR_ACC_FULL, tile & 1u, q8::SITE_ACC_FULL, w)) break;
-                ptx::tc_fence_after();
+                if (d.add || d.bias) {  // the old values, or the bias, two chunks ahead
+                    const float* src = d.add ? D : static_cast<const float*>(d.bias) + col0;
+                    const int wide = d.add ? d.wide : d.bias_wide;
+                    uint32_t old[2][32];
+                    auto fetch = [&](int k) {
+                        const int c = chunk(k) * 32;
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    if (k >= nk) break;
-                    uint32_t v[32];
-                    const int c = chunk(k) * 32;
-                    ptx::tmem_ld32(acc + c, v);
-                    release(k);
-                    if (d.bias) {
-                        const float* b = static_cast<const float*>(d.bias) + col0 + c;
+                        for (int g = 0; g < 4; ++g) q8::ld256(src + c + 8 * g, old[k & 1] + 8 * g, in_row ? d.N - col0 - c - 8 * g : 0, 4, wide);
+                    };
+                    fetch(0), fetch(1);
+                    if (!wt.wait_warp(bars + 8u * BAR_ACC_FULL, tile & 1u, q8::SITE_ACC_FULL, w)) break;
+                    ptx::tc_fence_after();
 #pragma unroll
-                        for (int g = 0; g < 8; ++g)
-                            if (col0 + c + 4 * g < d.N) {
-                                const float4 f = __ldg(reinterpret_cast<const float4*>(b) + g);
-                                v[4 * g] = __float_as_uint(__uint_as_float(v[4 * g]) + f.x);
-                                v[4 * g + 1] = __float_as_uint(__uint_as_float(v[4 * g + 1]) + f.y);
-                                v[4 * g + 2] = __float_as_uint(__uint_as_float(v[4 * g + 2]) + f.z);
-                                v[4 * g + 3] = __float_as_uint(__uint_as_float(v[4 * g + 3]) + f.w);
-                            }
-                    }
-                    if (d.add) {
+                    for (int k = 0; k < 4; ++k) {
+                        if (k >= nk) break;
+                        uint32_t v[32];
+                        const int c = chunk(k) * 32;
+                        ptx::tmem_ld32(acc + c, v);
+                        release(k);
 #pragma unroll
                         for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) + __uint_as_float(old[k & 1][e]));
                         if (k + 2 < nk) fetch(k + 2);
+                        store(c, v);
                     }
-#pragma unroll
-                    for (int g = 0; g < 4; ++g) q8::st256(D + c + 8 * g, v + 8 * g, in_row ? d.N - col0 - c - 8 * g : 0, 4, d.wide);
+                } else {
+                    if (!wt.wait_warp(bars + 8u * BAR_ACC_FULL, tile & 1u, q8::SITE_ACC_FULL, w)) break;
+                    ptx::tc_fence_after();
+#pragma unroll 1
+                    for (int k = 0; k < nk; ++k) {
+                        uint32_t v[32];
+                        const int c = chunk(k) * 32;
+                        ptx::tmem_ld32(acc + c, v);
+                        release(k);
+                        store(c, v);
+                    }
                 }
             } else {
                 __nv_bfloat16* D = static_cast<__nv_bfloat16*>(d.D) + row * d.N + col0;
-                uint32_t old[2][16];
-                auto fetch = [&](int k) {
-                    const int c = chunk(k) * 32;
+                auto store = [&](int c, const uint32_t (&o)[16]) {
 #pragma unroll
-                    for (int g = 0; g < 2; ++g) q8::ld256(D + c + 16 * g, old[k & 1] + 8 * g, in_row ? d.N - col0 - c - 16 * g : 0, 8, d.wide);
+                    for (int g = 0; g < 2; ++g) q8::st256(D + c + 16 * g, o + 8 * g, in_row ? d.N - col0 - c - 16 * g : 0, 8, d.wide);
                 };
-                if (d.add) fetch(0), fetch(1);
-                if (!wt.wait_warp(bars + 8u * BAR_ACC_FULL, tile & 1u, q8::SITE_ACC_FULL, w)) break;
-                ptx::tc_fence_after();
+                if (d.add || d.bias) {
+                    const __nv_bfloat16* src = d.add ? D : static_cast<const __nv_bfloat16*>(d.bias) + col0;
+                    const int wide = d.add ? d.wide : d.bias_wide;
+                    uint32_t old[2][16];
+                    auto fetch = [&](int k) {
+                        const int c = chunk(k) * 32;
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    if (k >= nk) break;
-                    uint32_t v[32], o[16];
-                    const int c = chunk(k) * 32;
-                    ptx::tmem_ld32(acc + c, v);
-                    release(k);
-                    if (d.add) {
+                        for (int g = 0; g < 2; ++g) q8::ld256(src + c + 16 * g, old[k & 1] + 8 * g, in_row ? d.N - col0 - c - 16 * g : 0, 8, wide);
+                    };
+                    fetch(0), fetch(1);
+                    if (!wt.wait_warp(bars + 8u * BAR_ACC_FULL, tile & 1u, q8::SITE_ACC_FULL, w)) break;
+                    ptx::tc_fence_after();
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        if (k >= nk) break;
+                        uint32_t v[32], o[16];
+                        const int c = chunk(k) * 32;
+                        ptx::tmem_ld32(acc + c, v);
+                        release(k);
 #pragma unroll
                         for (int e = 0; e < 16; ++e)
                             o[e] = pack_bf16(__uint_as_float(v[2 * e]) + lo_bf16(old[k & 1][e]),
                                              __uint_as_float(v[2 * e + 1]) + hi_bf16(old[k & 1][e]));
                         if (k + 2 < nk) fetch(k + 2);
-                    } else if (d.bias) {
-                        const __nv_bfloat16* b = static_cast<const __nv_bfloat16*>(d.bias) + col0 + c;
-#pragma unroll
-                        for (int g = 0; g < 4; ++g) {
-                            const uint2 none = make_uint2(0u, 0u);
-                            const uint2 f0 = col0 + c + 8 * g < d.N ? __ldg(reinterpret_cast<const uint2*>(b) + 2 * g) : none;
-                            const uint2 f1 = col0 + c + 8 * g + 4 < d.N ? __ldg(reinterpret_cast<const uint2*>(b) + 2 * g + 1) : none;
-                            const uint32_t fw[4] = {f0.x, f0.y, f1.x, f1.y};
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                o[4 * g + e] = pack_bf16(__uint_as_float(v[8 * g + 2 * e]) + lo_bf16(fw[e]),
-                                                         __uint_as_float(v[8 * g + 2 * e + 1]) + hi_bf16(fw[e]));
-                        }
-                    } else {
+                        store(c, o);
+                    }
+                } else {
+                    if (!wt.wait_warp(bars + 8u * BAR_ACC_FULL, tile & 1u, q8::SITE_ACC_FULL, w)) break;
+                    ptx::tc_fence_after();
+#pragma unroll 1
+                    for (int k = 0; k < nk; ++k) {
+                        uint32_t v[32], o[16];
+                        const int c = chunk(k) * 32;
+                        ptx::tmem_ld32(acc + c, v);
+                        release(k);
 #pragma unroll
                         for (int e = 0; e < 16; ++e) o[e] = pack_bf16(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1]));
+                        store(c, o);
                     }
-#pragma unroll
-                    for (int g = 0; g < 2; ++g) q8::st256(D + c + 16 * g, o + 8 * g, in_row ? d.N - col0 - c - 16 * g : 0, 8, d.wide);
                 }
             }
         }
@@ -757,6 +764,8 @@ cudaError_t launch_pair(const Plan& pl, const Q8Product* prod, uint8_t* ws, cuda
         d.D = q.D, d.partials = reinterpret_cast<float*>(ws + pp.ws_off);
         const uint64_t at = reinterpret_cast<uintptr_t>(q.D) | n * (f32 ? 4 : 2);  // (N is a multiple of 4)
         d.wide = at % 32 == 0 ? 2 : at % 16 == 0 ? 1 : 0;
+        const uint64_t bias_at = reinterpret_cast<uintptr_t>(q.bias) | n * (f32 ? 4 : 2);
+        d.bias_wide = bias_at % 32 == 0 ? 2 : bias_at % 16 == 0 ? 1 : 0;
         d.M = q.M, d.N = q.N;
         d.groups = static_cast<int>(q8_groups(q.K));
         d.bn = pp.bn, d.tiles_m = pp.tiles_m, d.tiles_n = pp.tiles_n, d.kb = pp.kb;

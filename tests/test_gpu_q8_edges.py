@@ -52,6 +52,34 @@ def test_quantize_writes_its_outputs_only(size, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("shape", [(5, 77, 12), (300, 140, 4), (300, 140, 24), (300, 140, 1004), (513, 264, 528), (2500, 136, 640)],
+                         ids=lambda s: "x".join(map(str, s)))
+def test_forward_bias_at_any_16_bytes(shape, dtype):
+    """The bias on 32 bytes and on 16 only, between NaN, with rows of the output on
+    32, 16 and 8 bytes: the same results, none of them from outside the bias."""
+    import torch
+
+    T, C, OC = shape
+    iq, isc, iv = q8(normal((T, C), "bf16", 1), mm.E4M3)
+    wq, wsc, wv = q8(normal((OC, C), "bf16", 2, 0.02), mm.E4M3)
+    bias = normal((OC,), dtype, 3)
+    want, tol = ref.product_bound(iv, wv, dtype, bias)
+    outs = []
+    for off in (32, 16):
+        room_ = torch.full((OC + 64,), float("nan"), dtype=tdt(dtype), device="cuda")
+        first = off // (2 if dtype == "bf16" else 4)
+        b = room_[first:first + OC]
+        b.copy_(dev(bias, dtype))
+        assert b.data_ptr() % 32 == off % 32
+        out = torch.full((T, OC), 7.0, dtype=tdt(dtype), device="cuda")
+        assert mm.mmbwd_q8_forward(out, iq, isc, wq, wsc, b, 1, T, C, OC, 0, 0, DT[dtype]) == mm.OK
+        torch.cuda.synchronize()
+        assert np.all(np.abs(host(out) - want) <= tol)
+        outs.append(out)
+    assert torch.equal(*outs)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("shape", [(1, 77, 12), (50, 264, 1004), (130, 1160, 136), (300, 140, 1004), (513, 264, 4)],
                          ids=lambda s: "x".join(map(str, s)))
 def test_forward_writes_its_output_only(shape, dtype):
