@@ -25,7 +25,7 @@
 // Warp roles (10 warps per CTA): 0 TMA producer; 1 MMA issuer (even CTA) or
 // forwarder of "stage full" to the even CTA (odd CTA); 2-9 epilogue, two warps per
 // tensor-memory lane quadrant, each taking every other 32-column chunk of its 32
-// rows: accumulator (+ bias or old values, requested two chunks ahead) rounded once
+// rows: accumulator (+ bias, or old values requested two chunks ahead) rounded once
 // and stored from registers, 32 bytes of a row per thread and store.
 //
 // Work list: the tiles of one or two products (dinp and dweight), each product's
@@ -83,7 +83,8 @@ static_assert(STAGES <= 4 * SF_BUFS - 3 && SF_BUFS * SF_STRIDE <= 64, "scale buf
 constexpr int BAR_FULL = 0, BAR_EMPTY = STAGES, BAR_ACC_FULL = 2 * STAGES, BAR_ACC_FREE = 2 * STAGES + 1,
               BAR_TEARDOWN = 2 * STAGES + 2, N_BARS = 2 * STAGES + 3;
 constexpr int OFF_SF = STAGES * STAGE_BYTES;
-constexpr int OFF_BARS = OFF_SF + STAGES * SF_BYTES;
+constexpr int OFF_BIAS = OFF_SF + STAGES * SF_BYTES;  // the bias of each epilogue warp's columns, fp32, in its order of chunks
+constexpr int OFF_BARS = OFF_BIAS + EPI_WARPS * 128 * 4;
 constexpr int OFF_MISC = OFF_BARS + N_BARS * 8;  // [0] tensor-memory base, [1] abort flag
 constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;
 static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
@@ -105,7 +106,6 @@ struct Prod {
     int bn, tiles_m, tiles_n, kb, splits, kb_per_split, item0;
     int f32, add;
     int wide;  // rows of D start on multiples of 32 bytes (2), 16 (1), 8 (0)
-    int bias_wide;  // the same of the bias and its length
     uint32_t idesc;
 };
 
@@ -311,6 +311,30 @@ __global__ void __launch_bounds__(THREADS, 1)
         const int q = warp & 3;                  // tensor-memory lane quadrant this warp may read
         const int h = (warp - FIRST_EPI) >> 2;   // which of the quadrant's two warps
         const uint32_t free_bar = ptx::mapa(bars + 8u * BAR_ACC_FREE, 0);
+        // 32-column chunk that this warp takes in step k of its t-th tile: the shared
+        // columns (the last 64 of the even accumulator, the first 64 of the odd one) first
+        auto chunk_of = [&](int bn, uint32_t t, int k) {
+            return (bn == 256 && (t & 1u) == 0) ? (k == 0 ? 6 + h : 2 * (k - 1) + h) : 2 * k + h;
+        };
+        // The bias of the columns of tile r, one a lane and step: requested a tile
+        // ahead and then kept in shared memory, where all lanes read the same value
+        // (the L1 that the stages leave loses it to the stores: loads in the epilogue
+        // took 4096 tokens 768 -> 50304 from 122 us without a bias to 226, and 350 with
+        // an fp32 output; this way 150 and 222).
+        float* const bias_s = reinterpret_cast<float*>(smem_raw + (base - raw) + OFF_BIAS) + (warp - FIRST_EPI) * 128;
+        uint32_t bias_r[4] = {0u, 0u, 0u, 0u};  // as loaded: converting here would wait for the load
+        const Prod& only = p.prod[0];           // (two products in one launch have no bias)
+        auto fetch_bias = [&](int r) {
+            const int w = only.bias ? item_at(p, sch, r) : p.n_items;
+            if (w >= p.n_items) return;
+            const int first = w % only.tiles_n * only.bn;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int64_t c = first + chunk_of(only.bn, static_cast<uint32_t>(r), k) * 32 + lane, at = c < only.N ? c : only.N - 1;
+                bias_r[k] = only.f32 ? static_cast<const uint32_t*>(only.bias)[at] : static_cast<const uint16_t*>(only.bias)[at];
+            }
+        };
+        fetch_bias(0);
         uint32_t tile = 0;
         for (int r = 0;; ++r, ++tile) {
             const int w = item_at(p, sch, r);
@@ -321,17 +345,30 @@ __global__ void __launch_bounds__(THREADS, 1)
             const int col0 = it.n_tile * d.bn;
             const int nk = d.bn / 64;  // this warp's 32-column chunks of the tile
             const bool in_row = row < d.M;
-            // chunk of step k: the shared columns (the last 64 of the even
-            // accumulator, the first 64 of the odd one) come first
-            auto chunk = [&](int k) {
-                return (d.bn == 256 && (tile & 1u) == 0) ? (k == 0 ? 6 + h : 2 * (k - 1) + h) : 2 * k + h;
-            };
+            auto chunk = [&](int k) { return chunk_of(d.bn, tile, k); };
             const uint32_t acc = tmem + (static_cast<uint32_t>(q * 32) << 16) + (tile & 1u) * ACC1;
             auto release = [&](int k) {  // after the first chunk has been read
                 if (k > 0) return;
                 ptx::tc_fence_before();
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive_cluster_relaxed(free_bar);
+            };
+            if (d.bias) {
+                __syncwarp();  // the tile before has read its own
+#pragma unroll
+                for (int k = 0; k < 4; ++k) bias_s[32 * k + lane] = __uint_as_float(d.f32 ? bias_r[k] : bias_r[k] << 16);
+                __syncwarp();
+                fetch_bias(r + 1);
+            }
+            auto add_bias = [&](int k, uint32_t (&v)[32]) {
+#pragma unroll
+                for (int g = 0; g < 8; ++g) {
+                    const float4 b = reinterpret_cast<const float4*>(bias_s + 32 * k)[g];
+                    v[4 * g] = __float_as_uint(__uint_as_float(v[4 * g]) + b.x);
+                    v[4 * g + 1] = __float_as_uint(__uint_as_float(v[4 * g + 1]) + b.y);
+                    v[4 * g + 2] = __float_as_uint(__uint_as_float(v[4 * g + 2]) + b.z);
+                    v[4 * g + 3] = __float_as_uint(__uint_as_float(v[4 * g + 3]) + b.w);
+                }
             };
             if (d.splits > 1) {  // partial sums: [128-row tile x column tile][split][128][bn]
                 if (!wt.wait_warp(bars + 8u * BAR_ACC_FULL, tile & 1u, q8::SITE_ACC_FULL, w)) break;
@@ -356,14 +393,12 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
                     for (int g = 0; g < 4; ++g) q8::st256(D + c + 8 * g, v + 8 * g, in_row ? d.N - col0 - c - 8 * g : 0, 4, d.wide);
                 };
-                if (d.add || d.bias) {  // the old values, or the bias, two chunks ahead
-                    const float* src = d.add ? D : static_cast<const float*>(d.bias) + col0;
-                    const int wide = d.add ? d.wide : d.bias_wide;
+                if (d.add) {  // the old values two chunks ahead
                     uint32_t old[2][32];
                     auto fetch = [&](int k) {
                         const int c = chunk(k) * 32;
 #pragma unroll
-                        for (int g = 0; g < 4; ++g) q8::ld256(src + c + 8 * g, old[k & 1] + 8 * g, in_row ? d.N - col0 - c - 8 * g : 0, 4, wide);
+                        for (int g = 0; g < 4; ++g) q8::ld256(D + c + 8 * g, old[k & 1] + 8 * g, in_row ? d.N - col0 - c - 8 * g : 0, 4, d.wide);
                     };
                     fetch(0), fetch(1);
                     if (!wt.wait_warp(bars + 8u * BAR_ACC_FULL, tile & 1u, q8::SITE_ACC_FULL, w)) break;
@@ -389,6 +424,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                         const int c = chunk(k) * 32;
                         ptx::tmem_ld32(acc + c, v);
                         release(k);
+                        if (d.bias) add_bias(k, v);
                         store(c, v);
                     }
                 }
@@ -398,14 +434,12 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
                     for (int g = 0; g < 2; ++g) q8::st256(D + c + 16 * g, o + 8 * g, in_row ? d.N - col0 - c - 16 * g : 0, 8, d.wide);
                 };
-                if (d.add || d.bias) {
-                    const __nv_bfloat16* src = d.add ? D : static_cast<const __nv_bfloat16*>(d.bias) + col0;
-                    const int wide = d.add ? d.wide : d.bias_wide;
+                if (d.add) {
                     uint32_t old[2][16];
                     auto fetch = [&](int k) {
                         const int c = chunk(k) * 32;
 #pragma unroll
-                        for (int g = 0; g < 2; ++g) q8::ld256(src + c + 16 * g, old[k & 1] + 8 * g, in_row ? d.N - col0 - c - 16 * g : 0, 8, wide);
+                        for (int g = 0; g < 2; ++g) q8::ld256(D + c + 16 * g, old[k & 1] + 8 * g, in_row ? d.N - col0 - c - 16 * g : 0, 8, d.wide);
                     };
                     fetch(0), fetch(1);
                     if (!wt.wait_warp(bars + 8u * BAR_ACC_FULL, tile & 1u, q8::SITE_ACC_FULL, w)) break;
@@ -433,6 +467,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                         const int c = chunk(k) * 32;
                         ptx::tmem_ld32(acc + c, v);
                         release(k);
+                        if (d.bias) add_bias(k, v);
 #pragma unroll
                         for (int e = 0; e < 16; ++e) o[e] = pack_bf16(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1]));
                         store(c, o);
@@ -764,8 +799,6 @@ cudaError_t launch_pair(const Plan& pl, const Q8Product* prod, uint8_t* ws, cuda
         d.D = q.D, d.partials = reinterpret_cast<float*>(ws + pp.ws_off);
         const uint64_t at = reinterpret_cast<uintptr_t>(q.D) | n * (f32 ? 4 : 2);  // (N is a multiple of 4)
         d.wide = at % 32 == 0 ? 2 : at % 16 == 0 ? 1 : 0;
-        const uint64_t bias_at = reinterpret_cast<uintptr_t>(q.bias) | n * (f32 ? 4 : 2);
-        d.bias_wide = bias_at % 32 == 0 ? 2 : bias_at % 16 == 0 ? 1 : 0;
         d.M = q.M, d.N = q.N;
         d.groups = static_cast<int>(q8_groups(q.K));
         d.bn = pp.bn, d.tiles_m = pp.tiles_m, d.tiles_n = pp.tiles_n, d.kb = pp.kb;

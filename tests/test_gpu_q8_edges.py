@@ -80,6 +80,26 @@ def test_forward_bias_at_any_16_bytes(shape, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("width", ["128,128", "256,256"])
+def test_forward_bias_over_many_tiles(monkeypatch, width, dtype):
+    """Several tiles for each CTA pair, the last column of tiles cut: every tile
+    adds the bias of its own columns, which is all there is to its result."""
+    import torch
+
+    monkeypatch.setenv("MMBWD_Q8_TILE_N", width)
+    T, C, OC = 20_100, 8, 1180
+    x = torch.zeros(T, C, dtype=tdt(dtype), device="cuda")
+    iq, isc, _ = q8(host(x), mm.E4M3)
+    wq, wsc, _ = q8(normal((OC, C), dtype, 2), mm.E4M3)
+    bias = dev(normal((OC,), dtype, 3), dtype)
+    out = torch.full((T + 1, OC), 7.0, dtype=tdt(dtype), device="cuda")
+    assert mm.mmbwd_q8_forward(out, iq, isc, wq, wsc, bias, 1, T, C, OC, 0, 0, DT[dtype]) == mm.OK
+    torch.cuda.synchronize()
+    assert torch.equal(out[:T], bias.expand(T, OC))
+    assert torch.all(out[T] == 7.0)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("shape", [(1, 77, 12), (50, 264, 1004), (130, 1160, 136), (300, 140, 1004), (513, 264, 4)],
                          ids=lambda s: "x".join(map(str, s)))
 def test_forward_writes_its_output_only(shape, dtype):
