@@ -53,6 +53,11 @@
  * so calls with their own workspaces may overlap on different streams or in
  * different captured graphs, from one thread or several.
  *
+ * The waits inside the product kernels are bounded: by MMBWD_WAIT_TIMEOUT_NS
+ * nanoseconds each, read from the environment at every call (2 s where it is not set), as
+ * in the bf16 kernel. One that runs out leaves the call's outputs incomplete and is
+ * reported by mmbwd_device_status.
+ *
  * For tuning and tests the environment overrides the work split:
  * MMBWD_Q8_SPLITS = "<dinp>,<dweight>" (pieces of each product's reduction, 0: the
  * planner's choice) and MMBWD_Q8_TILE_N = "<dinp>,<dweight>" (tile widths, 128 or
@@ -158,6 +163,13 @@ int mmbwd_q8_backward(void* dinp_or_null, void* dweight_or_null, const void* dou
                       int64_t B, int64_t T, int64_t C, int64_t OC, int dout_format, int inp_format, int weight_format,
                       int dinp_dtype, int dweight_dtype, int accumulate, cudaStream_t stream);
 size_t mmbwd_q8_backward_workspace_bytes(int64_t B, int64_t T, int64_t C, int64_t OC);
+
+/* Self-test of the bounded waits: one thread waits as the product kernel (kernel 0) or
+ * the few-tokens kernel (1) does, on a barrier that nothing completes, and gives up
+ * after timeout_ns (0: the limit the kernels take). Synchronises the device; the
+ * failure is then in the status word, for mmbwd_device_status to report and clear.
+ * Returns a status of the launch (ERR_SHAPE: no such kernel). */
+int mmbwd_q8_selftest_wait_timeout(int kernel, uint64_t timeout_ns);
 
 #ifdef __cplusplus
 }

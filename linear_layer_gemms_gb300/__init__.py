@@ -77,6 +77,7 @@ SIGNATURES = {
     "mmbwd_q8_forward": ([_vp] * 6 + [_i64] * 4 + [_ci] * 3 + [_vp], _ci),
     "mmbwd_q8_backward": ([_vp] * 11 + [_sz] + [_i64] * 4 + [_ci] * 6 + [_vp], _ci),
     "mmbwd_q8_backward_workspace_bytes": ([_i64] * 4, _sz),
+    "mmbwd_q8_selftest_wait_timeout": ([_ci, _u64], _ci),
 }
 LNBWD_MAX_C = {F32: 1 << 20, BF16: 1 << 20}  # LNBWD_MAX_C_F32, LNBWD_MAX_C_BF16
 ENCBWD_MAX_POSITIONS, ENCBWD_MAX_VOCAB, ENCBWD_MAX_CHANNELS = 1 << 24, 131071, 65536
@@ -231,6 +232,13 @@ def mmbwd_q8_backward(dinp, dweight, dout_q, dout_scale, dout_qt, dout_scale_t, 
 
 def mmbwd_q8_backward_workspace_bytes(B: int, T: int, C: int, OC: int) -> int:
     return int(load().mmbwd_q8_backward_workspace_bytes(B, T, C, OC))
+
+
+def mmbwd_q8_selftest_wait_timeout(kernel: int, timeout_ns: int = 0) -> int:
+    """Let a bounded wait of the product kernel (0) or the few-tokens kernel (1) run
+    out after timeout_ns (0: the limit the kernels take); the failure is then in
+    the device status word. Returns the status of the launch."""
+    return load().mmbwd_q8_selftest_wait_timeout(kernel, timeout_ns)
 
 
 def encbwd_run(dwte, dwpe, dout, inp, B: int, T: int, C: int, V: int, dtype: int, stream=None) -> int:

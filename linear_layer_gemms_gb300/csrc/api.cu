@@ -932,6 +932,20 @@ size_t q8_data_size(int64_t rows, int64_t K) { return static_cast<size_t>(rows) 
 
 }  // namespace
 
+int mmbwd_q8_selftest_wait_timeout(int kernel, uint64_t timeout_ns) {
+    if (kernel != 0 && kernel != 1) return MMBWD_ERR_SHAPE;
+    {
+        std::lock_guard<std::mutex> g(g_mutex);
+        DeviceState* d = nullptr;
+        int dev = 0;
+        const int rc = device_state(&d, &dev);
+        if (rc != MMBWD_OK) return rc;
+    }
+    const unsigned long long limit = timeout_ns ? timeout_ns : q8_wait_limit_ns();
+    const cudaError_t e = kernel == 0 ? q8_selftest_wait(limit) : q8_tokens_selftest_wait(limit);
+    return e == cudaSuccess && cudaDeviceSynchronize() == cudaSuccess ? MMBWD_OK : MMBWD_ERR_CUDA;
+}
+
 size_t mmbwd_q8_data_bytes(int64_t rows, int64_t K) { return q8_shape_ok(rows, K) ? q8_data_size(rows, K) : 0; }
 
 size_t mmbwd_q8_scale_bytes(int64_t rows, int64_t K) { return q8_shape_ok(rows, K) ? q8_scale_size(rows, K) : 0; }

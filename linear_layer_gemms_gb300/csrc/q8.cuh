@@ -124,16 +124,19 @@ __device__ __forceinline__ void ld256(const void* p, uint32_t* v, int64_t left, 
     }
 }
 
-constexpr unsigned long long TIMEOUT_NS = 2000000000ull;  // 2 s per wait
+constexpr unsigned long long TEARDOWN_NS = 2000000000ull;  // teardown waits, whatever the limit of the others
 
 // Where a wait gave up (device status word of the 8-bit products).
-enum Site : int { SITE_EMPTY = 1, SITE_ACC_FREE = 2, SITE_FULL = 3, SITE_ACC_FULL = 4, SITE_TEARDOWN = 8, SITE_FORWARD = 10 };
+enum Site : int { SITE_EMPTY = 1, SITE_ACC_FREE = 2, SITE_FULL = 3, SITE_ACC_FULL = 4, SITE_TEARDOWN = 8, SITE_SELFTEST = 9, SITE_FORWARD = 10 };
 
-// Bounded mbarrier wait: false after TIMEOUT_NS (recorded in `status`) or once
-// another warp of the CTA has given up; a teardown wait ignores the latter.
+// Bounded mbarrier wait: false after `limit_ns` (recorded in `status`) or once
+// another warp of the CTA has given up. A teardown wait ignores the latter, and
+// lasts up to TEARDOWN_NS however short the limit: copies and MMAs in flight have
+// to land before their memory goes.
 struct Waiter {
     volatile uint32_t* abort;
     unsigned int* status;
+    unsigned long long limit_ns;
 
     __device__ void record(int site, int item) const {
         *abort = 1u;
@@ -146,12 +149,12 @@ struct Waiter {
     }
     __device__ bool wait(uint32_t bar, uint32_t parity, int site, int item, bool teardown = false) const {
         if (ptx::mbar_try_wait(bar, parity)) return true;
-        const uint64_t t0 = ptx::globaltimer();
+        const uint64_t t0 = ptx::globaltimer(), limit = teardown ? TEARDOWN_NS : limit_ns;
         for (uint32_t i = 1;; ++i) {
             if (ptx::mbar_try_wait(bar, parity)) return true;
             if ((i & 31u) == 0) {
                 if (!teardown && *abort) return false;
-                if (ptx::globaltimer() - t0 > TIMEOUT_NS) {
+                if (ptx::globaltimer() - t0 > limit) {
                     record(site, item);
                     return false;
                 }
@@ -163,6 +166,17 @@ struct Waiter {
         return __all_sync(0xffffffffu, ok);
     }
 };
+
+// The body of each kernel's wait self-test (one thread): nothing ever arrives on
+// the barrier, so the wait has to give up and record it.
+__device__ __forceinline__ void selftest_wait(unsigned int* status, unsigned long long limit_ns) {
+    __shared__ alignas(8) uint64_t bar;
+    __shared__ uint32_t abort_flag;
+    abort_flag = 0u;
+    ptx::mbar_init(ptx::smem_u32(&bar), 1u);
+    ptx::fence_mbar_init();
+    Waiter{&abort_flag, status, limit_ns}.wait(ptx::smem_u32(&bar), 0u, SITE_SELFTEST, 0);
+}
 
 }  // namespace q8
 }  // namespace mmbwd

@@ -7,6 +7,7 @@
 
 #include <cstddef>
 #include <cstdint>
+#include <cstdlib>
 
 namespace mmbwd {
 
@@ -61,6 +62,17 @@ inline bool q8_few_tokens(int64_t tokens, int64_t N, int num_sms) {
 cudaError_t q8_tokens_launch(const Q8Product& product, int num_sms, cudaStream_t stream);
 cudaError_t q8_tokens_read_status(int* code, int* info3, bool reset);
 cudaError_t q8_read_status(int* code, int* info3, bool reset);
+
+// How long a wait of the two product kernels may last: MMBWD_WAIT_TIMEOUT_NS, as
+// for the bf16 kernel, else 2 s.
+inline unsigned long long q8_wait_limit_ns() {
+    const char* s = std::getenv("MMBWD_WAIT_TIMEOUT_NS");
+    char* end = nullptr;
+    const long long v = s && *s ? std::strtoll(s, &end, 10) : 0;
+    return v > 0 && *end == '\0' ? static_cast<unsigned long long>(v) : 2000000000ull;
+}
+cudaError_t q8_selftest_wait(unsigned long long limit_ns);
+cudaError_t q8_tokens_selftest_wait(unsigned long long limit_ns);
 
 cudaError_t ln_forward_launch(void* out, float* mean, float* rstd, const void* inp, const void* weight,
                               const void* bias, int64_t BT, int C, float eps, int dtype, int num_sms,

@@ -39,7 +39,7 @@
 // (3.0). A k-block (128 of K) of a 256-wide tile takes 0.33 us, which is the round trip
 // of six 32 KB stages; a tile's hand-over about 0.5.
 //
-// Every wait is bounded (2 s): one that gives up records the failure in the
+// Every wait is bounded (q8_wait_limit_ns): one that gives up records the failure in the
 // device status word and all roles unwind.
 #include "../../include/q8_linear.h"
 #include "internal.h"
@@ -112,6 +112,7 @@ struct Prod {
 struct Params {
     Prod prod[2];
     int n_items, n_prod, table;
+    unsigned long long wait_ns;  // limit of a wait
 };
 
 struct Maps {
@@ -183,7 +184,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     ptx::tc_fence_after();
     if (warp >= FIRST_EPI) ptx::grid_dependency_wait();
     const uint32_t tmem = misc[0];
-    const q8::Waiter wt{misc + 1, g_q8_status};
+    const q8::Waiter wt{misc + 1, g_q8_status, p.wait_ns};
 
     if (warp == 0) {
         // ------------------------------------------------------------ producer
@@ -787,6 +788,7 @@ cudaError_t launch_pair(const Plan& pl, const Q8Product* prod, uint8_t* ws, cuda
     par.n_prod = pl.n;
     par.n_items = pl.n_items;
     par.table = pl.table;
+    par.wait_ns = q8_wait_limit_ns();
     for (int i = 0; i < pl.n; ++i) {
         const Q8Product& q = prod[i];
         const ProductPlan& pp = pl.p[i];
@@ -859,6 +861,13 @@ cudaError_t q8_products_launch(const Q8Product* products, int n, bool may_split,
     const Plan& pl = plan_for(s, n, may_split, num_sms);
     if (pl.n_items == 0 || pl.ws_bytes > ws_bytes) return cudaErrorInvalidValue;
     return launch_pair(pl, products, static_cast<uint8_t*>(ws), stream);
+}
+
+__global__ void q8_selftest_kernel(unsigned long long limit_ns) { q8::selftest_wait(g_q8_status, limit_ns); }
+
+cudaError_t q8_selftest_wait(unsigned long long limit_ns) {
+    q8_selftest_kernel<<<1, 1>>>(limit_ns);
+    return cudaGetLastError();
 }
 
 cudaError_t q8_read_status(int* code, int* info3, bool reset) {

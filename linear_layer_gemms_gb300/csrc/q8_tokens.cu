@@ -21,7 +21,7 @@
 // Warps: 0 producer, 1 MMA issuer, 2-5 epilogue (lane = weight row, so that 32
 // lanes write neighbouring outputs).
 //
-// Every wait is bounded (2 s) and recorded when it gives up; all threads still
+// Every wait is bounded (q8_wait_limit_ns) and recorded when it gives up; all threads still
 // reach the cluster barriers.
 #include "../../include/q8_linear.h"
 #include "internal.h"
@@ -76,6 +76,7 @@ struct Params {
     int64_t groups;
     int kb, tiles, tiles_n, splits, f32;
     uint32_t idesc;
+    unsigned long long wait_ns;  // limit of a wait
 };
 
 template <int NT>
@@ -122,7 +123,7 @@ __global__ void __launch_bounds__(THREADS, 2)
     ptx::grid_launch_dependents();
     ptx::grid_dependency_wait();
     const uint32_t tmem = misc[0];
-    const q8::Waiter wt{misc + 1, g_q8_tokens_status};
+    const q8::Waiter wt{misc + 1, g_q8_tokens_status, p.wait_ns};
     bool ok = true;
 
     if (warp == 0) {
@@ -372,6 +373,7 @@ cudaError_t q8_tokens_launch(const Q8Product& q, int num_sms, cudaStream_t strea
     p.T = q.M, p.N = q.N, p.groups = q8_groups(q.K);
     p.kb = static_cast<int>(q8_blocks(q.K));
     p.f32 = q.dtype == MMBWD_F32 ? 1 : 0;
+    p.wait_ns = q8_wait_limit_ns();
     p.tiles_n = static_cast<int>((q.N + ROWS - 1) / ROWS);
     const int64_t tiles = p.tiles_n * (q.M <= 64 ? 1 : (q.M + 63) / 64);
     if (tiles > INT32_MAX / 8) return cudaErrorInvalidValue;
@@ -379,6 +381,15 @@ cudaError_t q8_tokens_launch(const Q8Product& q, int num_sms, cudaStream_t strea
     if (q.M <= 16) return launch<16>(q, p, num_sms, stream);
     if (q.M <= 32) return launch<32>(q, p, num_sms, stream);
     return launch<64>(q, p, num_sms, stream);
+}
+
+__global__ void q8_tokens_selftest_kernel(unsigned long long limit_ns) {
+    q8::selftest_wait(g_q8_tokens_status, limit_ns);
+}
+
+cudaError_t q8_tokens_selftest_wait(unsigned long long limit_ns) {
+    q8_tokens_selftest_kernel<<<1, 1>>>(limit_ns);
+    return cudaGetLastError();
 }
 
 cudaError_t q8_tokens_read_status(int* code, int* info3, bool reset) {
