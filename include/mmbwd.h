@@ -223,6 +223,11 @@ void mmbwd_debug_fail_next_alloc(int n);
  * entry point returns MMBWD_ERR_CUDA and the outputs are untouched. */
 void mmbwd_debug_fail_next_launch(int n);
 
+/* Test hook: enqueue one thread that allows the next launch on `stream` to begin
+ * at once (programmatic dependent launch) and then stays for `ns` nanoseconds, one
+ * second at most: what follows is resident, and has to wait, for that long. */
+int mmbwd_debug_hold_stream(uint64_t ns, cudaStream_t stream);
+
 /* Size of the library's fixed scratch buffer used by mmbwd_run_static_scratch. */
 #define MMBWD_STATIC_SCRATCH_BYTES (32u << 20)
 #define MMBWD_ERR_SCRATCH (-11) /* the problem needs more scratch than that buffer holds */

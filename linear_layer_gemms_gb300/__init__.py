@@ -58,6 +58,7 @@ SIGNATURES = {
     "mmbwd_selftest_wait_timeout": ([_u64], _ci),
     "mmbwd_debug_fail_next_alloc": ([_ci], None),
     "mmbwd_debug_fail_next_launch": ([_ci], None),
+    "mmbwd_debug_hold_stream": ([_u64, _vp], _ci),
     "mmbwd_run_static_scratch": ([_vp] * 6 + [_i64] * 4 + [_ci, _vp], _ci),
     "mmbwd_forward": ([_vp] * 4 + [_i64] * 4 + [_ci, _vp], _ci),
     "mmbwd_forward_path": ([_i64] * 4 + [_ci], _ci),
@@ -338,6 +339,10 @@ def mmbwd_debug_fail_next_alloc(n: int) -> None:
 
 def mmbwd_debug_fail_next_launch(n: int) -> None:
     load().mmbwd_debug_fail_next_launch(n)
+
+
+def mmbwd_debug_hold_stream(ns: int, stream=None) -> int:
+    return load().mmbwd_debug_hold_stream(ns, _stream(stream))
 
 
 def matmul_backward(dinp, dweight, dbias, dout, inp, weight, stream=None) -> None:

@@ -505,6 +505,10 @@ void mmbwd_debug_fail_next_alloc(int n) { g_fail_allocs.store(n < 0 ? 0 : n); }
 
 void mmbwd_debug_fail_next_launch(int n) { g_fail_launches.store(n < 0 ? 0 : n); }
 
+int mmbwd_debug_hold_stream(uint64_t ns, cudaStream_t stream) {
+    return hold_launch(std::min<uint64_t>(ns, 1000000000ull), stream) == cudaSuccess ? MMBWD_OK : MMBWD_ERR_CUDA;
+}
+
 int mmbwd_forward(void* out, const void* inp, const void* weight, const void* bias, int64_t B, int64_t T,
                   int64_t C, int64_t OC, int dtype, cudaStream_t stream) {
     NvtxRange nvtx("mmbwd_forward");

@@ -17,6 +17,10 @@ namespace mmbwd {
 // of each entry point can be exercised without a GPU fault.
 bool take_injected_launch_failure();
 
+// Test hook (mmbwd_debug_hold_stream): one thread that lets the next launch on the
+// stream begin and stays for `ns`.
+cudaError_t hold_launch(uint64_t ns, cudaStream_t stream);
+
 // ------------------------------------------------------------ fp32 SIMT path
 constexpr int SIMT_BM = 128;
 constexpr int SIMT_BN = 128;

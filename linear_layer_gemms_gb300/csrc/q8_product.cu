@@ -182,7 +182,11 @@ __global__ void __launch_bounds__(THREADS, 1)
     __syncthreads();
     ptx::cluster_sync();
     ptx::tc_fence_after();
-    if (warp >= FIRST_EPI) ptx::grid_dependency_wait();
+    // The launch before this one may still run. The producer waits for it just ahead
+    // of its first load, so that its set-up overlaps; all others here: the epilogue
+    // touches global memory, and the MMA issuer's and forwarder's first wait would
+    // count the other launch's time against its limit.
+    if (warp != 0) ptx::grid_dependency_wait();
     const uint32_t tmem = misc[0];
     const q8::Waiter wt{misc + 1, g_q8_status, p.wait_ns};
 

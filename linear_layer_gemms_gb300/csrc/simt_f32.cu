@@ -16,6 +16,7 @@
 // and overwrite dbias. No split of K, so each output has one writer.
 #include "../../include/mmbwd.h"
 #include "ops.h"
+#include "ptx.cuh"
 #include "sr.cuh"
 
 #include <algorithm>
@@ -208,6 +209,21 @@ __global__ void fill_rows_kernel(T* __restrict__ out, const T* __restrict__ bias
     for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < n;
          i += static_cast<int64_t>(gridDim.x) * blockDim.x)
         out[i] = bias ? bias[i % cols] : static_cast<T>(0.f);
+}
+
+// One thread that lets the next launch begin and then stays for `ns`; the loop
+// ends after MAX_HOLD_STEPS sleeps whatever the clock says.
+constexpr int MAX_HOLD_STEPS = 4000000;
+
+__global__ void hold_kernel(unsigned long long ns) {
+    ptx::grid_launch_dependents();
+    const uint64_t t0 = ptx::globaltimer();
+    for (int i = 0; i < MAX_HOLD_STEPS && ptx::globaltimer() - t0 < ns; ++i) __nanosleep(500);
+}
+
+cudaError_t hold_launch(uint64_t ns, cudaStream_t stream) {
+    hold_kernel<<<1, 1, 0, stream>>>(ns);
+    return cudaGetLastError();
 }
 
 cudaError_t fill_rows_launch(void* out, const void* bias, int64_t rows, int64_t cols, int dtype,
