@@ -441,14 +441,14 @@ __global__ void __launch_bounds__(Smem<MODE>::THREADS, 1)
     __syncthreads();
     ptx::cluster_sync();  // both CTAs' barriers exist before any remote arrive or commit
     ptx::tc_fence_after();
-    // Everything above overlaps the previous launch on the stream. Threads that
-    // touch global memory wait for it to complete first: the epilogue warps
-    // here, the producer only just ahead of its first load, so that its first
+    // Everything above overlaps the previous launch on the stream. All warps but
+    // the producer wait here for it to complete: the epilogue warps touch global
+    // memory, and the first waits of the MMA and bias warps, which read only
+    // shared and tensor memory, would count its time against their limit. The
+    // producer waits only just ahead of its first load, so that its first
     // item's schedule entry, geometry and barrier steps (first-touch latencies
-    // of about 2 us in all) also overlap the previous launch. The MMA and bias
-    // warps read only shared and tensor memory.
-    const bool defer_wait = warp < WARP_EPI;
-    if (!defer_wait) ptx::grid_dependency_wait();
+    // of about 2 us in all) also overlap the previous launch.
+    if (warp != WARP_TMA) ptx::grid_dependency_wait();
     const uint32_t tmem_base = misc[0];
     const Waiter wt{misc + 1, p.timeout_ns};
 
