@@ -164,6 +164,11 @@ int mmbwd_q8_backward(void* dinp_or_null, void* dweight_or_null, const void* dou
                       int dinp_dtype, int dweight_dtype, int accumulate, cudaStream_t stream);
 size_t mmbwd_q8_backward_workspace_bytes(int64_t B, int64_t T, int64_t C, int64_t OC);
 
+/* Test hook: how many times the library has searched for a work split of the products.
+ * The outcome is remembered per shape (for about two thousand), so a shape seen
+ * before is not searched for again, whatever the types and the accumulate bits. */
+long long mmbwd_q8_debug_plan_searches(void);
+
 /* Self-test of the bounded waits: one thread waits as the product kernel (kernel 0) or
  * the few-tokens kernel (1) does, on a barrier that nothing completes, and gives up
  * after timeout_ns (0: the limit the kernels take). Synchronises the device; the

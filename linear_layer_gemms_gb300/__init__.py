@@ -78,6 +78,7 @@ SIGNATURES = {
     "mmbwd_q8_forward": ([_vp] * 6 + [_i64] * 4 + [_ci] * 3 + [_vp], _ci),
     "mmbwd_q8_backward": ([_vp] * 11 + [_sz] + [_i64] * 4 + [_ci] * 6 + [_vp], _ci),
     "mmbwd_q8_backward_workspace_bytes": ([_i64] * 4, _sz),
+    "mmbwd_q8_debug_plan_searches": ([], ctypes.c_longlong),
     "mmbwd_q8_selftest_wait_timeout": ([_ci, _u64], _ci),
 }
 LNBWD_MAX_C = {F32: 1 << 20, BF16: 1 << 20}  # LNBWD_MAX_C_F32, LNBWD_MAX_C_BF16
@@ -233,6 +234,11 @@ def mmbwd_q8_backward(dinp, dweight, dout_q, dout_scale, dout_qt, dout_scale_t, 
 
 def mmbwd_q8_backward_workspace_bytes(B: int, T: int, C: int, OC: int) -> int:
     return int(load().mmbwd_q8_backward_workspace_bytes(B, T, C, OC))
+
+
+def mmbwd_q8_debug_plan_searches() -> int:
+    """How many times the work split of a shape of 8-bit products has been searched for."""
+    return int(load().mmbwd_q8_debug_plan_searches())
 
 
 def mmbwd_q8_selftest_wait_timeout(kernel: int, timeout_ns: int = 0) -> int:

@@ -876,6 +876,16 @@ int check_device(const Arg* a, int n, DeviceState** d) {
     return MMBWD_OK;
 }
 
+// The same for a call that plans and launches without g_mutex; `sms`: the CTAs the
+// device keeps resident.
+int check_device_unlocked(const Arg* a, int n, int* sms) {
+    std::lock_guard<std::mutex> g(g_mutex);
+    DeviceState* d = nullptr;
+    const int rc = check_device(a, n, &d);
+    if (rc == MMBWD_OK) *sms = d->num_sms;
+    return rc;
+}
+
 }  // namespace
 
 int lnbwd_forward(void* out, float* mean, float* rstd, const void* inp, const void* weight, const void* bias,
@@ -935,6 +945,8 @@ size_t q8_scale_size(int64_t rows, int64_t K) {
 size_t q8_data_size(int64_t rows, int64_t K) { return static_cast<size_t>(rows) * static_cast<size_t>(q8_ld(K)); }
 
 }  // namespace
+
+long long mmbwd_q8_debug_plan_searches(void) { return q8_plan_searches(); }
 
 int mmbwd_q8_selftest_wait_timeout(int kernel, uint64_t timeout_ns) {
     if (kernel != 0 && kernel != 1) return MMBWD_ERR_SHAPE;
@@ -1020,9 +1032,8 @@ int mmbwd_q8_forward(void* out, const void* inp_q, const void* inp_scale, const 
                          {bias, static_cast<size_t>(OC) * s.es, false}};
     rc = check_args(args, 6);
     if (rc != MMBWD_OK) return rc;
-    std::lock_guard<std::mutex> g(g_mutex);
-    DeviceState* d = nullptr;
-    rc = check_device(args, 6, &d);
+    int sms = 0;
+    rc = check_device_unlocked(args, 6, &sms);
     if (rc != MMBWD_OK) return rc;
     if (s.BT == 0 || OC == 0) return MMBWD_OK;
     cudaError_t e;
@@ -1035,8 +1046,8 @@ int mmbwd_q8_forward(void* out, const void* inp_q, const void* inp_scale, const 
         p.B = static_cast<const uint8_t*>(weight_q), p.b_scale = static_cast<const uint8_t*>(weight_scale);
         p.M = s.BT, p.N = OC, p.K = C;
         p.a_format = inp_format, p.b_format = weight_format, p.dtype = dtype;
-        e = q8_few_tokens(s.BT, OC, d->num_sms) ? q8_tokens_launch(p, d->num_sms, stream)
-                                                : q8_products_launch(&p, 1, false, nullptr, 0, d->num_sms, stream);
+        e = q8_few_tokens(s.BT, OC, sms) ? q8_tokens_launch(p, sms, stream)
+                                         : q8_products_launch(&p, 1, false, nullptr, 0, sms, stream);
     }
     return e == cudaSuccess ? MMBWD_OK : MMBWD_ERR_CUDA;
 }
@@ -1100,9 +1111,8 @@ int mmbwd_q8_backward(void* dinp, void* dweight, const void* dout_q, const void*
                           {dinp ? weight_scale_t : nullptr, q8_scale_size(C, OC), false}};
     rc = check_args(args, 11);
     if (rc != MMBWD_OK) return rc;
-    std::lock_guard<std::mutex> g(g_mutex);
-    DeviceState* d = nullptr;
-    rc = check_device(args, 11, &d);
+    int sms = 0;
+    rc = check_device_unlocked(args, 11, &sms);
     if (rc != MMBWD_OK) return rc;
 
     Q8Product prod[2];
@@ -1135,7 +1145,7 @@ int mmbwd_q8_backward(void* dinp, void* dweight, const void* dout_q, const void*
         }
     }
     if (e == cudaSuccess && n > 0)
-        e = q8_products_launch(prod, n, true, workspace, workspace_bytes, d->num_sms, stream);
+        e = q8_products_launch(prod, n, true, workspace, workspace_bytes, sms, stream);
     return e == cudaSuccess ? MMBWD_OK : MMBWD_ERR_CUDA;
 }
 

@@ -48,6 +48,8 @@ struct Q8Product {
 size_t q8_products_workspace(const Q8Product* products, int n, int num_sms);
 cudaError_t q8_products_launch(const Q8Product* products, int n, bool may_split, void* ws, size_t ws_bytes, int num_sms,
                                cudaStream_t stream);
+// How many times a shape's tile widths and splits have been searched for.
+long long q8_plan_searches();
 // Whether the forward takes the few-tokens kernel: always up to 64 tokens, and
 // up to 256 while its 128 x 64 tiles are at most half the SMs, so that several
 // CTAs share each tile's K. Measured (us, this kernel against the pair kernel): 1 token

@@ -51,6 +51,7 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <atomic>
 #include <climits>
 #include <cstdio>
 #include <cstdlib>
@@ -605,14 +606,12 @@ double assign(Plan& pl, int pairs) {
 
 struct Shape3 {
     int64_t M, N, K;
-    int f32, add;  // what its epilogue stores
 };
 
 // Overrides for tuning and tests: MMBWD_Q8_TILE_N and MMBWD_Q8_SPLITS = "<first
 // product>,<second product>" (dinp, dweight; 0: the planner's choice).
 struct Forced {
     int bn[2], splits[2];
-    bool operator==(const Forced& o) const { return std::memcmp(this, &o, sizeof(o)) == 0; }
 };
 
 Forced forced_from_env() {
@@ -631,23 +630,62 @@ Forced forced_from_env() {
     return f;
 }
 
-// The best plan by the time model over tile widths and, where allowed, splits;
-// n_items == 0 where no candidate is possible (an override that asks for more items
-// than the schedule holds).
-void make_plan(const Shape3* s, int n, bool may_split, const Forced& force, int num_sms, Plan* out) {
-    static thread_local Plan c;
+// What a search finds: tile width and split count of each product; bn[0] == 0 where
+// no candidate is possible (an override that asks for more items than the
+// schedule holds).
+struct Choice {
+    int bn[2], splits[2];
+};
+
+// The plan of a choice, its items not yet assigned to pairs; false where it is
+// not possible.
+bool lay_out(const Shape3* s, int n, const Choice& ch, int num_sms, Plan* pl) {
     const int max_pairs = std::max(1, std::min(num_sms / 2, MAX_PAIRS));
+    pl->n = n;
+    pl->n_items = 0;
+    pl->ws_bytes = 0;
+    int64_t total = 0;
+    for (int i = 0; i < n; ++i) {
+        ProductPlan& p = pl->p[i];
+        p.bn = ch.bn[i];
+        p.epi = EPI_SEARCH;
+        p.tiles_m = ceil_div(s[i].M, PAIR_M);
+        p.tiles_n = ceil_div(s[i].N, p.bn);
+        p.kb = ceil_div(s[i].K, 128);
+        p.kb_per_split = ceil_div(p.kb, std::min(ch.splits[i], p.kb));
+        p.splits = ceil_div(p.kb, p.kb_per_split);
+        if (ch.splits[i] > 1 && p.splits != ch.splits[i]) return false;
+        const int64_t tiles = static_cast<int64_t>(p.tiles_m) * p.tiles_n;
+        p.item0 = static_cast<int>(total);
+        total += tiles * p.splits;
+        if (total > INT32_MAX) return false;
+        p.items = static_cast<int>(tiles * p.splits);
+        p.ws_off = pl->ws_bytes;
+        const int64_t part_rows = 2 * tiles * p.splits * BM;
+        if (p.splits > 1 && (part_rows > INT32_MAX || total > MAX_ITEMS)) return false;
+        p.ws_bytes = p.splits > 1 ? static_cast<size_t>(part_rows) * p.bn * 4 : 0;
+        pl->ws_bytes += p.ws_bytes;
+    }
+    pl->n_items = static_cast<int>(total);
+    pl->table = pl->n_items <= MAX_ITEMS ? 1 : 0;
+    pl->grid = 2 * static_cast<int>(std::min<int64_t>(total, max_pairs));
+    return true;
+}
+
+// The best choice by the time model over tile widths and, where allowed, splits.
+Choice search(const Shape3* s, int n, bool may_split, const Forced& force, int num_sms) {
+    static thread_local Plan c;
     double best = 1e300;
-    *out = Plan{};
+    Choice found{};
     static const int kSplits[] = {1, 2, 3, 4, 6, 8, 12, 16};
     for (int widths = 0; widths < (n == 2 ? 4 : 2); ++widths)
         for (int s0 : kSplits)
             for (int s1 : kSplits) {
                 if ((n == 1 && s1 > 1) || (!may_split && (s0 > 1 || s1 > 1))) continue;
+                const Choice ch{{widths & 1 ? 128 : 256, widths & 2 ? 128 : 256}, {s0, s1}};
                 bool skip = false;
                 for (int i = 0; i < n; ++i) {
-                    const int bn = (widths >> i) & 1 ? 128 : 256, want = i == 0 ? s0 : s1;
-                    if (force.bn[i] && force.bn[i] != bn) skip = true;
+                    if (force.bn[i] && force.bn[i] != ch.bn[i]) skip = true;
                     // a forced count above the number of blocks, or one that would leave
                     // an empty range, is lowered to the nearest that does not
                     if (may_split && force.splits[i]) {
@@ -656,106 +694,126 @@ void make_plan(const Shape3* s, int n, bool may_split, const Forced& force, int 
                         int usable = 1;
                         for (int o : kSplits)
                             if (o <= count && ceil_div(kb, ceil_div(kb, o)) == o) usable = o;
-                        if (want != usable) skip = true;
+                        if (ch.splits[i] != usable) skip = true;
                     }
                 }
-                if (skip) continue;
-                c.n = n;
-                c.n_items = 0;
-                c.ws_bytes = 0;
-                bool ok = true;
+                if (skip || !lay_out(s, n, ch, num_sms, &c)) continue;
                 double work = 0.0, longest = 0.0, tail = 0.0;
-                int64_t total = 0;
                 for (int i = 0; i < n; ++i) {
-                    ProductPlan& p = c.p[i];
-                    p.bn = (widths >> i) & 1 ? 128 : 256;
-                    p.epi = EPI_SEARCH;
-                    p.tiles_m = ceil_div(s[i].M, PAIR_M);
-                    p.tiles_n = ceil_div(s[i].N, p.bn);
-                    p.kb = ceil_div(s[i].K, 128);
-                    const int want = i == 0 ? s0 : s1;
-                    p.kb_per_split = ceil_div(p.kb, std::min(want, p.kb));
-                    p.splits = ceil_div(p.kb, p.kb_per_split);
-                    if (want > 1 && p.splits != want) ok = false;
-                    const int64_t tiles = static_cast<int64_t>(p.tiles_m) * p.tiles_n;
-                    p.item0 = static_cast<int>(total);
-                    total += tiles * p.splits;
-                    if (total > INT32_MAX) {
-                        ok = false;
-                        break;
-                    }
-                    p.items = static_cast<int>(tiles * p.splits);
-                    p.ws_off = c.ws_bytes;
-                    const int64_t part_rows = 2 * tiles * p.splits * BM;
-                    if (p.splits > 1 && (part_rows > INT32_MAX || total > MAX_ITEMS)) ok = false;
-                    p.ws_bytes = p.splits > 1 ? static_cast<size_t>(part_rows) * p.bn * 4 : 0;
-                    c.ws_bytes += p.ws_bytes;
+                    const ProductPlan& p = c.p[i];
                     for (int k = 0; k < p.splits; ++k) {
-                        work += item_us(p, k) * tiles;
+                        work += item_us(p, k) * (p.items / p.splits);
                         longest = std::max(longest, item_us(p, k));
                     }
                     tail += join_us(p, s[i].M, s[i].N);
                 }
-                if (!ok) continue;
-                c.n_items = static_cast<int>(total);
-                c.table = c.n_items <= MAX_ITEMS ? 1 : 0;
-                const int pairs = static_cast<int>(std::min<int64_t>(total, max_pairs));
-                c.grid = 2 * pairs;
+                const int pairs = c.grid / 2;
                 if (std::max(work / pairs, longest) + tail >= best) continue;
                 double t = tail;
                 if (c.table)
                     t += assign(c, pairs);
                 else
-                    t += std::ceil(static_cast<double>(total) / pairs) * longest;
+                    t += std::ceil(static_cast<double>(c.n_items) / pairs) * longest;
                 if (t < best) {
                     best = t;
-                    *out = c;
+                    found = ch;
                 }
             }
+    return found;
 }
 
-// Plans are pure functions of the shape and the device's resident pairs; the
-// search is remembered for the last shapes seen.
+// Choices and plans are pure functions of their keys, remembered for the last shapes
+// seen: the choice by shapes, SM count and overrides; the plan, whose items are
+// assigned by what the epilogues store, by that too. Both are made without a lock.
 struct Key {
-    Shape3 s[2];
-    int n, split, sms;
-    Forced force;
+    int64_t v[15];
 };
-constexpr int CACHE = 32;
-std::mutex g_plan_mutex;
-Key g_keys[CACHE];
-Plan g_plans[CACHE];
-int g_plan_count = 0, g_plan_next = 0;
 
-bool same_key(const Key& a, const Key& b) {
-    if (a.n != b.n || a.split != b.split || a.sms != b.sms || !(a.force == b.force)) return false;
-    for (int i = 0; i < a.n; ++i)
-        if (a.s[i].M != b.s[i].M || a.s[i].N != b.s[i].N || a.s[i].K != b.s[i].K || a.s[i].f32 != b.s[i].f32 ||
-            a.s[i].add != b.s[i].add)
-            return false;
-    return true;
+Key make_key(const Shape3* s, int n, bool may_split, const Forced& f, int num_sms) {
+    Key k{};
+    for (int i = 0; i < n; ++i) k.v[3 * i] = s[i].M, k.v[3 * i + 1] = s[i].N, k.v[3 * i + 2] = s[i].K;
+    k.v[6] = n, k.v[7] = may_split ? 1 : 0, k.v[8] = num_sms;
+    for (int i = 0; i < 2; ++i) k.v[9 + i] = f.bn[i], k.v[11 + i] = f.splits[i];
+    return k;
 }
 
-// Caller holds g_plan_mutex while it uses the result.
-const Plan& plan_for(const Shape3* s, int n, bool may_split, int num_sms) {
-    Key k{};
-    k.n = n;
-    k.split = may_split ? 1 : 0;
-    k.sms = num_sms;
-    k.force = forced_from_env();
-    for (int i = 0; i < n; ++i) k.s[i] = s[i];
-    for (int i = 0; i < g_plan_count; ++i)
-        if (same_key(g_keys[i], k)) return g_plans[i];
-    const int slot = g_plan_next;
-    g_plan_next = (g_plan_next + 1) % CACHE;
-    if (g_plan_count < CACHE) ++g_plan_count;
-    g_keys[slot] = k;
-    make_plan(s, n, may_split, k.force, num_sms, &g_plans[slot]);
-    Plan& pl = g_plans[slot];
-    if (pl.n_items == 0) make_plan(s, n, may_split, Forced{}, num_sms, &pl);
-    for (int i = 0; i < pl.n; ++i) pl.p[i].epi = epi_of(s[i].f32 != 0, s[i].add != 0);
-    if (pl.n_items > 0 && pl.table) assign(pl, pl.grid / 2);
-    return pl;
+// SETS sets (a power of two) of WAYS entries; the least recently used of a set goes.
+template <typename V, int SETS, int WAYS>
+struct Cache {
+    struct Entry {
+        Key key;
+        uint64_t used;  // 0: empty
+        V value;
+    };
+    Entry e[SETS][WAYS];
+    uint64_t clock;
+    std::mutex m;
+
+    Entry* set_of(const Key& k) {
+        uint64_t h = 1469598103934665603ull;
+        for (int64_t x : k.v) {
+            h = (h ^ static_cast<uint64_t>(x)) * 0x9E3779B97F4A7C15ull;
+            h ^= h >> 32;
+        }
+        return e[h & (SETS - 1)];
+    }
+    bool get(const Key& k, V* out) {
+        std::lock_guard<std::mutex> g(m);
+        Entry* s = set_of(k);
+        for (int i = 0; i < WAYS; ++i)
+            if (s[i].used && std::memcmp(&s[i].key, &k, sizeof(k)) == 0) {
+                s[i].used = ++clock;
+                *out = s[i].value;
+                return true;
+            }
+        return false;
+    }
+    void put(const Key& k, const V& v) {
+        std::lock_guard<std::mutex> g(m);
+        Entry* s = set_of(k);
+        int at = 0;
+        for (int i = 0; i < WAYS; ++i) {
+            if (s[i].used && std::memcmp(&s[i].key, &k, sizeof(k)) == 0) return;  // another thread was first
+            if (s[i].used < s[at].used) at = i;
+        }
+        s[at].key = k;
+        s[at].value = v;
+        s[at].used = ++clock;
+    }
+};
+Cache<Choice, 256, 8> g_choices;
+Cache<Plan, 32, 8> g_plans;
+std::atomic<long long> g_searches{0};
+
+Choice choice_for(const Shape3* s, int n, bool may_split, const Forced& force, int num_sms, const Key& k) {
+    Choice ch;
+    if (g_choices.get(k, &ch)) return ch;
+    ++g_searches;
+    ch = search(s, n, may_split, force, num_sms);
+    if (ch.bn[0] == 0) ch = search(s, n, may_split, Forced{}, num_sms);
+    g_choices.put(k, ch);
+    return ch;
+}
+
+// The plan of a launch in `out`; n_items == 0: none is possible.
+void plan_for(const Shape3* s, const Q8Product* products, int n, bool may_split, int num_sms, Plan* out) {
+    const Forced force = forced_from_env();
+    const Key k = make_key(s, n, may_split, force, num_sms);
+    Key with_types = k;
+    double epi[2] = {0.0, 0.0};
+    for (int i = 0; i < n; ++i) {
+        epi[i] = epi_of(products[i].dtype == MMBWD_F32, products[i].add != 0);
+        with_types.v[13 + i] = static_cast<int64_t>(epi[i] * 16.0);
+    }
+    if (g_plans.get(with_types, out)) return;
+    const Choice ch = choice_for(s, n, may_split, force, num_sms, k);
+    if (ch.bn[0] == 0 || !lay_out(s, n, ch, num_sms, out)) {
+        out->n_items = 0;
+        return;
+    }
+    for (int i = 0; i < n; ++i) out->p[i].epi = epi[i];
+    if (out->table) assign(*out, out->grid / 2);
+    g_plans.put(with_types, *out);
 }
 
 // ------------------------------------------------------------------ launch
@@ -851,21 +909,25 @@ cudaError_t launch_pair(const Plan& pl, const Q8Product* prod, uint8_t* ws, cuda
 
 size_t q8_products_workspace(const Q8Product* products, int n, int num_sms) {
     Shape3 s[2];
-    for (int i = 0; i < n; ++i) s[i] = {products[i].M, products[i].N, products[i].K, products[i].dtype == MMBWD_F32 ? 1 : 0, products[i].add};
-    std::lock_guard<std::mutex> g(g_plan_mutex);
-    return plan_for(s, n, true, num_sms).ws_bytes;
+    for (int i = 0; i < n; ++i) s[i] = {products[i].M, products[i].N, products[i].K};
+    const Forced force = forced_from_env();
+    const Choice ch = choice_for(s, n, true, force, num_sms, make_key(s, n, true, force, num_sms));
+    static thread_local Plan pl;
+    return ch.bn[0] != 0 && lay_out(s, n, ch, num_sms, &pl) ? pl.ws_bytes : 0;
 }
 
 cudaError_t q8_products_launch(const Q8Product* products, int n, bool may_split, void* ws, size_t ws_bytes, int num_sms,
                                cudaStream_t stream) {
     if (take_injected_launch_failure()) return cudaErrorLaunchFailure;
     Shape3 s[2];
-    for (int i = 0; i < n; ++i) s[i] = {products[i].M, products[i].N, products[i].K, products[i].dtype == MMBWD_F32 ? 1 : 0, products[i].add};
-    std::lock_guard<std::mutex> g(g_plan_mutex);
-    const Plan& pl = plan_for(s, n, may_split, num_sms);
+    for (int i = 0; i < n; ++i) s[i] = {products[i].M, products[i].N, products[i].K};
+    static thread_local Plan pl;
+    plan_for(s, products, n, may_split, num_sms, &pl);
     if (pl.n_items == 0 || pl.ws_bytes > ws_bytes) return cudaErrorInvalidValue;
     return launch_pair(pl, products, static_cast<uint8_t*>(ws), stream);
 }
+
+long long q8_plan_searches() { return g_searches.load(); }
 
 __global__ void q8_selftest_kernel(unsigned long long limit_ns) { q8::selftest_wait(g_q8_status, limit_ns); }
 

@@ -15,3 +15,35 @@ def built():
 def test_selftest_of_no_kernel_is_refused():
     assert mm.mmbwd_q8_selftest_wait_timeout(2, 1000) == mm.ERR_SHAPE
     assert mm.mmbwd_q8_selftest_wait_timeout(-1, 1000) == mm.ERR_SHAPE
+
+
+def test_shapes_in_rotation_are_planned_once():
+    """64 layer shapes, as a model with batches of changing length has: the second
+    time round no work split is searched for again, and the sizes are the same."""
+    shapes = [(1, 300 + 37 * i, C, OC) for i in range(16)
+              for C, OC in ((328, 520), (520, 328), (264, 1032), (1032, 264))]
+    before = mm.mmbwd_q8_debug_plan_searches()
+    first = [mm.mmbwd_q8_backward_workspace_bytes(*s) for s in shapes]
+    made = mm.mmbwd_q8_debug_plan_searches()
+    assert made > before
+    assert [mm.mmbwd_q8_backward_workspace_bytes(*s) for s in shapes] == first
+    assert mm.mmbwd_q8_debug_plan_searches() == made
+
+
+def test_queries_from_several_threads_agree():
+    import threading
+
+    shapes = [(1, 900 + 41 * i, 392, 520) for i in range(24)]
+    got = [None] * 4
+
+    def work(k):
+        order = shapes if k % 2 else shapes[::-1]
+        sizes = {s: mm.mmbwd_q8_backward_workspace_bytes(*s) for s in order * 2}
+        got[k] = [sizes[s] for s in shapes]
+
+    threads = [threading.Thread(target=work, args=(k,)) for k in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert got[0] is not None and all(g == got[0] for g in got)
