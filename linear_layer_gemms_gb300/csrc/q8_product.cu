@@ -604,6 +604,26 @@ double assign(Plan& pl, int pairs) {
     return m;
 }
 
+// The makespan where pairs take the items in turn (more items than the schedule
+// holds): pair c has those of c, c + pairs, ...
+double in_turn_us(const Plan& pl, int pairs) {
+    double m = 0.0;
+    for (int c = 0; c < pairs; ++c) {
+        auto before = [&](int w) { return w > c ? (w - c + pairs - 1) / pairs : 0; };  // of this pair's items
+        double t = 0.0;
+        for (int i = 0; i < pl.n; ++i) {
+            const ProductPlan& p = pl.p[i];
+            const int tiles = p.tiles_m * p.tiles_n;
+            for (int k = 0; k < p.splits; ++k) {
+                const int first = p.item0 + k * tiles;
+                t += (before(first + tiles) - before(first)) * item_us(p, k);
+            }
+        }
+        m = std::max(m, t);
+    }
+    return m;
+}
+
 struct Shape3 {
     int64_t M, N, K;
 };
@@ -631,8 +651,8 @@ Forced forced_from_env() {
 }
 
 // What a search finds: tile width and split count of each product; bn[0] == 0 where
-// no candidate is possible (an override that asks for more items than the
-// schedule holds).
+// no candidate is possible (an override that cuts a product into more items than
+// the schedule holds).
 struct Choice {
     int bn[2], splits[2];
 };
@@ -662,7 +682,7 @@ bool lay_out(const Shape3* s, int n, const Choice& ch, int num_sms, Plan* pl) {
         p.items = static_cast<int>(tiles * p.splits);
         p.ws_off = pl->ws_bytes;
         const int64_t part_rows = 2 * tiles * p.splits * BM;
-        if (p.splits > 1 && (part_rows > INT32_MAX || total > MAX_ITEMS)) return false;
+        if (p.splits > 1 && (part_rows > INT32_MAX || p.items > MAX_ITEMS)) return false;  // (bounds the workspace)
         p.ws_bytes = p.splits > 1 ? static_cast<size_t>(part_rows) * p.bn * 4 : 0;
         pl->ws_bytes += p.ws_bytes;
     }
@@ -709,11 +729,7 @@ Choice search(const Shape3* s, int n, bool may_split, const Forced& force, int n
                 }
                 const int pairs = c.grid / 2;
                 if (std::max(work / pairs, longest) + tail >= best) continue;
-                double t = tail;
-                if (c.table)
-                    t += assign(c, pairs);
-                else
-                    t += std::ceil(static_cast<double>(c.n_items) / pairs) * longest;
+                const double t = tail + (c.table ? assign(c, pairs) : in_turn_us(c, pairs));
                 if (t < best) {
                     best = t;
                     found = ch;

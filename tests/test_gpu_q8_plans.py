@@ -47,3 +47,47 @@ def test_types_and_accumulation_search_no_further_split():
         for add in range(4):
             layer.check(types, add)
     assert mm.mmbwd_q8_debug_plan_searches() == made
+
+
+@pytest.mark.parametrize("shape, splits", [((200, 8200, 26_000), None), ((200, 8200, 26_000), "1,1"),
+                                           ((200, 8200, 26_000), "2,1"), ((26_000, 8200, 200), "1,2")],
+                         ids=["planned", "unsplit", "dinp split", "dweight split"])
+def test_backward_of_more_items_than_the_table_holds(monkeypatch, shape, splits):
+    """Over 3000 tiles and splits, which the pairs take in turn: every element is
+    written, and sampled elements of every tile, the last ones among them, are right."""
+    import torch
+
+    if splits:
+        monkeypatch.setenv("MMBWD_Q8_SPLITS", splits)
+    T, C, OC = shape
+    g = torch.Generator(device="cuda")
+    g.manual_seed(6)
+
+    def operand(R, K, std):
+        x = (torch.randn(R, K, generator=g, device="cuda") * std).bfloat16()
+        row = (torch.empty(R, ref.ld(K), dtype=torch.uint8, device="cuda"),
+               torch.empty(mm.mmbwd_q8_scale_bytes(R, K), dtype=torch.uint8, device="cuda"))
+        col = (torch.empty(K, ref.ld(R), dtype=torch.uint8, device="cuda"),
+               torch.empty(mm.mmbwd_q8_scale_bytes(K, R), dtype=torch.uint8, device="cuda"))
+        assert mm.mmbwd_q8_quantize(*row, *col, None, x, None, 0, R, K, mm.BF16, mm.E4M3) == mm.OK
+        return x, row, col
+
+    d, d8, d8t = operand(T, OC, 1e-2)
+    x, _, i8t = operand(T, C, 1.0)
+    w, _, w8t = operand(OC, C, 0.02)
+    n = mm.mmbwd_q8_backward_workspace_bytes(1, T, C, OC)
+    ws = torch.full((max(n, 1),), 0xFF, dtype=torch.uint8, device="cuda")  # NaN where a partial sum is missed
+    dinp = torch.full((T, C), float("nan"), dtype=torch.bfloat16, device="cuda")
+    dw = torch.full((OC, C), float("nan"), device="cuda")
+    assert mm.mmbwd_q8_backward(dinp, dw, *d8, *d8t, *i8t, *w8t, ws, n, 1, T, C, OC, 0, 0, 0, mm.BF16, mm.F32, 0) == mm.OK
+    torch.cuda.synchronize()
+    assert torch.isfinite(dinp).all() and torch.isfinite(dw).all()
+
+    def some(size, step):  # spread over all 128-wide pieces, and the last two
+        return np.r_[np.arange(3, size - 2, step), size - 2, size - 1]
+
+    cols = some(C, 61)
+    for got, a, b, rows, dtype in ((dinp, host(d), host(w[:, cols]).T, some(T, 97), "bf16"),
+                                   (dw, host(d).T, host(x[:, cols]).T, some(OC, 97), "f32")):
+        want, tol = ref.product_bound(ref.quantize(a[rows], mm.E4M3)[2], ref.quantize(b, mm.E4M3)[2], dtype)
+        assert np.all(np.abs(host(got[rows][:, cols]) - want) <= tol)

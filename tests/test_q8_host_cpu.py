@@ -47,3 +47,19 @@ def test_queries_from_several_threads_agree():
     for t in threads:
         t.join()
     assert got[0] is not None and all(g == got[0] for g in got)
+
+
+@pytest.mark.parametrize("shape, splits", [((1, 16384, 8192, 2048), "1,2"), ((1, 2048, 8192, 16384), "2,1")],
+                         ids=["dweight", "dinp"])
+def test_a_forced_split_is_taken_whatever_the_other_products_items(monkeypatch, shape, splits):
+    """1024 items of the split product beside 4096 of the other, which comes after it
+    in one case and before it in the other."""
+    monkeypatch.setenv("MMBWD_Q8_TILE_N", "128,128")
+    monkeypatch.setenv("MMBWD_Q8_SPLITS", splits)
+    assert mm.mmbwd_q8_backward_workspace_bytes(*shape) == 1024 * 256 * 128 * 4
+
+
+def test_many_items_are_not_split_for_the_other_products_length():
+    """5120 tiles for 76 pairs: a product with four times the other's reduction has
+    enough of them unsplit."""
+    assert mm.mmbwd_q8_backward_workspace_bytes(1, 8192, 8192, 32768) == 0
