@@ -61,8 +61,10 @@
  * For tuning and tests the environment overrides the work split:
  * MMBWD_Q8_SPLITS = "<dinp>,<dweight>" (pieces of each product's reduction, 0: the
  * planner's choice) and MMBWD_Q8_TILE_N = "<dinp>,<dweight>" (tile widths, 128 or
- * 256) of the backward, MMBWD_Q8_TOKEN_SPLITS (1, 2, 4 or 8 CTAs to a tile) of the
- * forward for few tokens. The workspace size follows the first two.
+ * 256; 0: the planner's) of the backward, whether a call wants one output or both;
+ * the first width is the forward's too. MMBWD_Q8_TOKEN_SPLITS (1, 2, 4 or 8 CTAs to a
+ * tile) of the forward for few tokens. The workspace size follows the first two. An
+ * override that no work split can meet is dropped.
  */
 #ifndef Q8_LINEAR_H
 #define Q8_LINEAR_H

@@ -1068,6 +1068,7 @@ size_t mmbwd_q8_backward_workspace_bytes(int64_t B, int64_t T, int64_t C, int64_
     Q8Product p[2];
     p[0].M = s.BT, p[0].N = C, p[0].K = OC;
     p[1].M = OC, p[1].N = C, p[1].K = s.BT;
+    p[1].slot = 1;
     // both products, or one of them alone: whichever plan needs most
     const size_t most = std::max(q8_products_workspace(p, 2, sms),
                                  std::max(q8_products_workspace(p, 1, sms), q8_products_workspace(p + 1, 1, sms)));
@@ -1142,6 +1143,7 @@ int mmbwd_q8_backward(void* dinp, void* dweight, const void* dout_q, const void*
             p.M = OC, p.N = C, p.K = s.BT;
             p.a_format = dout_format, p.b_format = inp_format, p.dtype = dweight_dtype;
             p.add = (accumulate & MMBWD_Q8_ADD_DWEIGHT) ? 1 : 0;
+            p.slot = 1;
         }
     }
     if (e == cudaSuccess && n > 0)

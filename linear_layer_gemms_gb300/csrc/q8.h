@@ -40,6 +40,7 @@ struct Q8Product {
     int a_format = 0, b_format = 0;
     int dtype = 0;  // of D and bias
     int add = 0;    // add to the old D
+    int slot = 0;   // which value of an override is its: 0 the first (dinp, the forward), 1 the second (dweight)
 };
 
 // One or two products in one launch (their K ranges split where that fills the

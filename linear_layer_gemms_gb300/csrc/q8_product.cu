@@ -628,13 +628,14 @@ struct Shape3 {
     int64_t M, N, K;
 };
 
-// Overrides for tuning and tests: MMBWD_Q8_TILE_N and MMBWD_Q8_SPLITS = "<first
-// product>,<second product>" (dinp, dweight; 0: the planner's choice).
+// Overrides for tuning and tests: MMBWD_Q8_TILE_N and MMBWD_Q8_SPLITS = "<dinp>,<dweight>"
+// (0: the planner's choice; the forward's tile width is the first), here in the
+// order of a launch's products.
 struct Forced {
     int bn[2], splits[2];
 };
 
-Forced forced_from_env() {
+Forced forced_from_env(const Q8Product* products, int n) {
     Forced f{};
     if (const char* t = std::getenv("MMBWD_Q8_TILE_N")) {
         int a = 0, b = 0;
@@ -646,6 +647,10 @@ Forced forced_from_env() {
     if (const char* t = std::getenv("MMBWD_Q8_SPLITS")) {
         int a = 0, b = 0;
         if (std::sscanf(t, "%d,%d", &a, &b) == 2) f.splits[0] = std::max(0, std::min(a, 16)), f.splits[1] = std::max(0, std::min(b, 16));
+    }
+    if (n == 1) {
+        f.bn[0] = f.bn[products[0].slot], f.splits[0] = f.splits[products[0].slot];
+        f.bn[1] = f.splits[1] = 0;
     }
     return f;
 }
@@ -813,7 +818,7 @@ Choice choice_for(const Shape3* s, int n, bool may_split, const Forced& force, i
 
 // The plan of a launch in `out`; n_items == 0: none is possible.
 void plan_for(const Shape3* s, const Q8Product* products, int n, bool may_split, int num_sms, Plan* out) {
-    const Forced force = forced_from_env();
+    const Forced force = forced_from_env(products, n);
     const Key k = make_key(s, n, may_split, force, num_sms);
     Key with_types = k;
     double epi[2] = {0.0, 0.0};
@@ -926,7 +931,7 @@ cudaError_t launch_pair(const Plan& pl, const Q8Product* prod, uint8_t* ws, cuda
 size_t q8_products_workspace(const Q8Product* products, int n, int num_sms) {
     Shape3 s[2];
     for (int i = 0; i < n; ++i) s[i] = {products[i].M, products[i].N, products[i].K};
-    const Forced force = forced_from_env();
+    const Forced force = forced_from_env(products, n);
     const Choice ch = choice_for(s, n, true, force, num_sms, make_key(s, n, true, force, num_sms));
     static thread_local Plan pl;
     return ch.bn[0] != 0 && lay_out(s, n, ch, num_sms, &pl) ? pl.ws_bytes : 0;

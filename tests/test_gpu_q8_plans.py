@@ -91,3 +91,22 @@ def test_backward_of_more_items_than_the_table_holds(monkeypatch, shape, splits)
                                    (dw, host(d).T, host(x[:, cols]).T, some(OC, 97), "f32")):
         want, tol = ref.product_bound(ref.quantize(a[rows], mm.E4M3)[2], ref.quantize(b, mm.E4M3)[2], dtype)
         assert np.all(np.abs(host(got[rows][:, cols]) - want) <= tol)
+
+
+@pytest.mark.parametrize("splits", ["4,1", "1,4"])
+def test_one_output_takes_its_own_override(monkeypatch, splits):
+    """Each output alone has the bits of a call for both with the same overrides."""
+    import torch
+
+    monkeypatch.setenv("MMBWD_Q8_SPLITS", splits)
+    monkeypatch.setenv("MMBWD_Q8_TILE_N", "128,256")
+    layer = Layer(1400, 256, 2048)
+    (T, C, OC), got = layer.shape, []
+    for want in ((1, 1), (1, 0), (0, 1)):
+        dinp = torch.full((T, C), float("nan"), device="cuda") if want[0] else None
+        dw = torch.full((OC, C), float("nan"), device="cuda") if want[1] else None
+        assert layer.call(dinp, dw, ("f32", "f32"), 0) == mm.OK
+        got.append((dinp, dw))
+    torch.cuda.synchronize()
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[2][1])
+    layer.check()

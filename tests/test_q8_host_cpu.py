@@ -63,3 +63,15 @@ def test_many_items_are_not_split_for_the_other_products_length():
     """5120 tiles for 76 pairs: a product with four times the other's reduction has
     enough of them unsplit."""
     assert mm.mmbwd_q8_backward_workspace_bytes(1, 8192, 8192, 32768) == 0
+
+
+def test_an_override_of_dinp_leaves_dweight_alone(monkeypatch):
+    """The size covers dweight alone, which takes the second value: with only dinp
+    split, what is needed are dinp's partial tiles (6 tiles of 256 x 256 in 4 splits
+    of 16 blocks), not four times dweight's eight tiles."""
+    shape = (1, 1400, 256, 2048)
+    monkeypatch.setenv("MMBWD_Q8_TILE_N", "256,256")
+    monkeypatch.setenv("MMBWD_Q8_SPLITS", "4,1")
+    assert mm.mmbwd_q8_backward_workspace_bytes(*shape) == 6 * 4 * 256 * 256 * 4
+    monkeypatch.setenv("MMBWD_Q8_SPLITS", "1,4")  # (11 blocks of 128 tokens: 3, 3, 3, 2)
+    assert mm.mmbwd_q8_backward_workspace_bytes(*shape) == 8 * 4 * 256 * 256 * 4
