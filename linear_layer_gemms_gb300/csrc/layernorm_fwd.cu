@@ -93,6 +93,18 @@ __device__ __forceinline__ float team_sum(float s, float* slot, int which, int w
     }
 }
 
+// A row's mean from its sum. The product with the rounded 1 / C alone can miss the
+// quotient by a step, and a constant row would not give the bias; one correction by
+// the remainder, which a fused multiply-add forms exactly, makes the mean of an exact
+// sum exact: the remainder is (mean - q) C, and its product with 1 / C is mean - q to
+// one part in 2^23, far below the half step at which q + (mean - q) rounds to the mean.
+// (Quotients in their place: 8192 x 768 bf16 4.3 -> 4.8 us from L2, this: 4.3.) An
+// infinite sum has no remainder and stays as it is.
+__device__ __forceinline__ float mean_of(float sum, int C, float inv_c) {
+    const float q = sum * inv_c, rest = fmaf(-q, static_cast<float>(C), sum);
+    return rest == rest ? fmaf(rest, inv_c, q) : q;
+}
+
 // Teams of one warp share a block of four rows; larger teams are a block.
 template <int P>
 constexpr int TEAMS_PER_BLOCK = P == 1 ? 4 : 1;
@@ -102,7 +114,7 @@ constexpr int TEAMS_PER_BLOCK = P == 1 ? 4 : 1;
 template <typename T, int P, int VPT, bool AHEAD>
 __global__ void __launch_bounds__(32 * P * TEAMS_PER_BLOCK<P>)
     ln_fwd_kernel(T* out, float* mean_out, float* rstd_out, const T* inp, const T* __restrict__ weight,
-                  const T* __restrict__ bias, int64_t rows, int C, float eps) {
+                  const T* __restrict__ bias, int64_t rows, int C, float inv_c, float eps) {
     using V = Vec<T>;
     constexpr int N = V::N;
     constexpr int TEAMS = TEAMS_PER_BLOCK<P>;
@@ -110,7 +122,6 @@ __global__ void __launch_bounds__(32 * P * TEAMS_PER_BLOCK<P>)
     const int warp = static_cast<int>(threadIdx.x >> 5), lane = static_cast<int>(threadIdx.x & 31);
     const int team = warp / P, wt = warp % P, t = wt * 32 + lane;
     const int nvec = C / N;
-    const float inv_c = 1.f / static_cast<float>(C);
     const int64_t stride = static_cast<int64_t>(gridDim.x) * TEAMS;
     ptx::grid_launch_dependents();
     ptx::grid_dependency_wait();
@@ -134,7 +145,7 @@ __global__ void __launch_bounds__(32 * P * TEAMS_PER_BLOCK<P>)
         for (int j = 0; j < VPT; ++j)
 #pragma unroll
             for (int e = 0; e < N; ++e) s = V::plus(x[j], e, s);
-        const float mean = team_sum<P>(s, slots[team], 0, wt, team) * inv_c;
+        const float mean = mean_of(team_sum<P>(s, slots[team], 0, wt, team), C, inv_c);
         s = 0.f;
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
@@ -170,30 +181,31 @@ __global__ void __launch_bounds__(32 * P * TEAMS_PER_BLOCK<P>)
 }
 
 // Rows wider than a team of 32 warps holds: a block of 32 warps per row, read
-// three times.
+// three times, four vectors a thread in flight (100 x 131072 bf16 16.1 us; two: 25.3).
 template <typename T>
 __global__ void __launch_bounds__(1024) ln_fwd_wide_kernel(T* out, float* mean_out, float* rstd_out, const T* inp,
                                                            const T* __restrict__ weight, const T* __restrict__ bias,
-                                                           int64_t rows, int C, float eps) {
+                                                           int64_t rows, int C, float inv_c, float eps) {
     using V = Vec<T>;
     constexpr int N = V::N;
     __shared__ float slots[2 * 32];
     const int t = static_cast<int>(threadIdx.x), wt = t >> 5;
     const int nvec = C / N;
-    const float inv_c = 1.f / static_cast<float>(C);
     ptx::grid_launch_dependents();
     ptx::grid_dependency_wait();
     for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
         const uint4* xr = reinterpret_cast<const uint4*>(inp + r * C);
         float s = 0.f;
+#pragma unroll 4
         for (int v = t; v < nvec; v += 1024) {
             float f[N];
             V::get(xr[v], f);
 #pragma unroll
             for (int e = 0; e < N; ++e) s += f[e];
         }
-        const float mean = team_sum<32>(s, slots, 0, wt, 0) * inv_c;
+        const float mean = mean_of(team_sum<32>(s, slots, 0, wt, 0), C, inv_c);
         s = 0.f;
+#pragma unroll 4
         for (int v = t; v < nvec; v += 1024) {
             float f[N];
             V::get(xr[v], f);
@@ -202,6 +214,7 @@ __global__ void __launch_bounds__(1024) ln_fwd_wide_kernel(T* out, float* mean_o
         }
         const float var = team_sum<32>(s, slots, 1, wt, 0) * inv_c;
         const float rstd = 1.f / sqrtf(var + eps);
+#pragma unroll 4
         for (int v = t; v < nvec; v += 1024) {
             float f[N], w[N], b[N];
             V::get(xr[v], f);
@@ -219,7 +232,7 @@ __global__ void __launch_bounds__(1024) ln_fwd_wide_kernel(T* out, float* mean_o
 }
 
 template <typename T>
-using LnFwdKernel = void (*)(T*, float*, float*, const T*, const T*, const T*, int64_t, int, float);
+using LnFwdKernel = void (*)(T*, float*, float*, const T*, const T*, const T*, int64_t, int, float, float);
 
 template <typename T>
 struct Choice {
@@ -277,7 +290,8 @@ cudaError_t launch(T* out, float* mean, float* rstd, const T* inp, const T* weig
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, c.kernel, out, mean, rstd, inp, weight, bias, BT, C, eps);
+    const float inv_c = 1.f / static_cast<float>(C);
+    return cudaLaunchKernelEx(&cfg, c.kernel, out, mean, rstd, inp, weight, bias, BT, C, inv_c, eps);
 }
 
 }  // namespace
