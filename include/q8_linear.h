@@ -173,8 +173,8 @@ long long mmbwd_q8_debug_plan_searches(void);
 
 /* Self-test of the bounded waits: one thread waits as the product kernel (kernel 0) or
  * the few-tokens kernel (1) does, on a barrier that nothing completes, and gives up
- * after timeout_ns (0: the limit the kernels take). Synchronises the device; the
- * failure is then in the status word, for mmbwd_device_status to report and clear.
+ * after timeout_ns (0: the limit the kernels take), two seconds at most. Synchronises
+ * the device; the failure is then in the status word, for mmbwd_device_status to report and clear.
  * Returns a status of the launch (ERR_SHAPE: no such kernel). */
 int mmbwd_q8_selftest_wait_timeout(int kernel, uint64_t timeout_ns);
 

@@ -243,8 +243,8 @@ def mmbwd_q8_debug_plan_searches() -> int:
 
 def mmbwd_q8_selftest_wait_timeout(kernel: int, timeout_ns: int = 0) -> int:
     """Let a bounded wait of the product kernel (0) or the few-tokens kernel (1) run
-    out after timeout_ns (0: the limit the kernels take); the failure is then in
-    the device status word. Returns the status of the launch."""
+    out after timeout_ns (0: the limit the kernels take), two seconds at most; the
+    failure is then in the device status word. Returns the status of the launch."""
     return load().mmbwd_q8_selftest_wait_timeout(kernel, timeout_ns)
 
 

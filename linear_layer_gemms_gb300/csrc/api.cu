@@ -957,7 +957,8 @@ int mmbwd_q8_selftest_wait_timeout(int kernel, uint64_t timeout_ns) {
         const int rc = device_state(&d, &dev);
         if (rc != MMBWD_OK) return rc;
     }
-    const unsigned long long limit = timeout_ns ? timeout_ns : q8_wait_limit_ns();
+    // two seconds at most, whatever is asked for: the thread holds the GPU meanwhile
+    const unsigned long long asked = timeout_ns ? timeout_ns : q8_wait_limit_ns(), limit = std::min(asked, 2000000000ull);
     const cudaError_t e = kernel == 0 ? q8_selftest_wait(limit) : q8_tokens_selftest_wait(limit);
     return e == cudaSuccess && cudaDeviceSynchronize() == cudaSuccess ? MMBWD_OK : MMBWD_ERR_CUDA;
 }

@@ -48,6 +48,13 @@ def test_the_limit_is_the_one_of_the_environment(monkeypatch, kernel):
     assert mm.mmbwd_device_status() == (mm.ERR_DEVICE_TIMEOUT, [0, SELFTEST, 0])
 
 
+def test_the_selftest_ends_whatever_is_asked_for():
+    t0 = time.perf_counter()
+    assert mm.mmbwd_q8_selftest_wait_timeout(0, 1 << 62) == mm.OK
+    assert time.perf_counter() - t0 < 4
+    assert mm.mmbwd_device_status() == (mm.ERR_DEVICE_TIMEOUT, [0, SELFTEST, 0])
+
+
 @pytest.mark.parametrize("T", [300, 5], ids=["products", "few tokens"])
 def test_the_launch_before_does_not_count_against_the_forward(monkeypatch, T):
     """A launch that lets the forward begin early and stays ten times as long as a
