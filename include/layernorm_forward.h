@@ -1,16 +1,15 @@
 /*
  * layernorm_forward.h -- C ABI of the GPT-2 LayerNorm forward in the same
- * library (libmmbwd.so): `layernorm_forward_cpu` of llm.c's
- * dev/cuda/layernorm_backward.cu (offset 547), which caches
- * the row statistics that lnbwd_run (layernorm_backward.h) reads. For every
- * row of BT = B*T rows of width C
+ * library (libmmbwd.so), with the row statistics that lnbwd_run
+ * (layernorm_backward.h) reads. For every row of BT = B*T rows of width C
  *
  *     mean = (1/C) sum_i x_i,   var = (1/C) sum_i (x_i - mean)^2,
  *     rstd = 1 / sqrt(var + eps),
  *     out_i = (x_i - mean) * rstd * weight_i + bias_i
  *
  * Sums are formed in fp32 from the row held on chip (the variance from the
- * differences, not from the squares); out is rounded once. Rows are
+ * differences, not from the squares); the mean of a sum that is exact is exact, so
+ * that a row of one value gives the bias; out is rounded once. Rows are
  * independent and each row's sums run in a fixed order: repeated calls give
  * bitwise identical results.
  */

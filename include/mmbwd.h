@@ -105,7 +105,7 @@ extern "C" {
  * Synchronisation: asynchronous. The call validates, enqueues and returns; the
  * caller synchronises the stream before reading results. Invalid arguments
  * enqueue nothing and return a negative code. A kernel that gives up a bounded
- * wait records MMBWD_ERR_DEVICE_TIMEOUT in the device status word, read by
+ * wait (2 s, or MMBWD_WAIT_TIMEOUT_NS nanoseconds where the environment sets it) records MMBWD_ERR_DEVICE_TIMEOUT in the device status word, read by
  * mmbwd_device_status(); nothing in the library calls exit() or traps.
  *
  * Degenerate sizes: B*T == 0 sets dbias to 0 (the empty sum) and leaves dinp

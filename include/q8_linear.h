@@ -13,8 +13,9 @@
  *         (0 for a block without a nonzero finite value)
  *     q = x * 2^-s rounded once to the 8-bit format, to nearest even
  *
- * so no value saturates, and q * 2^s is exact in fp32 and in bf16. The scale
- * is a power of two: an 8-bit float keeps the same relative step at every
+ * so no value saturates, and q * 2^s is exact in fp32 (but for values that round up to
+ * 2^128, an infinity there) and, where s is at least -124 (E4M3) or -117 (E5M2), in bf16
+ * too: below that the least values fall under bf16's smallest. The scale is a power of two: an 8-bit float keeps the same relative step at every
  * scale, so a finer scale would only move the range's lower end by part of a
  * binade. An infinity or a NaN becomes the format's NaN (it does not enter amax).
  *
@@ -48,10 +49,12 @@
  * float atomics; every sum in an order fixed by shape and device).
  *
  * Every call enqueues on `stream` and returns MMBWD_OK or a negative
- * MMBWD_ERR_* code with nothing enqueued. The library keeps no state between
- * calls: what a call needs beyond its tensors is a workspace of the caller's,
- * so calls with their own workspaces may overlap on different streams or in
- * different captured graphs, from one thread or several.
+ * MMBWD_ERR_* code with nothing enqueued. No result depends on anything kept
+ * between calls (the library remembers how it split a shape's work): what a call
+ * needs beyond its tensors is a workspace of the caller's, so calls with their own
+ * workspaces may overlap on different streams or in different captured graphs, from
+ * one thread or several. The first call of a shape searches for the split on the host
+ * (0.2 to 1 ms for a backward); calls of other threads do not wait for it.
  *
  * The waits inside the product kernels are bounded: by MMBWD_WAIT_TIMEOUT_NS
  * nanoseconds each, read from the environment at every call (2 s where it is not set), as

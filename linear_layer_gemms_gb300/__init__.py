@@ -202,7 +202,8 @@ def mmbwd_q8_quantize(q, scale, qt, scale_t, colsum, x, workspace, workspace_byt
                       dtype: int, format: int, stream=None) -> int:
     """Enqueue x (rows x cols) into its row form (q, scale) and / or column form
     (qt, scale_t; either pair may be None), with the column sums in colsum
-    (None: not wanted; they need a workspace). Returns the C status code."""
+    (None: not wanted; above 1024 rows they need the workspace). Returns the C
+    status code."""
     return load().mmbwd_q8_quantize(_ptr(q), _ptr(scale), _ptr(qt), _ptr(scale_t), _ptr(colsum), _ptr(x),
                                     _ptr(workspace), workspace_bytes, rows, cols, dtype, format, _stream(stream))
 

@@ -279,9 +279,9 @@ const char* mmbwd_strerror(int code) {
     switch (code) {
         case MMBWD_OK: return "ok";
         case MMBWD_ERR_NULL: return "a required pointer is NULL";
-        case MMBWD_ERR_DTYPE: return "dtype must be MMBWD_F32 or MMBWD_BF16";
-        case MMBWD_ERR_SHAPE: return "a size is negative, too large, or a product overflows";
-        case MMBWD_ERR_ALIGN: return "pointers must be 16-byte aligned and C, OC times the element size multiples of 16 bytes";
+        case MMBWD_ERR_DTYPE: return "dtype must be MMBWD_F32 or MMBWD_BF16 (or an 8-bit format is neither MMBWD_E4M3 nor MMBWD_E5M2)";
+        case MMBWD_ERR_SHAPE: return "a size is negative, too large, or a product overflows; a workspace is too small; an option is out of range";
+        case MMBWD_ERR_ALIGN: return "pointers must be 16-byte aligned (workspaces 256) and rows multiples of 16 bytes (of 4 elements in the 8-bit products)";
         case MMBWD_ERR_ALIAS: return "an output overlaps an input or another output";
         case MMBWD_ERR_ALLOC: return "workspace allocation failed";
         case MMBWD_ERR_CUDA: return "a CUDA runtime call or kernel launch failed";

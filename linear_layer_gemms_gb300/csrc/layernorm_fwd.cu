@@ -1,5 +1,5 @@
-// LayerNorm forward (llm.c dev/cuda/layernorm_backward.cu, layernorm_forward_cpu):
-// per row mean, variance, rstd, and out = (x - mean) * rstd * weight + bias.
+// LayerNorm forward (include/layernorm_forward.h): per row mean, variance, rstd, and
+// out = (x - mean) * rstd * weight + bias.
 //
 // Bound by HBM: each row read once and written once. A team of P warps owns a
 // row and keeps it in registers (VPT 16-byte vectors per thread), so the

@@ -34,9 +34,10 @@
 // a cut product are fp32, in the caller's workspace, and a second kernel adds
 // them in split order, so no result depends on timing.
 //
-// Measured (device time): 8192 tokens 1600 -> 6400 57 us (2.95 PFLOP/s), 6400 -> 1600
-// 54 us (3.1), 768 -> 50304 246 us (2.6); backward of the first, both products, 111 us
-// (3.0). A k-block (128 of K) of a 256-wide tile takes 0.33 us, which is the round trip
+// Measured (device time in short runs, 2070 MHz): 8192 tokens 1600 -> 6400 59 us (2.9
+// PFLOP/s), 6400 -> 1600 54 us (3.1), 768 -> 50304 246 us (2.6); backward of the first, both
+// products, 111 us (3.0). Held for seconds the power cap takes a tenth: 65, 61 and 126 us
+// for the first, second and last. A k-block (128 of K) of a 256-wide tile takes 0.33 us, which is the round trip
 // of six 32 KB stages; a tile's hand-over about 0.5.
 //
 // Every wait is bounded (q8_wait_limit_ns): one that gives up records the failure in the

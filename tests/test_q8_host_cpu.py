@@ -75,3 +75,26 @@ def test_an_override_of_dinp_leaves_dweight_alone(monkeypatch):
     assert mm.mmbwd_q8_backward_workspace_bytes(*shape) == 6 * 4 * 256 * 256 * 4
     monkeypatch.setenv("MMBWD_Q8_SPLITS", "1,4")  # (11 blocks of 128 tokens: 3, 3, 3, 2)
     assert mm.mmbwd_q8_backward_workspace_bytes(*shape) == 8 * 4 * 256 * 256 * 4
+
+
+@pytest.mark.parametrize("fmt, least", [(mm.E4M3, -124), (mm.E5M2, -117)], ids=["e4m3", "e5m2"])
+def test_where_values_times_scales_are_exact(fmt, least):
+    """The header's ranges of s: fp32 holds every q 2^s that is under 2^128, bf16 those
+    from `least` on and not all below."""
+    import numpy as np
+    import torch
+
+    import q8_reference as ref
+
+    q = ref.decode(np.arange(256, dtype=np.uint8), fmt)
+    q = q[np.isfinite(q)]
+    for s in (-127, least, 0, 112, 120):
+        v = np.ldexp(q, s)
+        v = v[np.abs(v) < 2.0 ** 128]
+        np.testing.assert_array_equal(v.astype(np.float32).astype(np.float64), v)
+
+    def bf16_holds(s):
+        v = torch.from_numpy(np.ldexp(q, s))
+        return torch.equal(v.float().bfloat16().double(), v)
+
+    assert bf16_holds(least) and bf16_holds(0) and not bf16_holds(least - 1)
