@@ -377,22 +377,22 @@ def _library(s):
     kinds = {"bf16": mm.BF16, "f32": mm.F32}
     if op == "clip":
         if "list" not in s:
-            s["list"] = mm.gradclip_list([(g, None if case["in_place"] else o, n, kinds[dt]) for g, o, n, dt in s["pairs"]])
-        ws, n = room(lambda: mm.gradclip_workspace_bytes(s["list"]))
-        ok(mm.gradclip_run(s["norm"], s["list"], s["max_norm"], ws, n))
+            s["list"] = mm.grad_list([(g, None if case["in_place"] else o, n, kinds[dt]) for g, o, n, dt in s["pairs"]])
+        ws, n = room(lambda: mm.mmbwd_grad_workspace_bytes(s["list"]))
+        ok(mm.mmbwd_grad_clip(s["norm"], s["list"], s["max_norm"], ws, n))
         return {"norm": s["norm"], **{dt: s[dt + "_out"] for dt, _ in _parts(case)}}
     dt = kinds[case["dtype"]]
     if op in ("norm", "norm_backward"):
-        names = {"none": mm.RESNORM_NONE, "layer": mm.RESNORM_LAYER, "rms": mm.RESNORM_RMS}
+        names = {"none": mm.NORM_NONE, "layer": mm.NORM_LAYER, "rms": mm.NORM_RMS}
         post, norm = names[case["post"]], names[case["norm"]]
         B, T, C = case["B"], case["T"], case["C"]
         if op == "norm":
-            ok(mm.resnorm_forward(s["out"], s["residual_out"], s["mean_post"], s["rstd_post"], s["mean"], s["rstd"],
+            ok(mm.lnbwd_residual_forward(s["out"], s["residual_out"], s["mean_post"], s["rstd_post"], s["mean"], s["rstd"],
                                   s["x"], s["branch"], s["gate"], s["weight_post"], s["bias_post"], s["weight"],
                                   s["bias"], B, T, C, case["scale"], EPS, post, norm, dt))
             return {k: s[k] for k in ("out", "residual_out", "mean_post", "rstd_post", "mean", "rstd")}
-        ws, n = room(lambda: mm.resnorm_backward_workspace_bytes(B, T, C, dt))
-        ok(mm.resnorm_backward(s["dx"], s["dbranch"], s["dgate"], s["dweight_post"], s["dbias_post"], s["dweight"],
+        ws, n = room(lambda: mm.lnbwd_residual_backward_workspace_bytes(B, T, C, dt))
+        ok(mm.lnbwd_residual_backward(s["dx"], s["dbranch"], s["dgate"], s["dweight_post"], s["dbias_post"], s["dweight"],
                                s["dbias"], s["dout"], s["dresidual"], s["residual"], s["branch"], s["gate"],
                                s["weight_post"], s["bias_post"], s["weight"], s["mean_post"], s["rstd_post"], s["mean"],
                                s["rstd"], ws, n, B, T, C, case["scale"], post, norm, dt))
