@@ -13,9 +13,15 @@ first use instead of falling back to anything else.
 and the layer's forward, out = inp . weight^T + bias (mmbwd_forward); plus the
 LayerNorm forward and backward of a GPT-2 block (lnbwd_forward,
 include/layernorm_forward.h; lnbwd_run, include/layernorm_backward.h), the
-encoder backward (encbwd_run, include/encoder_backward.h), and the linear layer
+encoder backward (encbwd_run, include/encoder_backward.h), the linear layer
 in 8-bit floats with a scale per block of 128 (mmbwd_q8_quantize,
-mmbwd_q8_forward, mmbwd_q8_backward, include/q8_linear.h).
+mmbwd_q8_forward, mmbwd_q8_backward, include/q8_linear.h), and what stands around
+the layer in a block: an activation and a residual in its epilogue, with the
+gradients (mmbwd_forward_act, mmbwd_run_act, mmbwd_act_backward,
+include/linear_epilogue.h), the norms before and after a block with its gate and
+residual (lnbwd_residual_forward, lnbwd_residual_backward,
+include/residual_norm.h), and the gradients' global norm and clipping
+(mmbwd_grad_norm, mmbwd_grad_clip, mmbwd_grad_scale, include/grad_clip.h).
 
 Pointers may be given as integers or as objects with ``data_ptr()`` (for
 example torch tensors on the current CUDA device); ``stream`` is a raw
@@ -37,6 +43,9 @@ ERR_SCRATCH, ERR_MEMORY = -11, -12
 E4M3 = 0  # MMBWD_E4M3, MMBWD_E5M2: 8-bit formats
 E5M2 = 1
 Q8_BLOCK = 128
+ACT_NONE, ACT_GELU, ACT_SILU, ACT_RELU = 0, 1, 2, 3  # MMBWD_ACT_*
+NORM_NONE, NORM_LAYER, NORM_RMS = 0, 1, 2  # LNBWD_NORM_*
+RESIDUAL_MAX_C = 32768  # LNBWD_RESIDUAL_MAX_C
 Q8_ADD_DINP, Q8_ADD_DWEIGHT = 1, 2  # MMBWD_Q8_ADD_*: mmbwd_q8_backward's accumulate bits
 STATIC_SCRATCH_BYTES = 32 << 20  # MMBWD_STATIC_SCRATCH_BYTES
 
@@ -46,6 +55,15 @@ LIB_PATH = os.path.join(_HERE, "_build", "libmmbwd.so")
 # Names and C signatures of every entry point declared in include/*.h.
 _vp, _i64, _ci, _u64, _sz, _f32 = (ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_uint64,
                                    ctypes.c_size_t, ctypes.c_float)
+
+
+class Grad(ctypes.Structure):
+    """mmbwd_grad: one tensor of a list for the gradient norm (see grad_list)."""
+
+    _fields_ = [("grad", _vp), ("out", _vp), ("count", _i64), ("dtype", _i64)]
+
+
+_grads = ctypes.POINTER(Grad)
 SIGNATURES = {
     "mmbwd_run": ([_vp] * 6 + [_i64] * 4 + [_ci, _vp], _ci),
     "mmbwd_run_sr": ([_vp] * 6 + [_i64] * 4 + [_ci, _u64, _vp], _ci),
@@ -78,6 +96,17 @@ SIGNATURES = {
     "mmbwd_q8_forward": ([_vp] * 6 + [_i64] * 4 + [_ci] * 3 + [_vp], _ci),
     "mmbwd_q8_backward": ([_vp] * 11 + [_sz] + [_i64] * 4 + [_ci] * 6 + [_vp], _ci),
     "mmbwd_q8_backward_workspace_bytes": ([_i64] * 4, _sz),
+    "mmbwd_forward_act": ([_vp] * 6 + [_i64] * 4 + [_ci] * 2 + [_vp], _ci),
+    "mmbwd_run_act": ([_vp] * 8 + [_sz] + [_i64] * 4 + [_ci] * 2 + [_vp], _ci),
+    "mmbwd_run_act_workspace_bytes": ([_i64] * 4 + [_ci], _sz),
+    "mmbwd_act_backward": ([_vp] * 3 + [_i64] + [_ci] * 2 + [_vp], _ci),
+    "lnbwd_residual_forward": ([_vp] * 13 + [_i64] * 3 + [_f32] * 2 + [_ci] * 3 + [_vp], _ci),
+    "lnbwd_residual_backward": ([_vp] * 20 + [_sz] + [_i64] * 3 + [_f32] + [_ci] * 3 + [_vp], _ci),
+    "lnbwd_residual_backward_workspace_bytes": ([_i64] * 3 + [_ci], _sz),
+    "mmbwd_grad_norm": ([_vp, _grads, _ci, _vp, _sz, _vp], _ci),
+    "mmbwd_grad_clip": ([_vp, _grads, _ci, _f32, _vp, _sz, _vp], _ci),
+    "mmbwd_grad_scale": ([_grads, _ci, _vp, _f32, _vp], _ci),
+    "mmbwd_grad_workspace_bytes": ([_ci], _sz),
     "mmbwd_q8_debug_plan_searches": ([], ctypes.c_longlong),
     "mmbwd_q8_selftest_wait_timeout": ([_ci, _u64], _ci),
 }
@@ -247,6 +276,95 @@ def mmbwd_q8_selftest_wait_timeout(kernel: int, timeout_ns: int = 0) -> int:
     out after timeout_ns (0: the limit the kernels take), two seconds at most; the
     failure is then in the device status word. Returns the status of the launch."""
     return load().mmbwd_q8_selftest_wait_timeout(kernel, timeout_ns)
+
+
+def mmbwd_forward_act(out, pre, inp, weight, bias, residual, B: int, T: int, C: int, OC: int, act: int, dtype: int,
+                      stream=None) -> int:
+    """Enqueue out = act(inp . weight^T + bias) + residual, act being one of ACT_*,
+    and the argument of act into pre (None: not wanted); bias and residual may be
+    None, residual may be out. Returns the C status code."""
+    return load().mmbwd_forward_act(_ptr(out), _ptr(pre), _ptr(inp), _ptr(weight), _ptr(bias), _ptr(residual), B, T, C,
+                                    OC, act, dtype, _stream(stream))
+
+
+def mmbwd_run_act(dpre, dweight, dbias, dout, inp, weight, pre, workspace, workspace_bytes: int, B: int, T: int, C: int,
+                  OC: int, act: int, dtype: int, stream=None) -> int:
+    """Enqueue the backward of a layer whose inp is act(pre): dpre = (dout . weight) *
+    act'(pre) (overwritten; may be pre), dweight += dout^T . inp and dbias (None
+    skips it). Returns the C status code."""
+    return load().mmbwd_run_act(_ptr(dpre), _ptr(dweight), _ptr(dbias), _ptr(dout), _ptr(inp), _ptr(weight), _ptr(pre),
+                                _ptr(workspace), workspace_bytes, B, T, C, OC, act, dtype, _stream(stream))
+
+
+def mmbwd_run_act_workspace_bytes(B: int, T: int, C: int, OC: int, dtype: int) -> int:
+    return int(load().mmbwd_run_act_workspace_bytes(B, T, C, OC, dtype))
+
+
+def mmbwd_act_backward(dpre, dout, pre, n: int, act: int, dtype: int, stream=None) -> int:
+    """Enqueue dpre = dout * act'(pre) over n values; dpre may be dout or pre.
+    Returns the C status code."""
+    return load().mmbwd_act_backward(_ptr(dpre), _ptr(dout), _ptr(pre), n, act, dtype, _stream(stream))
+
+
+def lnbwd_residual_forward(out, residual_out, mean_post, rstd_post, mean, rstd, x, branch, gate, weight_post, bias_post,
+                           weight, bias, B: int, T: int, C: int, scale: float, eps: float, post: int, norm: int,
+                           dtype: int, stream=None) -> int:
+    """Enqueue residual_out = x + scale * gate * post(branch) and out =
+    norm(residual_out), post and norm being NORM_NONE, NORM_LAYER or NORM_RMS;
+    residual_out may be x. What a norm does not have, and what is not wanted, may be
+    None. Returns the C status code."""
+    return load().lnbwd_residual_forward(_ptr(out), _ptr(residual_out), _ptr(mean_post), _ptr(rstd_post), _ptr(mean),
+                                         _ptr(rstd), _ptr(x), _ptr(branch), _ptr(gate), _ptr(weight_post),
+                                         _ptr(bias_post), _ptr(weight), _ptr(bias), B, T, C, scale, eps, post, norm,
+                                         dtype, _stream(stream))
+
+
+def lnbwd_residual_backward(dx, dbranch, dgate, dweight_post, dbias_post, dweight, dbias, dout, dresidual, residual,
+                            branch, gate, weight_post, bias_post, weight, mean_post, rstd_post, mean, rstd, workspace,
+                            workspace_bytes: int, B: int, T: int, C: int, scale: float, post: int, norm: int, dtype: int,
+                            stream=None) -> int:
+    """Enqueue the gradients of lnbwd_residual_forward: dx and dbranch overwritten
+    (dx may be dresidual), those of the parameters added to. Returns the C status code."""
+    return load().lnbwd_residual_backward(_ptr(dx), _ptr(dbranch), _ptr(dgate), _ptr(dweight_post), _ptr(dbias_post),
+                                          _ptr(dweight), _ptr(dbias), _ptr(dout), _ptr(dresidual), _ptr(residual),
+                                          _ptr(branch), _ptr(gate), _ptr(weight_post), _ptr(bias_post), _ptr(weight),
+                                          _ptr(mean_post), _ptr(rstd_post), _ptr(mean), _ptr(rstd), _ptr(workspace),
+                                          workspace_bytes, B, T, C, scale, post, norm, dtype, _stream(stream))
+
+
+def lnbwd_residual_backward_workspace_bytes(B: int, T: int, C: int, dtype: int) -> int:
+    return int(load().lnbwd_residual_backward_workspace_bytes(B, T, C, dtype))
+
+
+def grad_list(tensors):
+    """The list that the gradient norm and clipping take: (grad, out, count, dtype)
+    for each tensor, out None or grad itself to clip in place. It holds addresses, so
+    it is good while the tensors are; a program makes it once and keeps it."""
+    return (Grad * len(tensors))(*[(_ptr(g), _ptr(o), n, t) for g, o, n, t in tensors])
+
+
+def mmbwd_grad_norm(norm, tensors, workspace, workspace_bytes: int, stream=None) -> int:
+    """Enqueue norm (one fp32 on the device) = the 2-norm over all tensors of a
+    grad_list. Returns the C status code."""
+    return load().mmbwd_grad_norm(_ptr(norm), tensors, len(tensors), _ptr(workspace), workspace_bytes, _stream(stream))
+
+
+def mmbwd_grad_clip(norm, tensors, max_norm: float, workspace, workspace_bytes: int, stream=None) -> int:
+    """Enqueue the norm and out = grad * min(1, max_norm / (norm + 1e-6)) for each
+    tensor of a grad_list. Returns the C status code."""
+    return load().mmbwd_grad_clip(_ptr(norm), tensors, len(tensors), max_norm, _ptr(workspace), workspace_bytes,
+                                  _stream(stream))
+
+
+def mmbwd_grad_scale(tensors, norm, max_norm: float, stream=None) -> int:
+    """The second half of mmbwd_grad_clip, with a norm that is already on the
+    device. Returns the C status code."""
+    return load().mmbwd_grad_scale(tensors, len(tensors), _ptr(norm), max_norm, _stream(stream))
+
+
+def mmbwd_grad_workspace_bytes(tensors) -> int:
+    """Bytes of workspace for a grad_list (or for a number of tensors)."""
+    return int(load().mmbwd_grad_workspace_bytes(tensors if isinstance(tensors, int) else len(tensors)))
 
 
 def encbwd_run(dwte, dwpe, dout, inp, B: int, T: int, C: int, V: int, dtype: int, stream=None) -> int:

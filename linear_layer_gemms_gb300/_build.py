@@ -19,8 +19,9 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libmmbwd.so")
 SOURCES = ["api.cu", "tc_gemm.cu", "simt_f32.cu", "layernorm_bwd.cu", "split_tf32.cu", "encoder_bwd.cu",
-           "layernorm_fwd.cu", "q8_quantize.cu", "q8_product.cu", "q8_tokens.cu"]
-HEADERS = ["internal.h", "ops.h", "ptx.cuh", "q8.h", "q8.cuh", "sr.cuh"]
+           "layernorm_fwd.cu", "q8_quantize.cu", "q8_product.cu", "q8_tokens.cu", "act_rows.cu", "residual_norm.cu",
+           "grad_clip.cu"]
+HEADERS = ["act.cuh", "internal.h", "ops.h", "ptx.cuh", "q8.h", "q8.cuh", "sr.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -38,7 +39,8 @@ def _cuda_lib_dir(nvcc: str) -> str:
 def _inputs():
     return ([os.path.join(CSRC, s) for s in SOURCES + HEADERS] +
             [os.path.join(ROOT, "include", h) for h in ("mmbwd.h", "layernorm_backward.h", "encoder_backward.h",
-                                                     "layernorm_forward.h", "q8_linear.h")] +
+                                                     "layernorm_forward.h", "q8_linear.h", "linear_epilogue.h",
+                                                     "residual_norm.h", "grad_clip.h")] +
             [os.path.abspath(__file__)])
 
 

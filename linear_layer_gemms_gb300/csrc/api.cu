@@ -6,6 +6,9 @@
 #include "../../include/encoder_backward.h"
 #include "../../include/layernorm_forward.h"
 #include "../../include/q8_linear.h"
+#include "../../include/linear_epilogue.h"
+#include "../../include/residual_norm.h"
+#include "../../include/grad_clip.h"
 #include "internal.h"
 #include "ops.h"
 #include "q8.h"
@@ -21,7 +24,9 @@
 #include <cstdio>
 #include <cstdlib>
 #include <cstring>
+#include <exception>
 #include <mutex>
+#include <vector>
 
 namespace mmbwd {
 
@@ -1150,6 +1155,377 @@ int mmbwd_q8_backward(void* dinp, void* dweight, const void* dout_q, const void*
     if (e == cudaSuccess && n > 0)
         e = q8_products_launch(prod, n, true, workspace, workspace_bytes, sms, stream);
     return e == cudaSuccess ? MMBWD_OK : MMBWD_ERR_CUDA;
+}
+
+// ---------------------------------------------------------------------------
+// Epilogues with an activation (linear_epilogue.h)
+
+namespace {
+
+bool act_ok(int act) { return act >= MMBWD_ACT_NONE && act <= MMBWD_ACT_RELU; }
+
+}  // namespace
+
+int mmbwd_forward_act(void* out, void* pre, const void* inp, const void* weight, const void* bias, const void* residual,
+                      int64_t B, int64_t T, int64_t C, int64_t OC, int act, int dtype, cudaStream_t stream) {
+    NvtxRange nvtx("mmbwd_forward_act");
+    Shape s;
+    int rc = check_shape(B, T, C, OC, dtype, &s);
+    if (rc != MMBWD_OK) return rc;
+    if (!act_ok(act) || (OC + 127) / 128 > 65535) return MMBWD_ERR_SHAPE;
+    const size_t b_out = static_cast<size_t>(s.n_dout) * s.es, b_inp = static_cast<size_t>(s.n_dinp) * s.es,
+                 b_w = static_cast<size_t>(s.n_dw) * s.es, b_col = static_cast<size_t>(OC) * s.es;
+    if ((b_out && !out) || (b_inp && !inp) || (b_w && !weight)) return MMBWD_ERR_NULL;
+    if ((static_cast<size_t>(C) * s.es) % 16 != 0 || b_col % 16 != 0) return MMBWD_ERR_ALIGN;
+    // in place: an element of the residual is read by the thread that writes it, before
+    const Arg args[6] = {{out, b_out, true},   {pre, b_out, true},   {inp, b_inp, false},
+                         {weight, b_w, false}, {bias, b_col, false}, {residual == out ? nullptr : residual, b_out, false}};
+    rc = check_args(args, 6);
+    if (rc != MMBWD_OK) return rc;
+
+    std::lock_guard<std::mutex> g(g_mutex);
+    DeviceState* d = nullptr;
+    rc = check_device(args, 6, &d);
+    if (rc != MMBWD_OK) return rc;
+    if (s.BT == 0 || OC == 0) return MMBWD_OK;
+    cudaError_t e = cudaSuccess;
+    if (C == 0)
+        e = act_rows_launch(out, pre, bias, residual, s.BT, OC, act, dtype, stream);
+    else if (dtype == MMBWD_F32)
+        e = simt_forward_act_launch(static_cast<float*>(out), static_cast<float*>(pre), static_cast<const float*>(inp),
+                                    static_cast<const float*>(weight), static_cast<const float*>(bias),
+                                    static_cast<const float*>(residual), s.BT, C, OC, act, stream);
+    else
+        e = tc_launch_forward_act(cached_plan(s.BT, C, OC, d->num_sms, 1), out, pre, inp, weight, bias, residual, s.BT,
+                                  C, OC, act, stream);
+    return e == cudaSuccess ? MMBWD_OK : MMBWD_ERR_CUDA;
+}
+
+size_t mmbwd_run_act_workspace_bytes(int64_t B, int64_t T, int64_t C, int64_t OC, int dtype) {
+    return mmbwd_workspace_bytes(B, T, C, OC, dtype);  // the same plans
+}
+
+int mmbwd_run_act(void* dpre, void* dweight, void* dbias, const void* dout, const void* inp, const void* weight,
+                  const void* pre, void* workspace, size_t workspace_bytes, int64_t B, int64_t T, int64_t C, int64_t OC,
+                  int act, int dtype, cudaStream_t stream) {
+    NvtxRange nvtx("mmbwd_run_act");
+    Shape s;
+    int rc = check_shape(B, T, C, OC, dtype, &s);
+    if (rc != MMBWD_OK) return rc;
+    if (!act_ok(act)) return MMBWD_ERR_SHAPE;
+    const size_t b_inp = static_cast<size_t>(s.n_dinp) * s.es, b_w = static_cast<size_t>(s.n_dw) * s.es,
+                 b_col = static_cast<size_t>(OC) * s.es, b_dout = static_cast<size_t>(s.n_dout) * s.es;
+    if ((b_inp && (!dpre || !inp || !pre)) || (b_w && (!dweight || !weight)) || (b_dout && !dout)) return MMBWD_ERR_NULL;
+    if ((static_cast<size_t>(C) * s.es) % 16 != 0 || b_col % 16 != 0) return MMBWD_ERR_ALIGN;
+    if (reinterpret_cast<uintptr_t>(workspace) & 255u) return MMBWD_ERR_ALIGN;
+
+    std::lock_guard<std::mutex> g(g_mutex);
+    // The plan ahead of the other checks, so that the workspace that it needs takes
+    // part in them; without a usable device, the plan of a full GB300.
+    DeviceState* d = nullptr;
+    int dev = 0;
+    const int no_device = device_state(&d, &dev);
+    const bool product = s.BT != 0 && C != 0 && OC != 0;
+    const TcPlan* plan = nullptr;
+    if (product && dtype == MMBWD_BF16) plan = &cached_plan(s.BT, C, OC, no_device == MMBWD_OK ? d->num_sms : 152);
+    const size_t need = plan ? plan->ws_bytes() : 0;
+    if (need && !workspace) return MMBWD_ERR_NULL;
+    if (need > workspace_bytes) return MMBWD_ERR_SHAPE;
+    // in place: an element of pre is read by the thread that writes dpre there, before
+    const Arg args[8] = {{dpre, b_inp, true},   {dweight, b_w, true}, {dbias, b_col, true},
+                         {dout, b_dout, false}, {inp, b_inp, false},  {weight, b_w, false},
+                         {pre == dpre ? nullptr : pre, b_inp, false}, {need ? workspace : nullptr, need, true}};
+    rc = check_args(args, 8);
+    if (rc != MMBWD_OK) return rc;
+    if (no_device != MMBWD_OK) return no_device;
+    rc = check_device(args, 8, &d);
+    if (rc != MMBWD_OK) return rc;
+
+    cudaError_t e = cudaSuccess;
+    if (OC == 0 || s.BT == 0) {  // empty sums
+        if (b_inp) e = cudaMemsetAsync(dpre, 0, b_inp, stream);
+        if (e == cudaSuccess && dbias && b_col) e = cudaMemsetAsync(dbias, 0, b_col, stream);
+    } else if (C == 0) {
+        if (dbias) e = colsum_launch(dbias, dout, s.BT, OC, dtype, false, 0, stream);
+    } else if (dtype == MMBWD_F32) {
+        e = simt_run_act_launch(static_cast<float*>(dpre), static_cast<float*>(dweight), static_cast<float*>(dbias),
+                                static_cast<const float*>(dout), static_cast<const float*>(inp),
+                                static_cast<const float*>(weight), static_cast<const float*>(pre), s.BT, C, OC, act, stream);
+    } else {
+        e = tc_launch(*plan, dpre, dweight, dbias, dout, inp, weight, s.BT, C, OC, workspace, stream, false, 0, pre, act);
+    }
+    return e == cudaSuccess ? MMBWD_OK : MMBWD_ERR_CUDA;
+}
+
+int mmbwd_act_backward(void* dpre, const void* dout, const void* pre, int64_t n, int act, int dtype,
+                       cudaStream_t stream) {
+    NvtxRange nvtx("mmbwd_act_backward");
+    if (dtype != MMBWD_F32 && dtype != MMBWD_BF16) return MMBWD_ERR_DTYPE;
+    if (!act_ok(act) || n < 0 || n > (int64_t(1) << 42)) return MMBWD_ERR_SHAPE;
+    if (n && (!dpre || !dout || !pre)) return MMBWD_ERR_NULL;
+    const size_t bytes = static_cast<size_t>(n) * (dtype == MMBWD_F32 ? 4 : 2);
+    const Arg args[3] = {{dpre, bytes, true},
+                         {dout == dpre ? nullptr : dout, bytes, false},
+                         {pre == dpre ? nullptr : pre, bytes, false}};
+    int rc = check_args(args, 3);
+    if (rc != MMBWD_OK) return rc;
+    std::lock_guard<std::mutex> g(g_mutex);
+    DeviceState* d = nullptr;
+    rc = check_device(args, 3, &d);
+    if (rc != MMBWD_OK || n == 0) return rc;
+    return act_backward_launch(dpre, dout, pre, n, act, dtype, stream) == cudaSuccess ? MMBWD_OK : MMBWD_ERR_CUDA;
+}
+
+// ---------------------------------------------------------------------------
+// Norms around a block (residual_norm.h)
+
+namespace {
+
+bool norm_ok(int kind) { return kind >= LNBWD_NORM_NONE && kind <= LNBWD_NORM_RMS; }
+
+// Sizes, options and the row's alignment, which both directions share.
+int residual_check(int64_t B, int64_t T, int64_t C, float scale, int post, int norm, int dtype, LnShape* s) {
+    const int rc = ln_check_shape(B, T, C, dtype, s);
+    if (rc != MMBWD_OK) return rc;
+    if (C > LNBWD_RESIDUAL_MAX_C || !std::isfinite(scale) || !norm_ok(post) || !norm_ok(norm)) return MMBWD_ERR_SHAPE;
+    return (static_cast<size_t>(C) * s->es) % 16 != 0 ? MMBWD_ERR_ALIGN : MMBWD_OK;
+}
+
+// check_args, with statistics (4-byte alignment) among the tensors.
+int check_args_and_stats(const Arg* a, int n, const Arg* stats, int n_stats) {
+    const int rc = check_args(a, n);
+    if (rc != MMBWD_OK) return rc;
+    for (int i = 0; i < n_stats; ++i)
+        if (reinterpret_cast<uintptr_t>(stats[i].p) & 3u) return MMBWD_ERR_ALIGN;
+    auto clash = [](const Arg& x, const Arg& y) { return (x.out || y.out) && overlaps(x.p, x.n, y.p, y.n); };
+    for (int i = 0; i < n_stats; ++i) {
+        for (int j = 0; j < n; ++j)
+            if (clash(stats[i], a[j])) return MMBWD_ERR_ALIAS;
+        for (int j = i + 1; j < n_stats; ++j)
+            if (clash(stats[i], stats[j])) return MMBWD_ERR_ALIAS;
+    }
+    return MMBWD_OK;
+}
+
+}  // namespace
+
+int lnbwd_residual_forward(void* out, void* residual_out, float* mean_post, float* rstd_post, float* mean, float* rstd,
+                           const void* x, const void* branch, const void* gate, const void* weight_post,
+                           const void* bias_post, const void* weight, const void* bias, int64_t B, int64_t T, int64_t C,
+                           float scale, float eps, int post, int norm, int dtype, cudaStream_t stream) {
+    NvtxRange nvtx("lnbwd_residual_forward");
+    LnShape s;
+    int rc = residual_check(B, T, C, scale, post, norm, dtype, &s);
+    if (rc != MMBWD_OK) return rc;
+    if (!(eps >= 0.f) || std::isinf(eps)) return MMBWD_ERR_SHAPE;
+    const size_t b_rows = static_cast<size_t>(s.n) * s.es, b_col = static_cast<size_t>(C) * s.es,
+                 b_stat = C > 0 ? static_cast<size_t>(s.BT) * 4 : 0;
+    const bool has_norm = norm != LNBWD_NORM_NONE, has_post = post != LNBWD_NORM_NONE;
+    const bool layer = norm == LNBWD_NORM_LAYER, layer_post = post == LNBWD_NORM_LAYER;
+    ResidualNorm a;  // (what the norms do not have: null)
+    a.out = has_norm ? out : nullptr;
+    a.residual_out = residual_out, a.x = x, a.branch = branch, a.gate = gate;
+    a.mean_post = layer_post ? mean_post : nullptr, a.rstd_post = has_post ? rstd_post : nullptr;
+    a.mean = layer ? mean : nullptr, a.rstd = has_norm ? rstd : nullptr;
+    a.weight_post = has_post ? weight_post : nullptr, a.bias_post = layer_post ? bias_post : nullptr;
+    a.weight = has_norm ? weight : nullptr, a.bias = layer ? bias : nullptr;
+    a.rows = s.BT, a.C = static_cast<int>(C), a.scale = scale, a.eps = eps, a.post = post, a.norm = norm;
+    if (b_rows && (!residual_out || !x || !branch || (has_norm && (!out || !weight)) || (has_post && !weight_post)))
+        return MMBWD_ERR_NULL;
+    // in place: a row of x is read whole, by the threads that write it, before any of it is written
+    const Arg args[13] = {{a.out, b_rows, true},       {residual_out, b_rows, true}, {x == residual_out ? nullptr : x, b_rows, false},
+                          {branch, b_rows, false},     {gate, b_col, false},         {a.weight_post, b_col, false},
+                          {a.bias_post, b_col, false}, {a.weight, b_col, false},     {a.bias, b_col, false},
+                          {a.mean_post, b_stat, true}, {a.rstd_post, b_stat, true},  {a.mean, b_stat, true},
+                          {a.rstd, b_stat, true}};
+    rc = check_args_and_stats(args, 9, args + 9, 4);
+    if (rc != MMBWD_OK) return rc;
+    std::lock_guard<std::mutex> g(g_mutex);
+    DeviceState* d = nullptr;
+    rc = check_device(args, 13, &d);
+    if (rc != MMBWD_OK || s.BT == 0 || C == 0) return rc;
+    int sms = 0;
+    rc = ln_num_sms(&sms);
+    if (rc != MMBWD_OK) return rc;
+    return residual_forward_launch(a, dtype, sms, stream) == cudaSuccess ? MMBWD_OK : MMBWD_ERR_CUDA;
+}
+
+size_t lnbwd_residual_backward_workspace_bytes(int64_t B, int64_t T, int64_t C, int dtype) {
+    LnShape s;
+    if (residual_check(B, T, C, 1.f, 0, 0, dtype, &s) != MMBWD_OK || s.BT == 0 || C == 0) return 0;
+    return residual_backward_workspace(s.BT, C, dtype);
+}
+
+int lnbwd_residual_backward(void* dx, void* dbranch, void* dgate, void* dweight_post, void* dbias_post, void* dweight,
+                            void* dbias, const void* dout, const void* dresidual, const void* residual,
+                            const void* branch, const void* gate, const void* weight_post, const void* bias_post,
+                            const void* weight, const float* mean_post, const float* rstd_post, const float* mean,
+                            const float* rstd, void* workspace, size_t workspace_bytes, int64_t B, int64_t T, int64_t C,
+                            float scale, int post, int norm, int dtype, cudaStream_t stream) {
+    NvtxRange nvtx("lnbwd_residual_backward");
+    LnShape s;
+    int rc = residual_check(B, T, C, scale, post, norm, dtype, &s);
+    if (rc != MMBWD_OK) return rc;
+    const size_t b_rows = static_cast<size_t>(s.n) * s.es, b_col = static_cast<size_t>(C) * s.es,
+                 b_stat = C > 0 ? static_cast<size_t>(s.BT) * 4 : 0;
+    const bool has_norm = norm != LNBWD_NORM_NONE, has_post = post != LNBWD_NORM_NONE;
+    const bool layer = norm == LNBWD_NORM_LAYER, layer_post = post == LNBWD_NORM_LAYER;
+    ResidualNorm a;  // (what the norms do not have, and what no wanted gradient needs: null)
+    a.dx = dx, a.dbranch = dbranch, a.gate = gate, a.dresidual = dresidual;
+    a.dgate = gate ? dgate : nullptr;
+    a.dweight_post = has_post ? dweight_post : nullptr, a.dbias_post = layer_post ? dbias_post : nullptr;
+    a.dweight = has_norm ? dweight : nullptr, a.dbias = layer ? dbias : nullptr;
+    a.dout = has_norm ? dout : nullptr, a.residual = has_norm ? residual : nullptr;
+    const bool need_branch = a.dgate || (has_post && (dbranch || dweight_post));
+    a.branch = need_branch ? branch : nullptr;
+    a.weight_post = has_post ? weight_post : nullptr;
+    a.bias_post = layer_post && a.dgate ? bias_post : nullptr;
+    a.weight = has_norm ? weight : nullptr;
+    a.mean_post = need_branch && layer_post ? const_cast<float*>(mean_post) : nullptr;
+    a.rstd_post = need_branch && has_post ? const_cast<float*>(rstd_post) : nullptr;
+    a.mean = layer ? const_cast<float*>(mean) : nullptr;
+    a.rstd = has_norm ? const_cast<float*>(rstd) : nullptr;
+    a.rows = s.BT, a.C = static_cast<int>(C), a.scale = scale, a.post = post, a.norm = norm;
+    if (b_rows) {
+        if (!dx || (has_norm ? !dout || !residual || !weight || !rstd || (layer && !mean) : !dresidual)) return MMBWD_ERR_NULL;
+        if (has_post && !weight_post) return MMBWD_ERR_NULL;
+        if (need_branch && (!branch || (has_post && !rstd_post) || (layer_post && !mean_post))) return MMBWD_ERR_NULL;
+    }
+    const size_t need = b_rows ? residual_backward_workspace(s.BT, C, dtype) : 0;
+    if (need && !workspace) return MMBWD_ERR_NULL;
+    if (need > workspace_bytes) return MMBWD_ERR_SHAPE;
+    if (reinterpret_cast<uintptr_t>(workspace) & 255u) return MMBWD_ERR_ALIGN;
+    a.ws = static_cast<float*>(workspace);
+    const Arg args[20] = {{dx, b_rows, true},
+                          {dbranch, b_rows, true},
+                          {a.dgate, b_col, true},
+                          {a.dweight_post, b_col, true},
+                          {a.dbias_post, b_col, true},
+                          {a.dweight, b_col, true},
+                          {a.dbias, b_col, true},
+                          {need ? workspace : nullptr, need, true},
+                          {a.dout, b_rows, false},
+                          // in place: read by the thread that writes dx there, before
+                          {dresidual == dx ? nullptr : dresidual, b_rows, false},
+                          {a.residual, b_rows, false},
+                          {a.branch, b_rows, false},
+                          {gate, b_col, false},
+                          {a.weight_post, b_col, false},
+                          {a.bias_post, b_col, false},
+                          {a.weight, b_col, false},
+                          {a.mean_post, b_stat, false},
+                          {a.rstd_post, b_stat, false},
+                          {a.mean, b_stat, false},
+                          {a.rstd, b_stat, false}};
+    rc = check_args_and_stats(args, 16, args + 16, 4);
+    if (rc != MMBWD_OK) return rc;
+    std::lock_guard<std::mutex> g(g_mutex);
+    DeviceState* d = nullptr;
+    rc = check_device(args, 20, &d);
+    if (rc != MMBWD_OK || s.BT == 0 || C == 0) return rc;
+    int sms = 0;
+    rc = ln_num_sms(&sms);
+    if (rc != MMBWD_OK) return rc;
+    return residual_backward_launch(a, dtype, sms, stream) == cudaSuccess ? MMBWD_OK : MMBWD_ERR_CUDA;
+}
+
+// ---------------------------------------------------------------------------
+// Gradient norm and clipping (grad_clip.h)
+
+namespace {
+
+// Whether a written range overlaps another range. Sorts `a` by address.
+bool ranges_clash(std::vector<Arg>& a) {
+    auto before = [](const Arg& x, const Arg& y) { return x.p < y.p; };
+    if (!std::is_sorted(a.begin(), a.end(), before)) std::sort(a.begin(), a.end(), before);
+    uintptr_t end_any = 0, end_out = 0;
+    for (const Arg& x : a) {
+        const uintptr_t p = reinterpret_cast<uintptr_t>(x.p), end = p + x.n;
+        if (p < (x.out ? end_any : end_out)) return true;
+        end_any = std::max(end_any, end);
+        if (x.out) end_out = std::max(end_out, end);
+    }
+    return false;
+}
+
+// The three entry points: the norm into `norm` unless one is `given`, the outs if `scale`.
+int grad_call(float* norm, const float* given, const mmbwd_grad* list, int n, bool scale, float max_norm,
+              void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+    if (n < 0 || (scale && (!(max_norm >= 0.f) || std::isinf(max_norm)))) return MMBWD_ERR_SHAPE;
+    if ((n && !list) || (!norm && !given)) return MMBWD_ERR_NULL;
+    const float* scalar = given ? given : norm;
+    if (reinterpret_cast<uintptr_t>(scalar) & 3u) return MMBWD_ERR_ALIGN;
+    const size_t need = given ? 0 : mmbwd_grad_workspace_bytes(n);
+    if (need && !workspace) return MMBWD_ERR_NULL;
+    if (need > workspace_bytes) return MMBWD_ERR_SHAPE;
+    if (need && (reinterpret_cast<uintptr_t>(workspace) & 255u)) return MMBWD_ERR_ALIGN;
+    std::vector<GradTensor> tensors;
+    std::vector<Arg> args;
+    tensors.reserve(static_cast<size_t>(n));
+    args.reserve(2 * static_cast<size_t>(n) + 2);
+    args.push_back({scalar, 4, !given});
+    if (need) args.push_back({workspace, need, true});
+    for (int i = 0; i < n; ++i) {
+        const mmbwd_grad& t = list[i];
+        if (t.dtype != MMBWD_F32 && t.dtype != MMBWD_BF16) return MMBWD_ERR_DTYPE;
+        if (t.count < 0 || t.count > (int64_t(1) << 42)) return MMBWD_ERR_SHAPE;
+        if (t.count == 0) continue;
+        if (!t.grad) return MMBWD_ERR_NULL;
+        const uintptr_t es = t.dtype == MMBWD_F32 ? 4 : 2;
+        void* out = t.out && scale ? t.out : t.grad;
+        if ((reinterpret_cast<uintptr_t>(t.grad) | reinterpret_cast<uintptr_t>(out)) & (es - 1)) return MMBWD_ERR_ALIGN;
+        const size_t bytes = static_cast<size_t>(t.count) * es;
+        tensors.push_back({t.grad, out, t.count, t.dtype == MMBWD_BF16});
+        args.push_back({out, bytes, scale});
+        if (out != t.grad) args.push_back({t.grad, bytes, false});
+    }
+    if (ranges_clash(args)) return MMBWD_ERR_ALIAS;
+    std::lock_guard<std::mutex> g(g_mutex);
+    DeviceState* d = nullptr;
+    int rc = check_device(args.data(), static_cast<int>(args.size()), &d);
+    if (rc != MMBWD_OK) return rc;
+    int sms = 0;
+    rc = ln_num_sms(&sms);
+    if (rc != MMBWD_OK) return rc;
+    const cudaError_t e = grad_launch(tensors.data(), static_cast<int>(tensors.size()), norm, given, scale, max_norm,
+                                      static_cast<double*>(workspace), sms, stream);
+    return e == cudaSuccess ? MMBWD_OK : MMBWD_ERR_CUDA;
+}
+
+// The vectors' memory may run out; no exception leaves a C entry point.
+int grad_call_c(float* norm, const float* given, const mmbwd_grad* list, int n, bool scale, float max_norm,
+                void* workspace, size_t workspace_bytes, cudaStream_t stream) noexcept {
+    try {
+        return grad_call(norm, given, list, n, scale, max_norm, workspace, workspace_bytes, stream);
+    } catch (const std::exception&) {
+        return MMBWD_ERR_ALLOC;
+    }
+}
+
+}  // namespace
+
+size_t mmbwd_grad_workspace_bytes(int n) {
+    if (n < 0) return 0;
+    const size_t tables = std::max<size_t>(1, (static_cast<size_t>(n) + GRAD_TABLE - 1) / GRAD_TABLE);
+    return tables * GRAD_MAX_BLOCKS * sizeof(double);
+}
+
+int mmbwd_grad_norm(float* norm, const mmbwd_grad* list, int n, void* workspace, size_t workspace_bytes,
+                    cudaStream_t stream) {
+    NvtxRange nvtx("mmbwd_grad_norm");
+    return grad_call_c(norm, nullptr, list, n, false, 0.f, workspace, workspace_bytes, stream);
+}
+
+int mmbwd_grad_clip(float* norm, const mmbwd_grad* list, int n, float max_norm, void* workspace, size_t workspace_bytes,
+                    cudaStream_t stream) {
+    NvtxRange nvtx("mmbwd_grad_clip");
+    return grad_call_c(norm, nullptr, list, n, true, max_norm, workspace, workspace_bytes, stream);
+}
+
+int mmbwd_grad_scale(const mmbwd_grad* list, int n, const float* norm, float max_norm, cudaStream_t stream) {
+    NvtxRange nvtx("mmbwd_grad_scale");
+    if (!norm) return MMBWD_ERR_NULL;
+    return grad_call_c(nullptr, norm, list, n, true, max_norm, nullptr, 0, stream);
 }
 
 }  // extern "C"

@@ -1,0 +1,323 @@
+// The global gradient norm over many tensors and clipping (include/grad_clip.h).
+//
+// Bound by HBM: the norm reads every value once, clipping reads and writes it once
+// more. The list travels in the kernel parameters (up to 1024 tensors a launch), cut
+// into chunks of 32 KB that blocks take in contiguous runs. A thread sums the squares
+// of its (at most 64) values of a chunk in fp32, four sums side by side, and adds that
+// to its 64-bit sum; one 64-bit partial per block, joined in block order by whoever
+// needs the norm, so no float atomics and the same bits on every call.
+#include "../../include/grad_clip.h"
+#include "ops.h"
+#include "ptx.cuh"
+
+#include <cuda_bf16.h>
+
+#include <algorithm>
+#include <cfloat>
+#include <cstdint>
+
+namespace mmbwd {
+namespace {
+
+constexpr int THREADS = 256;
+constexpr int VECS = 8;                                  // 16-byte vectors of a chunk to a thread
+constexpr int CHUNK_BYTES = THREADS * VECS * 16;
+
+// The tensors of a launch: tensor t has the chunks first[t] .. first[t + 1).
+template <int N>
+struct Table {
+    void* grad[N];
+    void* out[N];
+    int64_t count[N];  // values, times 2, plus 1 for bf16
+    int first[N + 1];
+    int n;
+};
+
+struct Values {  // what a chunk covers: `vecs` vectors from `base`, and loose values before and after them
+    int64_t base, vecs, head, tail;
+};
+
+// Chunk k of a tensor: its vectors start at the tensor's first 16-byte boundary, after
+// `head` loose values (chunk 0's); the last chunk has the loose tail.
+__device__ __forceinline__ Values chunk_values(uintptr_t p, int64_t count, int es, int64_t k) {
+    const int per = 16 / es;
+    const int64_t head = min(static_cast<int64_t>((16 - (p & 15)) & 15) / es, count);
+    const int64_t all = (count - head) / per;
+    Values v;
+    v.base = head + k * (CHUNK_BYTES / es);
+    v.vecs = min(static_cast<int64_t>(THREADS * VECS), all - k * (THREADS * VECS));
+    v.head = k == 0 ? head : 0;
+    v.tail = k * (THREADS * VECS) + v.vecs == all ? count - head - all * per : 0;
+    return v;
+}
+
+template <typename T>
+__device__ __forceinline__ float value(const T* p) {
+    if constexpr (sizeof(T) == 2) return __bfloat162float(*p);
+    else return *p;
+}
+
+// The squares of a vector's values times `by`^2, onto four sums.
+template <typename T>
+__device__ __forceinline__ void squares(const uint4& v, float (&s)[4], float by = 1.f) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (sizeof(T) == 2) {
+            const float a = __uint_as_float(w[i] << 16) * by, b = __uint_as_float(w[i] & 0xFFFF0000u) * by;
+            s[i] = fmaf(a, a, fmaf(b, b, s[i]));
+        } else {
+            const float a = __uint_as_float(w[i]) * by;
+            s[i] = fmaf(a, a, s[i]);
+        }
+    }
+}
+
+// A thread's part of a chunk, in 64 bits. Where the fp32 sum is so large that a square
+// may have overflowed (an infinity or a NaN among them), or so small that squares may
+// have been lost, it is formed again from values scaled by a power of two; that only
+// happens to values beyond 2^60 or all below 2^-40.
+template <typename T>
+__device__ double chunk_squares(const T* p, int64_t count, int64_t k) {
+    const Values c = chunk_values(reinterpret_cast<uintptr_t>(p), count, sizeof(T), k);
+    const int t = static_cast<int>(threadIdx.x);
+    const uint4* src = reinterpret_cast<const uint4*>(p + c.base);
+    uint4 v[VECS];
+    uint32_t any = 0;
+#pragma unroll
+    for (int j = 0; j < VECS; ++j) v[j] = t + j * THREADS < c.vecs ? src[t + j * THREADS] : make_uint4(0u, 0u, 0u, 0u);
+    const int per = 16 / sizeof(T);
+    float loose = 0.f;  // at most one of the chunk's loose values to a thread: thread t the t-th before, 8 + t the t-th after
+    if (t < c.head) loose = value(p + t);
+    else if (t >= 8 && t < 8 + c.tail) loose = value(p + c.base + c.vecs * per + (t - 8));
+    float s[4] = {loose * loose, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int j = 0; j < VECS; ++j) {
+        squares<T>(v[j], s);
+        any |= v[j].x | v[j].y;
+        any |= v[j].z | v[j].w;
+    }
+    const float sum = (s[0] + s[1]) + (s[2] + s[3]);
+    const uint32_t magnitude = (any & (sizeof(T) == 2 ? 0x7FFF7FFFu : 0x7FFFFFFFu)) | (__float_as_uint(loose) & 0x7FFFFFFFu);
+    if (sum < 0x1p120f && (sum > 0x1p-80f || magnitude == 0)) return static_cast<double>(sum);
+    const float by = sum > 1.f || sum != sum ? 0x1p-80f : 0x1p100f;
+    s[0] = (loose * by) * (loose * by);
+    s[1] = s[2] = s[3] = 0.f;
+#pragma unroll
+    for (int j = 0; j < VECS; ++j) squares<T>(v[j], s, by);
+    const double back = by < 1.f ? 0x1p160 : 0x1p-200;
+    return static_cast<double>((s[0] + s[1]) + (s[2] + s[3])) * back;
+}
+
+// The chunk run of this block, [lo, hi), and the tensor of its chunk `c`.
+template <int N>
+__device__ __forceinline__ int tensor_of(const Table<N>& tab, int c) {
+    int lo = 0, hi = tab.n - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (tab.first[mid] <= c) lo = mid;
+        else hi = mid - 1;
+    }
+    return lo;
+}
+
+__device__ __forceinline__ int run_start(int chunks, int b, int blocks) {
+    return static_cast<int>(static_cast<int64_t>(chunks) * b / blocks);
+}
+
+// The sum of `x` over the block, in a fixed order, in every thread.
+__device__ double block_sum(double x) {
+    __shared__ double part[THREADS / 32];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = x;
+    __syncthreads();
+    double s = part[0];
+#pragma unroll
+    for (int w = 1; w < THREADS / 32; ++w) s += part[w];
+    return s;
+}
+
+template <int N>
+__global__ void __launch_bounds__(THREADS) grad_squares_kernel(const __grid_constant__ Table<N> tab, double* partials) {
+    ptx::grid_launch_dependents();
+    ptx::grid_dependency_wait();
+    const int chunks = tab.first[tab.n];
+    const int lo = run_start(chunks, blockIdx.x, gridDim.x), hi = run_start(chunks, blockIdx.x + 1, gridDim.x);
+    double s = 0.0;
+    int t = lo < hi ? tensor_of(tab, lo) : 0;
+    for (int c = lo; c < hi; ++c) {
+        while (c >= tab.first[t + 1]) ++t;
+        const int64_t k = c - tab.first[t], count = tab.count[t] >> 1;
+        s += tab.count[t] & 1 ? chunk_squares(static_cast<const __nv_bfloat16*>(tab.grad[t]), count, k)
+                              : chunk_squares(static_cast<const float*>(tab.grad[t]), count, k);
+    }
+    s = block_sum(s);
+    if (threadIdx.x == 0) partials[blockIdx.x] = s;
+}
+
+// The norm from the partial sums, the same in every block.
+__device__ float norm_of(const double* partials, int n) {
+    double s = 0.0;
+    for (int i = static_cast<int>(threadIdx.x); i < n; i += THREADS) s += __ldcg(partials + i);
+    return static_cast<float>(sqrt(block_sum(s)));
+}
+
+__global__ void __launch_bounds__(THREADS) grad_norm_kernel(float* norm, const double* partials, int n) {
+    ptx::grid_launch_dependents();
+    ptx::grid_dependency_wait();
+    const float v = norm_of(partials, n);
+    if (threadIdx.x == 0) *norm = v;
+}
+
+__device__ __forceinline__ float scaled(float x, float coef) { return x * coef; }
+
+template <typename T>
+__device__ void scale_chunk(T* out, const T* p, int64_t count, int64_t k, float coef) {
+    const Values c = chunk_values(reinterpret_cast<uintptr_t>(p), count, sizeof(T), k);
+    const int t = static_cast<int>(threadIdx.x), per = 16 / sizeof(T);
+    auto put = [&](int64_t i) {
+        if constexpr (sizeof(T) == 2) out[i] = __float2bfloat16_rn(value(p + i) * coef);
+        else out[i] = p[i] * coef;
+    };
+    if (t < c.head) put(t);
+    else if (t >= 8 && t < 8 + c.tail) put(c.base + c.vecs * per + (t - 8));
+    if ((reinterpret_cast<uintptr_t>(p) ^ reinterpret_cast<uintptr_t>(out)) & 15) {  // no vector lies on both sides
+        for (int64_t i = t; i < c.vecs * per; i += THREADS) put(c.base + i);
+        return;
+    }
+    const uint4* src = reinterpret_cast<const uint4*>(p + c.base);
+    uint4* dst = reinterpret_cast<uint4*>(out + c.base);
+    uint4 v[VECS];
+#pragma unroll
+    for (int j = 0; j < VECS; ++j)
+        if (t + j * THREADS < c.vecs) v[j] = src[t + j * THREADS];
+#pragma unroll
+    for (int j = 0; j < VECS; ++j) {
+        if (t + j * THREADS >= c.vecs) break;
+        uint32_t w[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (sizeof(T) == 2) {
+                const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(w[i] << 16) * coef,
+                                                               __uint_as_float(w[i] & 0xFFFF0000u) * coef);
+                w[i] = *reinterpret_cast<const uint32_t*>(&h);
+            } else {
+                w[i] = __float_as_uint(__uint_as_float(w[i]) * coef);
+            }
+        }
+        dst[t + j * THREADS] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+}
+
+// out = coef * g. The norm comes from `n` partial sums (n > 0, or no `given`), and is
+// stored to `norm` by block 0 where that is not null, or is `given`.
+template <int N>
+__global__ void __launch_bounds__(THREADS) grad_scale_kernel(const __grid_constant__ Table<N> tab, const float* given,
+                                                             const double* partials, int n, float* norm,
+                                                             float max_norm) {
+    ptx::grid_launch_dependents();
+    ptx::grid_dependency_wait();
+    const float total = given ? __ldcg(given) : norm_of(partials, n);
+    if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = total;
+    const float ratio = max_norm / (total + 1e-6f), coef = ratio >= 1.f ? 1.f : ratio;  // (a NaN stays one)
+    const int chunks = tab.first[tab.n];
+    const int lo = run_start(chunks, blockIdx.x, gridDim.x), hi = run_start(chunks, blockIdx.x + 1, gridDim.x);
+    int t = lo < hi ? tensor_of(tab, hi - 1) : 0;
+    for (int c = hi - 1; c >= lo; --c) {  // backwards: what the norm read last is still in L2
+        while (c < tab.first[t]) --t;
+        void* out = tab.out[t];
+        if (coef == 1.f && out == tab.grad[t]) continue;
+        const int64_t k = c - tab.first[t], count = tab.count[t] >> 1;
+        if (tab.count[t] & 1)
+            scale_chunk(static_cast<__nv_bfloat16*>(out), static_cast<const __nv_bfloat16*>(tab.grad[t]), count, k, coef);
+        else
+            scale_chunk(static_cast<float*>(out), static_cast<const float*>(tab.grad[t]), count, k, coef);
+    }
+}
+
+int64_t chunks_of(const GradTensor& t) {
+    const int es = t.bf16 ? 2 : 4;
+    const int64_t head = std::min<int64_t>(((16 - (reinterpret_cast<uintptr_t>(t.grad) & 15)) & 15) / es, t.count);
+    const int64_t vecs = (t.count - head) / (16 / es);
+    return std::max<int64_t>(1, (vecs + THREADS * VECS - 1) / (THREADS * VECS));
+}
+
+template <int N>
+bool fill(Table<N>* tab, const GradTensor* t, int n) {
+    int64_t at = 0;
+    for (int i = 0; i < n; ++i) {
+        tab->grad[i] = const_cast<void*>(t[i].grad);
+        tab->out[i] = t[i].out;
+        tab->count[i] = t[i].count * 2 + (t[i].bf16 ? 1 : 0);
+        tab->first[i] = static_cast<int>(at);
+        at += chunks_of(t[i]);
+        if (at > INT32_MAX) return false;
+    }
+    tab->first[n] = static_cast<int>(at);
+    tab->n = n;
+    return true;
+}
+
+cudaLaunchConfig_t config(int blocks, cudaStream_t stream, cudaLaunchAttribute* attr) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(blocks), 1, 1);
+    cfg.blockDim = dim3(THREADS, 1, 1);
+    cfg.stream = stream;
+    attr->id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr->val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cfg;
+}
+
+// One launch over at most N tensors: the squares (with `partials` to write) or the scaling.
+template <int N>
+cudaError_t launch(const GradTensor* t, int n, bool scale, const float* given, double* partials, int n_partials,
+                   float* norm, float max_norm, int num_sms, int* blocks_out, cudaStream_t stream) {
+    static thread_local Table<N> tab;
+    if (!fill(&tab, t, n)) return cudaErrorInvalidValue;
+    const int blocks = std::max(1, std::min(tab.first[n], std::min(num_sms * GRAD_BLOCKS_PER_SM, GRAD_MAX_BLOCKS)));
+    if (blocks_out) *blocks_out = blocks;
+    cudaLaunchAttribute attr[1];
+    const cudaLaunchConfig_t cfg = config(blocks, stream, attr);
+    if (!scale) return cudaLaunchKernelEx(&cfg, grad_squares_kernel<N>, tab, partials);
+    return cudaLaunchKernelEx(&cfg, grad_scale_kernel<N>, tab, given, static_cast<const double*>(partials), n_partials, norm,
+                              max_norm);
+}
+
+template <typename... A>
+cudaError_t launch_any(const GradTensor* t, int n, A... a) {
+    return n <= 32 ? launch<32>(t, n, a...) : n <= 256 ? launch<256>(t, n, a...) : launch<GRAD_TABLE>(t, n, a...);
+}
+
+}  // namespace
+
+cudaError_t grad_launch(const GradTensor* list, int n, float* norm, const float* given, bool scale, float max_norm,
+                        double* ws, int num_sms, cudaStream_t stream) {
+    if (take_injected_launch_failure()) return cudaErrorLaunchFailure;
+    int partials = 0;
+    if (!given) {
+        for (int i = 0; i < n; i += GRAD_TABLE) {
+            int blocks = 0;
+            const cudaError_t e = launch_any(list + i, std::min(n - i, GRAD_TABLE), false, static_cast<const float*>(nullptr),
+                                             ws + partials, 0, static_cast<float*>(nullptr), 0.f, num_sms, &blocks, stream);
+            if (e != cudaSuccess) return e;
+            partials += blocks;
+        }
+        if (!scale || n == 0) {
+            cudaLaunchAttribute attr[1];
+            const cudaLaunchConfig_t cfg = config(1, stream, attr);
+            return cudaLaunchKernelEx(&cfg, grad_norm_kernel, norm, static_cast<const double*>(ws), partials);
+        }
+    }
+    for (int i = 0; i < n; i += GRAD_TABLE) {
+        const cudaError_t e = launch_any(list + i, std::min(n - i, GRAD_TABLE), true, given, ws, partials,
+                                         given || i ? static_cast<float*>(nullptr) : norm, max_norm, num_sms,
+                                         static_cast<int*>(nullptr), stream);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
+}
+
+}  // namespace mmbwd

@@ -113,6 +113,10 @@ struct TcParams {
     // MODE 2: fp32 dbias (overwritten) = the sums over K of A's rows, formed
     // on the items of column tile 0 whose A arrives MN-major; null: none
     float* x3_dbias;
+    // MODE 4 and 5
+    int act;                        // MMBWD_ACT_*
+    int has_pre;                    // MODE 4: the argument of the activation is stored too
+    const __nv_bfloat16* residual;  // MODE 4; may be null, may be the output
 };
 
 // MODE 2 reductions longer than this keep the two correction products in an
@@ -161,14 +165,21 @@ cudaError_t tc_launch_x3_pair(const TcPlan& plan, float* dinp, float* dweight, f
                               cudaStream_t stream);
 cudaError_t tc_launch_forward(const TcPlan& plan, void* out, const void* inp, const void* weight,
                               const void* bias, int64_t BT, int64_t C, int64_t OC, cudaStream_t stream);
+// out = act(inp . weight^T + bias) + residual, and the activation's argument in pre; pre,
+// bias and residual may be null, residual may be out. The forward's plans.
+cudaError_t tc_launch_forward_act(const TcPlan& plan, void* out, void* pre, const void* inp, const void* weight,
+                                  const void* bias, const void* residual, int64_t BT, int64_t C, int64_t OC, int act,
+                                  cudaStream_t stream);
 
 // Launch the tensor-core kernel (and, with split dweight, the fixed-order
 // split reduction after it on the same stream). `ws` must hold plan.ws_bytes()
 // bytes. `sr`: stochastic rounding of the outputs with `sr_seed` (sr.cuh).
+// With `pre` (not with sr): dinp = product * act'(pre), overwritten; pre may be dinp.
 // Returns a cudaError_t.
 cudaError_t tc_launch(const TcPlan& plan, void* dinp, void* dweight, void* dbias, const void* dout,
                       const void* inp, const void* weight, int64_t BT, int64_t C, int64_t OC,
-                      void* ws, cudaStream_t stream, bool sr = false, uint64_t sr_seed = 0);
+                      void* ws, cudaStream_t stream, bool sr = false, uint64_t sr_seed = 0,
+                      const void* pre = nullptr, int act = 0);
 
 size_t tc_smem_bytes();
 

@@ -90,4 +90,58 @@ cudaError_t ln_launch(const LnPlan& plan, void* dinp, void* dweight, void* dbias
                       int C, int dtype, void* ws, cudaStream_t stream);
 cudaError_t ln_read_status(int* code, int* info3, bool reset);
 
+// ---------------------------------------------------------------- epilogues with an activation
+
+// fp32 on the CUDA cores: out = act(inp . weight^T + bias) + residual, pre (may be
+// null) the argument of act; dpre = (dout . weight) * act'(pre).
+cudaError_t simt_forward_act_launch(float* out, float* pre, const float* inp, const float* weight, const float* bias,
+                                    const float* residual, int64_t BT, int64_t C, int64_t OC, int act,
+                                    cudaStream_t stream);
+cudaError_t simt_run_act_launch(float* dpre, float* dweight, float* dbias, const float* dout, const float* inp,
+                                const float* weight, const float* pre, int64_t BT, int64_t C, int64_t OC, int act,
+                                cudaStream_t stream);
+// dpre = dout * act'(pre), n values
+cudaError_t act_backward_launch(void* dpre, const void* dout, const void* pre, int64_t n, int act, int dtype,
+                                cudaStream_t stream);
+// the forward without a product (C == 0): pre = bias, out = act(bias) + residual
+cudaError_t act_rows_launch(void* out, void* pre, const void* bias, const void* residual, int64_t rows, int64_t cols,
+                            int act, int dtype, cudaStream_t stream);
+
+// ---------------------------------------------------------------- norms around a block
+
+struct ResidualNorm {
+    // forward: out, residual_out, the statistics written; backward: the statistics read
+    void *out = nullptr, *residual_out = nullptr;
+    float *mean_post = nullptr, *rstd_post = nullptr, *mean = nullptr, *rstd = nullptr;
+    const void *x = nullptr, *branch = nullptr, *gate = nullptr;
+    const void *weight_post = nullptr, *bias_post = nullptr, *weight = nullptr, *bias = nullptr;
+    // backward
+    void *dx = nullptr, *dbranch = nullptr;
+    void *dgate = nullptr, *dweight_post = nullptr, *dbias_post = nullptr, *dweight = nullptr, *dbias = nullptr;
+    const void *dout = nullptr, *dresidual = nullptr, *residual = nullptr;
+    float* ws = nullptr;
+    int64_t rows = 0;
+    int C = 0;
+    float scale = 1.f, eps = 0.f;
+    int post = 0, norm = 0;
+};
+cudaError_t residual_forward_launch(const ResidualNorm& a, int dtype, int num_sms, cudaStream_t stream);
+cudaError_t residual_backward_launch(const ResidualNorm& a, int dtype, int num_sms, cudaStream_t stream);
+size_t residual_backward_workspace(int64_t rows, int64_t C, int dtype);
+
+// ---------------------------------------------------------------- gradient norm and clipping
+
+struct GradTensor {
+    const void* grad;
+    void* out;
+    int64_t count;  // > 0
+    bool bf16;
+};
+constexpr int GRAD_TABLE = 1024;       // tensors of one launch (28 KB of kernel parameters)
+constexpr int GRAD_BLOCKS_PER_SM = 8;  // as many of 256 threads as are resident
+constexpr int GRAD_MAX_BLOCKS = 1536;  // partial sums of one launch
+// given == nullptr: the norm of the list first, into `ws` and `norm`; `scale`: the outs.
+cudaError_t grad_launch(const GradTensor* list, int n, float* norm, const float* given, bool scale, float max_norm,
+                        double* ws, int num_sms, cudaStream_t stream);
+
 }  // namespace mmbwd

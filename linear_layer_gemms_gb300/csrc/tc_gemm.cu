@@ -49,6 +49,7 @@
 // unwind; copies and MMAs in flight are waited for before tensor memory is
 // released.
 #include "../../include/mmbwd.h"
+#include "act.cuh"
 #include "internal.h"
 #include "ptx.cuh"
 #include "sr.cuh"
@@ -246,6 +247,17 @@ __device__ __forceinline__ uint32_t add_round_pair(uint32_t old, float a, float 
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// Eight values rounded to bf16.
+__device__ __forceinline__ uint4 round8(const float (&f)[8]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const __nv_bfloat162 r = __floats2bfloat162_rn(f[2 * e], f[2 * e + 1]);
+        w[e] = *reinterpret_cast<const uint32_t*>(&r);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
 __device__ __forceinline__ uint4 add_round8(uint4 old, const float (&s)[8]) {
     uint4 r;
     r.x = add_round_pair(old.x, s[0], s[1]);
@@ -350,8 +362,10 @@ __device__ __forceinline__ void x3_split_mn(uint32_t hi, uint32_t lo, int nbox, 
 // operand as its tf32 truncation) and the low part (the exact remainder) --
 // and each K step issues three tf32 MMAs, hi.hi + hi.lo + lo.hi; fp32
 // read-modify-write epilogue. MODE 3: the backward with stochastic rounding of the bf16 outputs
-// (seeded; sr.cuh). Four instantiations, so that none pays for the
-// others' branches.
+// (seeded; sr.cuh). MODE 4: the forward with an activation and a residual in its
+// epilogue (mmbwd_forward_act). MODE 5: the backward whose dinp items are overwritten
+// with the product times act'(pre) (mmbwd_run_act). Six instantiations, so that none
+// pays for the others' branches.
 template <int MODE>
 __global__ void __launch_bounds__(Smem<MODE>::THREADS, 1)
     tc_mmbwd_kernel(const __grid_constant__ CUtensorMap tm_dout_k,   // dout, A of dinp (K-major)
@@ -374,8 +388,12 @@ __global__ void __launch_bounds__(Smem<MODE>::THREADS, 1)
                     // fp32 partial tiles of a split dweight reduction, 32 x 32
                     // boxes, 128-byte swizzle (MODE 0 and 3 with splits > 1)
                     const __grid_constant__ CUtensorMap tm_part,
+                    // MODE 5: pre in the boxes of tm_dinp_rmw
+                    const __grid_constant__ CUtensorMap tm_pre,
                     const TcParams p, const __grid_constant__ TcSchedule sch) {
-    constexpr bool FWD = MODE == 1 || MODE == 2;  // dinp-type items only, K-major B
+    constexpr bool EPI = MODE == 4;               // forward: activation, residual, pre
+    constexpr bool DACT = MODE == 5;              // backward: dinp = product * act'(pre)
+    constexpr bool FWD = MODE == 1 || MODE == 2 || EPI;  // dinp-type items only, K-major B
     constexpr bool X3 = MODE == 2;                // fp32 from three tf32 products
     constexpr bool SR = MODE == 3;                // stochastic rounding of the outputs
     // MODE 2 stages hold A hi | A lo | B hi | B lo (twice the bytes, half the
@@ -485,7 +503,8 @@ __global__ void __launch_bounds__(Smem<MODE>::THREADS, 1)
                 for (int j = 0; j < half / 64; ++j) nb += (col0 + j * 64 < n_extent) ? 1 : 0;
                 // Output tile of this CTA, prefetched into L2 a few k-blocks before the
                 // main loop ends so that the epilogue's read of the old values hits L2.
-                const bool direct = X3 || (!(it.is_dw && p.splits > 1) && !FWD);  // forward: nothing to read back
+                // (forward: nothing to read back but MODE 4's residual)
+                const bool direct = X3 || (EPI ? p.residual != nullptr : !(it.is_dw && p.splits > 1) && !FWD);
                 const int64_t out_rows = it.is_dw ? p.OC : p.BT;
                 const int pf_kb = max(it.kb0, it.kb1 - 8);
                 // A of a bf16 dweight item, or an MN-major fp32 A: 64-row boxes
@@ -917,8 +936,9 @@ __global__ void __launch_bounds__(Smem<MODE>::THREADS, 1)
             // goes back out with one bulk store. Rows and columns outside the
             // tensor read as zero and are not stored.
             const bool tma_rmw = !FWD && !X3 && !split_mode;
-            constexpr bool TMA_FWD = FWD && !X3;  // the forward's stores through TMA as well
+            constexpr bool TMA_FWD = FWD && !X3 && !EPI;  // the forward's stores through TMA as well
             const void* tmo = it.is_dw ? static_cast<const void*>(&tm_dw_rmw) : static_cast<const void*>(&tm_dinp_rmw);
+            const void* tml = DACT && !it.is_dw ? static_cast<const void*>(&tm_pre) : tmo;  // a chunk is loaded through
             const int nvc = (ncols + 31) / 32;  // chunks holding columns of the tensor
             const int nloc = nvc > h ? (nvc - h + NH - 1) / NH : 0;  // of them this warp's
             const int nloc_all = (nchunks - h + NH - 1) / NH;       // this warp's of the tile
@@ -933,7 +953,7 @@ __global__ void __launch_bounds__(Smem<MODE>::THREADS, 1)
                 for (int k = 0; k < OLD_SLOTS && k < nloc; ++k) {
                     const uint32_t b = oldbar0 + 8u * k;
                     ptx::mbar_arrive_expect_tx(b, OLD_CHUNK_BYTES);
-                    ptx::tma_load_2d(oldbuf + k * OLD_CHUNK_BYTES, tmo, b, col0 + (h + NH * k) * 32,
+                    ptx::tma_load_2d(oldbuf + k * OLD_CHUNK_BYTES, tml, b, col0 + (h + NH * k) * 32,
                                      static_cast<int32_t>(qrow0));
                     oldpend |= 1u << k;
                 }
@@ -955,6 +975,21 @@ __global__ void __launch_bounds__(Smem<MODE>::THREADS, 1)
                 }
             };
             if constexpr (X3) x3_load_old(0, olda, oldb);
+            // MODE 4: this thread's row of the residual's first chunk, likewise; each
+            // later chunk's is requested while the chunk before is worked on
+            uint4 res[4];
+            const __nv_bfloat16* resrow = nullptr;
+            [[maybe_unused]] auto load_res = [&](int k, uint4 (&to)[4]) {
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    const int at = (h + NH * k) * 32 + 8 * g;
+                    to[g] = resrow && at < ncols ? *reinterpret_cast<const uint4*>(resrow + at) : make_uint4(0u, 0u, 0u, 0u);
+                }
+            };
+            if constexpr (EPI) {
+                if (p.residual && qrow0 + lane < rows_total) resrow = p.residual + (qrow0 + lane) * n_extent + col0;
+                load_res(0, res);
+            }
             bool ok = wt.wait_warp(bars + 8u * (BAR_TFULL + acc), acc_phase, SITE_EPI_TMEM_FULL, w);
             if (!ptx::named_bar_and(1, L::EPI_THREADS, ok)) break;
             ptx::tc_fence_after();
@@ -1031,20 +1066,39 @@ __global__ void __launch_bounds__(Smem<MODE>::THREADS, 1)
                     // C is), so their eight words have consecutive counters
                     const uint64_t e_row = static_cast<uint64_t>(qrow0 + lane) * n_extent + col0 + c * 32;
                     const uint64_t z0 = SR ? sr::word_state(p.sr_seed, t_sr, e_row) : 0;
+                    if (DACT && !it.is_dw) {
+                        act::with(p.act, [&](auto kind) {
+                            constexpr int ACT = decltype(kind)::value;
 #pragma unroll
-                    for (int g = 0; g < 4; ++g) {
-                        const uint32_t a = rowaddr + ((static_cast<uint32_t>(g) ^ swz) << 4);
-                        const uint4 o = ptx::lds128(a);
-                        float s8[8];
+                            for (int g = 0; g < 4; ++g) {
+                                const uint32_t a = rowaddr + ((static_cast<uint32_t>(g) ^ swz) << 4);
+                                const uint4 x = ptx::lds128(a);
+                                const uint32_t xw[4] = {x.x, x.y, x.z, x.w};
+                                float f[8];
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) s8[e] = __uint_as_float(v[8 * g + e]);
-                        uint4 res;
-                        if constexpr (SR)
-                            res = add_sr8(o, s8, sr::sm64_mix(z0 + (2 * g) * sr::SM64_GAMMA),
-                                          sr::sm64_mix(z0 + (2 * g + 1) * sr::SM64_GAMMA));
-                        else
-                            res = add_round8(o, s8);
-                        ptx::sts128u(a, res);
+                                for (int e = 0; e < 4; ++e) {
+                                    f[2 * e] = __uint_as_float(v[8 * g + 2 * e]) * act::slope<ACT, true>(bf_lo(xw[e]));
+                                    f[2 * e + 1] = __uint_as_float(v[8 * g + 2 * e + 1]) * act::slope<ACT, true>(bf_hi(xw[e]));
+                                }
+                                ptx::sts128u(a, round8(f));
+                            }
+                        });
+                    } else {
+#pragma unroll
+                        for (int g = 0; g < 4; ++g) {
+                            const uint32_t a = rowaddr + ((static_cast<uint32_t>(g) ^ swz) << 4);
+                            const uint4 o = ptx::lds128(a);
+                            float s8[8];
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) s8[e] = __uint_as_float(v[8 * g + e]);
+                            uint4 res;
+                            if constexpr (SR)
+                                res = add_sr8(o, s8, sr::sm64_mix(z0 + (2 * g) * sr::SM64_GAMMA),
+                                              sr::sm64_mix(z0 + (2 * g + 1) * sr::SM64_GAMMA));
+                            else
+                                res = add_round8(o, s8);
+                            ptx::sts128u(a, res);
+                        }
                     }
                     ptx::fence_proxy_async_smem();
                     __syncwarp();
@@ -1057,7 +1111,7 @@ __global__ void __launch_bounds__(Smem<MODE>::THREADS, 1)
                         if (kn < nloc) {
                             ptx::bulk_wait_read_all();
                             ptx::mbar_arrive_expect_tx(b, OLD_CHUNK_BYTES);
-                            ptx::tma_load_2d(oldbuf + slot * OLD_CHUNK_BYTES, tmo, b, col0 + (h + NH * kn) * 32,
+                            ptx::tma_load_2d(oldbuf + slot * OLD_CHUNK_BYTES, tml, b, col0 + (h + NH * kn) * 32,
                                              static_cast<int32_t>(qrow0));
                             oldpend |= 1u << slot;
                         }
@@ -1097,6 +1151,72 @@ __global__ void __launch_bounds__(Smem<MODE>::THREADS, 1)
                         ptx::bulk_commit_group();
                     }
                     ++fwd_chunks;
+                }
+            }
+            if constexpr (EPI) {
+                // out = act(acc + bias) + residual and, where wanted, pre = acc + bias, each
+                // rounded once, row by row into a chunk buffer and out with one bulk store;
+                // the buffers alternate over the stores of both, and one is rewritten once the
+                // store before last has read it.
+                const uint32_t swz = static_cast<uint32_t>((lane >> 1) & 3);
+                auto store = [&](const void* map, int c, const float (&f)[32]) {
+                    const uint32_t slot = fwd_chunks & (OLD_SLOTS - 1);
+                    if (fwd_chunks >= OLD_SLOTS && lane == 0) ptx::bulk_wait_read_but_n<OLD_SLOTS - 1>();
+                    __syncwarp();
+                    const uint32_t rowaddr = oldbuf + slot * OLD_CHUNK_BYTES + lane * 64;
+#pragma unroll
+                    for (int g = 0; g < 4; ++g) {
+                        const float f8[8] = {f[8 * g],     f[8 * g + 1], f[8 * g + 2], f[8 * g + 3],
+                                             f[8 * g + 4], f[8 * g + 5], f[8 * g + 6], f[8 * g + 7]};
+                        ptx::sts128u(rowaddr + ((static_cast<uint32_t>(g) ^ swz) << 4), round8(f8));
+                    }
+                    ptx::fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        ptx::tma_store_2d(map, oldbuf + slot * OLD_CHUNK_BYTES, col0 + c * 32, static_cast<int32_t>(qrow0));
+                        ptx::bulk_commit_group();
+                    }
+                    ++fwd_chunks;
+                };
+                if (qvalid) {
+#pragma unroll 1
+                    for (int k = 0; k < nloc; ++k) {
+                        const int c = h + NH * k;
+                        uint32_t v[32];
+                        ptx::tmem_ld32(tbase + c * 32, v);
+                        float f[32];
+#pragma unroll
+                        for (int g = 0; g < 4; ++g) {
+                            const int cc = col0 + c * 32 + 8 * g;
+                            const uint4 b8 = (p.fwd_bias && cc < n_extent)
+                                                 ? __ldg(reinterpret_cast<const uint4*>(p.fwd_bias + cc))
+                                                 : make_uint4(0u, 0u, 0u, 0u);
+                            const uint32_t bw[4] = {b8.x, b8.y, b8.z, b8.w};
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                f[8 * g + 2 * e] = __uint_as_float(v[8 * g + 2 * e]) + bf_lo(bw[e]);
+                                f[8 * g + 2 * e + 1] = __uint_as_float(v[8 * g + 2 * e + 1]) + bf_hi(bw[e]);
+                            }
+                        }
+                        if (p.has_pre) store(&tm_dw_rmw, c, f);
+                        act::with(p.act, [&](auto kind) {
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) f[e] = act::value<decltype(kind)::value, true>(f[e]);
+                        });
+                        if (p.residual) {
+#pragma unroll
+                            for (int g = 0; g < 4; ++g) {
+                                const uint32_t rw[4] = {res[g].x, res[g].y, res[g].z, res[g].w};
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    f[8 * g + 2 * e] += bf_lo(rw[e]);
+                                    f[8 * g + 2 * e + 1] += bf_hi(rw[e]);
+                                }
+                            }
+                            if (k + 1 < nloc) load_res(k + 1, res);
+                        }
+                        store(tmo, c, f);
+                    }
                 }
             }
             if (!ptx::named_bar_and(1, L::EPI_THREADS, ok)) break;
@@ -1580,9 +1700,12 @@ struct MapSpec {
 };
 
 // Encodes the six tensor maps, completes the parameters from the plan, and
-// launches the kernel (and the split fixup when the plan splits dweight).
+// launches the kernel (and the split fixup when the plan splits dweight). `aux`: what
+// the dinp-type items read in place of their output's old values (MODE 4: the residual,
+// MODE 5: pre).
 cudaError_t launch_common(const TcPlan& plan, const MapSpec (&specs)[6], TcParams& p, int mode, cudaStream_t stream,
-                          const MapSpec* pair_specs = nullptr) {
+                          const MapSpec* pair_specs = nullptr, const MapSpec* aux = nullptr) {
+    const bool bwd = mode == 0 || mode == 3 || mode == 5;  // bf16 backward
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
@@ -1596,22 +1719,27 @@ cudaError_t launch_common(const TcPlan& plan, const MapSpec (&specs)[6], TcParam
                 e = cudaFuncSetAttribute(tc_mmbwd_kernel<2>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_TOTAL);
             if (e == cudaSuccess)
                 e = cudaFuncSetAttribute(tc_mmbwd_kernel<3>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_TOTAL);
+            if (e == cudaSuccess)
+                e = cudaFuncSetAttribute(tc_mmbwd_kernel<4>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_TOTAL);
+            if (e == cudaSuccess)
+                e = cudaFuncSetAttribute(tc_mmbwd_kernel<5>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_TOTAL);
             if (e != cudaSuccess) return e;
             if (dev >= 0 && dev < 64) g_attr_set[dev] = true;
         }
     }
     EncodeTiledFn encode = get_encode_tiled();
     if (!encode) return cudaErrorNotSupported;
-    CUtensorMap maps[12];
+    CUtensorMap maps[13];
     for (int i = 0; i < 6; ++i) {
-        const cuuint64_t dims[2] = {specs[i].inner, specs[i].outer};
+        const MapSpec& m = i == 4 && aux ? *aux : specs[i];
+        const cuuint64_t dims[2] = {m.inner, m.outer};
         const uint64_t es = mode == 2 ? 4 : 2;
-        const cuuint64_t strides[1] = {specs[i].pitch ? specs[i].pitch : specs[i].inner * es};
-        const cuuint32_t box[2] = {specs[i].box_inner, specs[i].box_outer};
+        const cuuint64_t strides[1] = {m.pitch ? m.pitch : m.inner * es};
+        const cuuint32_t box[2] = {m.box_inner, m.box_outer};
         const cuuint32_t estr[2] = {1, 1};
         const CUresult r = encode(&maps[i], mode == 2 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
-                                  2, const_cast<void*>(specs[i].base),
-                                  dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, specs[i].swz,
+                                  2, const_cast<void*>(m.base),
+                                  dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, m.swz,
                                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
         if (r != CUDA_SUCCESS) return cudaErrorInvalidValue;
     }
@@ -1626,7 +1754,7 @@ cudaError_t launch_common(const TcPlan& plan, const MapSpec (&specs)[6], TcParam
         maps[5 + i] = maps[i];  // placeholder where unused
         const MapSpec& m = specs[i];
         CUresult r = CUDA_SUCCESS;
-        if ((mode == 0 || mode == 3) && m.box_inner == 64 && m.inner >= 64 && m.inner % 64 == 0) {
+        if (bwd && m.box_inner == 64 && m.inner >= 64 && m.inner % 64 == 0) {
             const cuuint64_t dims[3] = {64, m.outer, m.inner / 64};
             const cuuint64_t strides[2] = {m.pitch ? m.pitch : m.inner * 2, 128};
             const cuuint32_t box[3] = {64, m.box_outer, 2};
@@ -1634,7 +1762,7 @@ cudaError_t launch_common(const TcPlan& plan, const MapSpec (&specs)[6], TcParam
             r = encode(&maps[5 + i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(m.base), dims, strides,
                        box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, m.swz, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-        } else if (mode == 1 && i == 1) {
+        } else if ((mode == 1 || mode == 4) && i == 1) {
             const cuuint64_t dims[2] = {m.inner, m.outer};
             const cuuint64_t strides[1] = {m.pitch ? m.pitch : m.inner * 2};
             const cuuint32_t box[2] = {m.box_inner, 2 * m.box_outer};
@@ -1650,15 +1778,17 @@ cudaError_t launch_common(const TcPlan& plan, const MapSpec (&specs)[6], TcParam
     }
     // Output maps of the bf16 epilogues (maps 4 and 5 give the tensors and
     // their extents): boxes of 32 columns x 32 rows.
-    for (int i = 0; i < 2; ++i) {
-        maps[9 + i] = maps[4 + i];  // placeholder where unused
-        if (mode == 2 || (mode == 1 && i == 1)) continue;  // the forward writes through map 9
-        const MapSpec& m = specs[4 + i];
+    // MODE 4 writes pre through map 10; MODE 5 loads pre through map 12.
+    for (int i = 0; i < 3; ++i) {
+        CUtensorMap& map = maps[i == 2 ? 12 : 9 + i];
+        map = maps[4];  // placeholder where unused
+        if (i == 2 ? !aux : mode == 2 || (mode == 1 && i == 1)) continue;  // the forward writes through map 9
+        const MapSpec& m = i == 2 ? *aux : specs[4 + i];
         const cuuint64_t dims[2] = {m.inner, m.outer};
         const cuuint64_t strides[1] = {m.inner * 2};
         const cuuint32_t box[2] = {32, 32};
         const cuuint32_t estr[2] = {1, 1};
-        const CUresult r = encode(&maps[9 + i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(m.base), dims,
+        const CUresult r = encode(&map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(m.base), dims,
                                   strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
                                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
         if (r != CUDA_SUCCESS) return cudaErrorInvalidValue;
@@ -1681,7 +1811,7 @@ cudaError_t launch_common(const TcPlan& plan, const MapSpec (&specs)[6], TcParam
         }
     }
     maps[11] = maps[0];  // placeholder where unused
-    if ((mode == 0 || mode == 3) && plan.splits > 1 && p.partials) {
+    if (bwd && plan.splits > 1 && p.partials) {
         const uint64_t rows = static_cast<uint64_t>(2 * plan.dw_tiles_m) * plan.dw_tiles_n * plan.splits * TC_BM;
         const cuuint64_t dims[2] = {static_cast<cuuint64_t>(plan.dw_bn), rows};
         const cuuint64_t strides[1] = {static_cast<cuuint64_t>(plan.dw_bn) * 4};
@@ -1725,16 +1855,22 @@ cudaError_t launch_common(const TcPlan& plan, const MapSpec (&specs)[6], TcParam
     cfg.attrs = attr;
     cfg.numAttrs = 2;
     if (mode == 2)
-        e = cudaLaunchKernelEx(&cfg, tc_mmbwd_kernel<2>, maps[0], maps[1], maps[2], maps[3], maps[4], maps[5], maps[6], maps[7], maps[8], maps[9], maps[10], maps[11], p,
+        e = cudaLaunchKernelEx(&cfg, tc_mmbwd_kernel<2>, maps[0], maps[1], maps[2], maps[3], maps[4], maps[5], maps[6], maps[7], maps[8], maps[9], maps[10], maps[11], maps[12], p,
                                plan.sched);
     else if (mode == 1)
-        e = cudaLaunchKernelEx(&cfg, tc_mmbwd_kernel<1>, maps[0], maps[1], maps[2], maps[3], maps[4], maps[5], maps[6], maps[7], maps[8], maps[9], maps[10], maps[11], p,
+        e = cudaLaunchKernelEx(&cfg, tc_mmbwd_kernel<1>, maps[0], maps[1], maps[2], maps[3], maps[4], maps[5], maps[6], maps[7], maps[8], maps[9], maps[10], maps[11], maps[12], p,
+                               plan.sched);
+    else if (mode == 4)
+        e = cudaLaunchKernelEx(&cfg, tc_mmbwd_kernel<4>, maps[0], maps[1], maps[2], maps[3], maps[4], maps[5], maps[6], maps[7], maps[8], maps[9], maps[10], maps[11], maps[12], p,
+                               plan.sched);
+    else if (mode == 5)
+        e = cudaLaunchKernelEx(&cfg, tc_mmbwd_kernel<5>, maps[0], maps[1], maps[2], maps[3], maps[4], maps[5], maps[6], maps[7], maps[8], maps[9], maps[10], maps[11], maps[12], p,
                                plan.sched);
     else if (mode == 3)
-        e = cudaLaunchKernelEx(&cfg, tc_mmbwd_kernel<3>, maps[0], maps[1], maps[2], maps[3], maps[4], maps[5], maps[6], maps[7], maps[8], maps[9], maps[10], maps[11], p,
+        e = cudaLaunchKernelEx(&cfg, tc_mmbwd_kernel<3>, maps[0], maps[1], maps[2], maps[3], maps[4], maps[5], maps[6], maps[7], maps[8], maps[9], maps[10], maps[11], maps[12], p,
                                plan.sched);
     else
-        e = cudaLaunchKernelEx(&cfg, tc_mmbwd_kernel<0>, maps[0], maps[1], maps[2], maps[3], maps[4], maps[5], maps[6], maps[7], maps[8], maps[9], maps[10], maps[11], p,
+        e = cudaLaunchKernelEx(&cfg, tc_mmbwd_kernel<0>, maps[0], maps[1], maps[2], maps[3], maps[4], maps[5], maps[6], maps[7], maps[8], maps[9], maps[10], maps[11], maps[12], p,
                                plan.sched);
     if (e != cudaSuccess || plan.splits == 1) return e;
     cudaLaunchConfig_t fcfg{};
@@ -1750,7 +1886,7 @@ cudaError_t launch_common(const TcPlan& plan, const MapSpec (&specs)[6], TcParam
 
 cudaError_t tc_launch(const TcPlan& plan, void* dinp, void* dweight, void* dbias, const void* dout,
                       const void* inp, const void* weight, int64_t BT, int64_t C, int64_t OC, void* ws,
-                      cudaStream_t stream, bool sr, uint64_t sr_seed) {
+                      cudaStream_t stream, bool sr, uint64_t sr_seed, const void* pre, int act) {
     if (take_injected_launch_failure()) return cudaErrorLaunchFailure;
     const uint64_t bt = static_cast<uint64_t>(BT), c = static_cast<uint64_t>(C), oc = static_cast<uint64_t>(OC);
     const MapSpec specs[6] = {
@@ -1778,7 +1914,9 @@ cudaError_t tc_launch(const TcPlan& plan, void* dinp, void* dweight, void* dbias
     // the bias warps (the variant the page's commented-out Sgemv suggests)
     const char* db = std::getenv("MMBWD_DBIAS");
     p.bias_mma = (dbias && db && std::strcmp(db, "ones") == 0) ? 1 : 0;
-    return launch_common(plan, specs, p, sr ? 3 : 0, stream);
+    p.act = act;
+    const MapSpec aux{pre, c, bt, 128, TC_BM, CU_TENSOR_MAP_SWIZZLE_NONE};
+    return launch_common(plan, specs, p, pre ? 5 : sr ? 3 : 0, stream, nullptr, pre ? &aux : nullptr);
 }
 
 cudaError_t tc_launch_forward(const TcPlan& plan, void* out, const void* inp, const void* weight, const void* bias,
@@ -1801,6 +1939,33 @@ cudaError_t tc_launch_forward(const TcPlan& plan, void* out, const void* inp, co
     p.fwd_bias = static_cast<const __nv_bfloat16*>(bias);
     p.dinp = static_cast<__nv_bfloat16*>(out);
     return launch_common(plan, specs, p, 1, stream);
+}
+
+cudaError_t tc_launch_forward_act(const TcPlan& plan, void* out, void* pre, const void* inp, const void* weight,
+                                  const void* bias, const void* residual, int64_t BT, int64_t C, int64_t OC, int act,
+                                  cudaStream_t stream) {
+    if (take_injected_launch_failure()) return cudaErrorLaunchFailure;
+    const uint64_t bt = static_cast<uint64_t>(BT), c = static_cast<uint64_t>(C), oc = static_cast<uint64_t>(OC);
+    const MapSpec specs[6] = {
+        {inp, c, bt, TC_BK, TC_BM, CU_TENSOR_MAP_SWIZZLE_128B},      // inp, K-major A
+        {weight, c, oc, TC_BK, 64, CU_TENSOR_MAP_SWIZZLE_128B},      // weight rows, K-major B (64 rows per box)
+        {inp, c, bt, TC_BK, TC_BM, CU_TENSOR_MAP_SWIZZLE_128B},      // unused by forward items
+        {weight, c, oc, TC_BK, 64, CU_TENSOR_MAP_SWIZZLE_128B},      // unused
+        {out, oc, bt, 128, TC_BM, CU_TENSOR_MAP_SWIZZLE_NONE},              // out (map 9)
+        {pre ? pre : out, oc, bt, 128, TC_BM, CU_TENSOR_MAP_SWIZZLE_NONE},  // pre (map 10)
+    };
+    const MapSpec aux{residual, oc, bt, 128, TC_BM, CU_TENSOR_MAP_SWIZZLE_NONE};
+    TcParams p{};
+    p.BT = BT;
+    p.C = C;
+    p.OC = OC;
+    p.n_dinp = OC;
+    p.fwd_bias = static_cast<const __nv_bfloat16*>(bias);
+    p.dinp = static_cast<__nv_bfloat16*>(out);
+    p.residual = static_cast<const __nv_bfloat16*>(residual);
+    p.has_pre = pre ? 1 : 0;
+    p.act = act;
+    return launch_common(plan, specs, p, 4, stream, nullptr, residual ? &aux : nullptr);
 }
 
 TcPlan tc_make_plan_x3_pair(int64_t BT, int64_t C, int64_t OC, int num_sms) {
