@@ -4,9 +4,11 @@
 // Bound by HBM. Forward: two rows read, two written. A team of P warps owns a row and
 // keeps it in registers (VPT 16-byte vectors per thread) from the branch's statistics to
 // the output, so nothing is read twice and each variance comes from the differences
-// (LAYER) of values at hand. Backward: four rows read and two written by column tiles
-// whose threads keep their columns' parameter sums in registers, after a pass that forms
-// each row's four sums.
+// (LAYER) of values at hand. Backward: four rows read, two written. A team owns a row as
+// well, a thread eight columns of it; it has the next row in flight, forms the row's
+// four sums in two rounds and keeps its columns' parameter sums in registers over all
+// rows of the team. Rows that no team of 16 warps holds (C > 4096) take two passes: one
+// forms the rows' sums, one goes down column tiles.
 #include "../../include/residual_norm.h"
 #include "ops.h"
 #include "ptx.cuh"
@@ -244,12 +246,21 @@ cudaError_t forward(const ResidualNorm& a, cudaStream_t stream) {
 
 // ---------------------------------------------------------------- backward
 
-// One row's terms of the gradients.
+// One row's statistics and sums.
 struct RowTerms {
     float mean, rstd, mean_post, rstd_post;  // 0 and 1 where there are none
     float a, c;                              // mean(g) (0 for RMS) and mean(g n)
     float e, h;                              // likewise of post
 };
+
+__device__ __forceinline__ RowTerms row_terms(const ResidualNorm& a, int64_t r) {
+    RowTerms q{0.f, 1.f, 0.f, 1.f, 0.f, 0.f, 0.f, 0.f};
+    if (a.norm == LAYER) q.mean = a.mean[r];
+    if (a.norm != NONE) q.rstd = a.rstd[r];
+    if (a.mean_post) q.mean_post = a.mean_post[r];
+    if (a.rstd_post) q.rstd_post = a.rstd_post[r];
+    return q;
+}
 
 // Per vector: dx from dout, dresidual, residual (n: the normalised residual).
 template <int N>
@@ -264,11 +275,188 @@ __device__ __forceinline__ void dx_of(const RowTerms& q, bool norm, const float 
 
 struct Backward {
     ResidualNorm a;
-    float* sums;      // [rows][4]: a, c, e, h
+    float* sums;      // [rows][4]: a, c, e, h (two passes)
     float* partials;  // [row blocks][4][C]: dweight, dbias, sum dx z, sum dx
+    int team_warps;   // one pass: warps of a team
     float inv_c;
     int row_blocks;
 };
+
+// ---- one pass
+
+constexpr int COLS = 8;         // columns of a thread
+constexpr int TEAM_WARPS = 16;  // warps of a block, at most
+
+// A thread's eight values of a row, as they are stored.
+template <typename T>
+struct Eight {
+    static constexpr int V = 8 / Vec<T>::N;
+    uint4 v[V];
+    // `p` at the row's first value; vector i is there if `on[i]`
+    __device__ void load(const T* p, int c0, const bool (&on)[V]) {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            v[i] = p && on[i] ? reinterpret_cast<const uint4*>(p + c0)[i] : make_uint4(0u, 0u, 0u, 0u);
+    }
+    __device__ void get(float (&f)[8]) const {
+#pragma unroll
+        for (int i = 0; i < V; ++i) Vec<T>::get(v[i], f + i * Vec<T>::N);
+    }
+};
+template <typename T>
+__device__ __forceinline__ void store8(T* p, int c0, const bool (&on)[Eight<T>::V], const float (&f)[8]) {
+#pragma unroll
+    for (int i = 0; i < Eight<T>::V; ++i)
+        if (on[i]) reinterpret_cast<uint4*>(p + c0)[i] = Vec<T>::put(f + i * Vec<T>::N);
+}
+
+// Two sums over a team, in warp order, in every thread; `at`: the team's slots. Consecutive
+// sums of a team alternate between two sets of slots, so that one barrier is enough.
+__device__ __forceinline__ float2 team_sum2(float x, float y, float2* at, int warp, int warps, int team) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        x += __shfl_xor_sync(0xffffffffu, x, o);
+        y += __shfl_xor_sync(0xffffffffu, y, o);
+    }
+    if (warps == 1) return make_float2(x, y);
+    if ((threadIdx.x & 31) == 0) at[warp] = make_float2(x, y);
+    ptx::named_bar_sync(static_cast<uint32_t>(1 + team), static_cast<uint32_t>(32 * warps));
+    float2 t = at[0];
+#pragma unroll
+    for (int w = 1; w < TEAM_WARPS; ++w)
+        if (w < warps) t.x += at[w].x, t.y += at[w].y;
+    return t;
+}
+
+template <typename T>
+struct RowData {
+    Eight<T> dout, res, dres, branch;
+    float mean, rstd, mean_post, rstd_post;
+};
+
+template <typename T>
+__global__ void __launch_bounds__(32 * TEAM_WARPS, 1) residual_rows_kernel(const __grid_constant__ Backward b) {
+    constexpr int V = Eight<T>::V;
+    __shared__ float2 slots[TEAM_WARPS][2][TEAM_WARPS];
+    __shared__ float joined[4 * 256 * (TEAM_WARPS / 2)];  // teams of at most half the warps are joined
+    const ResidualNorm& a = b.a;
+    const int warps = b.team_warps, warp = static_cast<int>(threadIdx.x >> 5), lane = static_cast<int>(threadIdx.x & 31);
+    const int teams = static_cast<int>(blockDim.x >> 5) / warps, team = warp / warps, wt = warp % warps;
+    const int c0 = (wt * 32 + lane) * COLS;
+    bool on[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) on[i] = c0 + i * Vec<T>::N < a.C;
+    const bool norm = a.norm != NONE, post = a.post != NONE;
+    float2* at = slots[team][0];
+    int which = 0;
+    ptx::grid_launch_dependents();
+    ptx::grid_dependency_wait();
+    // the weights of a thread's columns, 0 beyond the row: nothing there adds to a sum
+    float w[8], gw[8];  // gw: scale * gate * weight_post
+    {
+        Eight<T> t;
+        t.load(static_cast<const T*>(a.weight), c0, on);
+        t.get(w);
+        t.load(static_cast<const T*>(a.weight_post), c0, on);
+        t.get(gw);
+        float g[8];
+        t.load(static_cast<const T*>(a.gate), c0, on);
+        t.get(g);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float one = on[i / Vec<T>::N] ? 1.f : 0.f;
+            gw[i] = (post ? gw[i] : one) * (a.scale * (a.gate ? g[i] : one));
+        }
+    }
+    float s[4][8];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s[k][i] = 0.f;
+
+    auto fetch = [&](RowData<T>& q, int64_t r) {
+        const int64_t o = r * a.C;
+        auto row = [&](const void* p) { return p ? static_cast<const T*>(p) + o : nullptr; };
+        q.dout.load(row(a.dout), c0, on);
+        q.res.load(row(a.residual), c0, on);
+        q.dres.load(row(a.dresidual), c0, on);
+        q.branch.load(row(a.branch), c0, on);
+        const RowTerms t = row_terms(a, r);
+        q.mean = t.mean, q.rstd = t.rstd, q.mean_post = t.mean_post, q.rstd_post = t.rstd_post;
+    };
+    const int64_t stride = static_cast<int64_t>(gridDim.x) * teams;
+    int64_t r = static_cast<int64_t>(blockIdx.x) * teams + team;
+    RowData<T> q, next;
+    if (r < a.rows) fetch(q, r);
+    for (; r < a.rows; r += stride) {
+        if (r + stride < a.rows) fetch(next, r + stride);
+        float dx[8], z[8];
+        q.dres.get(dx);
+        if (norm) {
+            float d[8], n[8], g[8], s0 = 0.f, s1 = 0.f;
+            q.dout.get(d);
+            q.res.get(n);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                n[i] = (n[i] - q.mean) * q.rstd;
+                g[i] = w[i] * d[i];
+                s0 += g[i];
+                s1 = fmaf(g[i], n[i], s1);
+                s[0][i] = fmaf(d[i], n[i], s[0][i]);
+                s[1][i] += d[i];
+            }
+            const float2 t = team_sum2(s0, s1, at + which, wt, warps, team);
+            which ^= TEAM_WARPS;
+            const float m = a.norm == LAYER ? t.x * b.inv_c : 0.f, c = t.y * b.inv_c;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) dx[i] = fmaf(q.rstd, g[i] - fmaf(n[i], c, m), dx[i]);
+        }
+        store8(static_cast<T*>(a.dx) + r * a.C, c0, on, dx);
+        q.branch.get(z);
+        float y[8], s0 = 0.f, s1 = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            z[i] = (z[i] - q.mean_post) * q.rstd_post;
+            y[i] = gw[i] * dx[i];
+            s0 += y[i];
+            s1 = fmaf(y[i], z[i], s1);
+            s[2][i] = fmaf(dx[i], z[i], s[2][i]);
+            s[3][i] += dx[i];
+        }
+        if (a.dbranch) {
+            if (post) {
+                const float2 t = team_sum2(s0, s1, at + which, wt, warps, team);
+                which ^= TEAM_WARPS;
+                const float m = a.post == LAYER ? t.x * b.inv_c : 0.f, c = t.y * b.inv_c;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) y[i] = q.rstd_post * (y[i] - fmaf(z[i], c, m));
+            }
+            store8(static_cast<T*>(a.dbranch) + r * a.C, c0, on, y);
+        }
+        q = next;
+    }
+
+    // The block's sums over its rows: the teams' in team order.
+    float* to = b.partials + static_cast<int64_t>(blockIdx.x) * 4 * a.C;
+    for (int k = 0; k < teams; ++k) {
+        if (teams > 1) __syncthreads();
+        if (team != k) continue;
+#pragma unroll
+        for (int f = 0; f < 4; ++f)
+#pragma unroll
+            for (int i = 0; i < 8; i += 4) {
+                float4 v = make_float4(s[f][i], s[f][i + 1], s[f][i + 2], s[f][i + 3]);
+                if (teams > 1) {
+                    float4* mine = reinterpret_cast<float4*>(joined + f * 256 * warps + c0 + i);
+                    if (k > 0) v.x += mine->x, v.y += mine->y, v.z += mine->z, v.w += mine->w;
+                    if (k + 1 < teams) *mine = v;
+                }
+                if (k + 1 == teams && c0 + i < a.C) *reinterpret_cast<float4*>(to + static_cast<int64_t>(f) * a.C + c0 + i) = v;
+            }
+    }
+}
+
+// ---- two passes
 
 constexpr int SUM_THREADS = 256;
 
@@ -291,15 +479,6 @@ __device__ __forceinline__ void load_row(const void* p, int64_t at, float (&f)[V
 #pragma unroll
         for (int e = 0; e < Vec<T>::N; ++e) f[e] = 0.f;
     }
-}
-
-__device__ __forceinline__ RowTerms row_terms(const ResidualNorm& a, int64_t r) {
-    RowTerms q{0.f, 1.f, 0.f, 1.f, 0.f, 0.f, 0.f, 0.f};
-    if (a.norm == LAYER) q.mean = a.mean[r];
-    if (a.norm != NONE) q.rstd = a.rstd[r];
-    if (a.post == LAYER) q.mean_post = a.mean_post[r];
-    if (a.post != NONE) q.rstd_post = a.rstd_post[r];
-    return q;
 }
 
 // A block per row: the sums that dx and dbranch need.
@@ -472,19 +651,32 @@ __global__ void __launch_bounds__(32 * PARAM_WARPS) residual_params_kernel(const
     if (a.post == LAYER) add(a.dbias_post, g * s[3]);
 }
 
+// Warps of a team in one pass; 0: two passes.
+int team_warps_of(int64_t C) {
+    const int64_t w = (C + 32 * COLS - 1) / (32 * COLS);
+    return w <= TEAM_WARPS ? static_cast<int>(w) : 0;
+}
+
+constexpr int MAX_SMS = 152;  // of a full GB300; the workspace does not depend on the device
+
 int row_blocks_of(int64_t rows, int64_t C, int dtype) {
+    if (const int w = team_warps_of(C)) {
+        const int64_t teams = TEAM_WARPS / w;
+        return static_cast<int>(std::min<int64_t>((rows + teams - 1) / teams, MAX_SMS));
+    }
     const int64_t nvec = C / (dtype == MMBWD_F32 ? 4 : 8), tiles = (nvec + COL_THREADS - 1) / COL_THREADS;
     // some eight blocks of a column tile to an SM
-    return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(rows, 152 * 8 / tiles)));
+    return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(rows, MAX_SMS * 8 / tiles)));
 }
 
 size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
+size_t sums_bytes(int64_t rows, int64_t C) { return team_warps_of(C) ? 0 : align256(static_cast<size_t>(rows) * 16); }
+
 template <typename T>
-cudaError_t backward(const ResidualNorm& a, int dtype, cudaStream_t stream) {
-    Backward b{a, nullptr, nullptr, 1.f / static_cast<float>(a.C), row_blocks_of(a.rows, a.C, dtype)};
-    b.sums = a.ws;
-    b.partials = a.ws + align256(static_cast<size_t>(a.rows) * 16) / 4;
+cudaError_t backward(const ResidualNorm& a, int dtype, int num_sms, cudaStream_t stream) {
+    Backward b{a, a.ws, a.ws + sums_bytes(a.rows, a.C) / 4, team_warps_of(a.C), 1.f / static_cast<float>(a.C),
+               row_blocks_of(a.rows, a.C, dtype)};
     cudaLaunchConfig_t cfg{};
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -492,13 +684,21 @@ cudaError_t backward(const ResidualNorm& a, int dtype, cudaStream_t stream) {
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     cfg.stream = stream;
-    cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(a.rows, 152 * 8)), 1, 1);
-    cfg.blockDim = dim3(SUM_THREADS, 1, 1);
-    cudaError_t e = cudaLaunchKernelEx(&cfg, residual_sums_kernel<T>, b);
-    if (e != cudaSuccess) return e;
-    cfg.gridDim = dim3(static_cast<unsigned>((a.C / Vec<T>::N + COL_THREADS - 1) / COL_THREADS), static_cast<unsigned>(b.row_blocks), 1);
-    cfg.blockDim = dim3(COL_THREADS, 1, 1);
-    e = cudaLaunchKernelEx(&cfg, residual_cols_kernel<T>, b);
+    cudaError_t e;
+    if (b.team_warps) {
+        b.row_blocks = std::min(b.row_blocks, num_sms);
+        cfg.gridDim = dim3(static_cast<unsigned>(b.row_blocks), 1, 1);
+        cfg.blockDim = dim3(static_cast<unsigned>(32 * b.team_warps * (TEAM_WARPS / b.team_warps)), 1, 1);
+        e = cudaLaunchKernelEx(&cfg, residual_rows_kernel<T>, b);
+    } else {
+        cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(a.rows, MAX_SMS * 8)), 1, 1);
+        cfg.blockDim = dim3(SUM_THREADS, 1, 1);
+        e = cudaLaunchKernelEx(&cfg, residual_sums_kernel<T>, b);
+        if (e != cudaSuccess) return e;
+        cfg.gridDim = dim3(static_cast<unsigned>((a.C / Vec<T>::N + COL_THREADS - 1) / COL_THREADS), static_cast<unsigned>(b.row_blocks), 1);
+        cfg.blockDim = dim3(COL_THREADS, 1, 1);
+        e = cudaLaunchKernelEx(&cfg, residual_cols_kernel<T>, b);
+    }
     if (e != cudaSuccess) return e;
     const bool any = a.dgate || a.dweight_post || a.dbias_post || a.dweight || a.dbias;
     if (!any) return e;
@@ -510,7 +710,7 @@ cudaError_t backward(const ResidualNorm& a, int dtype, cudaStream_t stream) {
 }  // namespace
 
 size_t residual_backward_workspace(int64_t rows, int64_t C, int dtype) {
-    return align256(static_cast<size_t>(rows) * 16) +
+    return sums_bytes(rows, C) +
            align256(static_cast<size_t>(row_blocks_of(rows, C, dtype)) * 4 * static_cast<size_t>(C) * 4);
 }
 
@@ -519,9 +719,9 @@ cudaError_t residual_forward_launch(const ResidualNorm& a, int dtype, int /*num_
     return dtype == MMBWD_F32 ? forward<float>(a, stream) : forward<__nv_bfloat16>(a, stream);
 }
 
-cudaError_t residual_backward_launch(const ResidualNorm& a, int dtype, int /*num_sms*/, cudaStream_t stream) {
+cudaError_t residual_backward_launch(const ResidualNorm& a, int dtype, int num_sms, cudaStream_t stream) {
     if (take_injected_launch_failure()) return cudaErrorLaunchFailure;
-    return dtype == MMBWD_F32 ? backward<float>(a, dtype, stream) : backward<__nv_bfloat16>(a, dtype, stream);
+    return dtype == MMBWD_F32 ? backward<float>(a, dtype, num_sms, stream) : backward<__nv_bfloat16>(a, dtype, num_sms, stream);
 }
 
 }  // namespace mmbwd

@@ -154,7 +154,8 @@ def test_kinds(post, norm, gate, dtype):
         again = backward(x, s, scale, post, norm, dtype, in_place=True)
         for k, v in full.items():
             assert torch.equal(again[k], v), k
-        for skip in (("dbranch",), PARAMS, ("dgate", "dbranch"), ("dweight_post", "dbias")):
+        for skip in (("dbranch",), PARAMS, ("dgate", "dbranch"), ("dweight_post", "dbias"), ("dbranch", "dgate", "dweight_post"),
+                     ("dbranch",) + PARAMS):
             again = backward(x, s, scale, post, norm, dtype, skip=skip)
             for k, v in full.items():
                 if k not in skip:
