@@ -5,9 +5,9 @@
 // keeps it in registers (VPT 16-byte vectors per thread) from the branch's statistics to
 // the output, so nothing is read twice and each variance comes from the differences
 // (LAYER) of values at hand. Backward: four rows read, two written. A team owns a row as
-// well, a thread eight columns of it; it has the next row in flight, forms the row's
+// well, a thread 16 columns of it; it has the next rows in flight, forms the row's
 // four sums in two rounds and keeps its columns' parameter sums in registers over all
-// rows of the team. Rows that no team of 16 warps holds (C > 4096) take two passes: one
+// rows of the team. Rows that no team of 12 warps holds (C > 6144) take two passes: one
 // forms the rows' sums, one goes down column tiles.
 #include "../../include/residual_norm.h"
 #include "ops.h"
@@ -21,7 +21,7 @@
 namespace mmbwd {
 namespace {
 
-constexpr int NONE = LNBWD_NORM_NONE, LAYER = LNBWD_NORM_LAYER, RMS = LNBWD_NORM_RMS;
+constexpr int NONE = LNBWD_NORM_NONE, LAYER = LNBWD_NORM_LAYER;
 
 template <typename T>
 struct Vec;
@@ -68,31 +68,96 @@ __device__ __forceinline__ void column(const void* p, int v, float fill, float (
     }
 }
 
+// Two fp32 values side by side: one instruction works on both, so these kernels issue
+// fewer (8.0 million instead of 13.5 for 8192 x 1600).
+struct F2 {
+    unsigned long long v;
+    __device__ static F2 of(float a, float b) {
+        F2 r;
+        asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+        return r;
+    }
+    __device__ static F2 both(float a) { return of(a, a); }
+    __device__ float lo() const { return __uint_as_float(static_cast<uint32_t>(v)); }
+    __device__ float hi() const { return __uint_as_float(static_cast<uint32_t>(v >> 32)); }
+};
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+    F2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+
+// A 16-byte vector as pairs of fp32 values, and back.
+template <typename T>
+struct Pairs;
+template <>
+struct Pairs<float> {
+    static constexpr int H = 2;
+    __device__ static void get(const uint4& v, F2* f) {
+        f[0] = F2::of(__uint_as_float(v.x), __uint_as_float(v.y));
+        f[1] = F2::of(__uint_as_float(v.z), __uint_as_float(v.w));
+    }
+    __device__ static uint4 put(const F2* f) {
+        return make_uint4(__float_as_uint(f[0].lo()), __float_as_uint(f[0].hi()), __float_as_uint(f[1].lo()), __float_as_uint(f[1].hi()));
+    }
+};
+template <>
+struct Pairs<__nv_bfloat16> {
+    static constexpr int H = 4;
+    __device__ static void get(const uint4& v, F2* f) {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[i] = F2::of(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+    }
+    __device__ static uint4 put(const F2* f) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(f[i].lo(), f[i].hi());
+            w[i] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+};
 __device__ __forceinline__ float warp_sum(float s) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     return s;
 }
 
-// The sum of a team's P warp sums, in warp order, in every thread. Consecutive sums
-// alternate between two sets of slots, so that one barrier per sum is enough.
-template <int P>
+// The sums of R values over a team's P warps, in warp order, in every thread. Consecutive
+// sums alternate between two sets of slots, so that one barrier per sum is enough.
+template <int P, int R>
 struct TeamSum {
-    float* slots;  // 2 P floats
+    float* slots;  // 2 P R floats
     int warp, team, which = 0;
-    __device__ float operator()(float s) {
-        s = warp_sum(s);
-        if constexpr (P == 1) {
-            return s;
-        } else {
-            float* at = slots + which * P;
-            which ^= 1;
-            if ((threadIdx.x & 31) == 0) at[warp] = s;
-            ptx::named_bar_sync(static_cast<uint32_t>(1 + team), 32 * P);
-            float t = at[0];
+    __device__ void operator()(float (&s)[R]) {
 #pragma unroll
-            for (int w = 1; w < P; ++w) t += at[w];
-            return t;
+        for (int k = 0; k < R; ++k) s[k] = warp_sum(s[k]);
+        if constexpr (P > 1) {
+            float* at = slots + which * (P * R);
+            which ^= 1;
+            if ((threadIdx.x & 31) == 0) {
+#pragma unroll
+                for (int k = 0; k < R; ++k) at[warp * R + k] = s[k];
+            }
+            ptx::named_bar_sync(static_cast<uint32_t>(1 + team), 32 * P);
+#pragma unroll
+            for (int k = 0; k < R; ++k) {
+                s[k] = at[k];
+#pragma unroll
+                for (int w = 1; w < P; ++w) s[k] += at[w * R + k];
+            }
         }
     }
 };
@@ -105,143 +170,344 @@ __device__ __forceinline__ float mean_of(float sum, int C, float inv_c) {
     return rest == rest ? fmaf(rest, inv_c, q) : q;
 }
 
+// Teams of a block: four warps' worth, one team of more.
 template <int P>
-constexpr int TEAMS = P == 1 ? 4 : 1;  // teams of one warp share a block of four rows
+constexpr int TEAMS = P < 4 ? 4 / P : 1;
 
 struct Forward {
     ResidualNorm a;
     float inv_c;
 };
 
-// Mean (0 without one) and rstd of the team's row, v[0 .. VPT N) in each thread; the
-// values beyond the row are zero and `last` says whether the last vector is in it.
-template <int KIND, int P, int N, int VPT>
-__device__ __forceinline__ void statistics(const float (&v)[VPT * N], bool last, int C, float inv_c, float eps,
-                                           TeamSum<P>& sum, float* mean, float* rstd) {
-    float m = 0.f;
-    if (KIND == LAYER) {
-        float s = 0.f;
+// Mean (0 without one) and rstd of the team's R rows v; the values beyond a row are zero
+// and `last` says whether the last vector is in it.
+template <int P, int R, int VPT, int H>
+__device__ __forceinline__ void statistics(const F2 (&v)[R][VPT * H], bool layer, bool last, int C, float inv_c, float eps,
+                                           TeamSum<P, R>& sum, float (&mean)[R], float (&rstd)[R]) {
+    float s[R];
 #pragma unroll
-        for (int i = 0; i < VPT * N; ++i) s += v[i];
-        m = mean_of(sum(s), C, inv_c);
-    }
-    float s = 0.f;
+    for (int k = 0; k < R; ++k) mean[k] = 0.f;
+    if (layer) {
 #pragma unroll
-    for (int i = 0; i < VPT * N; ++i) {
-        const float d = i < (VPT - 1) * N || last ? v[i] - m : 0.f;
-        s = fmaf(d, d, s);
+        for (int k = 0; k < R; ++k) {
+            F2 t = v[k][0];
+#pragma unroll
+            for (int i = 1; i < VPT * H; ++i) t = add2(t, v[k][i]);
+            s[k] = t.lo() + t.hi();
+        }
+        sum(s);
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
+            mean[k] = mean_of(s[k], C, inv_c);
+            const F2 m = F2::both(-mean[k]);
+            F2 t = F2::both(0.f), u = F2::both(0.f);  // u: the last vector's
+#pragma unroll
+            for (int i = 0; i < VPT * H; ++i) {
+                const F2 d = add2(v[k][i], m);
+                if (i < (VPT - 1) * H) t = fma2(d, d, t);
+                else u = fma2(d, d, u);
+            }
+            s[k] = t.lo() + t.hi() + (last ? u.lo() + u.hi() : 0.f);
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
+            F2 t = F2::both(0.f);
+#pragma unroll
+            for (int i = 0; i < VPT * H; ++i) t = fma2(v[k][i], v[k][i], t);
+            s[k] = t.lo() + t.hi();
+        }
     }
-    *mean = m;
-    *rstd = 1.f / sqrtf(fmaf(sum(s), inv_c, eps));
+    sum(s);
+#pragma unroll
+    for (int k = 0; k < R; ++k) rstd[k] = 1.f / sqrtf(fmaf(s[k], inv_c, eps));
 }
 
-template <typename T, int P, int VPT>
+// 16 bytes on their way from global into shared memory.
+__device__ __forceinline__ void copy16(uint32_t to, const void* from) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait_but() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// R rows at a time to a team: the columns' weights are read and unpacked once for all of
+// them. AHEAD: the blocks are as many as are resident, and while a team works on its rows
+// the next ones are on their way into shared memory, each thread's vectors to places that
+// only it reads (no barrier); otherwise every team has R rows, loaded into registers.
+template <typename T, int P, int VPT, int R, bool AHEAD>
 __global__ void __launch_bounds__(32 * P * TEAMS<P>) residual_forward_kernel(const __grid_constant__ Forward f) {
-    using V = Vec<T>;
-    constexpr int N = V::N;
-    __shared__ float slots[TEAMS<P>][2 * P];
+    constexpr int N = Vec<T>::N, H = Pairs<T>::H, THREADS = 32 * P * TEAMS<P>;
+    extern __shared__ __align__(16) uint8_t buffer[];
+    __shared__ float slots[TEAMS<P>][2 * P * R];
     const ResidualNorm& a = f.a;
     const int warp = static_cast<int>(threadIdx.x >> 5), lane = static_cast<int>(threadIdx.x & 31);
     const int team = warp / P, wt = warp % P, t = wt * 32 + lane;
     const int nvec = a.C / N;
     const bool last = t + 32 * P * (VPT - 1) < nvec;
+    const uint32_t mine = ptx::smem_u32(buffer) + threadIdx.x * 16u;  // vector j of row k: at (k VPT + j) * 16 * THREADS
+    constexpr uint32_t X = R * VPT * THREADS * 16u;                   // the branch's vectors, then x's
+    if (AHEAD && !last) {  // what is beyond a row stays zero
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
+            ptx::sts128u(mine + (k * VPT + VPT - 1) * (THREADS * 16), make_uint4(0u, 0u, 0u, 0u));
+            ptx::sts128u(mine + X + (k * VPT + VPT - 1) * (THREADS * 16), make_uint4(0u, 0u, 0u, 0u));
+        }
+    }
     ptx::grid_launch_dependents();
     ptx::grid_dependency_wait();
-    const int64_t r = static_cast<int64_t>(blockIdx.x) * TEAMS<P> + team;
-    if (r >= a.rows) return;
-    TeamSum<P> sum{slots[team], wt, team};
-    const uint4* xr = reinterpret_cast<const uint4*>(static_cast<const T*>(a.x) + r * a.C);
-    const uint4* br = reinterpret_cast<const uint4*>(static_cast<const T*>(a.branch) + r * a.C);
-    uint4 x[VPT];
-    float v[VPT * N];
+    const int64_t step = static_cast<int64_t>(gridDim.x) * TEAMS<P> * R;
+    auto request = [&](const void* p, uint32_t to, int64_t r0) {
 #pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-        const bool on = j + 1 < VPT || last;
-        x[j] = on ? xr[t + 32 * P * j] : make_uint4(0u, 0u, 0u, 0u);
-        V::get(on ? br[t + 32 * P * j] : make_uint4(0u, 0u, 0u, 0u), v + j * N);
-    }
-    float mean = 0.f, rstd = 1.f;
-    if (a.post != NONE) {
-        if (a.post == LAYER) {
-            statistics<LAYER, P, N, VPT>(v, last, a.C, f.inv_c, a.eps, sum, &mean, &rstd);
-            if (a.mean_post && t == 0) a.mean_post[r] = mean;
-        } else {
-            statistics<RMS, P, N, VPT>(v, last, a.C, f.inv_c, a.eps, sum, &mean, &rstd);
-        }
-        if (a.rstd_post && t == 0) a.rstd_post[r] = rstd;
-    }
-    uint4* ro = reinterpret_cast<uint4*>(static_cast<T*>(a.residual_out) + r * a.C);
+        for (int k = 0; k < R; ++k) {
+            if (r0 + k < a.rows) {
+                const uint4* row = reinterpret_cast<const uint4*>(static_cast<const T*>(p) + (r0 + k) * a.C);
 #pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-        const int k = t + 32 * P * j;
-        if (j + 1 < VPT || last) {
-            float g[N], xv[N];
-            V::get(x[j], xv);
-            if (a.post != NONE) {
-                float w[N], b[N];
-                column<T>(a.weight_post, k, 1.f, w);
-                column<T>(a.post == LAYER ? a.bias_post : nullptr, k, 0.f, b);
-#pragma unroll
-                for (int e = 0; e < N; ++e) v[j * N + e] = fmaf((v[j * N + e] - mean) * rstd, w[e], b[e]);
+                for (int j = 0; j < VPT; ++j)
+                    if (j + 1 < VPT || last) copy16(to + (k * VPT + j) * (THREADS * 16), row + t + 32 * P * j);
             }
-            column<T>(a.gate, k, 1.f, g);
-#pragma unroll
-            for (int e = 0; e < N; ++e) v[j * N + e] = fmaf(a.scale * g[e], v[j * N + e], xv[e]);
-            ro[k] = V::put(v + j * N);
         }
-    }
-    if (a.norm == NONE) return;
-    if (a.norm == LAYER) {
-        statistics<LAYER, P, N, VPT>(v, last, a.C, f.inv_c, a.eps, sum, &mean, &rstd);
-        if (a.mean && t == 0) a.mean[r] = mean;
-    } else {
-        statistics<RMS, P, N, VPT>(v, last, a.C, f.inv_c, a.eps, sum, &mean, &rstd);
-    }
-    if (a.rstd && t == 0) a.rstd[r] = rstd;
-    uint4* o = reinterpret_cast<uint4*>(static_cast<T*>(a.out) + r * a.C);
+        copies_commit();
+    };
+    TeamSum<P, R> sum{slots[team], wt, team};
+    // The weights of a thread's columns as they are stored, requested ahead of the sums that
+    // they are needed behind (loaded where they are used, 8192 x 1600 with two LayerNorms
+    // took 36 us instead of 25); kept over all rows where a thread has few columns.
+    constexpr bool KEEP = AHEAD && VPT <= 2;
+    static_assert(R == 1 || AHEAD, "rows that are loaded come one at a time");
+    constexpr bool LATE = !AHEAD && VPT > 1;  // 64 registers: x and the weights are fetched where they are used
+    uint4 gate[VPT], weight_post[VPT], bias_post[VPT], weight[VPT], bias[VPT];
+    auto column_of = [&](const void* p, int j) {
+        return p && (j + 1 < VPT || last) ? __ldg(static_cast<const uint4*>(p) + t + 32 * P * j) : make_uint4(0u, 0u, 0u, 0u);
+    };
+    auto columns = [&](const void* p, uint4 (&to)[VPT]) {
 #pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-        const int k = t + 32 * P * j;
-        if (j + 1 < VPT || last) {
-            float w[N], b[N];
-            column<T>(a.weight, k, 1.f, w);
-            column<T>(a.norm == LAYER ? a.bias : nullptr, k, 0.f, b);
+        for (int j = 0; j < VPT; ++j) to[j] = column_of(p, j);
+    };
+    if (KEEP) {
+        columns(a.gate, gate);
+        columns(a.weight_post, weight_post);
+        columns(a.bias_post, bias_post);
+        columns(a.weight, weight);
+        columns(a.bias, bias);
+    }
+    int64_t r0 = (static_cast<int64_t>(blockIdx.x) * TEAMS<P> + team) * R;
+    if (AHEAD) {
+        request(a.branch, mine, r0);
+        request(a.x, mine + X, r0);
+    }
+    for (; r0 < a.rows; r0 += step) {
+        bool there[R];  // (nothing is stored of a row that is not)
 #pragma unroll
-            for (int e = 0; e < N; ++e) w[e] = fmaf((v[j * N + e] - mean) * rstd, w[e], b[e]);
-            __stcs(o + k, V::put(w));
+        for (int k = 0; k < R; ++k) there[k] = r0 + k < a.rows;
+        uint4 x[R][VPT];
+        F2 v[R][VPT * H];
+        if constexpr (AHEAD) {
+            copies_wait_but<1>();  // (x's request is the younger one)
+#pragma unroll
+            for (int k = 0; k < R; ++k)
+#pragma unroll
+                for (int j = 0; j < VPT; ++j) Pairs<T>::get(ptx::lds128(mine + (k * VPT + j) * (THREADS * 16)), v[k] + j * H);
+            request(a.branch, mine, r0 + step);
+        } else {
+            auto load = [&](const void* p, int k, int j) {
+                return (j + 1 < VPT || last) && there[k]
+                           ? reinterpret_cast<const uint4*>(static_cast<const T*>(p) + (r0 + k) * a.C)[t + 32 * P * j]
+                           : make_uint4(0u, 0u, 0u, 0u);
+            };
+#pragma unroll
+            for (int k = 0; k < R; ++k)
+#pragma unroll
+                for (int j = 0; j < VPT; ++j) {
+                    if (!LATE) x[k][j] = load(a.x, k, j);
+                    Pairs<T>::get(load(a.branch, k, j), v[k] + j * H);
+                }
         }
+        float mean[R], rstd[R];
+        if (!KEEP && !LATE) {
+            columns(a.gate, gate);
+            columns(a.weight_post, weight_post);
+            columns(a.bias_post, bias_post);
+        }
+        if (a.post != NONE) {
+            statistics<P, R, VPT, H>(v, a.post == LAYER, last, a.C, f.inv_c, a.eps, sum, mean, rstd);
+#pragma unroll
+            for (int k = 0; k < R; ++k) {
+                if (t == 0 && there[k] && a.mean_post) a.mean_post[r0 + k] = mean[k];
+                if (t == 0 && there[k] && a.rstd_post) a.rstd_post[r0 + k] = rstd[k];
+            }
+        }
+        if constexpr (AHEAD) {
+            copies_wait_but<1>();  // (the next branch's is the younger one)
+#pragma unroll
+            for (int k = 0; k < R; ++k)
+#pragma unroll
+                for (int j = 0; j < VPT; ++j) x[k][j] = ptx::lds128(mine + X + (k * VPT + j) * (THREADS * 16));
+            request(a.x, mine + X, r0 + step);
+        }
+        auto out_row = [&](void* p, int k) { return reinterpret_cast<uint4*>(static_cast<T*>(p) + (r0 + k) * a.C); };
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            const int c = t + 32 * P * j;
+            if (j + 1 < VPT || last) {
+                if (LATE) gate[j] = column_of(a.gate, j), weight_post[j] = column_of(a.weight_post, j), bias_post[j] = column_of(a.bias_post, j);
+                F2 up[H];  // scale * gate
+                if (a.gate) {
+                    Pairs<T>::get(gate[j], up);
+#pragma unroll
+                    for (int i = 0; i < H; ++i) up[i] = mul2(up[i], F2::both(a.scale));
+                } else {
+#pragma unroll
+                    for (int i = 0; i < H; ++i) up[i] = F2::both(a.scale);
+                }
+                if (a.post != NONE) {
+                    F2 w[H];
+                    Pairs<T>::get(weight_post[j], w);
+                    if (a.post == LAYER) {
+                        F2 b[H];
+                        Pairs<T>::get(bias_post[j], b);
+#pragma unroll
+                        for (int k = 0; k < R; ++k)
+#pragma unroll
+                            for (int i = 0; i < H; ++i)
+                                v[k][j * H + i] = fma2(mul2(add2(v[k][j * H + i], F2::both(-mean[k])), F2::both(rstd[k])), w[i], b[i]);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < H; ++i) up[i] = mul2(up[i], w[i]);
+#pragma unroll
+                        for (int k = 0; k < R; ++k)
+#pragma unroll
+                            for (int i = 0; i < H; ++i) v[k][j * H + i] = mul2(v[k][j * H + i], F2::both(rstd[k]));
+                    }
+                }
+#pragma unroll
+                for (int k = 0; k < R; ++k) {
+                    F2 xv[H];
+                    if constexpr (LATE) x[k][j] = reinterpret_cast<const uint4*>(static_cast<const T*>(a.x) + r0 * a.C)[c];
+                    Pairs<T>::get(x[k][j], xv);
+#pragma unroll
+                    for (int i = 0; i < H; ++i) v[k][j * H + i] = fma2(up[i], v[k][j * H + i], xv[i]);
+                    if (there[k]) out_row(a.residual_out, k)[c] = Pairs<T>::put(v[k] + j * H);
+                }
+            }
+        }
+        if (a.norm != NONE) {
+            if (!KEEP && !LATE) {
+                columns(a.weight, weight);
+                columns(a.bias, bias);
+            }
+            statistics<P, R, VPT, H>(v, a.norm == LAYER, last, a.C, f.inv_c, a.eps, sum, mean, rstd);
+#pragma unroll
+            for (int k = 0; k < R; ++k) {
+                if (t == 0 && there[k] && a.mean) a.mean[r0 + k] = mean[k];
+                if (t == 0 && there[k] && a.rstd) a.rstd[r0 + k] = rstd[k];
+            }
+#pragma unroll
+            for (int j = 0; j < VPT; ++j) {
+                const int c = t + 32 * P * j;
+                if (j + 1 < VPT || last) {
+                    if (LATE) weight[j] = column_of(a.weight, j), bias[j] = column_of(a.bias, j);
+                    F2 w[H];
+                    Pairs<T>::get(weight[j], w);
+                    if (a.norm == LAYER) {
+                        F2 b[H];
+                        Pairs<T>::get(bias[j], b);
+#pragma unroll
+                        for (int k = 0; k < R; ++k)
+#pragma unroll
+                            for (int i = 0; i < H; ++i)
+                                v[k][j * H + i] = fma2(mul2(add2(v[k][j * H + i], F2::both(-mean[k])), F2::both(rstd[k])), w[i], b[i]);
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < R; ++k)
+#pragma unroll
+                            for (int i = 0; i < H; ++i) v[k][j * H + i] = mul2(mul2(v[k][j * H + i], F2::both(rstd[k])), w[i]);
+                    }
+#pragma unroll
+                    for (int k = 0; k < R; ++k)
+                        if (there[k]) __stcs(out_row(a.out, k) + c, Pairs<T>::put(v[k] + j * H));
+                }
+            }
+        }
+        if (!AHEAD) break;
     }
 }
 
-// The kernel whose team holds a row in exactly `need` vectors a thread, VPT to MOST.
-template <typename T, int P, int VPT, int MOST>
-cudaError_t launch_team(const Forward& f, int need, cudaStream_t stream) {
-    if constexpr (VPT < MOST) {
-        if (need > VPT) return launch_team<T, P, VPT + 1, MOST>(f, need, stream);
+// Dynamic shared memory of a kernel allowed up to `bytes` on the current device, once; the
+// caller holds the library's lock.
+template <auto kernel>
+cudaError_t allow_smem(int bytes) {
+    static bool done[64];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess || (dev >= 0 && dev < 64 && done[dev])) return e;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess && dev >= 0 && dev < 64) done[dev] = true;
+    return e;
+}
+
+template <typename T, int P, int VPT, int R, bool AHEAD>
+cudaError_t launch_forward(const Forward& f, int num_sms, cudaStream_t stream) {
+    constexpr auto kernel = residual_forward_kernel<T, P, VPT, R, AHEAD>;
+    constexpr int threads = 32 * P * TEAMS<P>, smem = AHEAD ? 2 * R * VPT * threads * 16 : 0;
+    int64_t blocks = (f.a.rows + TEAMS<P> * R - 1) / (TEAMS<P> * R);
+    if (AHEAD) {
+        int per_sm = 0;
+        cudaError_t e = allow_smem<kernel>(smem);
+        if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, smem);
+        if (e != cudaSuccess) return e;
+        blocks = std::min<int64_t>(blocks, static_cast<int64_t>(num_sms) * std::max(per_sm, 1));
     }
-    const int64_t blocks = (f.a.rows + TEAMS<P> - 1) / TEAMS<P>;
     if (blocks > INT32_MAX) return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>(blocks), 1, 1);
-    cfg.blockDim = dim3(32 * P * TEAMS<P>, 1, 1);
+    cfg.blockDim = dim3(threads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, residual_forward_kernel<T, P, VPT>, f);
+    return cudaLaunchKernelEx(&cfg, kernel, f);
 }
 
+// The kernel whose team holds a row in exactly `need` vectors a thread, VPT to MOST.
+template <typename T, int P, int VPT, int MOST, int R, bool AHEAD>
+cudaError_t launch_team(const Forward& f, int need, int num_sms, cudaStream_t stream) {
+    if constexpr (VPT < MOST) {
+        if (need > VPT) return launch_team<T, P, VPT + 1, MOST, R, AHEAD>(f, need, num_sms, stream);
+    }
+    return launch_forward<T, P, VPT, R, AHEAD>(f, num_sms, stream);
+}
+
+// By the row's 16-byte vectors. Measured, us (post and norm RMS with a gate / norm LAYER
+// alone, bf16): 8192 x 768 a warp per row 11.1 / 10.4, four warps and two rows 11.8 / 11.4;
+// 8192 x 1600 four warps and two rows at a time 19.8 / 19.5, a warp 21.6 / 20.2, two warps 21.9
+// / 20.7, eight 24.2 / 22.6; 4096 x 4096 eight warps 24.3 / 24.1, with two rows 27.2 / 26.1, sixteen 29.1
+// / 27.4; 2000 x 8192 eight warps of four vectors 24.2 / 23.0, sixteen of two 25.0 / 24.8. Few
+// rows: as many warps as have a vector each, one row (512 x 1600 3.4, 1 x 1600 2.1; in teams
+// of two warps 4.7 and 3.3).
 template <typename T>
-cudaError_t forward(const ResidualNorm& a, cudaStream_t stream) {
+cudaError_t forward(const ResidualNorm& a, int num_sms, cudaStream_t stream) {
     const Forward f{a, 1.f / static_cast<float>(a.C)};
     const int nvec = a.C / Vec<T>::N;
-    if (nvec <= 32 * 8) return launch_team<T, 1, 1, 8>(f, (nvec + 31) / 32, stream);
-    if (nvec <= 128 * 4) return launch_team<T, 4, 3, 4>(f, (nvec + 127) / 128, stream);
-    if (nvec <= 256 * 4) return launch_team<T, 8, 3, 4>(f, (nvec + 255) / 256, stream);
-    if (nvec <= 512 * 4) return launch_team<T, 16, 3, 4>(f, (nvec + 511) / 512, stream);
-    return launch_team<T, 32, 3, LNBWD_RESIDUAL_MAX_C / Vec<T>::N / 1024>(f, (nvec + 1023) / 1024, stream);
+    if (a.rows <= 4 * num_sms && nvec <= 1024) {
+        if (nvec <= 32) return launch_forward<T, 1, 1, 1, false>(f, num_sms, stream);
+        if (nvec <= 64) return launch_forward<T, 2, 1, 1, false>(f, num_sms, stream);
+        if (nvec <= 128) return launch_forward<T, 4, 1, 1, false>(f, num_sms, stream);
+        if (nvec <= 256) return launch_forward<T, 8, 1, 1, false>(f, num_sms, stream);
+        if (nvec <= 512) return launch_forward<T, 16, 1, 1, false>(f, num_sms, stream);
+        return launch_forward<T, 32, 1, 1, false>(f, num_sms, stream);
+    }
+    if (nvec <= 32 * 4) return launch_team<T, 1, 1, 4, 1, true>(f, (nvec + 31) / 32, num_sms, stream);
+    if (nvec <= 128 * 2) return launch_forward<T, 4, 2, 2, true>(f, num_sms, stream);
+    if (nvec <= 256 * 4) return launch_team<T, 8, 2, 4, 1, true>(f, (nvec + 255) / 256, num_sms, stream);
+    if (nvec <= 512 * 4) return launch_team<T, 16, 3, 4, 1, true>(f, (nvec + 511) / 512, num_sms, stream);
+    // (64 registers a thread: some of a row goes through local memory, and no row is ahead)
+    return launch_team<T, 32, 3, LNBWD_RESIDUAL_MAX_C / Vec<T>::N / 1024, 1, false>(f, (nvec + 1023) / 1024, num_sms, stream);
 }
 
 // ---------------------------------------------------------------- backward
@@ -277,183 +543,195 @@ struct Backward {
     ResidualNorm a;
     float* sums;      // [rows][4]: a, c, e, h (two passes)
     float* partials;  // [row blocks][4][C]: dweight, dbias, sum dx z, sum dx
-    int team_warps;   // one pass: warps of a team
     float inv_c;
     int row_blocks;
 };
 
 // ---- one pass
 
-constexpr int COLS = 8;         // columns of a thread
-constexpr int TEAM_WARPS = 16;  // warps of a block, at most
-
-// A thread's eight values of a row, as they are stored.
-template <typename T>
-struct Eight {
-    static constexpr int V = 8 / Vec<T>::N;
-    uint4 v[V];
-    // `p` at the row's first value; vector i is there if `on[i]`
-    __device__ void load(const T* p, int c0, const bool (&on)[V]) {
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-            v[i] = p && on[i] ? reinterpret_cast<const uint4*>(p + c0)[i] : make_uint4(0u, 0u, 0u, 0u);
-    }
-    __device__ void get(float (&f)[8]) const {
-#pragma unroll
-        for (int i = 0; i < V; ++i) Vec<T>::get(v[i], f + i * Vec<T>::N);
-    }
-};
-template <typename T>
-__device__ __forceinline__ void store8(T* p, int c0, const bool (&on)[Eight<T>::V], const float (&f)[8]) {
-#pragma unroll
-    for (int i = 0; i < Eight<T>::V; ++i)
-        if (on[i]) reinterpret_cast<uint4*>(p + c0)[i] = Vec<T>::put(f + i * Vec<T>::N);
-}
-
-// Two sums over a team, in warp order, in every thread; `at`: the team's slots. Consecutive
-// sums of a team alternate between two sets of slots, so that one barrier is enough.
-__device__ __forceinline__ float2 team_sum2(float x, float y, float2* at, int warp, int warps, int team) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        x += __shfl_xor_sync(0xffffffffu, x, o);
-        y += __shfl_xor_sync(0xffffffffu, y, o);
-    }
-    if (warps == 1) return make_float2(x, y);
-    if ((threadIdx.x & 31) == 0) at[warp] = make_float2(x, y);
-    ptx::named_bar_sync(static_cast<uint32_t>(1 + team), static_cast<uint32_t>(32 * warps));
-    float2 t = at[0];
-#pragma unroll
-    for (int w = 1; w < TEAM_WARPS; ++w)
-        if (w < warps) t.x += at[w].x, t.y += at[w].y;
-    return t;
-}
+constexpr int ROW_WARPS = 12;  // warps of a block: 168 registers to a thread
+constexpr int COLS = 16;       // columns of a thread, in vectors 32 P apart
 
 template <typename T>
-struct RowData {
-    Eight<T> dout, res, dres, branch;
-    float mean, rstd, mean_post, rstd_post;
-};
-
+constexpr int RING = sizeof(T) == 2 ? 3 : 2;  // rows of a thread on their way or in use
 template <typename T>
-__global__ void __launch_bounds__(32 * TEAM_WARPS, 1) residual_rows_kernel(const __grid_constant__ Backward b) {
-    constexpr int V = Eight<T>::V;
-    __shared__ float2 slots[TEAM_WARPS][2][TEAM_WARPS];
-    __shared__ float joined[4 * 256 * (TEAM_WARPS / 2)];  // teams of at most half the warps are joined
+constexpr int ROW_BYTES = 4 * COLS * static_cast<int>(sizeof(T));  // of a thread: dout, residual, dresidual, branch
+
+// A team of P warps owns a row; a thread has the same 16 columns of all of its rows, their
+// weights and their sums in registers. The next rows are on their way into shared
+// memory, each thread's vectors to places that only it reads (no barrier).
+template <typename T, int P>
+__global__ void __launch_bounds__(32 * ROW_WARPS, 1) residual_rows_kernel(const __grid_constant__ Backward b) {
+    constexpr int N = Vec<T>::N, H = Pairs<T>::H, V = COLS / N, E = COLS / 2, TEAMS_ROWS = ROW_WARPS / P, THREADS = 32 * ROW_WARPS;
+    extern __shared__ __align__(16) uint8_t ring[];
+    __shared__ float slots[TEAMS_ROWS][2 * P * 2];
     const ResidualNorm& a = b.a;
-    const int warps = b.team_warps, warp = static_cast<int>(threadIdx.x >> 5), lane = static_cast<int>(threadIdx.x & 31);
-    const int teams = static_cast<int>(blockDim.x >> 5) / warps, team = warp / warps, wt = warp % warps;
-    const int c0 = (wt * 32 + lane) * COLS;
-    bool on[V];
-#pragma unroll
-    for (int i = 0; i < V; ++i) on[i] = c0 + i * Vec<T>::N < a.C;
+    const int warp = static_cast<int>(threadIdx.x >> 5), lane = static_cast<int>(threadIdx.x & 31);
+    const int team = warp / P, wt = warp % P, t = wt * 32 + lane;
+    const int nvec = a.C / N;
     const bool norm = a.norm != NONE, post = a.post != NONE;
-    float2* at = slots[team][0];
-    int which = 0;
+    const uint32_t mine = ptx::smem_u32(ring) + threadIdx.x * 16u;
+    constexpr uint32_t PART = V * THREADS * 16u, SLOT = 4 * PART;  // vector j of tensor i of a slot: at i PART + j 16 THREADS
+    // what is not there, a whole tensor or a vector beyond the row, is zero throughout
+    const void* tensors[4] = {a.dout, a.residual, a.dresidual, a.branch};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+            if (!tensors[i] || t + 32 * P * j >= nvec)
+                for (int k = 0; k < RING<T>; ++k) ptx::sts128u(mine + k * SLOT + i * PART + j * (THREADS * 16), make_uint4(0u, 0u, 0u, 0u));
     ptx::grid_launch_dependents();
     ptx::grid_dependency_wait();
-    // the weights of a thread's columns, 0 beyond the row: nothing there adds to a sum
-    float w[8], gw[8];  // gw: scale * gate * weight_post
-    {
-        Eight<T> t;
-        t.load(static_cast<const T*>(a.weight), c0, on);
-        t.get(w);
-        t.load(static_cast<const T*>(a.weight_post), c0, on);
-        t.get(gw);
-        float g[8];
-        t.load(static_cast<const T*>(a.gate), c0, on);
-        t.get(g);
+    const int64_t step = static_cast<int64_t>(gridDim.x) * TEAMS_ROWS, first = static_cast<int64_t>(blockIdx.x) * TEAMS_ROWS + team;
+    int64_t ahead = first;  // the next row to request, into slot `into`
+    uint32_t into = 0, from = 0;
+    auto request = [&]() {
+        if (ahead < a.rows) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float one = on[i / Vec<T>::N] ? 1.f : 0.f;
-            gw[i] = (post ? gw[i] : one) * (a.scale * (a.gate ? g[i] : one));
+            for (int i = 0; i < 4; ++i) {
+                if (!tensors[i]) continue;
+                const uint4* row = reinterpret_cast<const uint4*>(static_cast<const T*>(tensors[i]) + ahead * a.C);
+#pragma unroll
+                for (int j = 0; j < V; ++j)
+                    if (t + 32 * P * j < nvec) copy16(mine + into + i * PART + j * (THREADS * 16), row + t + 32 * P * j);
+            }
+        }
+        copies_commit();
+        ahead += step;
+        into = into + SLOT == RING<T> * SLOT ? 0 : into + SLOT;
+    };
+#pragma unroll
+    for (int i = 0; i + 1 < RING<T>; ++i) request();
+    // the weights of a thread's columns, 0 beyond the row: nothing there adds to a sum
+    uint4 w[V];
+    F2 gw[E], s[4][E];  // gw: scale * gate * weight_post
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        const int v = t + 32 * P * j;
+        w[j] = make_uint4(0u, 0u, 0u, 0u);
+        if (v < nvec && a.weight) w[j] = __ldg(static_cast<const uint4*>(a.weight) + v);
+        F2 f[H];
+#pragma unroll
+        for (int i = 0; i < H; ++i) gw[j * H + i] = F2::both(v < nvec ? a.scale : 0.f);
+        if (v < nvec && a.gate) {
+            Pairs<T>::get(__ldg(static_cast<const uint4*>(a.gate) + v), f);
+#pragma unroll
+            for (int i = 0; i < H; ++i) gw[j * H + i] = mul2(gw[j * H + i], f[i]);
+        }
+        if (v < nvec && a.weight_post) {
+            Pairs<T>::get(__ldg(static_cast<const uint4*>(a.weight_post) + v), f);
+#pragma unroll
+            for (int i = 0; i < H; ++i) gw[j * H + i] = mul2(gw[j * H + i], f[i]);
         }
     }
-    float s[4][8];
 #pragma unroll
     for (int k = 0; k < 4; ++k)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) s[k][i] = 0.f;
-
-    auto fetch = [&](RowData<T>& q, int64_t r) {
-        const int64_t o = r * a.C;
-        auto row = [&](const void* p) { return p ? static_cast<const T*>(p) + o : nullptr; };
-        q.dout.load(row(a.dout), c0, on);
-        q.res.load(row(a.residual), c0, on);
-        q.dres.load(row(a.dresidual), c0, on);
-        q.branch.load(row(a.branch), c0, on);
-        const RowTerms t = row_terms(a, r);
-        q.mean = t.mean, q.rstd = t.rstd, q.mean_post = t.mean_post, q.rstd_post = t.rstd_post;
-    };
-    const int64_t stride = static_cast<int64_t>(gridDim.x) * teams;
-    int64_t r = static_cast<int64_t>(blockIdx.x) * teams + team;
-    RowData<T> q, next;
-    if (r < a.rows) fetch(q, r);
-    for (; r < a.rows; r += stride) {
-        if (r + stride < a.rows) fetch(next, r + stride);
-        float dx[8], z[8];
-        q.dres.get(dx);
+        for (int i = 0; i < E; ++i) s[k][i] = F2::both(0.f);
+    TeamSum<P, 2> sum{slots[team], wt, team};
+    RowTerms q, next;
+    if (first < a.rows) q = row_terms(a, first);
+    for (int64_t r = first; r < a.rows; r += step) {
+        if (r + step < a.rows) next = row_terms(a, r + step);
+        copies_wait_but<RING<T> - 2>();
+        request();  // into the slot of the row before this one
+        auto take = [&](int i, F2 (&f)[E]) {
+#pragma unroll
+            for (int j = 0; j < V; ++j) Pairs<T>::get(ptx::lds128(mine + from + i * PART + j * (THREADS * 16)), f + j * H);
+        };
+        auto put = [&](void* p, const F2 (&f)[E]) {
+            uint4* row = reinterpret_cast<uint4*>(static_cast<T*>(p) + r * a.C);
+#pragma unroll
+            for (int j = 0; j < V; ++j)
+                if (t + 32 * P * j < nvec) row[t + 32 * P * j] = Pairs<T>::put(f + j * H);
+        };
+        F2 dx[E];
+        take(2, dx);
         if (norm) {
-            float d[8], n[8], g[8], s0 = 0.f, s1 = 0.f;
-            q.dout.get(d);
-            q.res.get(n);
+            F2 n[E], g[E], s0 = F2::both(0.f), s1 = F2::both(0.f);
+            take(0, g);
+            take(1, n);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                n[i] = (n[i] - q.mean) * q.rstd;
-                g[i] = w[i] * d[i];
-                s0 += g[i];
-                s1 = fmaf(g[i], n[i], s1);
-                s[0][i] = fmaf(d[i], n[i], s[0][i]);
-                s[1][i] += d[i];
+            for (int i = 0; i < E; ++i) {
+                n[i] = mul2(add2(n[i], F2::both(-q.mean)), F2::both(q.rstd));
+                s[0][i] = fma2(g[i], n[i], s[0][i]);
+                s[1][i] = add2(s[1][i], g[i]);
             }
-            const float2 t = team_sum2(s0, s1, at + which, wt, warps, team);
-            which ^= TEAM_WARPS;
-            const float m = a.norm == LAYER ? t.x * b.inv_c : 0.f, c = t.y * b.inv_c;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) dx[i] = fmaf(q.rstd, g[i] - fmaf(n[i], c, m), dx[i]);
+            for (int j = 0; j < V; ++j) {
+                F2 wj[H];
+                Pairs<T>::get(w[j], wj);
+#pragma unroll
+                for (int i = 0; i < H; ++i) {
+                    g[j * H + i] = mul2(g[j * H + i], wj[i]);
+                    s0 = add2(s0, g[j * H + i]);
+                    s1 = fma2(g[j * H + i], n[j * H + i], s1);
+                }
+            }
+            float both[2] = {s0.lo() + s0.hi(), s1.lo() + s1.hi()};
+            sum(both);
+            const F2 m = F2::both(a.norm == LAYER ? -both[0] * b.inv_c : 0.f), c = F2::both(-both[1] * b.inv_c);
+#pragma unroll
+            for (int i = 0; i < E; ++i) dx[i] = fma2(F2::both(q.rstd), add2(g[i], fma2(n[i], c, m)), dx[i]);
         }
-        store8(static_cast<T*>(a.dx) + r * a.C, c0, on, dx);
-        q.branch.get(z);
-        float y[8], s0 = 0.f, s1 = 0.f;
+        put(a.dx, dx);
+        F2 z[E], s0 = F2::both(0.f), s1 = F2::both(0.f);
+        take(3, z);
+        from = from + SLOT == RING<T> * SLOT ? 0 : from + SLOT;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            z[i] = (z[i] - q.mean_post) * q.rstd_post;
-            y[i] = gw[i] * dx[i];
-            s0 += y[i];
-            s1 = fmaf(y[i], z[i], s1);
-            s[2][i] = fmaf(dx[i], z[i], s[2][i]);
-            s[3][i] += dx[i];
+        for (int i = 0; i < E; ++i) {
+            z[i] = mul2(add2(z[i], F2::both(-q.mean_post)), F2::both(q.rstd_post));
+            s[2][i] = fma2(dx[i], z[i], s[2][i]);
+            s[3][i] = add2(s[3][i], dx[i]);
+            dx[i] = mul2(gw[i], dx[i]);
+            s0 = add2(s0, dx[i]);
+            s1 = fma2(dx[i], z[i], s1);
         }
         if (a.dbranch) {
             if (post) {
-                const float2 t = team_sum2(s0, s1, at + which, wt, warps, team);
-                which ^= TEAM_WARPS;
-                const float m = a.post == LAYER ? t.x * b.inv_c : 0.f, c = t.y * b.inv_c;
+                float both[2] = {s0.lo() + s0.hi(), s1.lo() + s1.hi()};
+                sum(both);
+                const F2 m = F2::both(a.post == LAYER ? -both[0] * b.inv_c : 0.f), c = F2::both(-both[1] * b.inv_c);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) y[i] = q.rstd_post * (y[i] - fmaf(z[i], c, m));
+                for (int i = 0; i < E; ++i) dx[i] = mul2(F2::both(q.rstd_post), add2(dx[i], fma2(z[i], c, m)));
             }
-            store8(static_cast<T*>(a.dbranch) + r * a.C, c0, on, y);
+            put(a.dbranch, dx);
         }
         q = next;
     }
 
-    // The block's sums over its rows: the teams' in team order.
+    // The block's sums over its rows: the teams' in team order, through the ring's memory.
+    copies_wait_but<0>();
+    __syncthreads();
+    float4* joined = reinterpret_cast<float4*>(ring);
     float* to = b.partials + static_cast<int64_t>(blockIdx.x) * 4 * a.C;
-    for (int k = 0; k < teams; ++k) {
-        if (teams > 1) __syncthreads();
+    for (int k = 0; k < TEAMS_ROWS; ++k) {
+        if (k > 0) __syncthreads();
         if (team != k) continue;
 #pragma unroll
         for (int f = 0; f < 4; ++f)
 #pragma unroll
-            for (int i = 0; i < 8; i += 4) {
-                float4 v = make_float4(s[f][i], s[f][i + 1], s[f][i + 2], s[f][i + 3]);
-                if (teams > 1) {
-                    float4* mine = reinterpret_cast<float4*>(joined + f * 256 * warps + c0 + i);
-                    if (k > 0) v.x += mine->x, v.y += mine->y, v.z += mine->z, v.w += mine->w;
-                    if (k + 1 < teams) *mine = v;
-                }
-                if (k + 1 == teams && c0 + i < a.C) *reinterpret_cast<float4*>(to + static_cast<int64_t>(f) * a.C + c0 + i) = v;
+            for (int i = 0; i < E; i += 2) {
+                const int j = i / H, c = (t + 32 * P * j) * N + 2 * (i % H);
+                float4 v = make_float4(s[f][i].lo(), s[f][i].hi(), s[f][i + 1].lo(), s[f][i + 1].hi());
+                float4* at = joined + (f * E / 2 + i / 2) * (32 * P) + t;
+                if (k > 0) v.x += at->x, v.y += at->y, v.z += at->z, v.w += at->w;
+                if (k + 1 < TEAMS_ROWS) *at = v;
+                else if (c < a.C) *reinterpret_cast<float4*>(to + static_cast<int64_t>(f) * a.C + c) = v;
             }
     }
+}
+
+template <typename T, int P>
+cudaError_t launch_rows(const Backward& b, cudaLaunchConfig_t cfg) {
+    constexpr auto kernel = residual_rows_kernel<T, P>;
+    constexpr int smem = RING<T> * ROW_BYTES<T> * 32 * ROW_WARPS;
+    static_assert(smem >= 4 * COLS * 4 * 32 * P && smem <= 220 * 1024, "the ring holds a team's sums, a block the ring");
+    cfg.gridDim = dim3(static_cast<unsigned>(b.row_blocks), 1, 1);
+    cfg.blockDim = dim3(32 * ROW_WARPS, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    const cudaError_t e = allow_smem<kernel>(smem);
+    return e == cudaSuccess ? cudaLaunchKernelEx(&cfg, kernel, b) : e;
 }
 
 // ---- two passes
@@ -651,17 +929,18 @@ __global__ void __launch_bounds__(32 * PARAM_WARPS) residual_params_kernel(const
     if (a.post == LAYER) add(a.dbias_post, g * s[3]);
 }
 
-// Warps of a team in one pass; 0: two passes.
-int team_warps_of(int64_t C) {
-    const int64_t w = (C + 32 * COLS - 1) / (32 * COLS);
-    return w <= TEAM_WARPS ? static_cast<int>(w) : 0;
-}
-
 constexpr int MAX_SMS = 152;  // of a full GB300; the workspace does not depend on the device
+
+// Warps of a team in one pass, a divisor of a block's; 0: two passes.
+int team_warps_of(int64_t C) {
+    for (const int w : {1, 2, 3, 4, 6, 12})
+        if (C <= 32 * w * COLS) return w;
+    return 0;
+}
 
 int row_blocks_of(int64_t rows, int64_t C, int dtype) {
     if (const int w = team_warps_of(C)) {
-        const int64_t teams = TEAM_WARPS / w;
+        const int64_t teams = ROW_WARPS / w;
         return static_cast<int>(std::min<int64_t>((rows + teams - 1) / teams, MAX_SMS));
     }
     const int64_t nvec = C / (dtype == MMBWD_F32 ? 4 : 8), tiles = (nvec + COL_THREADS - 1) / COL_THREADS;
@@ -675,8 +954,7 @@ size_t sums_bytes(int64_t rows, int64_t C) { return team_warps_of(C) ? 0 : align
 
 template <typename T>
 cudaError_t backward(const ResidualNorm& a, int dtype, int num_sms, cudaStream_t stream) {
-    Backward b{a, a.ws, a.ws + sums_bytes(a.rows, a.C) / 4, team_warps_of(a.C), 1.f / static_cast<float>(a.C),
-               row_blocks_of(a.rows, a.C, dtype)};
+    Backward b{a, a.ws, a.ws + sums_bytes(a.rows, a.C) / 4, 1.f / static_cast<float>(a.C), row_blocks_of(a.rows, a.C, dtype)};
     cudaLaunchConfig_t cfg{};
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -685,11 +963,14 @@ cudaError_t backward(const ResidualNorm& a, int dtype, int num_sms, cudaStream_t
     cfg.numAttrs = 1;
     cfg.stream = stream;
     cudaError_t e;
-    if (b.team_warps) {
+    if (const int w = team_warps_of(a.C)) {
         b.row_blocks = std::min(b.row_blocks, num_sms);
-        cfg.gridDim = dim3(static_cast<unsigned>(b.row_blocks), 1, 1);
-        cfg.blockDim = dim3(static_cast<unsigned>(32 * b.team_warps * (TEAM_WARPS / b.team_warps)), 1, 1);
-        e = cudaLaunchKernelEx(&cfg, residual_rows_kernel<T>, b);
+        e = w == 1   ? launch_rows<T, 1>(b, cfg)
+            : w == 2 ? launch_rows<T, 2>(b, cfg)
+            : w == 3 ? launch_rows<T, 3>(b, cfg)
+            : w == 4 ? launch_rows<T, 4>(b, cfg)
+            : w == 6 ? launch_rows<T, 6>(b, cfg)
+                     : launch_rows<T, 12>(b, cfg);
     } else {
         cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(a.rows, MAX_SMS * 8)), 1, 1);
         cfg.blockDim = dim3(SUM_THREADS, 1, 1);
@@ -714,9 +995,9 @@ size_t residual_backward_workspace(int64_t rows, int64_t C, int dtype) {
            align256(static_cast<size_t>(row_blocks_of(rows, C, dtype)) * 4 * static_cast<size_t>(C) * 4);
 }
 
-cudaError_t residual_forward_launch(const ResidualNorm& a, int dtype, int /*num_sms*/, cudaStream_t stream) {
+cudaError_t residual_forward_launch(const ResidualNorm& a, int dtype, int num_sms, cudaStream_t stream) {
     if (take_injected_launch_failure()) return cudaErrorLaunchFailure;
-    return dtype == MMBWD_F32 ? forward<float>(a, stream) : forward<__nv_bfloat16>(a, stream);
+    return dtype == MMBWD_F32 ? forward<float>(a, num_sms, stream) : forward<__nv_bfloat16>(a, num_sms, stream);
 }
 
 cudaError_t residual_backward_launch(const ResidualNorm& a, int dtype, int num_sms, cudaStream_t stream) {
