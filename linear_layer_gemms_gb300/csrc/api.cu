@@ -1191,6 +1191,8 @@ int mmbwd_forward_act(void* out, void* pre, const void* inp, const void* weight,
     cudaError_t e = cudaSuccess;
     if (C == 0)
         e = act_rows_launch(out, pre, bias, residual, s.BT, OC, act, dtype, stream);
+    else if (tokens_act_takes(s.BT, C, OC, dtype, d->num_sms))
+        e = tokens_act_launch(out, pre, inp, weight, bias, residual, s.BT, C, OC, act, dtype, stream);
     else if (dtype == MMBWD_F32)
         e = simt_forward_act_launch(static_cast<float*>(out), static_cast<float*>(pre), static_cast<const float*>(inp),
                                     static_cast<const float*>(weight), static_cast<const float*>(bias),

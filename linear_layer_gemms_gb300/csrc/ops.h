@@ -100,6 +100,11 @@ cudaError_t simt_forward_act_launch(float* out, float* pre, const float* inp, co
 cudaError_t simt_run_act_launch(float* dpre, float* dweight, float* dbias, const float* dout, const float* inp,
                                 const float* weight, const float* pre, int64_t BT, int64_t C, int64_t OC, int act,
                                 cudaStream_t stream);
+// The forward for few tokens, either type.
+bool tokens_act_takes(int64_t T, int64_t K, int64_t N, int dtype, int num_sms);
+cudaError_t tokens_act_launch(void* out, void* pre, const void* inp, const void* weight, const void* bias,
+                              const void* residual, int64_t T, int64_t K, int64_t N, int act, int dtype,
+                              cudaStream_t stream);
 // dpre = dout * act'(pre), n values
 cudaError_t act_backward_launch(void* dpre, const void* dout, const void* pre, int64_t n, int act, int dtype,
                                 cudaStream_t stream);
