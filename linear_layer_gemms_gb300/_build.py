@@ -20,7 +20,7 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libmmbwd.so")
 SOURCES = ["api.cu", "tc_gemm.cu", "simt_f32.cu", "layernorm_bwd.cu", "split_tf32.cu", "encoder_bwd.cu",
            "layernorm_fwd.cu", "q8_quantize.cu", "q8_product.cu", "q8_tokens.cu", "act_rows.cu", "residual_norm.cu",
-           "grad_clip.cu", "tokens_act.cu"]
+           "grad_clip.cu", "tokens_act.cu", "simt_small.cu"]
 HEADERS = ["act.cuh", "internal.h", "ops.h", "ptx.cuh", "q8.h", "q8.cuh", "sr.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

@@ -73,7 +73,7 @@ struct NvtxRange {
 // schedule search is cached so that a call costs a table lookup.
 struct PlanKey {
     int64_t BT, C, OC;
-    int sms, fwd;
+    int sms, fwd;  // fwd: 0 the backward, 1 the forward, 2 and 3 the fp32 forward and backward in spans
     long splitk, grid, tile_n;
     bool operator==(const PlanKey& o) const {
         return BT == o.BT && C == o.C && OC == o.OC && sms == o.sms && fwd == o.fwd && splitk == o.splitk &&
@@ -106,7 +106,10 @@ const TcPlan& cached_plan(int64_t BT, int64_t C, int64_t OC, int sms, int fwd = 
     g_plan_next = (g_plan_next + 1) % kPlanCache;
     if (g_plan_count < kPlanCache) ++g_plan_count;
     g_plan_keys[slot] = k;
-    g_plans[slot] = fwd ? tc_make_plan_forward(BT, C, OC, sms) : tc_make_plan(BT, C, OC, sms);
+    g_plans[slot] = fwd == 3   ? tc_make_plan_span(BT, C, OC, OC, sms)
+                    : fwd == 2 ? tc_make_plan_span(BT, OC, C, 0, sms)
+                    : fwd      ? tc_make_plan_forward(BT, C, OC, sms)
+                               : tc_make_plan(BT, C, OC, sms);
     return g_plans[slot];
 }
 
@@ -1164,6 +1167,22 @@ namespace {
 
 bool act_ok(int act) { return act >= MMBWD_ACT_NONE && act <= MMBWD_ACT_RELU; }
 
+// Caller holds g_mutex.
+cudaError_t forward_act_f32(ActPath path, float* out, float* pre, const float* inp, const float* weight, const float* bias,
+                            const float* residual, int64_t BT, int64_t C, int64_t OC, int act, int sms, cudaStream_t stream) {
+    if (path == ActPath::SPANS)
+        return tc_launch_span_forward(cached_plan(BT, C, OC, sms, 2), out, pre, inp, weight, bias, residual, BT, C, OC, act, stream);
+    return simt_small_forward_launch(path == ActPath::SMALL_32 ? 32 : 64, out, pre, inp, weight, bias, residual, BT, C, OC, act, stream);
+}
+
+cudaError_t run_act_f32(ActPath path, float* dpre, float* dweight, float* dbias, const float* dout, const float* inp,
+                        const float* weight, const float* pre, int64_t BT, int64_t C, int64_t OC, int act, int sms,
+                        cudaStream_t stream) {
+    if (path == ActPath::SPANS)
+        return tc_launch_span_run(cached_plan(BT, C, OC, sms, 3), dpre, dweight, dbias, dout, inp, weight, pre, BT, C, OC, act, stream);
+    return simt_small_run_launch(path == ActPath::SMALL_32 ? 32 : 64, dpre, dweight, dbias, dout, inp, weight, pre, BT, C, OC, act, stream);
+}
+
 }  // namespace
 
 int mmbwd_forward_act(void* out, void* pre, const void* inp, const void* weight, const void* bias, const void* residual,
@@ -1191,12 +1210,14 @@ int mmbwd_forward_act(void* out, void* pre, const void* inp, const void* weight,
     cudaError_t e = cudaSuccess;
     if (C == 0)
         e = act_rows_launch(out, pre, bias, residual, s.BT, OC, act, dtype, stream);
-    else if (tokens_act_takes(s.BT, C, OC, dtype, d->num_sms))
+    else if (dtype == MMBWD_F32 ? act_forward_path(s.BT, C, OC, d->num_sms) == ActPath::TOKENS
+                                : tokens_act_takes_bf16(s.BT, C, OC, d->num_sms))
         e = tokens_act_launch(out, pre, inp, weight, bias, residual, s.BT, C, OC, act, dtype, stream);
     else if (dtype == MMBWD_F32)
-        e = simt_forward_act_launch(static_cast<float*>(out), static_cast<float*>(pre), static_cast<const float*>(inp),
-                                    static_cast<const float*>(weight), static_cast<const float*>(bias),
-                                    static_cast<const float*>(residual), s.BT, C, OC, act, stream);
+        e = forward_act_f32(act_forward_path(s.BT, C, OC, d->num_sms), static_cast<float*>(out), static_cast<float*>(pre),
+                            static_cast<const float*>(inp), static_cast<const float*>(weight),
+                            static_cast<const float*>(bias), static_cast<const float*>(residual), s.BT, C, OC, act,
+                            d->num_sms, stream);
     else
         e = tc_launch_forward_act(cached_plan(s.BT, C, OC, d->num_sms, 1), out, pre, inp, weight, bias, residual, s.BT,
                                   C, OC, act, stream);
@@ -1250,9 +1271,10 @@ int mmbwd_run_act(void* dpre, void* dweight, void* dbias, const void* dout, cons
     } else if (C == 0) {
         if (dbias) e = colsum_launch(dbias, dout, s.BT, OC, dtype, false, 0, stream);
     } else if (dtype == MMBWD_F32) {
-        e = simt_run_act_launch(static_cast<float*>(dpre), static_cast<float*>(dweight), static_cast<float*>(dbias),
-                                static_cast<const float*>(dout), static_cast<const float*>(inp),
-                                static_cast<const float*>(weight), static_cast<const float*>(pre), s.BT, C, OC, act, stream);
+        e = run_act_f32(act_run_path(s.BT, C, OC, d->num_sms), static_cast<float*>(dpre), static_cast<float*>(dweight),
+                        static_cast<float*>(dbias), static_cast<const float*>(dout), static_cast<const float*>(inp),
+                        static_cast<const float*>(weight), static_cast<const float*>(pre), s.BT, C, OC, act, d->num_sms,
+                        stream);
     } else {
         e = tc_launch(*plan, dpre, dweight, dbias, dout, inp, weight, s.BT, C, OC, workspace, stream, false, 0, pre, act);
     }

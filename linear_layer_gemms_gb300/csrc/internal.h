@@ -71,7 +71,7 @@ struct TcPlan {
     int n_dinp_items;  // dinp_tiles_m * dinp_tiles_n
     int n_items;
     int table;         // 1: per-pair item lists in `sched`; 0: round-robin
-    int x3;            // fp32 (three tf32 products, operands split in the kernel): tf32 item costs
+    int x3;            // fp32 (three tf32 products, operands split in the kernel): tf32 item costs; 2: in spans
     int x3_corr;       // fp32: the correction products in their own accumulator
     int grid;          // CTAs (twice the number of CTA pairs)
     double est_us;     // the planner's time estimate
@@ -117,6 +117,12 @@ struct TcParams {
     int act;                        // MMBWD_ACT_*
     int has_pre;                    // MODE 4: the argument of the activation is stored too
     const __nv_bfloat16* residual;  // MODE 4; may be null, may be the output
+    // MODE 6: the forward (bias and pre may be null; x3_aux: the residual or null) or the
+    // backward (x3_aux: pre). x3_aux may be the output.
+    int x3_forward;
+    const float* x3_bias;
+    float* x3_pre;
+    const float* x3_aux;
 };
 
 // MODE 2 reductions longer than this keep the two correction products in an
@@ -163,6 +169,18 @@ TcPlan tc_make_plan_x3_pair(int64_t BT, int64_t C, int64_t OC, int num_sms);
 cudaError_t tc_launch_x3_pair(const TcPlan& plan, float* dinp, float* dweight, float* dbias, const float* dout,
                               const float* inp, const float* weight, int64_t BT, int64_t C, int64_t OC,
                               cudaStream_t stream);
+// The same three products with the accumulators added up in registers (MODE 6), for the
+// epilogues with an activation: out = act(inp . weight^T + bias) + residual (pre, bias and
+// residual may be null, residual may be out); dpre = (dout . weight) * act'(pre) (dpre may
+// be pre), dweight += dout^T . inp, dbias = column sums of dout (may be null). Plans: of a
+// product M x N over K, and of one dw_rows x N over M (0: none).
+TcPlan tc_make_plan_span(int64_t M, int64_t N, int64_t K, int64_t dw_rows, int num_sms);
+cudaError_t tc_launch_span_forward(const TcPlan& plan, float* out, float* pre, const float* inp, const float* weight,
+                                   const float* bias, const float* residual, int64_t BT, int64_t C, int64_t OC, int act,
+                                   cudaStream_t stream);
+cudaError_t tc_launch_span_run(const TcPlan& plan, float* dpre, float* dweight, float* dbias, const float* dout,
+                               const float* inp, const float* weight, const float* pre, int64_t BT, int64_t C, int64_t OC,
+                               int act, cudaStream_t stream);
 cudaError_t tc_launch_forward(const TcPlan& plan, void* out, const void* inp, const void* weight,
                               const void* bias, int64_t BT, int64_t C, int64_t OC, cudaStream_t stream);
 // out = act(inp . weight^T + bias) + residual, and the activation's argument in pre; pre,

@@ -92,16 +92,22 @@ cudaError_t ln_read_status(int* code, int* info3, bool reset);
 
 // ---------------------------------------------------------------- epilogues with an activation
 
-// fp32 on the CUDA cores: out = act(inp . weight^T + bias) + residual, pre (may be
-// null) the argument of act; dpre = (dout . weight) * act'(pre).
-cudaError_t simt_forward_act_launch(float* out, float* pre, const float* inp, const float* weight, const float* bias,
-                                    const float* residual, int64_t BT, int64_t C, int64_t OC, int act,
-                                    cudaStream_t stream);
-cudaError_t simt_run_act_launch(float* dpre, float* dweight, float* dbias, const float* dout, const float* inp,
-                                const float* weight, const float* pre, int64_t BT, int64_t C, int64_t OC, int act,
-                                cudaStream_t stream);
-// The forward for few tokens, either type.
-bool tokens_act_takes(int64_t T, int64_t K, int64_t N, int dtype, int num_sms);
+// fp32 on the CUDA cores: out = act(inp . weight^T + bias) + residual, pre (may be null)
+// the argument of act; dpre = (dout . weight) * act'(pre), dweight and dbias as in the
+// backward. `tile`: 32 or 64.
+cudaError_t simt_small_forward_launch(int tile, float* out, float* pre, const float* inp, const float* weight,
+                                      const float* bias, const float* residual, int64_t BT, int64_t C, int64_t OC,
+                                      int act, cudaStream_t stream);
+cudaError_t simt_small_run_launch(int tile, float* dpre, float* dweight, float* dbias, const float* dout,
+                                  const float* inp, const float* weight, const float* pre, int64_t BT, int64_t C,
+                                  int64_t OC, int act, cudaStream_t stream);
+// Which kernel takes these products in fp32.
+enum class ActPath { TOKENS, SMALL_32, SMALL_64, SPANS };  // tokens_act.cu, the two above, tc_launch_span_*
+ActPath act_forward_path(int64_t BT, int64_t C, int64_t OC, int num_sms);
+ActPath act_run_path(int64_t BT, int64_t C, int64_t OC, int num_sms);
+// The forward for few tokens: 64 at most (ACT_TOKENS).
+constexpr int64_t ACT_TOKENS = 64;
+bool tokens_act_takes_bf16(int64_t T, int64_t K, int64_t N, int num_sms);
 cudaError_t tokens_act_launch(void* out, void* pre, const void* inp, const void* weight, const void* bias,
                               const void* residual, int64_t T, int64_t K, int64_t N, int act, int dtype,
                               cudaStream_t stream);

@@ -15,7 +15,6 @@
 // the dout tile they stage in shared memory over its K (= BT) rows, in K order,
 // and overwrite dbias. No split of K, so each output has one writer.
 #include "../../include/mmbwd.h"
-#include "act.cuh"
 #include "ops.h"
 #include "ptx.cuh"
 #include "sr.cuh"
@@ -32,18 +31,11 @@ constexpr int PAD = 4;  // keeps 16-byte alignment of smem rows
 // or stored as (K x M) row-major (A_KM = true); B is (K x N) row-major, or
 // stored as (N x K) row-major (B_NK = true). With OVERWRITE, D = A . B + bias
 // (bias per column, may be null) instead of the accumulation.
-// EPI (with OVERWRITE): 1: s = A . B + bias into x.pre, if wanted, and D = act(s) +
-// x.residual (may be D); 2: D = (A . B) * act'(x.pre) (x.pre may be D).
-struct Extra {
-    float* pre = nullptr;
-    const float* residual = nullptr;
-    int act = 0;
-};
-template <bool A_KM, bool B_NK = false, bool OVERWRITE = false, int EPI = 0>
+template <bool A_KM, bool B_NK = false, bool OVERWRITE = false>
 __global__ void __launch_bounds__(SIMT_THREADS, 2)
-    simt_gemm_acc(float* D, const float* __restrict__ A, const float* __restrict__ Bm,
+    simt_gemm_acc(float* __restrict__ D, const float* __restrict__ A, const float* __restrict__ Bm,
                   int64_t M, int64_t N, int64_t K, float* __restrict__ dbias,
-                  const float* __restrict__ col_bias = nullptr, const Extra x = {}) {
+                  const float* __restrict__ col_bias = nullptr) {
     __shared__ __align__(16) float As[2][BK][BM + PAD];
     __shared__ __align__(16) float Bs[2][BK][BN + PAD];
 
@@ -159,25 +151,6 @@ __global__ void __launch_bounds__(SIMT_THREADS, 2)
             o.y += acc[i][h * 4 + 1];
             o.z += acc[i][h * 4 + 2];
             o.w += acc[i][h * 4 + 3];
-            if constexpr (EPI == 1) {
-                if (x.pre) *reinterpret_cast<float4*>(x.pre + m * N + n) = o;
-                float4 r = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (x.residual) r = *reinterpret_cast<const float4*>(x.residual + m * N + n);
-                act::with(x.act, [&](auto a) {
-                    constexpr int ACT = decltype(a)::value;
-                    o.x = act::value<ACT, false>(o.x), o.y = act::value<ACT, false>(o.y);
-                    o.z = act::value<ACT, false>(o.z), o.w = act::value<ACT, false>(o.w);
-                });
-                if (x.residual) o.x += r.x, o.y += r.y, o.z += r.z, o.w += r.w;
-            }
-            if constexpr (EPI == 2) {
-                const float4 r = *reinterpret_cast<const float4*>(x.pre + m * N + n);
-                act::with(x.act, [&](auto a) {
-                    constexpr int ACT = decltype(a)::value;
-                    o.x *= act::slope<ACT, false>(r.x), o.y *= act::slope<ACT, false>(r.y);
-                    o.z *= act::slope<ACT, false>(r.z), o.w *= act::slope<ACT, false>(r.w);
-                });
-            }
             *p = o;
         }
     }
@@ -226,28 +199,6 @@ cudaError_t simt_forward_launch(float* out, const float* inp, const float* weigh
     dim3 grid(static_cast<unsigned>((BT + BM - 1) / BM), static_cast<unsigned>((OC + BN - 1) / BN));
     if (grid.x && grid.y)
         simt_gemm_acc<false, true, true><<<grid, SIMT_THREADS, 0, stream>>>(out, inp, weight, BT, OC, C, nullptr, bias);
-    return cudaGetLastError();
-}
-
-cudaError_t simt_forward_act_launch(float* out, float* pre, const float* inp, const float* weight, const float* bias,
-                                    const float* residual, int64_t BT, int64_t C, int64_t OC, int act,
-                                    cudaStream_t stream) {
-    if (take_injected_launch_failure()) return cudaErrorLaunchFailure;
-    dim3 grid(static_cast<unsigned>((BT + BM - 1) / BM), static_cast<unsigned>((OC + BN - 1) / BN));
-    const Extra x{pre, residual, act};
-    simt_gemm_acc<false, true, true, 1><<<grid, SIMT_THREADS, 0, stream>>>(out, inp, weight, BT, OC, C, nullptr, bias, x);
-    return cudaGetLastError();
-}
-
-cudaError_t simt_run_act_launch(float* dpre, float* dweight, float* dbias, const float* dout, const float* inp,
-                                const float* weight, const float* pre, int64_t BT, int64_t C, int64_t OC, int act,
-                                cudaStream_t stream) {
-    if (take_injected_launch_failure()) return cudaErrorLaunchFailure;
-    const Extra x{const_cast<float*>(pre), nullptr, act};
-    dim3 rows(static_cast<unsigned>((BT + BM - 1) / BM), static_cast<unsigned>((C + BN - 1) / BN));
-    simt_gemm_acc<false, false, true, 2><<<rows, SIMT_THREADS, 0, stream>>>(dpre, dout, weight, BT, C, OC, nullptr, nullptr, x);
-    dim3 cols(static_cast<unsigned>((OC + BM - 1) / BM), static_cast<unsigned>((C + BN - 1) / BN));
-    simt_gemm_acc<true><<<cols, SIMT_THREADS, 0, stream>>>(dweight, dout, inp, OC, C, BT, dbias);
     return cudaGetLastError();
 }
 

@@ -102,7 +102,7 @@ constexpr int PART_CHUNK_BYTES = 32 * 32 * 4;
 // second (the split warps of both CTAs, on the even CTA's copy).
 template <int MODE>
 struct Smem {
-    static constexpr bool X3 = MODE == 2;
+    static constexpr bool X3 = MODE == 2 || MODE == 6;
     static constexpr int STAGES = X3 ? TC_STAGES_X3 : TC_STAGES;
     static constexpr int STG_BYTES = X3 ? 2 * STAGE_BYTES : STAGE_BYTES;
     // Epilogue warps: in the bf16 modes two per tensor-memory lane quadrant, each
@@ -138,6 +138,11 @@ struct Smem {
     static_assert(SMEM_TOTAL <= 227 * 1024, "shared memory budget");
 };
 constexpr int SMEM_TOTAL = Smem<0>::SMEM_TOTAL > Smem<2>::SMEM_TOTAL ? Smem<0>::SMEM_TOTAL : Smem<2>::SMEM_TOTAL;
+
+// MODE 6: k-blocks (of 32) that a pair of accumulators takes before they are read back.
+// Relative error (2-norm) of the sums at any length: 6e-7 with 4, 9e-7 with 8, in the same time
+// (2048 x 1600 -> 2400 110 us with either); without, 1.2e-5 at 1600 values.
+constexpr int X3_SPAN = 4;
 
 constexpr unsigned long long DEFAULT_TIMEOUT_NS = 2000000000ull;  // 2 s per wait
 
@@ -364,8 +369,11 @@ __device__ __forceinline__ void x3_split_mn(uint32_t hi, uint32_t lo, int nbox, 
 // read-modify-write epilogue. MODE 3: the backward with stochastic rounding of the bf16 outputs
 // (seeded; sr.cuh). MODE 4: the forward with an activation and a residual in its
 // epilogue (mmbwd_forward_act). MODE 5: the backward whose dinp items are overwritten
-// with the product times act'(pre) (mmbwd_run_act). Six instantiations, so that none
-// pays for the others' branches.
+// with the product times act'(pre) (mmbwd_run_act). MODE 6: MODE 2's products for both of
+// these in fp32, with the accumulators read back every X3_SPAN k-blocks and added up in
+// registers: the tensor core rounds toward zero, an addition in registers to nearest, so
+// that the error does not grow with the reduction. Seven instantiations, so that none pays for
+// the others' branches.
 template <int MODE>
 __global__ void __launch_bounds__(Smem<MODE>::THREADS, 1)
     tc_mmbwd_kernel(const __grid_constant__ CUtensorMap tm_dout_k,   // dout, A of dinp (K-major)
@@ -393,8 +401,9 @@ __global__ void __launch_bounds__(Smem<MODE>::THREADS, 1)
                     const TcParams p, const __grid_constant__ TcSchedule sch) {
     constexpr bool EPI = MODE == 4;               // forward: activation, residual, pre
     constexpr bool DACT = MODE == 5;              // backward: dinp = product * act'(pre)
-    constexpr bool FWD = MODE == 1 || MODE == 2 || EPI;  // dinp-type items only, K-major B
-    constexpr bool X3 = MODE == 2;                // fp32 from three tf32 products
+    constexpr bool SPAN = MODE == 6;              // fp32, accumulators added up in registers
+    constexpr bool X3 = MODE == 2 || SPAN;        // fp32 from three tf32 products
+    constexpr bool FWD = MODE == 1 || X3 || EPI;  // dinp-type items only, K-major B
     constexpr bool SR = MODE == 3;                // stochastic rounding of the outputs
     // MODE 2 stages hold A hi | A lo | B hi | B lo (twice the bytes, half the
     // stages: the same shared memory) and 32 fp32 of K per k-block (128 bytes).
@@ -504,7 +513,7 @@ __global__ void __launch_bounds__(Smem<MODE>::THREADS, 1)
                 // Output tile of this CTA, prefetched into L2 a few k-blocks before the
                 // main loop ends so that the epilogue's read of the old values hits L2.
                 // (forward: nothing to read back but MODE 4's residual)
-                const bool direct = X3 || (EPI ? p.residual != nullptr : !(it.is_dw && p.splits > 1) && !FWD);
+                const bool direct = SPAN ? it.is_dw || p.x3_aux != nullptr : X3 || (EPI ? p.residual != nullptr : !(it.is_dw && p.splits > 1) && !FWD);
                 const int64_t out_rows = it.is_dw ? p.OC : p.BT;
                 const int pf_kb = max(it.kb0, it.kb1 - 8);
                 // A of a bf16 dweight item, or an MN-major fp32 A: 64-row boxes
@@ -619,13 +628,26 @@ __global__ void __launch_bounds__(Smem<MODE>::THREADS, 1)
                     }
                     prev_bias = bias_item;
                     ptx::tc_fence_after();
-                    const uint32_t d_tmem = tmem_base + acc * acc_cols;
+                    uint32_t d_tmem = tmem_base + acc * acc_cols;
                     const uint32_t d_bias = tmem_base + (acc ^ 1u) * TC_BN;
                     const uint32_t ones = base + L::OFF_ONES;
                     const uint32_t idesc = X3 ? ptx::idesc_tf32_f32(TC_PAIR_BM, it.bn, 0, 0)
                                               : ptx::idesc_bf16_f32(TC_PAIR_BM, it.bn, /*A MN*/ it.is_dw,
                                                                     /*B MN*/ FWD ? 0 : 1);
                     for (int kb = it.kb0; kb < it.kb1; ++kb) {
+                        if (SPAN && kb > it.kb0 && (kb - it.kb0) % X3_SPAN == 0) {  // the next span, into the other set
+                            ptx::mma_commit_pair_multicast(bars + 8u * (BAR_TFULL + acc), pair_mask);
+                            if (++acc == acc_sets) {
+                                acc = 0;
+                                acc_phase ^= 1u;
+                            }
+                            if (!wt.wait(bars + 8u * (BAR_TEMPTY + acc), acc_phase ^ 1u, SITE_MMA_TMEM_EMPTY, w)) {
+                                ok = false;
+                                break;
+                            }
+                            ptx::tc_fence_after();
+                            d_tmem = tmem_base + acc * acc_cols;
+                        }
                         // Both CTAs' copies of this stage have landed (own bytes +
                         // the odd CTA's forwarded arrival); MODE 2: both CTAs'
                         // split warps have written the planes.
@@ -656,7 +678,7 @@ __global__ void __launch_bounds__(Smem<MODE>::THREADS, 1)
                                 // reductions: hi.hi alone in the main accumulator, hi.lo +
                                 // lo.hi (about 2^-11 of it) in the correction accumulator
                                 // beside it; short ones: all three in one.
-                                const uint32_t acc0 = (kb > it.kb0 || k > 0) ? 1u : 0u;
+                                const uint32_t acc0 = ((SPAN ? (kb - it.kb0) % X3_SPAN != 0 : kb > it.kb0) || k > 0) ? 1u : 0u;
                                 const uint32_t d_corr = corr ? d_tmem + it.bn : d_tmem;
                                 ptx::mma_tf32_pair(d_tmem, ah, bh, idesc, acc0);
                                 ptx::mma_tf32_pair(d_corr, ah, bl, idesc, corr ? acc0 : 1u);
@@ -974,7 +996,7 @@ __global__ void __launch_bounds__(Smem<MODE>::THREADS, 1)
                     }
                 }
             };
-            if constexpr (X3) x3_load_old(0, olda, oldb);
+            if constexpr (X3 && !SPAN) x3_load_old(0, olda, oldb);
             // MODE 4: this thread's row of the residual's first chunk, likewise; each
             // later chunk's is requested while the chunk before is worked on
             uint4 res[4];
@@ -989,6 +1011,109 @@ __global__ void __launch_bounds__(Smem<MODE>::THREADS, 1)
             if constexpr (EPI) {
                 if (p.residual && qrow0 + lane < rows_total) resrow = p.residual + (qrow0 + lane) * n_extent + col0;
                 load_res(0, res);
+            }
+            if constexpr (SPAN) {
+                // The spans' accumulators, main and correction, added up in order: row `lane` of
+                // the quadrant, all 128 columns.
+                float sum[4][32];
+                bool fine = true;
+                for (int kb = it.kb0; kb < it.kb1; kb += X3_SPAN) {
+                    const bool landed = wt.wait_warp(bars + 8u * (BAR_TFULL + acc), acc_phase, SITE_EPI_TMEM_FULL, w);
+                    fine = ptx::named_bar_and(1, L::EPI_THREADS, landed);
+                    if (!fine) break;
+                    ptx::tc_fence_after();
+                    const uint32_t at = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * acc_cols;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t v[32];
+                        ptx::tmem_ld32(at + c * 32, v);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) sum[c][e] = kb > it.kb0 ? sum[c][e] + __uint_as_float(v[e]) : __uint_as_float(v[e]);
+                        ptx::tmem_ld32(at + 128 + c * 32, v);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) sum[c][e] += __uint_as_float(v[e]);
+                    }
+                    ptx::tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive_cluster_relaxed(leader_tempty + 8u * acc);
+                    if (++acc == acc_sets) {
+                        acc = 0;
+                        acc_phase ^= 1u;
+                    }
+                }
+                if (!fine) break;
+                // out = act(sum + bias) + residual (and pre), or sum * act'(pre), for the
+                // dinp-type items, dweight += sum: row by row into the staging buffer, back out
+                // as 8 rows x 32 columns per instruction. The loops over the activation are not
+                // unrolled (four of them at each of 128 places), so what is loaded from global
+                // memory is loaded ahead of them.
+                const float* aux = it.is_dw ? Df : p.x3_aux;
+                const bool forward = !it.is_dw && p.x3_forward != 0, slope = !it.is_dw && !p.x3_forward;
+                const uint32_t own = stg + (r8 * STG_STRIDE + cg) * 4;  // this thread's four values of row r8
+                auto place = [&](int i) { return own + (8 * (i / 2) * STG_STRIDE + 4 * (i & 1)) * 4; };  // of row 8 (i / 2) + r8
+                auto there = [&](int c, int i) { return qrow0 + 8 * (i / 2) + r8 < rows_total && c * 32 + cg + 4 * (i & 1) < ncols; };
+                auto where = [&](int c, int i) { return (qrow0 + 8 * (i / 2) + r8) * n_extent + col0 + c * 32 + cg + 4 * (i & 1); };
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    float4 a4[8], b4[2];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        a4[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                        if (aux && there(c, i)) a4[i] = *reinterpret_cast<const float4*>(aux + where(c, i));
+                    }
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        b4[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                        if (forward && p.x3_bias && c * 32 + cg + 4 * i < ncols)
+                            b4[i] = __ldg(reinterpret_cast<const float4*>(p.x3_bias + col0 + c * 32 + cg + 4 * i));
+                    }
+                    if (slope) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) ptx::sts128(place(i), a4[i].x, a4[i].y, a4[i].z, a4[i].w);
+#pragma unroll 2
+                        for (int i = 0; i < 8; ++i) {
+                            float4 x = ptx::lds128f(place(i));
+                            act::with(p.act, [&](auto kind) {
+                                constexpr int ACT = decltype(kind)::value;
+                                x.x = act::slope<ACT, true>(x.x), x.y = act::slope<ACT, true>(x.y);
+                                x.z = act::slope<ACT, true>(x.z), x.w = act::slope<ACT, true>(x.w);
+                            });
+                            ptx::sts128(place(i), x.x, x.y, x.z, x.w);
+                        }
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) a4[i] = ptx::lds128f(place(i));
+                        __syncwarp();
+                    }
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        ptx::sts128(stg + (lane * STG_STRIDE + 4 * k) * 4, sum[c][4 * k], sum[c][4 * k + 1], sum[c][4 * k + 2], sum[c][4 * k + 3]);
+                    __syncwarp();
+                    if (forward) {
+#pragma unroll 2
+                        for (int i = 0; i < 8; ++i) {
+                            float4 o = ptx::lds128f(place(i));
+                            const float4 b = i & 1 ? b4[1] : b4[0];
+                            o.x += b.x, o.y += b.y, o.z += b.z, o.w += b.w;
+                            if (p.x3_pre && there(c, i)) *reinterpret_cast<float4*>(p.x3_pre + where(c, i)) = o;
+                            act::with(p.act, [&](auto kind) {
+                                constexpr int ACT = decltype(kind)::value;
+                                o.x = act::value<ACT, true>(o.x), o.y = act::value<ACT, true>(o.y);
+                                o.z = act::value<ACT, true>(o.z), o.w = act::value<ACT, true>(o.w);
+                            });
+                            ptx::sts128(place(i), o.x, o.y, o.z, o.w);
+                        }
+                    }
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        if (!there(c, i)) continue;
+                        float4 o = ptx::lds128f(place(i));
+                        if (slope) o.x *= a4[i].x, o.y *= a4[i].y, o.z *= a4[i].z, o.w *= a4[i].w;
+                        else o.x += a4[i].x, o.y += a4[i].y, o.z += a4[i].z, o.w += a4[i].w;
+                        *reinterpret_cast<float4*>(Df + where(c, i)) = o;
+                    }
+                    __syncwarp();
+                }
+                continue;
             }
             bool ok = wt.wait_warp(bars + 8u * (BAR_TFULL + acc), acc_phase, SITE_EPI_TMEM_FULL, w);
             if (!ptx::named_bar_and(1, L::EPI_THREADS, ok)) break;
@@ -1220,7 +1345,7 @@ __global__ void __launch_bounds__(Smem<MODE>::THREADS, 1)
                 }
             }
             if (!ptx::named_bar_and(1, L::EPI_THREADS, ok)) break;
-            if constexpr (X3) {  // MODE 2: fp32 read-modify-write through staging rows
+            if constexpr (X3 && !SPAN) {  // MODE 2: fp32 read-modify-write through staging rows
 #pragma unroll 1
                 for (int c = 0; c < nchunks; ++c) {
                     float4 nxa[4], nxb[4];
@@ -1410,6 +1535,7 @@ double x3_item_us(int kb, int bn, bool corr) { return kb * (bn == 256 ? 0.99 : 0
 ItemCost item_cost(const TcPlan& pl, int w) {
     if (pl.x3) {
         const bool dw = w < pl.n_dw_items;
+        if (pl.x3 == 2) return {(dw ? pl.dw_kb : pl.dinp_kb) * 0.72 + 4.0, 0.0};  // spans
         return {x3_item_us(dw ? pl.dw_kb : pl.dinp_kb, dw ? pl.dw_bn : pl.dinp_bn, pl.x3_corr != 0), 0.0};
     }
     if (w < pl.n_dw_items) {
@@ -1706,6 +1832,7 @@ struct MapSpec {
 cudaError_t launch_common(const TcPlan& plan, const MapSpec (&specs)[6], TcParams& p, int mode, cudaStream_t stream,
                           const MapSpec* pair_specs = nullptr, const MapSpec* aux = nullptr) {
     const bool bwd = mode == 0 || mode == 3 || mode == 5;  // bf16 backward
+    const bool x3 = mode == 2 || mode == 6;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
@@ -1723,6 +1850,8 @@ cudaError_t launch_common(const TcPlan& plan, const MapSpec (&specs)[6], TcParam
                 e = cudaFuncSetAttribute(tc_mmbwd_kernel<4>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_TOTAL);
             if (e == cudaSuccess)
                 e = cudaFuncSetAttribute(tc_mmbwd_kernel<5>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_TOTAL);
+            if (e == cudaSuccess)
+                e = cudaFuncSetAttribute(tc_mmbwd_kernel<6>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_TOTAL);
             if (e != cudaSuccess) return e;
             if (dev >= 0 && dev < 64) g_attr_set[dev] = true;
         }
@@ -1733,11 +1862,11 @@ cudaError_t launch_common(const TcPlan& plan, const MapSpec (&specs)[6], TcParam
     for (int i = 0; i < 6; ++i) {
         const MapSpec& m = i == 4 && aux ? *aux : specs[i];
         const cuuint64_t dims[2] = {m.inner, m.outer};
-        const uint64_t es = mode == 2 ? 4 : 2;
+        const uint64_t es = x3 ? 4 : 2;
         const cuuint64_t strides[1] = {m.pitch ? m.pitch : m.inner * es};
         const cuuint32_t box[2] = {m.box_inner, m.box_outer};
         const cuuint32_t estr[2] = {1, 1};
-        const CUresult r = encode(&maps[i], mode == 2 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+        const CUresult r = encode(&maps[i], x3 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
                                   2, const_cast<void*>(m.base),
                                   dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, m.swz,
                                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
@@ -1782,7 +1911,7 @@ cudaError_t launch_common(const TcPlan& plan, const MapSpec (&specs)[6], TcParam
     for (int i = 0; i < 3; ++i) {
         CUtensorMap& map = maps[i == 2 ? 12 : 9 + i];
         map = maps[4];  // placeholder where unused
-        if (i == 2 ? !aux : mode == 2 || (mode == 1 && i == 1)) continue;  // the forward writes through map 9
+        if (x3 || (i == 2 ? !aux : mode == 1 && i == 1)) continue;  // the forward writes through map 9
         const MapSpec& m = i == 2 ? *aux : specs[4 + i];
         const cuuint64_t dims[2] = {m.inner, m.outer};
         const cuuint64_t strides[1] = {m.inner * 2};
@@ -1797,7 +1926,7 @@ cudaError_t launch_common(const TcPlan& plan, const MapSpec (&specs)[6], TcParam
     // as rows of dw_bn floats, stored in 32 x 32 boxes (128-byte swizzle).
     // fp32 launches with the dweight product too: its raw A and B in maps 6
     // and 7 (slots the bf16 modes use for other maps)
-    if (mode == 2 && pair_specs) {
+    if (x3 && pair_specs) {
         for (int i = 0; i < 2; ++i) {
             const MapSpec& m = pair_specs[i];
             const cuuint64_t dims[2] = {m.inner, m.outer};
@@ -1840,7 +1969,7 @@ cudaError_t launch_common(const TcPlan& plan, const MapSpec (&specs)[6], TcParam
 
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>(plan.grid), 1, 1);
-    cfg.blockDim = dim3(mode == 2 ? Smem<2>::THREADS : Smem<0>::THREADS, 1, 1);
+    cfg.blockDim = dim3(x3 ? Smem<2>::THREADS : Smem<0>::THREADS, 1, 1);
     cfg.dynamicSmemBytes = SMEM_TOTAL;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
@@ -1859,6 +1988,9 @@ cudaError_t launch_common(const TcPlan& plan, const MapSpec (&specs)[6], TcParam
                                plan.sched);
     else if (mode == 1)
         e = cudaLaunchKernelEx(&cfg, tc_mmbwd_kernel<1>, maps[0], maps[1], maps[2], maps[3], maps[4], maps[5], maps[6], maps[7], maps[8], maps[9], maps[10], maps[11], maps[12], p,
+                               plan.sched);
+    else if (mode == 6)
+        e = cudaLaunchKernelEx(&cfg, tc_mmbwd_kernel<6>, maps[0], maps[1], maps[2], maps[3], maps[4], maps[5], maps[6], maps[7], maps[8], maps[9], maps[10], maps[11], maps[12], p,
                                plan.sched);
     else if (mode == 4)
         e = cudaLaunchKernelEx(&cfg, tc_mmbwd_kernel<4>, maps[0], maps[1], maps[2], maps[3], maps[4], maps[5], maps[6], maps[7], maps[8], maps[9], maps[10], maps[11], maps[12], p,
@@ -2063,6 +2195,81 @@ cudaError_t tc_launch_x3_pair(const TcPlan& plan, float* dinp, float* dweight, f
     p.dinp = reinterpret_cast<__nv_bfloat16*>(dinp);
     p.dweight = reinterpret_cast<__nv_bfloat16*>(dweight);
     return launch_common(plan, specs, p, 2, stream, pair);
+}
+
+// Items of 256 x 128: two sets of a main and a correction accumulator fill tensor memory.
+TcPlan tc_make_plan_span(int64_t M, int64_t N, int64_t K, int64_t dw_rows, int num_sms) {
+    TcPlan c{};
+    c.x3 = 2;
+    c.x3_corr = 1;
+    c.dinp_bn = c.dw_bn = 128;
+    c.dinp_kb = ceil_div_i(K, TC_BK / 2);
+    c.dw_kb = dw_rows > 0 ? ceil_div_i(M, TC_BK / 2) : 0;
+    c.dinp_tiles_m = ceil_div_i(M, TC_PAIR_BM);
+    c.dw_tiles_m = ceil_div_i(dw_rows, TC_PAIR_BM);
+    c.dinp_tiles_n = c.dw_tiles_n = ceil_div_i(N, 128);
+    c.n_dinp_items = c.dinp_tiles_m * c.dinp_tiles_n;
+    c.n_dw_items = c.dw_tiles_m * c.dw_tiles_n;
+    c.n_items = c.n_dinp_items + c.n_dw_items;
+    c.splits = 1;
+    c.kb_per_split = std::max(c.dw_kb, c.dinp_kb);
+    const int pairs = std::max(1, std::min(c.n_items, std::max(1, std::min(num_sms / 2, TC_MAX_PAIRS))));
+    c.grid = 2 * pairs;
+    c.table = c.n_items <= TC_MAX_SCHED_ITEMS ? 1 : 0;
+    c.est_us = c.table ? assign_lpt(c, pairs) : roundrobin_cost(c, pairs);
+    return c;
+}
+
+cudaError_t tc_launch_span_forward(const TcPlan& plan, float* out, float* pre, const float* inp, const float* weight,
+                                   const float* bias, const float* residual, int64_t BT, int64_t C, int64_t OC, int act,
+                                   cudaStream_t stream) {
+    if (take_injected_launch_failure()) return cudaErrorLaunchFailure;
+    const uint64_t bt = static_cast<uint64_t>(BT), c = static_cast<uint64_t>(C), oc = static_cast<uint64_t>(OC);
+    const MapSpec a = x3_operand(inp, false, bt, c, C, TC_BM), b = x3_operand(weight, false, oc, c, C, 64);
+    const MapSpec d{out, oc, bt, 128, TC_BM, CU_TENSOR_MAP_SWIZZLE_NONE, 0}, r{residual, oc, bt, 128, TC_BM, CU_TENSOR_MAP_SWIZZLE_NONE, 0};
+    const MapSpec specs[6] = {a, b, a, b, d, d};
+    TcParams p{};
+    p.BT = BT;
+    p.C = C;
+    p.OC = C;
+    p.n_dinp = OC;
+    p.x3_corr = 1;
+    p.dinp = reinterpret_cast<__nv_bfloat16*>(out);
+    p.x3_forward = 1;
+    p.x3_bias = bias;
+    p.x3_pre = pre;
+    p.x3_aux = residual;
+    p.act = act;
+    return launch_common(plan, specs, p, 6, stream, nullptr, residual ? &r : nullptr);
+}
+
+cudaError_t tc_launch_span_run(const TcPlan& plan, float* dpre, float* dweight, float* dbias, const float* dout,
+                               const float* inp, const float* weight, const float* pre, int64_t BT, int64_t C, int64_t OC,
+                               int act, cudaStream_t stream) {
+    if (take_injected_launch_failure()) return cudaErrorLaunchFailure;
+    const uint64_t bt = static_cast<uint64_t>(BT), c = static_cast<uint64_t>(C), oc = static_cast<uint64_t>(OC);
+    // (operands and maps as in tc_launch_x3_pair)
+    const MapSpec a1 = x3_operand(dout, false, bt, oc, OC, TC_BM), b1 = x3_operand(weight, true, c, oc, C, 64);
+    const MapSpec specs[6] = {
+        a1, b1, a1, b1,
+        {dpre, c, bt, 128, TC_BM, CU_TENSOR_MAP_SWIZZLE_NONE, 0},
+        {dweight, c, oc, 128, TC_BM, CU_TENSOR_MAP_SWIZZLE_NONE, 0},
+    };
+    const MapSpec pair[2] = {x3_operand(dout, true, oc, bt, OC, TC_BM), x3_operand(inp, true, c, bt, C, 64)};
+    const MapSpec aux{pre, c, bt, 128, TC_BM, CU_TENSOR_MAP_SWIZZLE_NONE, 0};
+    TcParams p{};
+    p.BT = BT;
+    p.C = C;
+    p.OC = OC;
+    p.n_dinp = C;
+    p.x3_corr = 1;
+    p.x3_mn = 2 | 4 | 8;
+    p.x3_dbias = dbias;
+    p.dinp = reinterpret_cast<__nv_bfloat16*>(dpre);
+    p.dweight = reinterpret_cast<__nv_bfloat16*>(dweight);
+    p.x3_aux = pre;
+    p.act = act;
+    return launch_common(plan, specs, p, 6, stream, pair, &aux);
 }
 
 cudaError_t tc_read_status(int* code, int* info3, bool reset) {

@@ -61,9 +61,9 @@ __device__ __forceinline__ void finish(const Params& p, int token, int64_t n, fl
 
 // red[warp][TOKENS][ROWS]: the sums of each group of `share` warps in warp order, the outputs.
 template <typename T, int TOKENS, int ROWS>
-__device__ __forceinline__ void join(const Params& p, const float* red, int64_t n0) {
+__device__ __forceinline__ void join(const Params& p, const float* red, int64_t n0, int t0, int tokens) {
     __syncthreads();
-    const int groups = static_cast<int>(blockDim.x >> 5) / p.share, pairs = groups * p.T * (ROWS / 2);
+    const int groups = static_cast<int>(blockDim.x >> 5) / p.share, pairs = groups * tokens * (ROWS / 2);
     for (int e = static_cast<int>(threadIdx.x); e < pairs; e += static_cast<int>(blockDim.x)) {
         const int row = e % (ROWS / 2) * 2, rest = e / (ROWS / 2), group = rest % groups, token = rest / groups;
         const int64_t n = n0 + group * ROWS + row;
@@ -74,7 +74,7 @@ __device__ __forceinline__ void join(const Params& p, const float* red, int64_t 
             const float2 v = *reinterpret_cast<const float2*>(at + w * TOKENS * ROWS);
             s.x += v.x, s.y += v.y;
         }
-        finish<T>(p, token, n, s.x, s.y);
+        finish<T>(p, t0 + token, n, s.x, s.y);
     }
 }
 
@@ -166,10 +166,11 @@ __global__ void __launch_bounds__(32 * MAX_WARPS) tokens_bf16_kernel(const __gri
                 if (16 * m + 8 * h + g < p.T)
                     *reinterpret_cast<float2*>(red + (warp * TOKENS + 16 * m + 8 * h + g) * ROWS + 8 * i + 2 * t) =
                         make_float2(c[m][i][2 * h], c[m][i][2 * h + 1]);
-    join<__nv_bfloat16, TOKENS, ROWS>(p, red, block0);
+    join<__nv_bfloat16, TOKENS, ROWS>(p, red, block0, 0, p.T);
 }
 
-// TOKENS tokens (those beyond T read the last one's), four weight rows to a warp.
+// TOKENS tokens from blockIdx.y on (those beyond T read the last one's), four weight rows to
+// a warp.
 template <int TOKENS, int AHEAD>
 __global__ void __launch_bounds__(32 * MAX_WARPS) tokens_f32_kernel(const __grid_constant__ Params p) {
     constexpr int ROWS = 4;
@@ -181,7 +182,8 @@ __global__ void __launch_bounds__(32 * MAX_WARPS) tokens_f32_kernel(const __grid
     ptx::grid_launch_dependents();
     ptx::grid_dependency_wait();
     const float* w = static_cast<const float*>(p.weight) + n0 * p.K + 4 * lane;
-    const float* x = static_cast<const float*>(p.inp) + 4 * lane;
+    const int t0 = static_cast<int>(blockIdx.y) * TOKENS, tokens = min(p.T - t0, TOKENS);
+    const float* x = static_cast<const float*>(p.inp) + static_cast<int64_t>(t0) * p.K + 4 * lane;
     float c[TOKENS][ROWS];
 #pragma unroll
     for (int m = 0; m < TOKENS; ++m)
@@ -197,7 +199,7 @@ __global__ void __launch_bounds__(32 * MAX_WARPS) tokens_f32_kernel(const __grid
         for (int i = 0; i < ROWS; ++i) wv[u][i] = in ? stream16(w + i * p.K + at) : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
         for (int m = 0; m < TOKENS; ++m)
-            xv[u][m] = in ? __ldg(reinterpret_cast<const uint4*>(x + static_cast<int64_t>(min(m, p.T - 1)) * p.K + at)) : make_uint4(0u, 0u, 0u, 0u);
+            xv[u][m] = in ? __ldg(reinterpret_cast<const uint4*>(x + static_cast<int64_t>(min(m, tokens - 1)) * p.K + at)) : make_uint4(0u, 0u, 0u, 0u);
     };
 #pragma unroll
     for (int u = 0; u < AHEAD; ++u) fetch(u, lo + u);
@@ -225,7 +227,7 @@ __global__ void __launch_bounds__(32 * MAX_WARPS) tokens_f32_kernel(const __grid
             for (int o = 16; o > 0; o >>= 1) c[m][i] += __shfl_xor_sync(0xffffffffu, c[m][i], o);
         if (lane == m) *reinterpret_cast<float4*>(red + (warp * TOKENS + m) * ROWS) = make_float4(c[m][0], c[m][1], c[m][2], c[m][3]);
     }
-    join<float, TOKENS, ROWS>(p, red, block0);
+    join<float, TOKENS, ROWS>(p, red, block0, t0, tokens);
 }
 
 template <auto kernel>
@@ -246,7 +248,7 @@ cudaError_t launch(Params p, int tokens, int rows, int share, cudaStream_t strea
     const int64_t per_block = static_cast<int64_t>(warps / share) * rows, blocks = (p.N + per_block - 1) / per_block;
     if (blocks > INT32_MAX) return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>(blocks), 1, 1);
+    cfg.gridDim = dim3(static_cast<unsigned>(blocks), static_cast<unsigned>((p.T + tokens - 1) / tokens), 1);
     cfg.blockDim = dim3(static_cast<unsigned>(32 * warps), 1, 1);
     cfg.dynamicSmemBytes = static_cast<size_t>(smem);
     cfg.stream = stream;
@@ -260,15 +262,13 @@ cudaError_t launch(Params p, int tokens, int rows, int share, cudaStream_t strea
 
 }  // namespace
 
-// Up to 8 tokens in fp32 and 32 in bf16. From 33 to 64 tokens in bf16 by the time of either
-// kernel (us, fitted to the sizes below): this one goes by the weight's bytes, the
-// tensor-core kernel by the k-blocks of its rounds of tiles. Measured, this / that: 64 tokens
-// 1600 -> 6400 16.9 / 13.9, 6400 -> 1600 16.3 / 36.2, 768 -> 768 5.0 / 8.7; 32 tokens 1600 ->
-// 6400 10.1 / 14.0, 6400 -> 1600 10.5 / 36.1; 16 tokens 768 -> 50304 16.6 / 29.3; one token
-// 1600 -> 6400 5.6 / 14.7.
-bool tokens_act_takes(int64_t T, int64_t K, int64_t N, int dtype, int num_sms) {
-    if (dtype == MMBWD_F32) return T <= 8;
-    if (T <= 32 || T > 64) return T <= 32;
+// Up to 32 tokens, and up to 64 by the time of either kernel (us, fitted to the sizes
+// below): this one goes by the weight's bytes, the tensor-core kernel by the k-blocks
+// of its rounds of tiles. Measured, this / that: 64 tokens 1600 -> 6400 16.9 / 13.9, 6400 ->
+// 1600 16.3 / 36.2, 768 -> 768 5.0 / 8.7; 32 tokens 1600 -> 6400 10.1 / 14.0, 6400 -> 1600 10.5 / 36.1; 16
+// tokens 768 -> 50304 16.6 / 29.3; one token 1600 -> 6400 5.6 / 14.7.
+bool tokens_act_takes_bf16(int64_t T, int64_t K, int64_t N, int num_sms) {
+    if (T <= 32 || T > ACT_TOKENS) return T <= 32;
     const double bytes = 2.0 * static_cast<double>(N) * static_cast<double>(K), tiles = static_cast<double>((N + 255) / 256);
     const double rounds = static_cast<double>(static_cast<int64_t>((tiles + num_sms / 2 - 1) / (num_sms / 2)));
     return 3.0 + bytes / 1.4e6 < 5.5 + rounds * 0.33 * static_cast<double>((K + 63) / 64);
@@ -289,7 +289,7 @@ cudaError_t tokens_act_launch(void* out, void* pre, const void* inp, const void*
         return share;
     };
     if (dtype == MMBWD_F32) {
-        const int share = shared_by(N / 4, (K + 127) / 128, T <= 4 ? 2400 : 1600);
+        const int share = shared_by(N / 4 * ((T + 7) / 8), (K + 127) / 128, T <= 4 ? 2400 : 1600);
         if (T <= 1) return launch<tokens_f32_kernel<1, 2>>(p, 1, 4, share, stream);
         if (T <= 4) return launch<tokens_f32_kernel<4, 2>>(p, 4, 4, share, stream);
         return launch<tokens_f32_kernel<8, 1>>(p, 8, 4, share, stream);

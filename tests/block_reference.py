@@ -97,10 +97,13 @@ def act_slope_bound(x, act):
 
 def product_bound(length, magnitudes, dtype):
     """What a sum of `length` products loses whose absolute values sum to `magnitudes`.
-    fp32: one rounding per fused multiply-add. bf16: the tensor core cuts (does not
-    round) each step of at most 16 products, a step's own sum to a few bits below its
-    largest term, so at most two whole fp32 steps per product are counted."""
-    return (length + 2) * U * magnitudes * (1 if dtype == "f32" else 4)
+    fp32: one rounding per fused multiply-add; or three tf32 products, where x = hi + lo with
+    |lo| < 2^-10 |x| (hi has 11 bits): lo lo' is left out, below 2^-20 |x x'|, and each lo is read
+    to 11 bits, 2^-21 |x| off, twice: 2^-19 = 32 U of each product in all, beside a sum in fp32.
+    bf16: the tensor core cuts (does not round) each step of at most 16 products, a step's
+    own sum to a few bits below its largest term, so at most two whole fp32 steps per
+    product are counted."""
+    return (length + 34) * U * magnitudes if dtype == "f32" else (length + 2) * 4 * U * magnitudes
 
 
 def forward_act(inp, weight, bias, residual, act, dtype):

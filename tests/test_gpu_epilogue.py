@@ -96,6 +96,46 @@ def test_forward_long_sum_f32():
         check_forward(x, "none", "f32")
 
 
+@pytest.mark.parametrize("path", ["32", "64", "spans"])
+@pytest.mark.parametrize("act", ref.ACTS)
+@pytest.mark.parametrize("size", [(1, 4, 4), (33, 100, 36), (65, 264, 1300), (300, 772, 132), (1030, 1156, 392)],
+                         ids=lambda s: "x".join(map(str, s)))
+def test_fp32_kernels(monkeypatch, size, act, path):
+    """Each fp32 kernel, forward and backward, at sizes that end inside its tiles and spans."""
+    monkeypatch.setenv("MMBWD_ACT_F32_PATH", path)
+    for options in (dict(), dict(bias=False, residual=False)):
+        x = inputs(*size, "f32", 21, **options)
+        full = check_forward(x, act, "f32")[0]
+        assert torch.equal(forward(x, act, "f32", pre=False)[0], full)
+        if x["residual"] is not None:
+            assert torch.equal(forward(x, act, "f32", in_place=True)[0], full)
+    x = gradient_inputs(*size, "f32", act, 22)
+    full = check_run(x, act, "f32")
+    for a, b in zip(run(x, act, "f32", bias=False)[:2] + run(x, act, "f32", in_place=True), full[:2] + full):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("path", ["32", "spans"])
+def test_fp32_long_sums_of_one_sign(monkeypatch, path):
+    """Reductions of 9000 and 5000 values of one sign: a sum that is cut instead of rounded
+    loses 2^-24 of itself a step and would be over the bound of 2-norms (2e-6: a random walk of 9000
+    roundings is 95 steps of 2^-24 on the last sums, 6e-6 at the very most, a third of that on
+    average over the way there)."""
+    monkeypatch.setenv("MMBWD_ACT_F32_PATH", path)
+    x = inputs(100, 9000, 40, "f32", 4, bias=False, residual=False)
+    x["inp"], x["weight"] = x["inp"].abs(), x["weight"].abs()
+    out = forward(x, "none", "f32")[0].double()
+    want = x["inp"] @ x["weight"].t()
+    assert (out - want).norm() <= 2e-6 * want.norm()
+    check_forward(x, "none", "f32")
+
+
+def test_fp32_many_items(monkeypatch):
+    monkeypatch.setenv("MMBWD_ACT_F32_PATH", "spans")
+    check_forward(inputs(3000, 520, 2052, "f32", 23), "gelu", "f32")
+    check_run(gradient_inputs(2600, 1604, 1000, "f32", "gelu", 24), "gelu", "f32")
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_without_inputs(dtype):
     """C == 0: the activation of the bias, over every kind of value."""
