@@ -1008,9 +1008,20 @@ __global__ void __launch_bounds__(Smem<MODE>::THREADS, 1)
                     to[g] = resrow && at < ncols ? *reinterpret_cast<const uint4*>(resrow + at) : make_uint4(0u, 0u, 0u, 0u);
                 }
             };
+            // and the bias of the chunk's columns
+            uint4 bias4[4];
+            [[maybe_unused]] auto load_bias = [&](int k) {
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    const int at = (h + NH * k) * 32 + 8 * g;
+                    bias4[g] = p.fwd_bias && at < ncols ? __ldg(reinterpret_cast<const uint4*>(p.fwd_bias + col0 + at))
+                                                        : make_uint4(0u, 0u, 0u, 0u);
+                }
+            };
             if constexpr (EPI) {
                 if (p.residual && qrow0 + lane < rows_total) resrow = p.residual + (qrow0 + lane) * n_extent + col0;
                 load_res(0, res);
+                load_bias(0);
             }
             if constexpr (SPAN) {
                 // The spans' accumulators, main and correction, added up in order: row `lane` of
@@ -1303,25 +1314,26 @@ __global__ void __launch_bounds__(Smem<MODE>::THREADS, 1)
                     }
                     ++fwd_chunks;
                 };
-                if (qvalid) {
+                if (qvalid && nloc > 0) {
+                    uint32_t v[32];
+                    ptx::tmem_ld32_issue(tbase + h * 32, v);
 #pragma unroll 1
                     for (int k = 0; k < nloc; ++k) {
                         const int c = h + NH * k;
-                        uint32_t v[32];
-                        ptx::tmem_ld32(tbase + c * 32, v);
+                        ptx::tmem_ld32_wait(v);
                         float f[32];
 #pragma unroll
                         for (int g = 0; g < 4; ++g) {
-                            const int cc = col0 + c * 32 + 8 * g;
-                            const uint4 b8 = (p.fwd_bias && cc < n_extent)
-                                                 ? __ldg(reinterpret_cast<const uint4*>(p.fwd_bias + cc))
-                                                 : make_uint4(0u, 0u, 0u, 0u);
-                            const uint32_t bw[4] = {b8.x, b8.y, b8.z, b8.w};
+                            const uint32_t bw[4] = {bias4[g].x, bias4[g].y, bias4[g].z, bias4[g].w};
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {
                                 f[8 * g + 2 * e] = __uint_as_float(v[8 * g + 2 * e]) + bf_lo(bw[e]);
                                 f[8 * g + 2 * e + 1] = __uint_as_float(v[8 * g + 2 * e + 1]) + bf_hi(bw[e]);
                             }
+                        }
+                        if (k + 1 < nloc) {  // the next chunk's, on their way while this one is worked on
+                            ptx::tmem_ld32_issue(tbase + (c + NH) * 32, v);
+                            load_bias(k + 1);
                         }
                         if (p.has_pre) store(&tm_dw_rmw, c, f);
                         act::with(p.act, [&](auto kind) {
