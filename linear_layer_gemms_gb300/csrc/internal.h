@@ -115,7 +115,8 @@ struct TcParams {
     float* x3_dbias;
     // MODE 4 and 5
     int act;                        // MMBWD_ACT_*
-    int has_pre;                    // MODE 4: the argument of the activation is stored too
+    __nv_bfloat16* pre;             // MODE 4: where the activation's argument goes too; may be null
+    int wide_rows;                  // MODE 4: rows of out and pre start at multiples of 32 bytes
     const __nv_bfloat16* residual;  // MODE 4; may be null, may be the output
     // MODE 6: the forward (bias and pre may be null; x3_aux: the residual or null) or the
     // backward (x3_aux: pre). x3_aux may be the output.

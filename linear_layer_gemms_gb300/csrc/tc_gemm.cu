@@ -103,7 +103,8 @@ constexpr int PART_CHUNK_BYTES = 32 * 32 * 4;
 template <int MODE>
 struct Smem {
     static constexpr bool X3 = MODE == 2 || MODE == 6;
-    static constexpr int STAGES = X3 ? TC_STAGES_X3 : TC_STAGES;
+    static constexpr bool DIRECT = MODE == 4;  // the epilogue stores from registers: its chunk buffers make a seventh stage
+    static constexpr int STAGES = X3 ? TC_STAGES_X3 : DIRECT ? TC_STAGES + 1 : TC_STAGES;
     static constexpr int STG_BYTES = X3 ? 2 * STAGE_BYTES : STAGE_BYTES;
     // Epilogue warps: in the bf16 modes two per tensor-memory lane quadrant, each
     // taking every other 32-column chunk of the quadrant's rows with two chunk
@@ -112,7 +113,7 @@ struct Smem {
     static constexpr int EPI_WARPS = X3 ? 4 : 8;
     static constexpr int EPI_THREADS = 32 * EPI_WARPS;
     static constexpr int THREADS = 32 * WARP_EPI + EPI_THREADS;
-    static constexpr int OLD_SLOTS = X3 ? 4 : 2;  // bf16 chunk buffers per epilogue warp
+    static constexpr int OLD_SLOTS = X3 ? 4 : DIRECT ? 1 : 2;  // bf16 chunk buffers per epilogue warp (DIRECT: not used)
     static constexpr int PART_SLOTS = 1;  // fp32 partial chunk buffers (same memory)
     static constexpr int OFF_BARS = STAGES * STG_BYTES;
     static constexpr int BAR_FULL = 0;                   // [stages] TMA landed (even CTA: and the peer's too)
@@ -125,14 +126,14 @@ struct Smem {
     static constexpr int N_BARS = BAR_CONV + (X3 ? STAGES : 0);
     static constexpr int OFF_MISC = OFF_BARS + N_BARS * 8;  // [0] tmem base, [1] abort flag
     static constexpr int OFF_STAGE = (OFF_MISC + 16 + 1023) & ~1023;
-    static constexpr int OLD_WARP_BYTES = OLD_SLOTS * OLD_CHUNK_BYTES;
+    static constexpr int OLD_WARP_BYTES = DIRECT ? 0 : OLD_SLOTS * OLD_CHUNK_BYTES;
     static constexpr int WARP_REGION =
         X3 ? (STG_WARP_BYTES > OLD_WARP_BYTES ? STG_WARP_BYTES : OLD_WARP_BYTES) : OLD_WARP_BYTES;
     // ones tile of the dbias-by-MMA variant: 8 rows (this CTA's half of N = 16)
     // of 64 bf16 ones, one 128-byte-swizzled 1 KB atom
     static constexpr int OFF_ONES = OFF_STAGE + EPI_WARPS * WARP_REGION;
-    static constexpr int SMEM_TOTAL = OFF_ONES + 1024 + 1024;  // + slack for aligning the base
-    static_assert(X3 || PART_SLOTS * PART_CHUNK_BYTES <= WARP_REGION, "partial chunks fit the warp region");
+    static constexpr int SMEM_TOTAL = OFF_ONES + (DIRECT ? 0 : 1024) + 1024;  // + slack for aligning the base
+    static_assert(X3 || DIRECT || PART_SLOTS * PART_CHUNK_BYTES <= WARP_REGION, "partial chunks fit the warp region");
     static_assert(EPI_WARPS % 4 == 0 && (!X3 || EPI_WARPS == 4), "whole quadrants; MODE 2 one warp each");
     static_assert(WARP_REGION % 1024 == 0, "chunk buffers stay 1024-byte aligned (128-byte swizzle)");
     static_assert(SMEM_TOTAL <= 227 * 1024, "shared memory budget");
@@ -1291,28 +1292,27 @@ __global__ void __launch_bounds__(Smem<MODE>::THREADS, 1)
             }
             if constexpr (EPI) {
                 // out = act(acc + bias) + residual and, where wanted, pre = acc + bias, each
-                // rounded once, row by row into a chunk buffer and out with one bulk store;
-                // the buffers alternate over the stores of both, and one is rewritten once the
-                // store before last has read it.
-                const uint32_t swz = static_cast<uint32_t>((lane >> 1) & 3);
-                auto store = [&](const void* map, int c, const float (&f)[32]) {
-                    const uint32_t slot = fwd_chunks & (OLD_SLOTS - 1);
-                    if (fwd_chunks >= OLD_SLOTS && lane == 0) ptx::bulk_wait_read_but_n<OLD_SLOTS - 1>();
-                    __syncwarp();
-                    const uint32_t rowaddr = oldbuf + slot * OLD_CHUNK_BYTES + lane * 64;
+                // rounded once and stored from registers, 32 bytes of its row a thread at a time
+                // (16 where rows are not multiples of 32 bytes).
+                const bool mine = qrow0 + lane < rows_total;
+                const int64_t row_at = (qrow0 + lane) * n_extent + col0;
+                auto store = [&](__nv_bfloat16* to, int c, const float (&f)[32]) {
+                    if (!mine) return;
+                    __nv_bfloat16* row = to + row_at + c * 32;
 #pragma unroll
-                    for (int g = 0; g < 4; ++g) {
-                        const float f8[8] = {f[8 * g],     f[8 * g + 1], f[8 * g + 2], f[8 * g + 3],
+                    for (int g = 0; g < 4; g += 2) {
+                        const float lo[8] = {f[8 * g],     f[8 * g + 1], f[8 * g + 2], f[8 * g + 3],
                                              f[8 * g + 4], f[8 * g + 5], f[8 * g + 6], f[8 * g + 7]};
-                        ptx::sts128u(rowaddr + ((static_cast<uint32_t>(g) ^ swz) << 4), round8(f8));
+                        const float hi[8] = {f[8 * g + 8],  f[8 * g + 9],  f[8 * g + 10], f[8 * g + 11],
+                                             f[8 * g + 12], f[8 * g + 13], f[8 * g + 14], f[8 * g + 15]};
+                        const int at = c * 32 + 8 * g;
+                        if (p.wide_rows && at + 8 < ncols) {
+                            ptx::stg256(row + 8 * g, round8(lo), round8(hi));
+                        } else {
+                            if (at < ncols) *reinterpret_cast<uint4*>(row + 8 * g) = round8(lo);
+                            if (at + 8 < ncols) *reinterpret_cast<uint4*>(row + 8 * g + 8) = round8(hi);
+                        }
                     }
-                    ptx::fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) {
-                        ptx::tma_store_2d(map, oldbuf + slot * OLD_CHUNK_BYTES, col0 + c * 32, static_cast<int32_t>(qrow0));
-                        ptx::bulk_commit_group();
-                    }
-                    ++fwd_chunks;
                 };
                 if (qvalid && nloc > 0) {
                     uint32_t v[32];
@@ -1335,7 +1335,7 @@ __global__ void __launch_bounds__(Smem<MODE>::THREADS, 1)
                             ptx::tmem_ld32_issue(tbase + (c + NH) * 32, v);
                             load_bias(k + 1);
                         }
-                        if (p.has_pre) store(&tm_dw_rmw, c, f);
+                        if (p.pre) store(p.pre, c, f);
                         act::with(p.act, [&](auto kind) {
 #pragma unroll
                             for (int e = 0; e < 32; ++e) f[e] = act::value<decltype(kind)::value, true>(f[e]);
@@ -1352,7 +1352,7 @@ __global__ void __launch_bounds__(Smem<MODE>::THREADS, 1)
                             }
                             if (k + 1 < nloc) load_res(k + 1, res);
                         }
-                        store(tmo, c, f);
+                        store(p.dinp, c, f);
                     }
                 }
             }
@@ -1859,7 +1859,7 @@ cudaError_t launch_common(const TcPlan& plan, const MapSpec (&specs)[6], TcParam
             if (e == cudaSuccess)
                 e = cudaFuncSetAttribute(tc_mmbwd_kernel<3>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_TOTAL);
             if (e == cudaSuccess)
-                e = cudaFuncSetAttribute(tc_mmbwd_kernel<4>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_TOTAL);
+                e = cudaFuncSetAttribute(tc_mmbwd_kernel<4>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<4>::SMEM_TOTAL);
             if (e == cudaSuccess)
                 e = cudaFuncSetAttribute(tc_mmbwd_kernel<5>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_TOTAL);
             if (e == cudaSuccess)
@@ -1919,11 +1919,11 @@ cudaError_t launch_common(const TcPlan& plan, const MapSpec (&specs)[6], TcParam
     }
     // Output maps of the bf16 epilogues (maps 4 and 5 give the tensors and
     // their extents): boxes of 32 columns x 32 rows.
-    // MODE 4 writes pre through map 10; MODE 5 loads pre through map 12.
+    // MODE 5 loads pre through map 12.
     for (int i = 0; i < 3; ++i) {
         CUtensorMap& map = maps[i == 2 ? 12 : 9 + i];
         map = maps[4];  // placeholder where unused
-        if (x3 || (i == 2 ? !aux : mode == 1 && i == 1)) continue;  // the forward writes through map 9
+        if (x3 || mode == 4 || (i == 2 ? !aux : mode == 1 && i == 1)) continue;  // the forward writes through map 9
         const MapSpec& m = i == 2 ? *aux : specs[4 + i];
         const cuuint64_t dims[2] = {m.inner, m.outer};
         const cuuint64_t strides[1] = {m.inner * 2};
@@ -1982,7 +1982,7 @@ cudaError_t launch_common(const TcPlan& plan, const MapSpec (&specs)[6], TcParam
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>(plan.grid), 1, 1);
     cfg.blockDim = dim3(x3 ? Smem<2>::THREADS : Smem<0>::THREADS, 1, 1);
-    cfg.dynamicSmemBytes = SMEM_TOTAL;
+    cfg.dynamicSmemBytes = mode == 4 ? Smem<4>::SMEM_TOTAL : SMEM_TOTAL;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -2095,8 +2095,8 @@ cudaError_t tc_launch_forward_act(const TcPlan& plan, void* out, void* pre, cons
         {weight, c, oc, TC_BK, 64, CU_TENSOR_MAP_SWIZZLE_128B},      // weight rows, K-major B (64 rows per box)
         {inp, c, bt, TC_BK, TC_BM, CU_TENSOR_MAP_SWIZZLE_128B},      // unused by forward items
         {weight, c, oc, TC_BK, 64, CU_TENSOR_MAP_SWIZZLE_128B},      // unused
-        {out, oc, bt, 128, TC_BM, CU_TENSOR_MAP_SWIZZLE_NONE},              // out (map 9)
-        {pre ? pre : out, oc, bt, 128, TC_BM, CU_TENSOR_MAP_SWIZZLE_NONE},  // pre (map 10)
+        {out, oc, bt, 128, TC_BM, CU_TENSOR_MAP_SWIZZLE_NONE},       // out, or the residual: L2 prefetch
+        {out, oc, bt, 128, TC_BM, CU_TENSOR_MAP_SWIZZLE_NONE},       // unused
     };
     const MapSpec aux{residual, oc, bt, 128, TC_BM, CU_TENSOR_MAP_SWIZZLE_NONE};
     TcParams p{};
@@ -2107,7 +2107,8 @@ cudaError_t tc_launch_forward_act(const TcPlan& plan, void* out, void* pre, cons
     p.fwd_bias = static_cast<const __nv_bfloat16*>(bias);
     p.dinp = static_cast<__nv_bfloat16*>(out);
     p.residual = static_cast<const __nv_bfloat16*>(residual);
-    p.has_pre = pre ? 1 : 0;
+    p.pre = static_cast<__nv_bfloat16*>(pre);
+    p.wide_rows = OC % 16 == 0 && ((reinterpret_cast<uintptr_t>(out) | reinterpret_cast<uintptr_t>(pre)) & 31u) == 0;
     p.act = act;
     return launch_common(plan, specs, p, 4, stream, nullptr, residual ? &aux : nullptr);
 }
