@@ -19,12 +19,12 @@ __device__ __forceinline__ uint4 slope_product(const uint4& d, const uint4& x) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         if constexpr (sizeof(T) == 2) {
-            const __nv_bfloat162 h = __floats2bfloat162_rn(
-                __uint_as_float(a[i] << 16) * act::slope<ACT, true>(__uint_as_float(b[i] << 16)),
-                __uint_as_float(a[i] & 0xFFFF0000u) * act::slope<ACT, true>(__uint_as_float(b[i] & 0xFFFF0000u)));
+            float lo = __uint_as_float(a[i] << 16), hi = __uint_as_float(a[i] & 0xFFFF0000u);
+            act::slope_fast<ACT>(lo, hi, __uint_as_float(b[i] << 16), __uint_as_float(b[i] & 0xFFFF0000u));
+            const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
             r[i] = *reinterpret_cast<const uint32_t*>(&h);
         } else {
-            r[i] = __float_as_uint(__uint_as_float(a[i]) * act::slope<ACT, false>(__uint_as_float(b[i])));
+            r[i] = __float_as_uint(__uint_as_float(a[i]) * act::slope<ACT>(__uint_as_float(b[i])));
         }
     }
     return make_uint4(r[0], r[1], r[2], r[3]);
@@ -51,7 +51,10 @@ __global__ void __launch_bounds__(THREADS) act_backward_kernel(T* dpre, const T*
             if (at + j * THREADS < vecs) o4[at + j * THREADS] = slope_product<T, decltype(a)::value>(d[j], x[j]);
         const int64_t i = vecs * PER + at;  // the loose values at the end: the first threads'
         if (i < n) {
-            const float v = static_cast<float>(dout[i]) * act::slope<decltype(a)::value, sizeof(T) == 2>(static_cast<float>(pre[i]));
+            float v = static_cast<float>(dout[i]), unused = 0.f;
+            const float x = static_cast<float>(pre[i]);
+            if constexpr (sizeof(T) == 2) act::slope_fast<decltype(a)::value>(v, unused, x, 0.f);
+            else v *= act::slope<decltype(a)::value>(x);
             dpre[i] = static_cast<T>(v);
         }
     });
@@ -65,7 +68,9 @@ __global__ void __launch_bounds__(THREADS) act_rows_kernel(T* out, T* pre, const
          i += static_cast<int64_t>(gridDim.x) * THREADS) {
         const float s = bias ? static_cast<float>(bias[i % cols]) : 0.f;
         act::with(act, [&](auto a) {
-            float v = act::value<decltype(a)::value, sizeof(T) == 2>(s);
+            float v = s, unused = 0.f;
+            if constexpr (sizeof(T) == 2) act::value_fast<decltype(a)::value>(v, unused);
+            else v = act::value<decltype(a)::value>(v);
             if (residual) v += static_cast<float>(residual[i]);
             out[i] = static_cast<T>(v);
         });

@@ -116,7 +116,7 @@ struct TcParams {
     // MODE 4 and 5
     int act;                        // MMBWD_ACT_*
     __nv_bfloat16* pre;             // MODE 4: where the activation's argument goes too; may be null
-    int wide_rows;                  // MODE 4: rows of out and pre start at multiples of 32 bytes
+    int wide_rows;                  // MODE 4: the outputs' and the residual's rows start at multiples of 32 bytes
     const __nv_bfloat16* residual;  // MODE 4; may be null, may be the output
     // MODE 6: the forward (bias and pre may be null; x3_aux: the residual or null) or the
     // backward (x3_aux: pre). x3_aux may be the output.

@@ -167,8 +167,8 @@ __device__ __forceinline__ void tile_product(const Params& p, const Product& q, 
             if (p.pre) *reinterpret_cast<float4*>(p.pre + at) = o;
             act::with(p.act, [&](auto kind) {
                 constexpr int ACT = decltype(kind)::value;
-                o.x = act::value<ACT, false>(o.x), o.y = act::value<ACT, false>(o.y);
-                o.z = act::value<ACT, false>(o.z), o.w = act::value<ACT, false>(o.w);
+                o.x = act::value<ACT>(o.x), o.y = act::value<ACT>(o.y);
+                o.z = act::value<ACT>(o.z), o.w = act::value<ACT>(o.w);
             });
         }
         const float* add = EPI == FORWARD ? p.residual : EPI == DWEIGHT ? q.D : nullptr;
@@ -180,8 +180,8 @@ __device__ __forceinline__ void tile_product(const Params& p, const Product& q, 
             const float4 x = *reinterpret_cast<const float4*>(p.pre + at);
             act::with(p.act, [&](auto kind) {
                 constexpr int ACT = decltype(kind)::value;
-                o.x *= act::slope<ACT, false>(x.x), o.y *= act::slope<ACT, false>(x.y);
-                o.z *= act::slope<ACT, false>(x.z), o.w *= act::slope<ACT, false>(x.w);
+                o.x *= act::slope<ACT>(x.x), o.y *= act::slope<ACT>(x.y);
+                o.z *= act::slope<ACT>(x.z), o.w *= act::slope<ACT>(x.w);
             });
         }
         *reinterpret_cast<float4*>(q.D + at) = o;

@@ -1004,9 +1004,14 @@ __global__ void __launch_bounds__(Smem<MODE>::THREADS, 1)
             const __nv_bfloat16* resrow = nullptr;
             [[maybe_unused]] auto load_res = [&](int k, uint4 (&to)[4]) {
 #pragma unroll
-                for (int g = 0; g < 4; ++g) {
+                for (int g = 0; g < 4; g += 2) {
                     const int at = (h + NH * k) * 32 + 8 * g;
-                    to[g] = resrow && at < ncols ? *reinterpret_cast<const uint4*>(resrow + at) : make_uint4(0u, 0u, 0u, 0u);
+                    if (resrow && p.wide_rows && at + 8 < ncols) {
+                        ptx::ldg256(resrow + at, to[g], to[g + 1]);
+                    } else {
+                        to[g] = resrow && at < ncols ? *reinterpret_cast<const uint4*>(resrow + at) : make_uint4(0u, 0u, 0u, 0u);
+                        to[g + 1] = resrow && at + 8 < ncols ? *reinterpret_cast<const uint4*>(resrow + at + 8) : make_uint4(0u, 0u, 0u, 0u);
+                    }
                 }
             };
             // and the bias of the chunk's columns
@@ -1084,13 +1089,14 @@ __global__ void __launch_bounds__(Smem<MODE>::THREADS, 1)
                         for (int i = 0; i < 8; ++i) ptx::sts128(place(i), a4[i].x, a4[i].y, a4[i].z, a4[i].w);
 #pragma unroll 2
                         for (int i = 0; i < 8; ++i) {
-                            float4 x = ptx::lds128f(place(i));
+                            const float4 x = ptx::lds128f(place(i));
                             act::with(p.act, [&](auto kind) {
                                 constexpr int ACT = decltype(kind)::value;
-                                x.x = act::slope<ACT, true>(x.x), x.y = act::slope<ACT, true>(x.y);
-                                x.z = act::slope<ACT, true>(x.z), x.w = act::slope<ACT, true>(x.w);
+                                float4 one = make_float4(1.f, 1.f, 1.f, 1.f);
+                                act::slope_fast<ACT>(one.x, one.y, x.x, x.y);
+                                act::slope_fast<ACT>(one.z, one.w, x.z, x.w);
+                                ptx::sts128(place(i), one.x, one.y, one.z, one.w);
                             });
-                            ptx::sts128(place(i), x.x, x.y, x.z, x.w);
                         }
 #pragma unroll
                         for (int i = 0; i < 8; ++i) a4[i] = ptx::lds128f(place(i));
@@ -1109,8 +1115,8 @@ __global__ void __launch_bounds__(Smem<MODE>::THREADS, 1)
                             if (p.x3_pre && there(c, i)) *reinterpret_cast<float4*>(p.x3_pre + where(c, i)) = o;
                             act::with(p.act, [&](auto kind) {
                                 constexpr int ACT = decltype(kind)::value;
-                                o.x = act::value<ACT, true>(o.x), o.y = act::value<ACT, true>(o.y);
-                                o.z = act::value<ACT, true>(o.z), o.w = act::value<ACT, true>(o.w);
+                                act::value_fast<ACT>(o.x, o.y);
+                                act::value_fast<ACT>(o.z, o.w);
                             });
                             ptx::sts128(place(i), o.x, o.y, o.z, o.w);
                         }
@@ -1214,8 +1220,9 @@ __global__ void __launch_bounds__(Smem<MODE>::THREADS, 1)
                                 float f[8];
 #pragma unroll
                                 for (int e = 0; e < 4; ++e) {
-                                    f[2 * e] = __uint_as_float(v[8 * g + 2 * e]) * act::slope<ACT, true>(bf_lo(xw[e]));
-                                    f[2 * e + 1] = __uint_as_float(v[8 * g + 2 * e + 1]) * act::slope<ACT, true>(bf_hi(xw[e]));
+                                    f[2 * e] = __uint_as_float(v[8 * g + 2 * e]);
+                                    f[2 * e + 1] = __uint_as_float(v[8 * g + 2 * e + 1]);
+                                    act::slope_fast<ACT>(f[2 * e], f[2 * e + 1], bf_lo(xw[e]), bf_hi(xw[e]));
                                 }
                                 ptx::sts128u(a, round8(f));
                             }
@@ -1338,7 +1345,7 @@ __global__ void __launch_bounds__(Smem<MODE>::THREADS, 1)
                         if (p.pre) store(p.pre, c, f);
                         act::with(p.act, [&](auto kind) {
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) f[e] = act::value<decltype(kind)::value, true>(f[e]);
+                            for (int e = 0; e < 32; e += 2) act::value_fast<decltype(kind)::value>(f[e], f[e + 1]);
                         });
                         if (p.residual) {
 #pragma unroll
@@ -2108,7 +2115,8 @@ cudaError_t tc_launch_forward_act(const TcPlan& plan, void* out, void* pre, cons
     p.dinp = static_cast<__nv_bfloat16*>(out);
     p.residual = static_cast<const __nv_bfloat16*>(residual);
     p.pre = static_cast<__nv_bfloat16*>(pre);
-    p.wide_rows = OC % 16 == 0 && ((reinterpret_cast<uintptr_t>(out) | reinterpret_cast<uintptr_t>(pre)) & 31u) == 0;
+    p.wide_rows = OC % 16 == 0 && ((reinterpret_cast<uintptr_t>(out) | reinterpret_cast<uintptr_t>(pre) |
+                                    reinterpret_cast<uintptr_t>(residual)) & 31u) == 0;
     p.act = act;
     return launch_common(plan, specs, p, 4, stream, nullptr, residual ? &aux : nullptr);
 }

@@ -50,7 +50,8 @@ __device__ __forceinline__ void finish(const Params& p, int token, int64_t n, fl
     if (p.pre) store(p.pre, s0, s1);
     act::with(p.act, [&](auto kind) {
         constexpr int ACT = decltype(kind)::value;
-        s0 = act::value<ACT, FAST>(s0), s1 = act::value<ACT, FAST>(s1);
+        if constexpr (FAST) act::value_fast<ACT>(s0, s1);
+        else s0 = act::value<ACT>(s0), s1 = act::value<ACT>(s1);
     });
     if (p.residual) {
         const T* r = static_cast<const T*>(p.residual) + at;
