@@ -556,6 +556,43 @@ __global__ void __launch_bounds__(Smem<MODE>::THREADS, 1)
                     }
                     continue;
                 }
+                if constexpr (DACT) {
+                    const bool a_wide = it.is_dw && na == 2 && (p.wide_maps & TC_WIDE_DOUT_MN);
+                    const bool b_wide = nb == 2 && (p.wide_maps & (it.is_dw ? TC_WIDE_INP : TC_WIDE_WEIGHT));
+                    const void* tb = it.is_dw ? (b_wide ? &tm_inp_w : &tm_inp) : (b_wide ? &tm_weight_w : &tm_weight);
+                    const void* ta = it.is_dw ? (a_wide ? &tm_dout_mn_w : &tm_dout_mn) : &tm_dout_k;
+                    for (int kb = it.kb0; kb < it.kb1; ++kb) {
+                        if (!wt.wait(bars + 8u * (BAR_EMPTY + stage), phase ^ 1u, SITE_PRODUCER_EMPTY, w)) {
+                            ok = false;
+                            break;
+                        }
+                        const uint32_t sA = base + stage * STG_BYTES, sB = sA + A_BYTES, fb = bars + 8u * (BAR_FULL + stage);
+                        ptx::mbar_arrive_expect_tx(fb, bytes);
+                        if (!waited) {  // the previous launch has completed before any load
+                            ptx::grid_dependency_wait();
+                            waited = true;
+                        }
+                        if (!it.is_dw) {
+                            if (na) ptx::tma_load_2d(sA, ta, fb, kb * KBLK, row0);
+                        } else if (a_wide) {
+                            ptx::tma_load_3d(sA, ta, fb, 0, kb * KBLK, row0 / 64);
+                        } else {
+                            for (int j = 0; j < na; ++j) ptx::tma_load_2d(sA + j * BOX_BYTES, ta, fb, row0 + j * 64, kb * KBLK);
+                        }
+                        if (b_wide) {
+                            ptx::tma_load_3d(sB, tb, fb, 0, kb * KBLK, col0 / 64);
+                        } else {
+                            for (int j = 0; j < nb; ++j) ptx::tma_load_2d(sB + j * BOX_BYTES, tb, fb, col0 + j * 64, kb * KBLK);
+                        }
+                        issued |= 1u << stage;
+                        last_parity = (last_parity & ~(1u << stage)) | (phase << stage);
+                        if (++stage == STAGES) {
+                            stage = 0;
+                            phase ^= 1u;
+                        }
+                    }
+                    continue;
+                }
                 for (int kb = it.kb0; kb < it.kb1; ++kb) {
                     if (!wt.wait(bars + 8u * (BAR_EMPTY + stage), phase ^ 1u, SITE_PRODUCER_EMPTY, w)) {
                         ok = false;
