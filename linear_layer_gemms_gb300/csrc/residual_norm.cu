@@ -5,7 +5,7 @@
 // keeps it in registers (VPT 16-byte vectors per thread) from the branch's statistics to
 // the output, so nothing is read twice and each variance comes from the differences
 // (LAYER) of values at hand. Backward: four rows read, two written. A team owns a row as
-// well, a thread 16 columns of it; it has the next rows in flight, forms the row's
+// well, a thread 8 or 16 columns of it; it has the next rows in flight, forms the row's
 // four sums in two rounds and keeps its columns' parameter sums in registers over all
 // rows of the team. Rows that no team of 12 warps holds (C > 6144) take two passes: one
 // forms the rows' sums, one goes down column tiles.
@@ -545,192 +545,283 @@ struct Backward {
     float* partials;  // [row blocks][4][C]: dweight, dbias, sum dx z, sum dx
     float inv_c;
     int row_blocks;
+    int team_warps;
 };
 
 // ---- one pass
 
-constexpr int ROW_WARPS = 12;  // warps of a block: 168 registers to a thread
-constexpr int COLS = 16;       // columns of a thread, in vectors 32 P apart
+// E pairs of columns to a thread, R rows at a time, WARPS warps to a block, RING requests of
+// R rows on their way or in use.
+template <typename T_, int E_, int R_, int WARPS_, int RING_>
+struct RowsConfig {
+    using T = T_;
+    static constexpr int E = E_, R = R_, WARPS = WARPS_, RING = RING_;
+    static constexpr int V = 2 * E / Vec<T>::N, THREADS = 32 * WARPS;
+    static constexpr uint32_t PART = R * V * THREADS * 16u, SLOT = 4 * PART;
+    static constexpr int SMEM = static_cast<int>(RING * SLOT);
+    static constexpr int MAX_C = THREADS * 2 * E;
+    static_assert(SMEM >= 4 * 2 * E * 4 * THREADS / 2 && SMEM <= 220 * 1024, "the ring holds the sums of a team of half the warps, a block the ring");
+};
 
-template <typename T>
-constexpr int RING = sizeof(T) == 2 ? 3 : 2;  // rows of a thread on their way or in use
-template <typename T>
-constexpr int ROW_BYTES = 4 * COLS * static_cast<int>(sizeof(T));  // of a thread: dout, residual, dresidual, branch
+// 2 R sums over a team, in a fixed order, in every thread. The 2 R values of a lane are
+// halved in number with every exchange while there are several (lane group j of the warp
+// ends with value j), so that a warp sums four in six exchanges; the warps' sums of a
+// value are then summed by every warp the same way. `slots`: 2 x [warps][2 R] of the
+// team, which alternate, so that one barrier is enough.
+template <int R>
+struct TeamSums {
+    static constexpr int K = 2 * R;
+    float* slots;
+    int warp, warps, team;
+    int which = 0;
+    __device__ void operator()(float (&s)[K]) {
+        const int lane = static_cast<int>(threadIdx.x & 31);
+        float v;
+        if constexpr (K == 4) {
+            const bool upper = lane & 16, odd = lane & 8;
+            const float a = (upper ? s[2] : s[0]) + __shfl_xor_sync(0xffffffffu, upper ? s[0] : s[2], 16);
+            const float b = (upper ? s[3] : s[1]) + __shfl_xor_sync(0xffffffffu, upper ? s[1] : s[3], 16);
+            v = (odd ? b : a) + __shfl_xor_sync(0xffffffffu, odd ? a : b, 8);
+        } else {
+            const bool upper = lane & 16;
+            v = (upper ? s[1] : s[0]) + __shfl_xor_sync(0xffffffffu, upper ? s[0] : s[1], 16);
+            v += __shfl_xor_sync(0xffffffffu, v, 8);
+        }
+#pragma unroll
+        for (int o = 4; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+        if (warps == 1) {  // value j is lane group j's
+#pragma unroll
+            for (int k = 0; k < K; ++k) s[k] = __shfl_sync(0xffffffffu, v, k * (32 / K));
+            return;
+        }
+        float* at = slots + which;
+        which ^= warps * K;
+        if (lane % (32 / K) == 0) at[warp * K + lane / (32 / K)] = v;
+        ptx::named_bar_sync(static_cast<uint32_t>(1 + team), static_cast<uint32_t>(32 * warps));
+        v = lane < warps * K ? at[lane] : 0.f;  // value lane % K of warp lane / K
+        if (lane + 32 < warps * K) v += at[lane + 32];
+#pragma unroll
+        for (int o = K; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+#pragma unroll
+        for (int k = 0; k < K; ++k) s[k] = __shfl_sync(0xffffffffu, v, k);
+    }
+};
 
-// A team of P warps owns a row; a thread has the same 16 columns of all of its rows, their
-// weights and their sums in registers. The next rows are on their way into shared
-// memory, each thread's vectors to places that only it reads (no barrier).
-template <typename T, int P>
-__global__ void __launch_bounds__(32 * ROW_WARPS, 1) residual_rows_kernel(const __grid_constant__ Backward b) {
-    constexpr int N = Vec<T>::N, H = Pairs<T>::H, V = COLS / N, E = COLS / 2, TEAMS_ROWS = ROW_WARPS / P, THREADS = 32 * ROW_WARPS;
+// A team of warps owns R rows at a time; a thread has the same columns of all of its rows
+// (16-byte vectors, 32 warps apart), their weights and their sums in registers. The next
+// rows are on their way into shared memory, each thread's vectors to places that only it
+// reads (no barrier).
+template <typename L>
+__global__ void __launch_bounds__(L::THREADS, 1) residual_rows_kernel(const __grid_constant__ Backward b) {
+    using T = typename L::T;
+    constexpr int H = Pairs<T>::H, V = L::V, E = L::E, R = L::R, THREADS = L::THREADS;
+    constexpr uint32_t PART = L::PART, SLOT = L::SLOT;  // vector j of row k of tensor i of a slot: at i PART + (k V + j) 16 THREADS
     extern __shared__ __align__(16) uint8_t ring[];
-    __shared__ float slots[TEAMS_ROWS][2 * P * 2];
+    __shared__ float slots[2 * L::WARPS * 2 * R];
     const ResidualNorm& a = b.a;
+    const int warps = b.team_warps, teams = L::WARPS / warps;
     const int warp = static_cast<int>(threadIdx.x >> 5), lane = static_cast<int>(threadIdx.x & 31);
-    const int team = warp / P, wt = warp % P, t = wt * 32 + lane;
-    const int nvec = a.C / N;
+    const int team = warp / warps, wt = warp % warps, t = wt * 32 + lane;
+    if (team >= teams) return;  // (the block's warps beyond whole teams; no block-wide barrier waits for them)
+    const int nvec = a.C / Vec<T>::N;
     const bool norm = a.norm != NONE, post = a.post != NONE;
     const uint32_t mine = ptx::smem_u32(ring) + threadIdx.x * 16u;
-    constexpr uint32_t PART = V * THREADS * 16u, SLOT = 4 * PART;  // vector j of tensor i of a slot: at i PART + j 16 THREADS
+    int at[V];  // the thread's vectors of a row
+    bool on[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) at[j] = t + 32 * warps * j, on[j] = at[j] < nvec;
     // what is not there, a whole tensor or a vector beyond the row, is zero throughout
     const void* tensors[4] = {a.dout, a.residual, a.dresidual, a.branch};
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int j = 0; j < V; ++j)
-            if (!tensors[i] || t + 32 * P * j >= nvec)
-                for (int k = 0; k < RING<T>; ++k) ptx::sts128u(mine + k * SLOT + i * PART + j * (THREADS * 16), make_uint4(0u, 0u, 0u, 0u));
+            if (!tensors[i] || !on[j])
+                for (int k = 0; k < L::RING * R; ++k)
+                    ptx::sts128u(mine + (k / R) * SLOT + i * PART + (k % R * V + j) * (THREADS * 16), make_uint4(0u, 0u, 0u, 0u));
     ptx::grid_launch_dependents();
     ptx::grid_dependency_wait();
-    const int64_t step = static_cast<int64_t>(gridDim.x) * TEAMS_ROWS, first = static_cast<int64_t>(blockIdx.x) * TEAMS_ROWS + team;
-    int64_t ahead = first;  // the next row to request, into slot `into`
+    const int64_t step = static_cast<int64_t>(gridDim.x) * teams * R, first = (static_cast<int64_t>(blockIdx.x) * teams + team) * R;
+    int64_t ahead = first;  // the next rows to request, into slot `into`
     uint32_t into = 0, from = 0;
     auto request = [&]() {
-        if (ahead < a.rows) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if (!tensors[i]) continue;
-                const uint4* row = reinterpret_cast<const uint4*>(static_cast<const T*>(tensors[i]) + ahead * a.C);
+        for (int k = 0; k < R; ++k) {
+            if (ahead + k < a.rows) {
+                const int64_t row = (ahead + k) * nvec;
 #pragma unroll
-                for (int j = 0; j < V; ++j)
-                    if (t + 32 * P * j < nvec) copy16(mine + into + i * PART + j * (THREADS * 16), row + t + 32 * P * j);
+                for (int i = 0; i < 4; ++i) {
+                    if (!tensors[i]) continue;
+                    const uint4* p = static_cast<const uint4*>(tensors[i]) + row;
+#pragma unroll
+                    for (int j = 0; j < V; ++j)
+                        if (on[j]) copy16(mine + into + i * PART + (k * V + j) * (THREADS * 16), p + at[j]);
+                }
             }
         }
         copies_commit();
         ahead += step;
-        into = into + SLOT == RING<T> * SLOT ? 0 : into + SLOT;
+        into = into + SLOT == L::RING * SLOT ? 0 : into + SLOT;
     };
 #pragma unroll
-    for (int i = 0; i + 1 < RING<T>; ++i) request();
+    for (int i = 0; i + 1 < L::RING; ++i) request();
     // the weights of a thread's columns, 0 beyond the row: nothing there adds to a sum
-    uint4 w[V];
-    F2 gw[E], s[4][E];  // gw: scale * gate * weight_post
+    F2 w[E], gw[E], s[4][E];  // gw: scale * gate * weight_post
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-        const int v = t + 32 * P * j;
-        w[j] = make_uint4(0u, 0u, 0u, 0u);
-        if (v < nvec && a.weight) w[j] = __ldg(static_cast<const uint4*>(a.weight) + v);
-        F2 f[H];
+        auto column = [&](const void* p, float fill, F2 (&f)[H]) {
+            if (on[j] && p) Pairs<T>::get(__ldg(static_cast<const uint4*>(p) + at[j]), f);
 #pragma unroll
-        for (int i = 0; i < H; ++i) gw[j * H + i] = F2::both(v < nvec ? a.scale : 0.f);
-        if (v < nvec && a.gate) {
-            Pairs<T>::get(__ldg(static_cast<const uint4*>(a.gate) + v), f);
+            for (int i = 0; i < H; ++i)
+                if (!on[j] || !p) f[i] = F2::both(on[j] ? fill : 0.f);
+        };
+        F2 f[H], g[H];
+        column(a.weight, 0.f, f);
 #pragma unroll
-            for (int i = 0; i < H; ++i) gw[j * H + i] = mul2(gw[j * H + i], f[i]);
-        }
-        if (v < nvec && a.weight_post) {
-            Pairs<T>::get(__ldg(static_cast<const uint4*>(a.weight_post) + v), f);
+        for (int i = 0; i < H; ++i) w[j * H + i] = f[i];
+        column(a.gate, 1.f, g);
+        column(a.weight_post, 1.f, f);
 #pragma unroll
-            for (int i = 0; i < H; ++i) gw[j * H + i] = mul2(gw[j * H + i], f[i]);
-        }
+        for (int i = 0; i < H; ++i) gw[j * H + i] = mul2(mul2(F2::both(a.scale), g[i]), f[i]);
     }
 #pragma unroll
     for (int k = 0; k < 4; ++k)
 #pragma unroll
         for (int i = 0; i < E; ++i) s[k][i] = F2::both(0.f);
-    TeamSum<P, 2> sum{slots[team], wt, team};
-    RowTerms q, next;
-    if (first < a.rows) q = row_terms(a, first);
+    TeamSums<R> sums{slots + team * (4 * R * warps), wt, warps, team};
+    RowTerms q[R], next[R];
+    auto terms = [&](RowTerms (&to)[R], int64_t r) {
+#pragma unroll
+        for (int k = 0; k < R; ++k) to[k] = row_terms(a, min(r + k, a.rows - 1));
+    };
+    if (first < a.rows) terms(q, first);
     for (int64_t r = first; r < a.rows; r += step) {
-        if (r + step < a.rows) next = row_terms(a, r + step);
-        copies_wait_but<RING<T> - 2>();
-        request();  // into the slot of the row before this one
-        auto take = [&](int i, F2 (&f)[E]) {
+        if (r + step < a.rows) terms(next, r + step);
+        copies_wait_but<L::RING - 2>();
+        request();  // into the slot of the rows before these
+        bool there[R];  // (a row beyond the last: nothing of it is stored or summed)
 #pragma unroll
-            for (int j = 0; j < V; ++j) Pairs<T>::get(ptx::lds128(mine + from + i * PART + j * (THREADS * 16)), f + j * H);
-        };
-        auto put = [&](void* p, const F2 (&f)[E]) {
-            uint4* row = reinterpret_cast<uint4*>(static_cast<T*>(p) + r * a.C);
-#pragma unroll
-            for (int j = 0; j < V; ++j)
-                if (t + 32 * P * j < nvec) row[t + 32 * P * j] = Pairs<T>::put(f + j * H);
-        };
-        F2 dx[E];
-        take(2, dx);
-        if (norm) {
-            F2 n[E], g[E], s0 = F2::both(0.f), s1 = F2::both(0.f);
-            take(0, g);
-            take(1, n);
-#pragma unroll
-            for (int i = 0; i < E; ++i) {
-                n[i] = mul2(add2(n[i], F2::both(-q.mean)), F2::both(q.rstd));
-                s[0][i] = fma2(g[i], n[i], s[0][i]);
-                s[1][i] = add2(s[1][i], g[i]);
-            }
+        for (int k = 0; k < R; ++k) there[k] = k == 0 || r + k < a.rows;
+        auto take = [&](int i, int k, F2 (&f)[E]) {
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                F2 wj[H];
-                Pairs<T>::get(w[j], wj);
-#pragma unroll
-                for (int i = 0; i < H; ++i) {
-                    g[j * H + i] = mul2(g[j * H + i], wj[i]);
-                    s0 = add2(s0, g[j * H + i]);
-                    s1 = fma2(g[j * H + i], n[j * H + i], s1);
-                }
+                const uint4 v = ptx::lds128(mine + from + i * PART + (k * V + j) * (THREADS * 16));
+                Pairs<T>::get(there[k] ? v : make_uint4(0u, 0u, 0u, 0u), f + j * H);
             }
-            float both[2] = {s0.lo() + s0.hi(), s1.lo() + s1.hi()};
-            sum(both);
-            const F2 m = F2::both(a.norm == LAYER ? -both[0] * b.inv_c : 0.f), c = F2::both(-both[1] * b.inv_c);
+        };
+        auto put = [&](void* p, int k, const F2 (&f)[E]) {
+            uint4* row = static_cast<uint4*>(p) + (r + k) * nvec;
 #pragma unroll
-            for (int i = 0; i < E; ++i) dx[i] = fma2(F2::both(q.rstd), add2(g[i], fma2(n[i], c, m)), dx[i]);
-        }
-        put(a.dx, dx);
-        F2 z[E], s0 = F2::both(0.f), s1 = F2::both(0.f);
-        take(3, z);
-        from = from + SLOT == RING<T> * SLOT ? 0 : from + SLOT;
+            for (int j = 0; j < V; ++j)
+                if (on[j] && there[k]) row[at[j]] = Pairs<T>::put(f + j * H);
+        };
+        F2 dx[R][E];
+        float both[2 * R];
+        if (norm) {
+            F2 n[R][E], g[R][E];
 #pragma unroll
-        for (int i = 0; i < E; ++i) {
-            z[i] = mul2(add2(z[i], F2::both(-q.mean_post)), F2::both(q.rstd_post));
-            s[2][i] = fma2(dx[i], z[i], s[2][i]);
-            s[3][i] = add2(s[3][i], dx[i]);
-            dx[i] = mul2(gw[i], dx[i]);
-            s0 = add2(s0, dx[i]);
-            s1 = fma2(dx[i], z[i], s1);
+            for (int k = 0; k < R; ++k) {
+                take(0, k, g[k]);
+                take(1, k, n[k]);
+                F2 s0 = F2::both(0.f), s1 = F2::both(0.f);
+                const F2 m = F2::both(-q[k].mean), rstd = F2::both(q[k].rstd);
+#pragma unroll
+                for (int i = 0; i < E; ++i) {
+                    n[k][i] = mul2(add2(n[k][i], m), rstd);
+                    s[0][i] = fma2(g[k][i], n[k][i], s[0][i]);
+                    s[1][i] = add2(s[1][i], g[k][i]);
+                    g[k][i] = mul2(g[k][i], w[i]);
+                    s0 = add2(s0, g[k][i]);
+                    s1 = fma2(g[k][i], n[k][i], s1);
+                }
+                both[2 * k] = s0.lo() + s0.hi(), both[2 * k + 1] = s1.lo() + s1.hi();
+            }
+            sums(both);
+#pragma unroll
+            for (int k = 0; k < R; ++k) {
+                const F2 m = F2::both(a.norm == LAYER ? -both[2 * k] * b.inv_c : 0.f), c = F2::both(-both[2 * k + 1] * b.inv_c), rstd = F2::both(q[k].rstd);
+                take(2, k, dx[k]);
+#pragma unroll
+                for (int i = 0; i < E; ++i) dx[k][i] = fma2(rstd, add2(g[k][i], fma2(n[k][i], c, m)), dx[k][i]);
+                put(a.dx, k, dx[k]);
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < R; ++k) {
+                take(2, k, dx[k]);
+                put(a.dx, k, dx[k]);
+            }
         }
+        F2 z[R][E];
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
+            take(3, k, z[k]);
+            F2 s0 = F2::both(0.f), s1 = F2::both(0.f);
+            const F2 m = F2::both(-q[k].mean_post), rstd = F2::both(q[k].rstd_post);
+#pragma unroll
+            for (int i = 0; i < E; ++i) {
+                if (post) z[k][i] = mul2(add2(z[k][i], m), rstd);
+                s[2][i] = fma2(dx[k][i], z[k][i], s[2][i]);
+                s[3][i] = add2(s[3][i], dx[k][i]);
+                dx[k][i] = mul2(gw[i], dx[k][i]);
+                s0 = add2(s0, dx[k][i]);
+                s1 = fma2(dx[k][i], z[k][i], s1);
+            }
+            both[2 * k] = s0.lo() + s0.hi(), both[2 * k + 1] = s1.lo() + s1.hi();
+        }
+        from = from + SLOT == L::RING * SLOT ? 0 : from + SLOT;
         if (a.dbranch) {
             if (post) {
-                float both[2] = {s0.lo() + s0.hi(), s1.lo() + s1.hi()};
-                sum(both);
-                const F2 m = F2::both(a.post == LAYER ? -both[0] * b.inv_c : 0.f), c = F2::both(-both[1] * b.inv_c);
+                sums(both);
 #pragma unroll
-                for (int i = 0; i < E; ++i) dx[i] = mul2(F2::both(q.rstd_post), add2(dx[i], fma2(z[i], c, m)));
+                for (int k = 0; k < R; ++k) {
+                    const F2 m = F2::both(a.post == LAYER ? -both[2 * k] * b.inv_c : 0.f), c = F2::both(-both[2 * k + 1] * b.inv_c), rstd = F2::both(q[k].rstd_post);
+#pragma unroll
+                    for (int i = 0; i < E; ++i) dx[k][i] = mul2(rstd, add2(dx[k][i], fma2(z[k][i], c, m)));
+                }
             }
-            put(a.dbranch, dx);
+#pragma unroll
+            for (int k = 0; k < R; ++k) put(a.dbranch, k, dx[k]);
         }
-        q = next;
+#pragma unroll
+        for (int k = 0; k < R; ++k) q[k] = next[k];
     }
 
     // The block's sums over its rows: the teams' in team order, through the ring's memory.
+    const uint32_t live = static_cast<uint32_t>(32 * teams * warps);
     copies_wait_but<0>();
-    __syncthreads();
+    ptx::named_bar_sync(0, live);
     float4* joined = reinterpret_cast<float4*>(ring);
     float* to = b.partials + static_cast<int64_t>(blockIdx.x) * 4 * a.C;
-    for (int k = 0; k < TEAMS_ROWS; ++k) {
-        if (k > 0) __syncthreads();
+    for (int k = 0; k < teams; ++k) {
+        if (k > 0) ptx::named_bar_sync(0, live);
         if (team != k) continue;
 #pragma unroll
         for (int f = 0; f < 4; ++f)
 #pragma unroll
             for (int i = 0; i < E; i += 2) {
-                const int j = i / H, c = (t + 32 * P * j) * N + 2 * (i % H);
+                const int j = i / H, c = at[j] * Vec<T>::N + 2 * (i % H);
                 float4 v = make_float4(s[f][i].lo(), s[f][i].hi(), s[f][i + 1].lo(), s[f][i + 1].hi());
-                float4* at = joined + (f * E / 2 + i / 2) * (32 * P) + t;
-                if (k > 0) v.x += at->x, v.y += at->y, v.z += at->z, v.w += at->w;
-                if (k + 1 < TEAMS_ROWS) *at = v;
-                else if (c < a.C) *reinterpret_cast<float4*>(to + static_cast<int64_t>(f) * a.C + c) = v;
+                float4* sofar = joined + (f * E / 2 + i / 2) * (32 * warps) + t;
+                if (k > 0) v.x += sofar->x, v.y += sofar->y, v.z += sofar->z, v.w += sofar->w;
+                if (k + 1 < teams) *sofar = v;
+                else if (on[j]) *reinterpret_cast<float4*>(to + static_cast<int64_t>(f) * a.C + c) = v;
             }
     }
 }
 
-template <typename T, int P>
+template <typename T>
+using NarrowRows = RowsConfig<T, 4, sizeof(T) == 2 ? 2 : 1, 16, 3>;  // up to 4096 columns
+template <typename T>
+using WideRows = RowsConfig<T, 8, 1, 12, sizeof(T) == 2 ? 3 : 2>;    // up to 6144
+
+template <typename L>
 cudaError_t launch_rows(const Backward& b, cudaLaunchConfig_t cfg) {
-    constexpr auto kernel = residual_rows_kernel<T, P>;
-    constexpr int smem = RING<T> * ROW_BYTES<T> * 32 * ROW_WARPS;
-    static_assert(smem >= 4 * COLS * 4 * 32 * P && smem <= 220 * 1024, "the ring holds a team's sums, a block the ring");
+    constexpr auto kernel = residual_rows_kernel<L>;
     cfg.gridDim = dim3(static_cast<unsigned>(b.row_blocks), 1, 1);
-    cfg.blockDim = dim3(32 * ROW_WARPS, 1, 1);
-    cfg.dynamicSmemBytes = smem;
-    const cudaError_t e = allow_smem<kernel>(smem);
+    cfg.blockDim = dim3(static_cast<unsigned>(L::THREADS), 1, 1);
+    cfg.dynamicSmemBytes = L::SMEM;
+    const cudaError_t e = allow_smem<kernel>(L::SMEM);
     return e == cudaSuccess ? cudaLaunchKernelEx(&cfg, kernel, b) : e;
 }
 
@@ -931,17 +1022,24 @@ __global__ void __launch_bounds__(32 * PARAM_WARPS) residual_params_kernel(const
 
 constexpr int MAX_SMS = 152;  // of a full GB300; the workspace does not depend on the device
 
-// Warps of a team in one pass, a divisor of a block's; 0: two passes.
+enum class Rows { NARROW, WIDE, TWO_PASSES };
+Rows rows_of(int64_t C) {
+    return C <= NarrowRows<float>::MAX_C ? Rows::NARROW : C <= WideRows<float>::MAX_C ? Rows::WIDE : Rows::TWO_PASSES;
+}
+static_assert(NarrowRows<float>::MAX_C == NarrowRows<__nv_bfloat16>::MAX_C && WideRows<float>::MAX_C == WideRows<__nv_bfloat16>::MAX_C);
+
+// Warps of a team in one pass.
 int team_warps_of(int64_t C) {
-    for (const int w : {1, 2, 3, 4, 6, 12})
-        if (C <= 32 * w * COLS) return w;
-    return 0;
+    const int64_t per_warp = 64 * (rows_of(C) == Rows::NARROW ? NarrowRows<float>::E : WideRows<float>::E);
+    return static_cast<int>((C + per_warp - 1) / per_warp);
 }
 
 int row_blocks_of(int64_t rows, int64_t C, int dtype) {
-    if (const int w = team_warps_of(C)) {
-        const int64_t teams = ROW_WARPS / w;
-        return static_cast<int>(std::min<int64_t>((rows + teams - 1) / teams, MAX_SMS));
+    if (rows_of(C) != Rows::TWO_PASSES) {
+        const bool narrow = rows_of(C) == Rows::NARROW;
+        const int64_t at_once = (narrow ? NarrowRows<float>::WARPS : WideRows<float>::WARPS) / team_warps_of(C) *
+                                (narrow && dtype == MMBWD_BF16 ? NarrowRows<__nv_bfloat16>::R : 1);
+        return static_cast<int>(std::min<int64_t>((rows + at_once - 1) / at_once, MAX_SMS));
     }
     const int64_t nvec = C / (dtype == MMBWD_F32 ? 4 : 8), tiles = (nvec + COL_THREADS - 1) / COL_THREADS;
     // some eight blocks of a column tile to an SM
@@ -950,11 +1048,11 @@ int row_blocks_of(int64_t rows, int64_t C, int dtype) {
 
 size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
-size_t sums_bytes(int64_t rows, int64_t C) { return team_warps_of(C) ? 0 : align256(static_cast<size_t>(rows) * 16); }
+size_t sums_bytes(int64_t rows, int64_t C) { return rows_of(C) != Rows::TWO_PASSES ? 0 : align256(static_cast<size_t>(rows) * 16); }
 
 template <typename T>
 cudaError_t backward(const ResidualNorm& a, int dtype, int num_sms, cudaStream_t stream) {
-    Backward b{a, a.ws, a.ws + sums_bytes(a.rows, a.C) / 4, 1.f / static_cast<float>(a.C), row_blocks_of(a.rows, a.C, dtype)};
+    Backward b{a, a.ws, a.ws + sums_bytes(a.rows, a.C) / 4, 1.f / static_cast<float>(a.C), row_blocks_of(a.rows, a.C, dtype), team_warps_of(a.C)};
     cudaLaunchConfig_t cfg{};
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -963,14 +1061,9 @@ cudaError_t backward(const ResidualNorm& a, int dtype, int num_sms, cudaStream_t
     cfg.numAttrs = 1;
     cfg.stream = stream;
     cudaError_t e;
-    if (const int w = team_warps_of(a.C)) {
+    if (rows_of(a.C) != Rows::TWO_PASSES) {
         b.row_blocks = std::min(b.row_blocks, num_sms);
-        e = w == 1   ? launch_rows<T, 1>(b, cfg)
-            : w == 2 ? launch_rows<T, 2>(b, cfg)
-            : w == 3 ? launch_rows<T, 3>(b, cfg)
-            : w == 4 ? launch_rows<T, 4>(b, cfg)
-            : w == 6 ? launch_rows<T, 6>(b, cfg)
-                     : launch_rows<T, 12>(b, cfg);
+        e = rows_of(a.C) == Rows::NARROW ? launch_rows<NarrowRows<T>>(b, cfg) : launch_rows<WideRows<T>>(b, cfg);
     } else {
         cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(a.rows, MAX_SMS * 8)), 1, 1);
         cfg.blockDim = dim3(SUM_THREADS, 1, 1);
