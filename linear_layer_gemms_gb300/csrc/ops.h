@@ -149,7 +149,8 @@ struct GradTensor {
     bool bf16;
 };
 constexpr int GRAD_TABLE = 1024;       // tensors of one launch (28 KB of kernel parameters)
-constexpr int GRAD_BLOCKS_PER_SM = 8;  // as many of 256 threads as are resident
+constexpr int GRAD_BLOCKS_PER_SM = 4;  // of the norm: as many of its 256-thread blocks as are resident
+constexpr int GRAD_SCALE_BLOCKS_PER_SM = 8;
 constexpr int GRAD_MAX_BLOCKS = 1536;  // partial sums of one launch
 // given == nullptr: the norm of the list first, into `ws` and `norm`; `scale`: the outs.
 cudaError_t grad_launch(const GradTensor* list, int n, float* norm, const float* given, bool scale, float max_norm,
