@@ -22,7 +22,9 @@
  * tensor cores. fp32 products are fp32 fused multiply-adds, or three tf32 products whose
  * accumulators are read back and added up in registers every 128 values of the
  * reduction (mmbwd_run's are not: the tensor core rounds toward zero): a relative error
- * of the sums of 6e-7 (2-norm, random operands) at every length, as of an fp32 sum.
+ * of the sums of 6e-7 (2-norm, random operands) at every length, as of an fp32 sum. An
+ * infinite fp32 operand may give NaN where the sum is infinite (infinity has no remainder
+ * to split off), in the outputs that it belongs to.
  * MMBWD_ACT_F32_PATH in the environment forces the fp32 kernel: "32", "64" (tiles of
  * fused multiply-adds) or "spans".
  */

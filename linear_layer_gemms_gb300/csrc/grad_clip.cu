@@ -257,7 +257,7 @@ bool fill(Table<N>* tab, const GradTensor* t, int n) {
         tab->count[i] = t[i].count * 2 + (t[i].bf16 ? 1 : 0);
         tab->first[i] = static_cast<int>(at);
         at += chunks_of(t[i]);
-        if (at > INT32_MAX) return false;
+        if (at > INT32_MAX / 2) return false;  // (a chunk's number plus a grid stays an int)
     }
     tab->first[n] = static_cast<int>(at);
     tab->n = n;

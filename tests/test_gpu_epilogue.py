@@ -378,3 +378,97 @@ def test_repeats_are_identical_and_failed_launches_write_nothing():
             assert (out == 9).all()
     host = torch.zeros(64, 64)
     assert mm.mmbwd_act_backward(d["inp"], host, d["inp"], 64, 1, mm.F32) == mm.ERR_MEMORY
+
+
+# ------------------------------------------------------------------ long lists of items, offsets beyond 32 bits
+
+def rows_of(T):
+    """Rows at both ends and around the middle."""
+    return sorted({*range(min(T, 70)), *range(T // 2 - 40, T // 2 + 40), *range(max(T - 300, 0), T)})
+
+
+def tall(T, n, dtype, k):
+    """T rows that repeat 997 different ones."""
+    few = ref.rounded(ref.normal(k, 997, n), dtype)
+    return few, few.to(ref.TDT[dtype]).repeat(T // 997 + 1, 1)[:T].contiguous()
+
+
+@pytest.mark.parametrize("dtype,T,OC", [("bf16", 66_000, 4096), ("bf16", 530_000, 4104), ("f32", 530_000, 4100)])
+def test_forward_of_many_rows(dtype, T, OC):
+    """More tiles than a launch's item table holds; more than 2^31 outputs."""
+    C = 16
+    few, inp = tall(T, C, dtype, 1)
+    x = inputs(1, C, OC, dtype, 2, residual=False)
+    d = {k: dev(v, dtype) for k, v in x.items()}
+    out = torch.full((T, OC), NAN, device="cuda", dtype=ref.TDT[dtype])
+    pre = torch.full_like(out, NAN)
+    ok(mm.mmbwd_forward_act(out, pre, inp, d["weight"], d["bias"], None, 1, T, C, OC, mm.ACT_GELU, DT[dtype]))
+    rows = torch.tensor(rows_of(T), device="cuda")
+    for got, want in zip((out, pre), ref.forward_act(few, x["weight"], x["bias"], None, "gelu", dtype)):
+        ref.check(got[rows], want[0][rows % 997], want[1][rows % 997])
+        for i in range(0, T - 997, 997):  # equal rows in, equal rows out
+            assert torch.equal(got[i:i + 997], got[:997]), i
+    # in place, from the residual
+    ok(mm.mmbwd_forward_act(out, None, inp, d["weight"], d["bias"], out, 1, T, C, OC, mm.ACT_GELU, DT[dtype]))
+    first = ref.forward_act(few, x["weight"], x["bias"], ref.rounded(ref.act_value(pre[:997].double(), "gelu"), dtype), "gelu", dtype)[0]
+    # (what was added is known to a step of its type, which the sum keeps)
+    ref.check(out[rows], first[0][rows % 997], (first[1] + 4 * ref.HALF[dtype] * first[0].abs().clamp(min=1))[rows % 997])
+
+
+@pytest.mark.parametrize("dtype,T,C", [("bf16", 66_000, 4096), ("bf16", 530_000, 4104), ("f32", 530_000, 4100)])
+def test_gradients_of_many_rows(dtype, T, C):
+    OC = 16
+    dout_few, dout = tall(T, OC, dtype, 3)
+    pre_few, dpre = tall(T, C, dtype, 4)
+    weight = ref.rounded(ref.normal(5, OC, C, std=0.1), dtype)
+    inp = torch.zeros_like(dpre)
+    inp[T - 1] = 2.0
+    dweight = torch.zeros(OC, C, device="cuda", dtype=ref.TDT[dtype])
+    ws, n = workspace(T, C, OC, dtype)
+    ok(mm.mmbwd_run_act(dpre, dweight, None, dout, inp, dev(weight, dtype), dpre, ws, n, 1, T, C, OC, mm.ACT_SILU, DT[dtype]))
+    (want, bound), _, _ = ref.run_act(dout_few, 0 * pre_few, weight, pre_few, 0 * weight, "silu", dtype)
+    rows = torch.tensor(rows_of(T), device="cuda")
+    ref.check(dpre[rows], want[rows % 997], bound[rows % 997])
+    for i in range(0, T - 997, 997):
+        assert torch.equal(dpre[i:i + 997], dpre[:997]), i
+    # One product beside zeros, which add without a rounding: exact in bf16. In fp32 hi * 2 + lo * 2,
+    # where lo (13 bits of x, below 2^-10 |x|) is read to 11 bits: the bound of one product.
+    want = (2 * dout[T - 1]).double()[:, None].expand(OC, C)
+    ref.check(dweight, want, ref.product_bound(1, want.abs(), "f32") if dtype == "f32" else 0 * want, "dweight")
+
+
+def test_alone_beyond_32_bits():
+    n = 2 ** 31 + 8 * 12345 + 3
+    pre = torch.full((n,), 1.0, device="cuda", dtype=torch.bfloat16)
+    dout = torch.full_like(pre, 2.0)
+    pre[-5:] = -1.0
+    ok(mm.mmbwd_act_backward(dout, dout, pre, n, mm.ACT_RELU, mm.BF16))
+    assert (dout[-5:] == 0).all() and (dout[:-5] == 2).all()
+
+
+@pytest.mark.parametrize("OC", [264, 392])
+def test_bias_gradient_by_a_product_of_ones(monkeypatch, OC):
+    x = gradient_inputs(600, 520, OC, "bf16", "gelu", 31)
+    plain = check_run(x, "gelu", "bf16")
+    monkeypatch.setenv("MMBWD_DBIAS", "ones")
+    for splits in ("1", "2"):
+        monkeypatch.setenv("MMBWD_SPLITK", splits)
+        check_run(x, "gelu", "bf16")
+    assert plain[0].numel()
+
+
+@pytest.mark.parametrize("shift", [8, 16, 24])
+@pytest.mark.parametrize("T", [20, 300])
+def test_rows_that_start_between_32_byte_boundaries(T, shift):
+    """Outputs, residual and pre 16-byte aligned, in rows that are multiples of 32 bytes."""
+    C, OC = 136, 272
+    x = inputs(T, C, OC, "bf16", 41)
+    want = check_forward(x, "silu", "bf16")
+    d = {k: dev(v, "bf16") for k, v in x.items()}
+    room = torch.full((3, T * OC + 64), 3.0, device="cuda", dtype=torch.bfloat16)
+    out, pre, res = (r[shift:shift + T * OC].view(T, OC) for r in room)
+    res.copy_(d["residual"])
+    ok(mm.mmbwd_forward_act(out, pre, d["inp"], d["weight"], d["bias"], res, 1, T, C, OC, mm.ACT_SILU, mm.BF16))
+    ok(mm.mmbwd_forward_act(res, None, d["inp"], d["weight"], d["bias"], res, 1, T, C, OC, mm.ACT_SILU, mm.BF16))
+    assert torch.equal(out, want[0]) and torch.equal(pre, want[1]) and torch.equal(res, want[0])
+    assert (room[:, :shift] == 3).all() and (room[:, shift + T * OC:] == 3).all()

@@ -268,3 +268,17 @@ def test_failed_launches_and_host_memory():
     assert norm.item() == 9.0
     assert mm.mmbwd_grad_norm(norm, mm.grad_list([entry(torch.zeros(5))]), ws, ws.numel()) == mm.ERR_MEMORY
     assert mm.mmbwd_grad_norm(torch.zeros(1), mm.grad_list([entry(t)]), ws, ws.numel()) == mm.ERR_MEMORY
+
+
+def test_a_tensor_of_more_than_2_31_values():
+    n = 2 ** 31 + 12345
+    t = torch.zeros(n, device="cuda", dtype=torch.bfloat16)
+    t[0], t[2 ** 31 + 3], t[n - 1] = 2.0, 1.0, 2.0
+    norm = torch.full((1,), float("nan"), device="cuda")
+    ws_bytes = mm.mmbwd_grad_workspace_bytes(1)
+    ws = torch.empty(ws_bytes, device="cuda", dtype=torch.uint8)
+    lst = mm.grad_list([(t, None, n, mm.BF16)])
+    assert mm.mmbwd_grad_clip(norm, lst, 1.5, ws, ws_bytes) == mm.OK
+    assert norm.item() == 3.0  # sums of squares that are exact
+    # (1.5 / 3.000001 rounds to 0.5 in bf16's eight bits)
+    assert t[0] == 1.0 and t[2 ** 31 + 3] == 0.5 and t[n - 1] == 1.0 and torch.count_nonzero(t) == 3

@@ -336,3 +336,44 @@ def test_failed_launches_and_host_memory():
     assert (r == 9).all()
     args[5] = torch.zeros(4, 64)
     assert mm.lnbwd_residual_forward(torch.empty_like(r), r, *args) == mm.ERR_MEMORY
+
+
+def test_offsets_beyond_32_bits():
+    """More than 2^31 values, rows that repeat 997 different ones: both ends against 64 bits,
+    and every repetition the same."""
+    T, C = 530_000, 4104
+    x = inputs(997, C, "bf16", "rms", "layer", seed=7)
+    many = lambda t: dev(t, "bf16").repeat(T // 997 + 1, 1)[:T].contiguous()  # noqa: E731
+    d = {k: dev(x[k], "bf16") for k in ("gate", "weight_post", "weight", "bias")}
+    r, branch = many(x["x"]), many(x["branch"])
+    s = {k: torch.full((T,), NAN, device="cuda") if k != "mean_post" else None for k in STATS}
+    out = torch.full((T, C), NAN, device="cuda", dtype=torch.bfloat16)
+    ok(mm.lnbwd_residual_forward(out, r, *s.values(), r, branch, d["gate"], d["weight_post"], None, d["weight"], d["bias"], 1, T, C, 0.5,
+                                 ref.EPS, mm.NORM_RMS, mm.NORM_LAYER, mm.BF16))
+    want = ref.residual_forward(x["x"], x["branch"], x["gate"], x["weight_post"], None, x["weight"], x["bias"], 0.5, "rms", "layer", "bf16")
+    got = {"out": out, "residual_out": r, **s}
+    rows = torch.tensor([*range(20), *range(T - 300, T)], device="cuda")
+    for k, (v, e) in want.items():
+        if k != "mean_post":
+            ref.check(got[k][rows], v[rows % 997], e[rows % 997], k)
+            for i in range(0, T - 997, 997):
+                assert torch.equal(got[k][i:i + 997], got[k][:997]), (k, i)
+    dres = many(x["dresidual"])
+    dout = torch.zeros_like(dres)
+    dout[T - 300:] = dev(x["dout"], "bf16")[rows[20:] % 997]
+    dbranch = out
+    dbias = torch.zeros(C, device="cuda", dtype=torch.bfloat16)
+    n = mm.lnbwd_residual_backward_workspace_bytes(1, T, C, mm.BF16)
+    ws = torch.empty(n, device="cuda", dtype=torch.uint8)
+    ok(mm.lnbwd_residual_backward(dres, dbranch, None, None, None, None, dbias, dout, dres, r, branch, d["gate"], d["weight_post"], None,
+                                  d["weight"], *s.values(), ws, n, 1, T, C, 0.5, mm.NORM_RMS, mm.NORM_LAYER, mm.BF16))
+    stats = [None if s[k] is None else s[k][rows].double() for k in STATS]
+    want = ref.residual_backward(dout[rows].double(), x["dresidual"][rows % 997], r[rows].double(), x["branch"][rows % 997], x["gate"],
+                                 x["weight_post"], None, x["weight"], stats, {}, 0.5, "rms", "layer", "bf16")
+    ref.check(dres[rows], *want["dx"], "dx")
+    ref.check(dbranch[rows], *want["dbranch"], "dbranch")
+    for i in range(0, T - 300 - 997, 997):
+        assert torch.equal(dres[i:i + 997], dres[:997]) and torch.equal(dbranch[i:i + 997], dbranch[:997]), i
+    total = dout[T - 300:].double()
+    e = 400 * ref.U * total.abs().sum(0)  # (zeros add without a rounding)
+    ref.check(dbias, total.sum(0), ref.stored(e, total.sum(0), "bf16"), "dbias")
