@@ -1,13 +1,17 @@
 // fp32 products of mmbwd_forward_act and mmbwd_run_act (include/linear_epilogue.h) that are
 // too small for the tensor-core kernel's tiles of 256 x 128: tiles of 64 x 64 or 32 x 32,
-// whose K is shared by the G groups of 64 threads of a block.
+// whose K is shared by the G warps of a block.
 //
 // Bound by fp32 fused multiply-adds (128 a clock and SM) where the tiles fill the device,
-// by the latency of a block's loads and barriers below that; sharing K inside a block
-// shortens that chain without a second launch or a workspace. Each group
-// accumulates every G-th K-tile (of 8) in registers, 8 x 8 or 4 x 4 outputs a thread, and the
-// groups' sums are added in group order through shared memory, where the epilogue
-// starts: the same bits on every call. The backward's two products share one launch.
+// by the latency of a block's loads below that; sharing K inside a block
+// shortens that chain without a second launch or a workspace. Each warp
+// accumulates every G-th K-tile (of 8) in registers, 8 x 16 or 4 x 8 outputs a thread, in pairs
+// (two multiply-adds to an instruction: 1000 x 1600 -> 1600 in tiles of 64 170 -> 141 us), and the
+// warps' sums are added in warp order through shared memory, where the epilogue
+// starts: the same bits on every call. Shared memory gives a warp 32 values a clock, so the
+// outputs of a thread are as many as its registers hold (8 x 8 of 64 threads, behind a barrier
+// of theirs: 141 us, 8 x 16 of one warp: 128; the multiply-add pipe is then busy for 62% of
+// the time). The backward's two products share one launch.
 #include "act.cuh"
 #include "ops.h"
 #include "ptx.cuh"
@@ -21,7 +25,7 @@
 namespace mmbwd {
 namespace {
 
-constexpr int BK = 8, PAD = 4, GROUP = 64;
+constexpr int BK = 8, PAD = 4, GROUP = 32;
 
 // One product D (M x N, row-major) = A . B: A (M x K) row-major, or stored (K x M) where
 // a_km; B (K x N) row-major, or stored (N x K) where b_nk.
@@ -33,7 +37,7 @@ struct Product {
 };
 
 struct Params {
-    Product first, second;     // blocks of the first product's tiles, then the second's
+    Product first, second;
     const float* bias;         // forward
     const float* residual;     // forward; may be D
     float* pre;                // forward: stored; backward: read, may be D
@@ -51,9 +55,9 @@ constexpr int smem_bytes() {
 
 template <int TM, int G, bool A_KM, bool B_NK, Epilogue EPI>
 __device__ __forceinline__ void tile_product(const Params& p, const Product& q, int tile, float* smem) {
-    constexpr int TILE = 8 * TM, LD = TILE + PAD, LOADS = TILE * BK / 4 / GROUP, H = TM / 4;
+    constexpr int TILE = 8 * TM, TN = 2 * TM, LD = TILE + PAD, LOADS = TILE * BK / 4 / GROUP, H = TM / 4, W = TN / 4;
     const int group = static_cast<int>(threadIdx.x) / GROUP, tid = static_cast<int>(threadIdx.x) % GROUP;
-    const int tx = tid % 8, ty = tid / 8;
+    const int tx = tid % 4, ty = tid / 4;
     const int64_t m0 = static_cast<int64_t>(tile / q.tiles_n) * TILE, n0 = static_cast<int64_t>(tile % q.tiles_n) * TILE;
     float* As = smem + group * 4 * BK * LD;  // [2][BK][LD]
     float* Bs = As + 2 * BK * LD;
@@ -96,12 +100,12 @@ __device__ __forceinline__ void tile_product(const Params& p, const Product& q, 
             put(Bs + buf * BK * LD, rb[l], tid + l * GROUP, B_NK);
         }
     };
-    float acc[TM][TM];
+    act::Two acc[TM][TN / 2];
 #pragma unroll
     for (int i = 0; i < TM; ++i)
 #pragma unroll
-        for (int j = 0; j < TM; ++j) acc[i][j] = 0.f;
-    float colsum = 0.f;
+        for (int j = 0; j < TN / 2; ++j) acc[i][j] = act::Two::both(0.f);
+    float colsum[TILE / GROUP] = {};
 
     const int64_t step = static_cast<int64_t>(G) * BK;
     int64_t k0 = static_cast<int64_t>(group) * BK;
@@ -109,32 +113,38 @@ __device__ __forceinline__ void tile_product(const Params& p, const Product& q, 
     if (k0 < q.K) {
         load(k0);
         store(0);
-        ptx::named_bar_sync(static_cast<uint32_t>(1 + group), GROUP);
+        __syncwarp();
     }
     for (; k0 < q.K; k0 += step, buf ^= 1) {
         if (k0 + step < q.K) load(k0 + step);
         const float *a_s = As + buf * BK * LD, *b_s = Bs + buf * BK * LD;
-        if (sums && tid < TILE) {
+        if (sums) {
 #pragma unroll
-            for (int k = 0; k < BK; ++k) colsum += a_s[k * LD + tid];
+            for (int k = 0; k < BK; ++k)
+#pragma unroll
+                for (int i = 0; i < TILE / GROUP; ++i) colsum[i] += a_s[k * LD + i * GROUP + tid];
         }
 #pragma unroll
         for (int k = 0; k < BK; ++k) {
-            float a[TM], b[TM];
+            float a[TM];
+            act::Two b[TN / 2];
 #pragma unroll
             for (int h = 0; h < H; ++h) {
                 const float4 av = *reinterpret_cast<const float4*>(a_s + k * LD + ty * 4 + 32 * h);
-                const float4 bv = *reinterpret_cast<const float4*>(b_s + k * LD + tx * 4 + 32 * h);
                 a[4 * h] = av.x, a[4 * h + 1] = av.y, a[4 * h + 2] = av.z, a[4 * h + 3] = av.w;
-                b[4 * h] = bv.x, b[4 * h + 1] = bv.y, b[4 * h + 2] = bv.z, b[4 * h + 3] = bv.w;
+            }
+#pragma unroll
+            for (int h = 0; h < W; ++h) {
+                const ulonglong2 bv = *reinterpret_cast<const ulonglong2*>(b_s + k * LD + tx * 4 + 16 * h);
+                b[2 * h].v = bv.x, b[2 * h + 1].v = bv.y;
             }
 #pragma unroll
             for (int i = 0; i < TM; ++i)
 #pragma unroll
-                for (int j = 0; j < TM; ++j) acc[i][j] = fmaf(a[i], b[j], acc[i][j]);
+                for (int j = 0; j < TN / 2; ++j) acc[i][j] = act::fma(act::Two::both(a[i]), b[j], acc[i][j]);
         }
         if (k0 + step < q.K) store(buf ^ 1);
-        ptx::named_bar_sync(static_cast<uint32_t>(1 + group), GROUP);
+        __syncwarp();
     }
 
     __syncthreads();  // the staged tiles have been read: their memory takes the groups' sums
@@ -143,10 +153,13 @@ __device__ __forceinline__ void tile_product(const Params& p, const Product& q, 
 #pragma unroll
     for (int i = 0; i < TM; ++i)
 #pragma unroll
-        for (int h = 0; h < H; ++h)
-            *reinterpret_cast<float4*>(part + (ty * 4 + (i & 3) + (i >> 2) * 32) * TILE + tx * 4 + 32 * h) =
-                make_float4(acc[i][4 * h], acc[i][4 * h + 1], acc[i][4 * h + 2], acc[i][4 * h + 3]);
-    if (sums && tid < TILE) colsums[group * TILE + tid] = colsum;
+        for (int h = 0; h < W; ++h)
+            *reinterpret_cast<float4*>(part + (ty * 4 + (i & 3) + (i >> 2) * 32) * TILE + tx * 4 + 16 * h) =
+                make_float4(acc[i][2 * h].lo(), acc[i][2 * h].hi(), acc[i][2 * h + 1].lo(), acc[i][2 * h + 1].hi());
+    if (sums) {
+#pragma unroll
+        for (int i = 0; i < TILE / GROUP; ++i) colsums[group * TILE + i * GROUP + tid] = colsum[i];
+    }
     __syncthreads();
     for (int e = static_cast<int>(threadIdx.x); e < TILE * TILE / 4; e += G * GROUP) {
         const int row = e / (TILE / 4), col = e % (TILE / 4) * 4;
@@ -207,9 +220,14 @@ __global__ void __launch_bounds__(G* GROUP) small_backward_kernel(const __grid_c
     extern __shared__ __align__(16) float smem[];
     ptx::grid_launch_dependents();
     ptx::grid_dependency_wait();
-    const int b = static_cast<int>(blockIdx.x);
-    if (b < p.first.tiles) tile_product<TM, G, true, false, DWEIGHT>(p, p.first, b, smem);
-    else tile_product<TM, G, false, false, DPRE>(p, p.second, b - p.first.tiles, smem);
+    // the tiles with the longer sums first: the others fill the gaps behind them
+    int b = static_cast<int>(blockIdx.x);
+    const bool first_first = p.first.K >= p.second.K;
+    const int ahead = first_first ? p.first.tiles : p.second.tiles;
+    const bool dweight = first_first == (b < ahead);
+    if (b >= ahead) b -= ahead;
+    if (dweight) tile_product<TM, G, true, false, DWEIGHT>(p, p.first, b, smem);
+    else tile_product<TM, G, false, false, DPRE>(p, p.second, b, smem);
 }
 
 template <auto kernel>
@@ -250,22 +268,26 @@ namespace {
 
 // Time models (us), fitted to the measurements below; times (us) on one GB300:
 //                         tokens  32 x 32  64 x 64  spans (forward | backward 32, 64, spans)
-//    16 x 6400 -> 1600        34      110      208    156 |
-//   100 x  768 -> 2304                 22       30     36 |   50   83   77
-//   200 x  264 ->  388                5.7     13.8   19.2 |  9.6 15.8 20.2
-//   333 x  772 -> 1300                 32       31     30 |   60   67   40
-//   500 x  768 ->  768                 33       31     30 |   50   44   29
-//  1000 x 1600 -> 1600                207      170     50 |  330  282   81
-//  2048 x 1600 -> 2400                592      454     93 |  958  910  261
-// A block of 32 x 32 outputs takes 0.0167 us per value of K alone on its SM and 0.013 beside
-// others, one of 64 x 64 0.0365; the tensor cores' items of 256 x 128 0.72 us a k-block of 32 and 4
-// for the epilogue, 8 for the launch and its first loads.
+//    16 x 6400 -> 1600        29.1     86.7      149    149 | 98.3  120 60.1
+//    40 x 1600 -> 6400                 51.9     43.8   47.1 |  117  163  154
+//    64 x  768 ->  768         9.7     10.1     23.0   27.0 | 15.5 22.1 26.0
+//   100 x  768 -> 2304               18.4     23.3   27.5 | 41.3 55.6 61.4
+//   200 x  264 ->  388                6.9     11.8   17.5 |  9.6 14.6 19.1
+//   333 x  772 -> 1300               26.2     23.7   28.5 | 46.6 44.0 39.2
+//   500 x  768 ->  768               26.6     23.3   28.1 | 39.3 36.6 27.6
+//  1000 x 1600 -> 1600                182      128     47 |  290  228   80
+//  2048 x 1600 -> 2400                525      342     89 |  839  641  260
+// A block of 32 x 32 outputs takes 0.0148 us per value of K alone on its SM and 0.0107 beside
+// others, and as long as 60 values more for its first loads and its sums; one of 64 x 64
+// 0.0265 and 0.0298, and 120 values more; below 64 values some warps have none. The tensor
+// cores' items of 256 x 128 take 0.72 us a k-block of 32 and 4 for the epilogue, 7 for the
+// launch and its first loads.
 double small_us(int tile, const Product* q, int n, int num_sms) {
     double work = 0.0, longest = 0.0;
     for (int i = 0; i < n; ++i) {
         const double K = static_cast<double>(q[i].K), tiles = static_cast<double>(tiles_of(q[i].M, q[i].N, tile));
-        work += tiles * (n > 1 ? K + 60.0 : K) * (tile == 32 ? 0.013 : 0.0365);
-        longest = std::max(longest, K * (tile == 32 ? 0.0167 : 0.0365));
+        work += tiles * (tile == 32 ? (std::max(K, 64.0) + 60.0) * 0.0107 : (std::max(K, 64.0) + 120.0) * 0.0298);
+        longest = std::max(longest, K * (tile == 32 ? 0.0148 : 0.0265));
     }
     return 3.0 + std::max(work / num_sms, longest);
 }
@@ -280,7 +302,7 @@ double spans_us(const Product* q, int n, int num_sms) {
         longest = std::max(longest, item);
     }
     // one product: whole rounds of equal items; two: the short ones fill the gaps
-    return 8.0 + (n == 1 ? std::ceil(items / pairs) * longest : std::max(longest, work / pairs + 0.3 * longest));
+    return 7.0 + (n == 1 ? std::ceil(items / pairs) * longest : std::max(longest, work / pairs + 0.3 * longest));
 }
 
 // MMBWD_ACT_F32_PATH = "32", "64" or "spans" forces a kernel (tests, tuning).
