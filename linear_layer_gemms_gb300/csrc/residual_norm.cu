@@ -7,8 +7,8 @@
 // (LAYER) of values at hand. Backward: four rows read, two written. A team owns a row as
 // well, a thread 8 or 16 columns of it; it has the next rows in flight, forms the row's
 // four sums in two rounds and keeps its columns' parameter sums in registers over all
-// rows of the team. Rows that no team of 12 warps holds (C > 6144) take two passes: one
-// forms the rows' sums, one goes down column tiles.
+// rows of the team. Rows that no team holds (C > 8192 in bf16, 6144 in fp32) take two
+// passes: one forms the rows' sums, one goes down column tiles.
 #include "../../include/residual_norm.h"
 #include "ops.h"
 #include "ptx.cuh"
@@ -821,6 +821,10 @@ template <typename T>
 using NarrowRows = RowsConfig<T, 4, sizeof(T) == 2 ? 2 : 1, 16, 3>;  // up to 4096 columns
 template <typename T>
 using WideRows = RowsConfig<T, 8, 1, 12, sizeof(T) == 2 ? 3 : 2>;    // up to 6144
+// Up to 8192, bf16 (the ring of fp32 rows does not fit): 128 registers a thread, a few of
+// which go through local memory; 2000 x 8192 with two RMS norms 63 us, with two LayerNorms 90, in
+// two passes 92 and 93.
+using WidestRows = RowsConfig<__nv_bfloat16, 8, 1, 16, 3>;
 
 template <typename L, bool MEAN, bool MEAN_POST>
 cudaError_t launch_rows(const Backward& b, cudaLaunchConfig_t cfg) {
@@ -1055,23 +1059,24 @@ __global__ void __launch_bounds__(32 * PARAM_WARPS) residual_params_kernel(const
 
 constexpr int MAX_SMS = 152;  // of a full GB300; the workspace does not depend on the device
 
-enum class Rows { NARROW, WIDE, TWO_PASSES };
-Rows rows_of(int64_t C) {
-    return C <= NarrowRows<float>::MAX_C ? Rows::NARROW : C <= WideRows<float>::MAX_C ? Rows::WIDE : Rows::TWO_PASSES;
+enum class Rows { NARROW, WIDE, WIDEST, TWO_PASSES };
+Rows rows_of(int64_t C, int dtype) {
+    if (C <= NarrowRows<float>::MAX_C) return Rows::NARROW;
+    if (C <= WideRows<float>::MAX_C) return Rows::WIDE;
+    return C <= WidestRows::MAX_C && dtype == MMBWD_BF16 ? Rows::WIDEST : Rows::TWO_PASSES;
 }
 static_assert(NarrowRows<float>::MAX_C == NarrowRows<__nv_bfloat16>::MAX_C && WideRows<float>::MAX_C == WideRows<__nv_bfloat16>::MAX_C);
 
 // Warps of a team in one pass.
-int team_warps_of(int64_t C) {
-    const int64_t per_warp = 64 * (rows_of(C) == Rows::NARROW ? NarrowRows<float>::E : WideRows<float>::E);
+int team_warps_of(int64_t C, int dtype) {
+    const int64_t per_warp = 64 * (rows_of(C, dtype) == Rows::NARROW ? NarrowRows<float>::E : WideRows<float>::E);
     return static_cast<int>((C + per_warp - 1) / per_warp);
 }
 
 int row_blocks_of(int64_t rows, int64_t C, int dtype) {
-    if (rows_of(C) != Rows::TWO_PASSES) {
-        const bool narrow = rows_of(C) == Rows::NARROW;
-        const int64_t at_once = (narrow ? NarrowRows<float>::WARPS : WideRows<float>::WARPS) / team_warps_of(C) *
-                                (narrow && dtype == MMBWD_BF16 ? NarrowRows<__nv_bfloat16>::R : 1);
+    if (rows_of(C, dtype) != Rows::TWO_PASSES) {
+        const bool narrow = rows_of(C, dtype) == Rows::NARROW;
+        const int64_t at_once = narrow ? NarrowRows<float>::WARPS / team_warps_of(C, dtype) * (dtype == MMBWD_BF16 ? NarrowRows<__nv_bfloat16>::R : 1) : 1;
         return static_cast<int>(std::min<int64_t>((rows + at_once - 1) / at_once, MAX_SMS));
     }
     const int64_t nvec = C / (dtype == MMBWD_F32 ? 4 : 8), tiles = (nvec + COL_THREADS - 1) / COL_THREADS;
@@ -1081,11 +1086,11 @@ int row_blocks_of(int64_t rows, int64_t C, int dtype) {
 
 size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
-size_t sums_bytes(int64_t rows, int64_t C) { return rows_of(C) != Rows::TWO_PASSES ? 0 : align256(static_cast<size_t>(rows) * 16); }
+size_t sums_bytes(int64_t rows, int64_t C, int dtype) { return rows_of(C, dtype) != Rows::TWO_PASSES ? 0 : align256(static_cast<size_t>(rows) * 16); }
 
 template <typename T>
 cudaError_t backward(const ResidualNorm& a, int dtype, int num_sms, cudaStream_t stream) {
-    Backward b{a, a.ws, a.ws + sums_bytes(a.rows, a.C) / 4, 1.f / static_cast<float>(a.C), row_blocks_of(a.rows, a.C, dtype), team_warps_of(a.C)};
+    Backward b{a, a.ws, a.ws + sums_bytes(a.rows, a.C, dtype) / 4, 1.f / static_cast<float>(a.C), row_blocks_of(a.rows, a.C, dtype), team_warps_of(a.C, dtype)};
     cudaLaunchConfig_t cfg{};
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1094,9 +1099,12 @@ cudaError_t backward(const ResidualNorm& a, int dtype, int num_sms, cudaStream_t
     cfg.numAttrs = 1;
     cfg.stream = stream;
     cudaError_t e;
-    if (rows_of(a.C) != Rows::TWO_PASSES) {
+    const Rows how = rows_of(a.C, dtype);
+    if (how != Rows::TWO_PASSES) {
         b.row_blocks = std::min(b.row_blocks, num_sms);
-        e = rows_of(a.C) == Rows::NARROW ? launch_rows<NarrowRows<T>>(b, cfg) : launch_rows<WideRows<T>>(b, cfg);
+        e = how == Rows::NARROW ? launch_rows<NarrowRows<T>>(b, cfg)
+            : how == Rows::WIDE ? launch_rows<WideRows<T>>(b, cfg)
+                                : launch_rows<WidestRows>(b, cfg);
     } else {
         cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(a.rows, MAX_SMS * 8)), 1, 1);
         cfg.blockDim = dim3(SUM_THREADS, 1, 1);
@@ -1117,7 +1125,7 @@ cudaError_t backward(const ResidualNorm& a, int dtype, int num_sms, cudaStream_t
 }  // namespace
 
 size_t residual_backward_workspace(int64_t rows, int64_t C, int dtype) {
-    return sums_bytes(rows, C) +
+    return sums_bytes(rows, C, dtype) +
            align256(static_cast<size_t>(row_blocks_of(rows, C, dtype)) * 4 * static_cast<size_t>(C) * 4);
 }
 
