@@ -12,7 +12,7 @@
 // four resident blocks with 64 registers a thread read faster than eight with 32 (205 M
 // fp32 values whose norm is below the limit, in place, 140 -> 134 us, 6.1 TB/s). The
 // scaling runs with 8 blocks an SM; 4, 16 and 32 cost up to 5%. The same list clipped
-// out of place: 373 us for two reads and a write of 0.82 GB (6.6 TB/s), in bf16 196.
+// out of place: 375 us for two reads and a write of 0.82 GB (6.6 TB/s), in bf16 192.
 #include "../../include/grad_clip.h"
 #include "ops.h"
 #include "ptx.cuh"
@@ -29,6 +29,9 @@ namespace {
 constexpr int THREADS = 256;
 constexpr int VECS = 8;                                  // 16-byte vectors of a chunk to a thread
 constexpr int CHUNK_BYTES = THREADS * VECS * 16;
+// The last 80 MB that the norm reads should stay in L2 for the scaling, all else is read and
+// written past it (evicted first): 205 M bf16 values 198 -> 192 us, fp32 379 -> 375.
+constexpr int KEEP_CHUNKS = (80 << 20) / CHUNK_BYTES;
 
 // The tensors of a launch: tensor t has the chunks first[t] .. first[t + 1).
 template <int N>
@@ -80,14 +83,19 @@ __device__ __forceinline__ void squares(const uint4& v, float (&s)[4], float by 
     }
 }
 
-// A thread's vectors of a chunk to `f`, all in flight together.
+// A thread's vectors of a chunk to `f`, all in flight together. `once`: they need not stay
+// in L2.
 template <typename T, typename F>
-__device__ __forceinline__ void for_chunk(const T* p, const Values& c, F f) {
+__device__ __forceinline__ void for_chunk(const T* p, const Values& c, bool once, F f) {
     const int t = static_cast<int>(threadIdx.x), vecs = static_cast<int>(c.vecs);
     const uint4* src = reinterpret_cast<const uint4*>(p + c.base) + t;
     uint4 v[VECS];
+    auto load = [&](auto get) {
 #pragma unroll
-    for (int j = 0; j < VECS; ++j) v[j] = t + j * THREADS < vecs ? src[j * THREADS] : make_uint4(0u, 0u, 0u, 0u);
+        for (int j = 0; j < VECS; ++j) v[j] = t + j * THREADS < vecs ? get(src + j * THREADS) : make_uint4(0u, 0u, 0u, 0u);
+    };
+    if (once) load([](const uint4* q) { return __ldcs(q); });
+    else load([](const uint4* q) { return *q; });
 #pragma unroll
     for (int j = 0; j < VECS; ++j) f(v[j], j, t + j * THREADS < vecs);
 }
@@ -104,14 +112,14 @@ __device__ __forceinline__ int64_t loose_at(const Values& c, int per) {
 // have been lost, it is formed again from values scaled by a power of two; that only
 // happens to values beyond 2^60 or all below 2^-40.
 template <typename T>
-__device__ __forceinline__ double chunk_squares(const T* p, int64_t count, int64_t k) {
+__device__ __forceinline__ double chunk_squares(const T* p, int64_t count, int64_t k, bool once) {
     constexpr int PER = 16 / sizeof(T);
     const Values c = chunk_values(reinterpret_cast<uintptr_t>(p), count, sizeof(T), k);
     const int64_t at = loose_at(c, PER);
     const float loose = at >= 0 ? value(p + at) : 0.f;
     float s[4] = {loose * loose, 0.f, 0.f, 0.f};
     uint32_t any = 0;
-    for_chunk(p, c, [&](const uint4& v, int, bool) {
+    for_chunk(p, c, once, [&](const uint4& v, int, bool) {
         squares<T>(v, s);
         any |= v.x | v.y;
         any |= v.z | v.w;
@@ -164,8 +172,9 @@ __global__ void __launch_bounds__(THREADS, GRAD_BLOCKS_PER_SM) grad_squares_kern
     for (int c = static_cast<int>(blockIdx.x); c < chunks; c += step) {
         while (c >= tab.first[t + 1]) ++t;
         const int64_t k = c - tab.first[t], count = tab.count[t] >> 1;
-        s += tab.count[t] & 1 ? chunk_squares(static_cast<const __nv_bfloat16*>(tab.grad[t]), count, k)
-                              : chunk_squares(static_cast<const float*>(tab.grad[t]), count, k);
+        const bool once = c + KEEP_CHUNKS < chunks;
+        s += tab.count[t] & 1 ? chunk_squares(static_cast<const __nv_bfloat16*>(tab.grad[t]), count, k, once)
+                              : chunk_squares(static_cast<const float*>(tab.grad[t]), count, k, once);
     }
     s = block_sum(s);
     if (threadIdx.x == 0) partials[blockIdx.x] = s;
@@ -200,7 +209,7 @@ __device__ __forceinline__ void scale_chunk(T* out, const T* p, int64_t count, i
         return;
     }
     uint4* dst = reinterpret_cast<uint4*>(out + c.base) + threadIdx.x;
-    for_chunk(p, c, [&](const uint4& v, int j, bool there) {
+    for_chunk(p, c, true, [&](const uint4& v, int j, bool there) {
         uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -212,7 +221,7 @@ __device__ __forceinline__ void scale_chunk(T* out, const T* p, int64_t count, i
                 w[i] = __float_as_uint(__uint_as_float(w[i]) * coef);
             }
         }
-        if (there) dst[j * THREADS] = make_uint4(w[0], w[1], w[2], w[3]);
+        if (there) __stcs(dst + j * THREADS, make_uint4(w[0], w[1], w[2], w[3]));
     });
 }
 
