@@ -545,7 +545,7 @@ struct Backward {
     float* partials;  // [row blocks][4][C]: dweight, dbias, sum dx z, sum dx
     float inv_c;
     int row_blocks;
-    int team_warps;
+    int team_warps, teams;  // warps of a team, teams of a block
 };
 
 // ---- one pass
@@ -560,7 +560,7 @@ struct RowsConfig {
     static constexpr uint32_t PART = R * V * THREADS * 16u, SLOT = 4 * PART;
     static constexpr int SMEM = static_cast<int>(RING * SLOT);
     static constexpr int MAX_C = THREADS * 2 * E;
-    static_assert(SMEM >= 4 * 2 * E * 4 * THREADS / 2 && SMEM <= 220 * 1024, "the ring holds the sums of a team of half the warps, a block the ring");
+    static_assert(SMEM >= 4 * 2 * E * 4 * THREADS && SMEM <= 220 * 1024, "the ring holds the sums of every thread, a block the ring");
 };
 
 // 2 R sums over a team, in a fixed order, in every thread. The 2 R values of a lane are
@@ -620,7 +620,7 @@ __global__ void __launch_bounds__(L::THREADS, 1) residual_rows_kernel(const __gr
     extern __shared__ __align__(16) uint8_t ring[];
     __shared__ float slots[2 * L::WARPS * 2 * R];
     const ResidualNorm& a = b.a;
-    const int warps = b.team_warps, teams = L::WARPS / warps;
+    const int warps = b.team_warps, teams = b.teams;
     const int warp = static_cast<int>(threadIdx.x >> 5), lane = static_cast<int>(threadIdx.x & 31);
     const int team = warp / warps, wt = warp % warps, t = wt * 32 + lane;
     if (team >= teams) return;  // (the block's warps beyond whole teams; no block-wide barrier waits for them)
@@ -794,26 +794,37 @@ __global__ void __launch_bounds__(L::THREADS, 1) residual_rows_kernel(const __gr
         for (int k = 0; k < R; ++k) q[k] = next[k];
     }
 
-    // The block's sums over its rows: the teams' in team order, through the ring's memory.
-    const uint32_t live = static_cast<uint32_t>(32 * teams * warps);
-    copies_wait_but<0>();
-    ptx::named_bar_sync(0, live);
-    float4* joined = reinterpret_cast<float4*>(ring);
+    // The block's sums over its rows: the teams' in team order, through the ring's memory, where
+    // value quad q of thread t of a team is at q * team + t.
+    const int team_threads = 32 * warps, live = teams * team_threads;
     float* to = b.partials + static_cast<int64_t>(blockIdx.x) * 4 * a.C;
-    for (int k = 0; k < teams; ++k) {
-        if (k > 0) ptx::named_bar_sync(0, live);
-        if (team != k) continue;
+    auto column = [&](int quad, int thread) {  // of the quad's first value
+        const int i = quad % (E / 2) * 2;
+        return (thread + team_threads * (i / H)) * Vec<T>::N + 2 * (i % H);
+    };
+    copies_wait_but<0>();
+    float4* joined = reinterpret_cast<float4*>(ring);
+    if (teams > 1) ptx::named_bar_sync(0, static_cast<uint32_t>(live));
 #pragma unroll
-        for (int f = 0; f < 4; ++f)
+    for (int f = 0; f < 4; ++f)
 #pragma unroll
-            for (int i = 0; i < E; i += 2) {
-                const int j = i / H, c = at[j] * Vec<T>::N + 2 * (i % H);
-                float4 v = make_float4(s[f][i].lo(), s[f][i].hi(), s[f][i + 1].lo(), s[f][i + 1].hi());
-                float4* sofar = joined + (f * E / 2 + i / 2) * (32 * warps) + t;
-                if (k > 0) v.x += sofar->x, v.y += sofar->y, v.z += sofar->z, v.w += sofar->w;
-                if (k + 1 < teams) *sofar = v;
-                else if (on[j]) *reinterpret_cast<float4*>(to + static_cast<int64_t>(f) * a.C + c) = v;
-            }
+        for (int i = 0; i < E; i += 2) {
+            const int quad = (f * E + i) / 2, c = column(quad, t);
+            const float4 v = make_float4(s[f][i].lo(), s[f][i].hi(), s[f][i + 1].lo(), s[f][i + 1].hi());
+            if (teams > 1) joined[(team * 2 * E + quad) * team_threads + t] = v;
+            else if (c < a.C) *reinterpret_cast<float4*>(to + static_cast<int64_t>(f) * a.C + c) = v;
+        }
+    if (teams == 1) return;
+    ptx::named_bar_sync(0, static_cast<uint32_t>(live));
+    for (int k = static_cast<int>(threadIdx.x); k < 2 * E * team_threads; k += live) {
+        const int quad = k / team_threads, c = column(quad, k % team_threads);
+        if (c >= a.C) continue;
+        float4 v = joined[k];
+        for (int m = 1; m < teams; ++m) {
+            const float4 u = joined[m * 2 * E * team_threads + k];
+            v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
+        }
+        *reinterpret_cast<float4*>(to + static_cast<int64_t>(quad / (E / 2)) * a.C + c) = v;
     }
 }
 
@@ -1073,10 +1084,21 @@ int team_warps_of(int64_t C, int dtype) {
     return static_cast<int>((C + per_warp - 1) / per_warp);
 }
 
+// Rows that a team has at once, and teams of a block: as few as take the rows in one round
+// over all SMs, up to what the block's warps give (with all of them 2364 x 80 bf16 took 11.5 us
+// instead of 6.7, 57 x 144 9.7 instead of 5.3).
+int rows_at_once(int64_t C, int dtype) {
+    return rows_of(C, dtype) == Rows::NARROW && dtype == MMBWD_BF16 ? NarrowRows<__nv_bfloat16>::R : 1;
+}
+int teams_of(int64_t rows, int64_t C, int dtype) {
+    if (rows_of(C, dtype) != Rows::NARROW) return 1;
+    const int64_t a_round = static_cast<int64_t>(MAX_SMS) * rows_at_once(C, dtype);
+    return static_cast<int>(std::min<int64_t>((rows + a_round - 1) / a_round, NarrowRows<float>::WARPS / team_warps_of(C, dtype)));
+}
+
 int row_blocks_of(int64_t rows, int64_t C, int dtype) {
     if (rows_of(C, dtype) != Rows::TWO_PASSES) {
-        const bool narrow = rows_of(C, dtype) == Rows::NARROW;
-        const int64_t at_once = narrow ? NarrowRows<float>::WARPS / team_warps_of(C, dtype) * (dtype == MMBWD_BF16 ? NarrowRows<__nv_bfloat16>::R : 1) : 1;
+        const int64_t at_once = static_cast<int64_t>(teams_of(rows, C, dtype)) * rows_at_once(C, dtype);
         return static_cast<int>(std::min<int64_t>((rows + at_once - 1) / at_once, MAX_SMS));
     }
     const int64_t nvec = C / (dtype == MMBWD_F32 ? 4 : 8), tiles = (nvec + COL_THREADS - 1) / COL_THREADS;
@@ -1090,7 +1112,7 @@ size_t sums_bytes(int64_t rows, int64_t C, int dtype) { return rows_of(C, dtype)
 
 template <typename T>
 cudaError_t backward(const ResidualNorm& a, int dtype, int num_sms, cudaStream_t stream) {
-    Backward b{a, a.ws, a.ws + sums_bytes(a.rows, a.C, dtype) / 4, 1.f / static_cast<float>(a.C), row_blocks_of(a.rows, a.C, dtype), team_warps_of(a.C, dtype)};
+    Backward b{a, a.ws, a.ws + sums_bytes(a.rows, a.C, dtype) / 4, 1.f / static_cast<float>(a.C), row_blocks_of(a.rows, a.C, dtype), team_warps_of(a.C, dtype), teams_of(a.rows, a.C, dtype)};
     cudaLaunchConfig_t cfg{};
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
