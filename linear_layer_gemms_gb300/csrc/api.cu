@@ -1172,7 +1172,7 @@ cudaError_t forward_act_f32(ActPath path, float* out, float* pre, const float* i
                             const float* residual, int64_t BT, int64_t C, int64_t OC, int act, int sms, cudaStream_t stream) {
     if (path == ActPath::SPANS)
         return tc_launch_span_forward(cached_plan(BT, C, OC, sms, 2), out, pre, inp, weight, bias, residual, BT, C, OC, act, stream);
-    return simt_small_forward_launch(path == ActPath::SMALL_32 ? 32 : 64, out, pre, inp, weight, bias, residual, BT, C, OC, act, stream);
+    return simt_small_forward_launch(path == ActPath::SMALL_32 ? 32 : 64, out, pre, inp, weight, bias, residual, BT, C, OC, act, sms, stream);
 }
 
 cudaError_t run_act_f32(ActPath path, float* dpre, float* dweight, float* dbias, const float* dout, const float* inp,
@@ -1180,7 +1180,7 @@ cudaError_t run_act_f32(ActPath path, float* dpre, float* dweight, float* dbias,
                         cudaStream_t stream) {
     if (path == ActPath::SPANS)
         return tc_launch_span_run(cached_plan(BT, C, OC, sms, 3), dpre, dweight, dbias, dout, inp, weight, pre, BT, C, OC, act, stream);
-    return simt_small_run_launch(path == ActPath::SMALL_32 ? 32 : 64, dpre, dweight, dbias, dout, inp, weight, pre, BT, C, OC, act, stream);
+    return simt_small_run_launch(path == ActPath::SMALL_32 ? 32 : 64, dpre, dweight, dbias, dout, inp, weight, pre, BT, C, OC, act, sms, stream);
 }
 
 }  // namespace

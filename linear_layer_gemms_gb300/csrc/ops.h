@@ -97,10 +97,10 @@ cudaError_t ln_read_status(int* code, int* info3, bool reset);
 // backward. `tile`: 32 or 64.
 cudaError_t simt_small_forward_launch(int tile, float* out, float* pre, const float* inp, const float* weight,
                                       const float* bias, const float* residual, int64_t BT, int64_t C, int64_t OC,
-                                      int act, cudaStream_t stream);
+                                      int act, int num_sms, cudaStream_t stream);
 cudaError_t simt_small_run_launch(int tile, float* dpre, float* dweight, float* dbias, const float* dout,
                                   const float* inp, const float* weight, const float* pre, int64_t BT, int64_t C,
-                                  int64_t OC, int act, cudaStream_t stream);
+                                  int64_t OC, int act, int num_sms, cudaStream_t stream);
 // Which kernel takes these products in fp32.
 enum class ActPath { TOKENS, SMALL_32, SMALL_64, SPANS };  // tokens_act.cu, the two above, tc_launch_span_*
 ActPath act_forward_path(int64_t BT, int64_t C, int64_t OC, int num_sms);

@@ -1,14 +1,15 @@
 // fp32 products of mmbwd_forward_act and mmbwd_run_act (include/linear_epilogue.h) that are
 // too small for the tensor-core kernel's tiles of 256 x 128: tiles of 64 x 64 or 32 x 32,
-// whose K is shared by the G warps of a block.
+// whose K is shared by the G warps of a block, and by the blocks of a cluster where the
+// tiles are few.
 //
 // Bound by fp32 fused multiply-adds (128 a clock and SM) where the tiles fill the device,
 // by the latency of a block's loads below that; sharing K inside a block
 // shortens that chain without a second launch or a workspace. Each warp
 // accumulates every G-th K-tile (of 8) in registers, 8 x 16 or 4 x 8 outputs a thread, in pairs
 // (two multiply-adds to an instruction: 1000 x 1600 -> 1600 in tiles of 64 170 -> 141 us), and the
-// warps' sums are added in warp order through shared memory, where the epilogue
-// starts: the same bits on every call. Shared memory gives a warp 32 values a clock, so the
+// warps' sums are added in warp order through shared memory, the blocks' in block order
+// from one another's, where the epilogue starts: the same bits on every call. Shared memory gives a warp 32 values a clock, so the
 // outputs of a thread are as many as its registers hold (8 x 8 of 64 threads, behind a barrier
 // of theirs: 141 us, 8 x 16 of one warp: 128; the multiply-add pipe is then busy for 62% of
 // the time). The backward's two products share one launch.
@@ -34,6 +35,8 @@ struct Product {
     const float *A = nullptr, *B = nullptr;
     int64_t M = 0, N = 0, K = 0;
     int tiles_n = 0, tiles = 0;
+    int share = 1;  // blocks (a whole cluster) that share K
+    __host__ __device__ int blocks(int cluster) const { return (tiles * share + cluster - 1) / cluster * cluster; }
 };
 
 struct Params {
@@ -43,7 +46,17 @@ struct Params {
     float* pre;                // forward: stored; backward: read, may be D
     float* dbias;              // second product
     int act;
+    int cluster;               // blocks of a cluster; a product is shared by all of them or by none
 };
+
+// Four values of shared memory anywhere in the cluster.
+__device__ __forceinline__ float4 ld_cluster(const float* p, int rank) {
+    const uint32_t at = ptx::mapa(ptx::smem_u32(p), static_cast<uint32_t>(rank));
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at) : "memory");
+    return v;
+}
+__device__ __forceinline__ void add(float4& o, const float4& v) { o.x += v.x, o.y += v.y, o.z += v.z, o.w += v.w; }
 
 enum Epilogue { FORWARD, DPRE, DWEIGHT };
 
@@ -54,7 +67,7 @@ constexpr int smem_bytes() {
 }
 
 template <int TM, int G, bool A_KM, bool B_NK, Epilogue EPI>
-__device__ __forceinline__ void tile_product(const Params& p, const Product& q, int tile, float* smem) {
+__device__ __forceinline__ void tile_product(const Params& p, const Product& q, int tile, int rank, float* smem) {
     constexpr int TILE = 8 * TM, TN = 2 * TM, LD = TILE + PAD, LOADS = TILE * BK / 4 / GROUP, H = TM / 4, W = TN / 4;
     const int group = static_cast<int>(threadIdx.x) / GROUP, tid = static_cast<int>(threadIdx.x) % GROUP;
     const int tx = tid % 4, ty = tid / 4;
@@ -63,27 +76,38 @@ __device__ __forceinline__ void tile_product(const Params& p, const Product& q, 
     float* Bs = As + 2 * BK * LD;
     const bool sums = EPI == DWEIGHT && p.dbias != nullptr && n0 == 0;
 
+    // What the thread stages of a K-tile: LOADS float4s of either operand, at a stride from one
+    // another, and the next K-tile's at another (no multiplication inside the loop).
+    const int64_t step = static_cast<int64_t>(q.share * G) * BK;
+    int64_t k0 = static_cast<int64_t>(rank * G + group) * BK;
+    constexpr int QUADS = TILE / 4, SPREAD = GROUP / QUADS;  // a row of the tile by k in float4s; k's that a load covers
+    struct Side {
+        const float* at;
+        int64_t between, ahead;
+        bool there[LOADS];
+        int k;  // of the first load, behind k0
+    } sa, sb;
+    auto side = [&](const float* base, bool by_k, int64_t first, int64_t extent) {
+        Side s;
+        s.k = by_k ? tid / QUADS : tid % 2 * 4;
+        const int64_t row = first + (by_k ? tid % QUADS * 4 : tid / 2);
+        s.at = by_k ? base + (k0 + s.k) * extent + row : base + row * q.K + k0 + s.k;
+        s.between = by_k ? SPREAD * extent : GROUP / 2 * q.K;
+        s.ahead = by_k ? step * extent : step;
+#pragma unroll
+        for (int l = 0; l < LOADS; ++l) s.there[l] = row + (by_k ? 0 : l * (GROUP / 2)) < extent;
+        return s;
+    };
+    sa = side(q.A, A_KM, m0, q.M), sb = side(q.B, !B_NK, n0, q.N);
     float4 ra[LOADS], rb[LOADS];
     const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
-    auto load = [&](int64_t k0) {
+    auto load = [&](int64_t k) {  // K-tile k, then on to the next
 #pragma unroll
         for (int l = 0; l < LOADS; ++l) {
-            const int i = tid + l * GROUP;
-            if (A_KM) {
-                const int64_t k = k0 + i / (TILE / 4), m = m0 + i % (TILE / 4) * 4;
-                ra[l] = k < q.K && m < q.M ? *reinterpret_cast<const float4*>(q.A + k * q.M + m) : zero;
-            } else {
-                const int64_t m = m0 + i / 2, k = k0 + i % 2 * 4;
-                ra[l] = m < q.M && k < q.K ? *reinterpret_cast<const float4*>(q.A + m * q.K + k) : zero;
-            }
-            if (B_NK) {
-                const int64_t n = n0 + i / 2, k = k0 + i % 2 * 4;
-                rb[l] = n < q.N && k < q.K ? *reinterpret_cast<const float4*>(q.B + n * q.K + k) : zero;
-            } else {
-                const int64_t k = k0 + i / (TILE / 4), n = n0 + i % (TILE / 4) * 4;
-                rb[l] = k < q.K && n < q.N ? *reinterpret_cast<const float4*>(q.B + k * q.N + n) : zero;
-            }
+            ra[l] = sa.there[l] && k + sa.k + (A_KM ? l * SPREAD : 0) < q.K ? *reinterpret_cast<const float4*>(sa.at + l * sa.between) : zero;
+            rb[l] = sb.there[l] && k + sb.k + (B_NK ? 0 : l * SPREAD) < q.K ? *reinterpret_cast<const float4*>(sb.at + l * sb.between) : zero;
         }
+        sa.at += sa.ahead, sb.at += sb.ahead;
     };
     auto put = [&](float* to, const float4& v, int i, bool across) {
         if (across) {
@@ -107,8 +131,6 @@ __device__ __forceinline__ void tile_product(const Params& p, const Product& q, 
         for (int j = 0; j < TN / 2; ++j) acc[i][j] = act::Two::both(0.f);
     float colsum[TILE / GROUP] = {};
 
-    const int64_t step = static_cast<int64_t>(G) * BK;
-    int64_t k0 = static_cast<int64_t>(group) * BK;
     int buf = 0;
     if (k0 < q.K) {
         load(k0);
@@ -161,15 +183,34 @@ __device__ __forceinline__ void tile_product(const Params& p, const Product& q, 
         for (int i = 0; i < TILE / GROUP; ++i) colsums[group * TILE + i * GROUP + tid] = colsum[i];
     }
     __syncthreads();
-    for (int e = static_cast<int>(threadIdx.x); e < TILE * TILE / 4; e += G * GROUP) {
+    auto of_block = [&](int at) {  // four values, the warps' sums in order
+        float4 o = *reinterpret_cast<const float4*>(smem + at);
+#pragma unroll
+        for (int k = 1; k < G; ++k) add(o, *reinterpret_cast<const float4*>(smem + k * TILE * TILE + at));
+        return o;
+    };
+    int e0 = 0, e1 = TILE * TILE / 4;  // the float4s that this block finishes
+    if (q.share > 1) {
+        for (int e = static_cast<int>(threadIdx.x); e < e1; e += G * GROUP) *reinterpret_cast<float4*>(smem + 4 * e) = of_block(4 * e);
+        if (sums && threadIdx.x < TILE) {
+            float t = colsums[threadIdx.x];
+#pragma unroll
+            for (int k = 1; k < G; ++k) t += colsums[k * TILE + threadIdx.x];
+            colsums[threadIdx.x] = t;
+        }
+        ptx::cluster_sync();
+        e1 /= q.share, e0 = rank * e1, e1 += e0;
+    }
+    for (int e = e0 + static_cast<int>(threadIdx.x); e < e1; e += G * GROUP) {
         const int row = e / (TILE / 4), col = e % (TILE / 4) * 4;
         const int64_t m = m0 + row, n = n0 + col;
         if (m >= q.M || n >= q.N) continue;  // N is a multiple of 4: a float4 is all in or all out
-        float4 o = *reinterpret_cast<const float4*>(smem + row * TILE + col);
-#pragma unroll
-        for (int k = 1; k < G; ++k) {
-            const float4 v = *reinterpret_cast<const float4*>(smem + k * TILE * TILE + row * TILE + col);
-            o.x += v.x, o.y += v.y, o.z += v.z, o.w += v.w;
+        float4 o;
+        if (q.share > 1) {
+            o = ld_cluster(smem + 4 * e, 0);
+            for (int r = 1; r < q.share; ++r) add(o, ld_cluster(smem + 4 * e, r));
+        } else {
+            o = of_block(4 * e);
         }
         const int64_t at = m * q.N + n;
         if constexpr (EPI == FORWARD) {
@@ -199,35 +240,53 @@ __device__ __forceinline__ void tile_product(const Params& p, const Product& q, 
         }
         *reinterpret_cast<float4*>(q.D + at) = o;
     }
-    if (sums && threadIdx.x < TILE && m0 + threadIdx.x < q.M) {
+    if (sums && q.share == 1 && threadIdx.x < TILE && m0 + threadIdx.x < q.M) {
         float s = colsums[threadIdx.x];
 #pragma unroll
         for (int k = 1; k < G; ++k) s += colsums[k * TILE + threadIdx.x];
         p.dbias[m0 + threadIdx.x] = s;
     }
+    if (q.share > 1) {
+        if (sums && rank == 0 && threadIdx.x < TILE / 4 && m0 + 4 * threadIdx.x < q.M) {  // (M is a multiple of 4 there)
+            float4 s = ld_cluster(colsums + 4 * threadIdx.x, 0);
+            for (int r = 1; r < q.share; ++r) add(s, ld_cluster(colsums + 4 * threadIdx.x, r));
+            *reinterpret_cast<float4*>(p.dbias + m0 + 4 * threadIdx.x) = s;
+        }
+        ptx::cluster_sync();  // a block's sums stay until the others have read them
+    }
+}
+
+// Tile and rank of block `b` of a product's blocks; the rank where K is not shared: 0.
+__device__ __forceinline__ int tile_of(const Product& q, int b, int& rank) {
+    rank = b % q.share;
+    return b / q.share;
 }
 
 template <int TM, int G>
-__global__ void __launch_bounds__(G* GROUP) small_forward_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(G* GROUP, TM == 4 ? 2 : 1) small_forward_kernel(const __grid_constant__ Params p) {
     extern __shared__ __align__(16) float smem[];
     ptx::grid_launch_dependents();
     ptx::grid_dependency_wait();
-    tile_product<TM, G, false, true, FORWARD>(p, p.first, static_cast<int>(blockIdx.x), smem);
+    int rank;
+    const int tile = tile_of(p.first, static_cast<int>(blockIdx.x), rank);
+    tile_product<TM, G, false, true, FORWARD>(p, p.first, tile, rank, smem);
 }
 
 template <int TM, int G>
-__global__ void __launch_bounds__(G* GROUP) small_backward_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(G* GROUP, TM == 4 ? 2 : 1) small_backward_kernel(const __grid_constant__ Params p) {
     extern __shared__ __align__(16) float smem[];
     ptx::grid_launch_dependents();
     ptx::grid_dependency_wait();
     // the tiles with the longer sums first: the others fill the gaps behind them
-    int b = static_cast<int>(blockIdx.x);
+    int b = static_cast<int>(blockIdx.x), rank;
     const bool first_first = p.first.K >= p.second.K;
-    const int ahead = first_first ? p.first.tiles : p.second.tiles;
+    const int ahead = first_first ? p.first.blocks(p.cluster) : p.second.blocks(p.cluster);
     const bool dweight = first_first == (b < ahead);
     if (b >= ahead) b -= ahead;
-    if (dweight) tile_product<TM, G, true, false, DWEIGHT>(p, p.first, b, smem);
-    else tile_product<TM, G, false, false, DPRE>(p, p.second, b, smem);
+    const int tile = tile_of(dweight ? p.first : p.second, b, rank);
+    if (tile >= (dweight ? p.first.tiles : p.second.tiles)) return;  // (fills a cluster that shares nothing)
+    if (dweight) tile_product<TM, G, true, false, DWEIGHT>(p, p.first, tile, rank, smem);
+    else tile_product<TM, G, false, false, DPRE>(p, p.second, tile, rank, smem);
 }
 
 template <auto kernel>
@@ -248,11 +307,14 @@ cudaError_t launch(const Params& p, int blocks, int threads, int smem, cudaStrea
     cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
     cfg.dynamicSmemBytes = static_cast<size_t>(smem);
     cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(p.cluster);
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = p.cluster > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
@@ -266,28 +328,53 @@ Product product(float* D, const float* A, const float* B, int64_t M, int64_t N, 
 
 namespace {
 
+// Blocks of a cluster that share the K of a product's tiles, a power of two: as many as have
+// an SM each, with a K-tile at least for every warp. Of two products the one that wants more is
+// shared, or both. (Up to two blocks an SM: 100 x 768 -> 768 16.4 -> 12.5 us, but 200 x 264 -> 388's gradients 8.2
+// -> 11.5, 40 x 600 -> 600 7.3 -> 10.1.)
+int share_products(Product* q, int n, int tile, int num_sms) {
+    int cluster = 1;
+    for (int i = 0; i < n; ++i) {
+        const int64_t tiles = tiles_of(q[i].M, q[i].N, tile);
+        q[i].share = 1;
+        while (q[i].share < 8 && 2 * q[i].share * tiles <= num_sms && 2 * q[i].share * 64 <= q[i].K) q[i].share *= 2;
+        cluster = std::max(cluster, q[i].share);
+    }
+    for (int i = 0; i < n; ++i)
+        if (q[i].share < cluster) q[i].share = 1;
+    return cluster;
+}
+
 // Time models (us), fitted to the measurements below; times (us) on one GB300:
 //                         tokens  32 x 32  64 x 64  spans (forward | backward 32, 64, spans)
-//    16 x 6400 -> 1600        29.1     86.7      149    149 | 98.3  120 60.1
-//    40 x 1600 -> 6400                 51.9     43.8   47.1 |  117  163  154
-//    64 x  768 ->  768         9.7     10.1     23.0   27.0 | 15.5 22.1 26.0
-//   100 x  768 -> 2304               18.4     23.3   27.5 | 41.3 55.6 61.4
-//   200 x  264 ->  388                6.9     11.8   17.5 |  9.6 14.6 19.1
-//   333 x  772 -> 1300               26.2     23.7   28.5 | 46.6 44.0 39.2
-//   500 x  768 ->  768               26.6     23.3   28.1 | 39.3 36.6 27.6
-//  1000 x 1600 -> 1600                182      128     47 |  290  228   80
-//  2048 x 1600 -> 2400                525      342     89 |  839  641  260
+//     6 x   92 -> 2072         3.6      3.5      5.8   11.7 |  7.4 12.2 53.6
+//    16 x 6400 -> 1600        29.0     61.6     55.7    148 |  108  127 59.7
+//    40 x  600 ->  600         7.6      7.4      8.6   23.6 |  8.9 14.3 22.3
+//    40 x 1600 -> 6400                 63.5     51.2   46.9 |  127  148  154
+//    64 x 4000 ->   64         5.8      9.6     18.7   95.4 |  7.2  7.7 13.0
+//   100 x  768 ->  768                 16.4     10.6   27.2 | 13.5 17.6 26.4
+//   100 x  768 -> 2304                 19.4     15.9   27.4 | 36.7 34.6 61.3
+//   200 x  264 ->  388                  7.4      7.7   17.6 |  8.2 10.3 19.1
+//   333 x  772 -> 1300                 27.2     24.4   28.6 | 46.5 44.9 39.1
+//   407 x 1120 ->  408                 26.5     20.8   35.8 | 26.2 28.0 21.2
+//   500 x  768 ->  768                 27.7     24.5   28.1 | 38.6 36.9 27.7
+//  1000 x 1600 -> 1600                  185      130   47.5 |  285  227 79.8
+//  2048 x 1600 -> 2400                  530      346   88.3 |  819  631  259
 // A block of 32 x 32 outputs takes 0.0148 us per value of K alone on its SM and 0.0107 beside
 // others, and as long as 60 values more for its first loads and its sums; one of 64 x 64
-// 0.0265 and 0.0298, and 120 values more; below 64 values some warps have none. The tensor
+// 0.0265 and 0.0298, and 120 values more; below 64 values some warps have none. Blocks that
+// share a tile take 1.5 to join (64 x 4000 -> 64 in tiles of 32 41 us alone, 9.6 shared by eight). The tensor
 // cores' items of 256 x 128 take 0.72 us a k-block of 32 and 4 for the epilogue, 7 for the
 // launch and its first loads.
 double small_us(int tile, const Product* q, int n, int num_sms) {
+    Product shared[2] = {q[0], q[n - 1]};
+    share_products(shared, n, tile, num_sms);
     double work = 0.0, longest = 0.0;
     for (int i = 0; i < n; ++i) {
-        const double K = static_cast<double>(q[i].K), tiles = static_cast<double>(tiles_of(q[i].M, q[i].N, tile));
-        work += tiles * (tile == 32 ? (std::max(K, 64.0) + 60.0) * 0.0107 : (std::max(K, 64.0) + 120.0) * 0.0298);
-        longest = std::max(longest, K * (tile == 32 ? 0.0148 : 0.0265));
+        const int share = shared[i].share;
+        const double K = static_cast<double>(q[i].K) / share, blocks = static_cast<double>(tiles_of(q[i].M, q[i].N, tile) * share);
+        work += blocks * (tile == 32 ? (std::max(K, 64.0) + 60.0) * 0.0107 : (std::max(K, 64.0) + 120.0) * 0.0298);
+        longest = std::max(longest, K * (tile == 32 ? 0.0148 : 0.0265) + (share > 1 ? 1.5 : 0.0));
     }
     return 3.0 + std::max(work / num_sms, longest);
 }
@@ -336,20 +423,25 @@ ActPath act_run_path(int64_t BT, int64_t C, int64_t OC, int num_sms) {
 
 cudaError_t simt_small_forward_launch(int tile, float* out, float* pre, const float* inp, const float* weight,
                                       const float* bias, const float* residual, int64_t BT, int64_t C, int64_t OC,
-                                      int act, cudaStream_t stream) {
+                                      int act, int num_sms, cudaStream_t stream) {
     if (take_injected_launch_failure()) return cudaErrorLaunchFailure;
-    Params p{product(out, inp, weight, BT, OC, C, tile), {}, bias, residual, pre, nullptr, act};
-    if (tile == 64) return launch<small_forward_kernel<8, 8>>(p, p.first.tiles, 8 * GROUP, smem_bytes<8, 8>(), stream);
-    return launch<small_forward_kernel<4, 8>>(p, p.first.tiles, 8 * GROUP, smem_bytes<4, 8>(), stream);
+    Params p{product(out, inp, weight, BT, OC, C, tile), {}, bias, residual, pre, nullptr, act, 1};
+    p.cluster = share_products(&p.first, 1, tile, num_sms);
+    const int blocks = p.first.blocks(p.cluster);
+    if (tile == 64) return launch<small_forward_kernel<8, 8>>(p, blocks, 8 * GROUP, smem_bytes<8, 8>(), stream);
+    return launch<small_forward_kernel<4, 8>>(p, blocks, 8 * GROUP, smem_bytes<4, 8>(), stream);
 }
 
 cudaError_t simt_small_run_launch(int tile, float* dpre, float* dweight, float* dbias, const float* dout,
                                   const float* inp, const float* weight, const float* pre, int64_t BT, int64_t C,
-                                  int64_t OC, int act, cudaStream_t stream) {
+                                  int64_t OC, int act, int num_sms, cudaStream_t stream) {
     if (take_injected_launch_failure()) return cudaErrorLaunchFailure;
     Params p{product(dweight, dout, inp, OC, C, BT, tile), product(dpre, dout, weight, BT, C, OC, tile), nullptr, nullptr,
-             const_cast<float*>(pre), dbias, act};
-    const int blocks = p.first.tiles + p.second.tiles;
+             const_cast<float*>(pre), dbias, act, 1};
+    Product q[2] = {p.first, p.second};
+    p.cluster = share_products(q, 2, tile, num_sms);
+    p.first = q[0], p.second = q[1];
+    const int blocks = p.first.blocks(p.cluster) + p.second.blocks(p.cluster);
     if (tile == 64) return launch<small_backward_kernel<8, 8>>(p, blocks, 8 * GROUP, smem_bytes<8, 8>(), stream);
     return launch<small_backward_kernel<4, 8>>(p, blocks, 8 * GROUP, smem_bytes<4, 8>(), stream);
 }
