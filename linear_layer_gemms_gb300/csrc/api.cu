@@ -1212,7 +1212,7 @@ int mmbwd_forward_act(void* out, void* pre, const void* inp, const void* weight,
         e = act_rows_launch(out, pre, bias, residual, s.BT, OC, act, dtype, stream);
     else if (dtype == MMBWD_F32 ? act_forward_path(s.BT, C, OC, d->num_sms) == ActPath::TOKENS
                                 : tokens_act_takes_bf16(s.BT, C, OC, d->num_sms))
-        e = tokens_act_launch(out, pre, inp, weight, bias, residual, s.BT, C, OC, act, dtype, stream);
+        e = tokens_act_launch(out, pre, inp, weight, bias, residual, s.BT, C, OC, act, dtype, d->num_sms, stream);
     else if (dtype == MMBWD_F32)
         e = forward_act_f32(act_forward_path(s.BT, C, OC, d->num_sms), static_cast<float*>(out), static_cast<float*>(pre),
                             static_cast<const float*>(inp), static_cast<const float*>(weight),

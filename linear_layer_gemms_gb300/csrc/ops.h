@@ -105,11 +105,11 @@ cudaError_t simt_small_run_launch(int tile, float* dpre, float* dweight, float* 
 enum class ActPath { TOKENS, SMALL_32, SMALL_64, SPANS };  // tokens_act.cu, the two above, tc_launch_span_*
 ActPath act_forward_path(int64_t BT, int64_t C, int64_t OC, int num_sms);
 ActPath act_run_path(int64_t BT, int64_t C, int64_t OC, int num_sms);
-// The forward for few tokens: 64 at most (ACT_TOKENS).
+// The forward for few tokens: fp32 64 at most (ACT_TOKENS), bf16 by the time of either kernel.
 constexpr int64_t ACT_TOKENS = 64;
 bool tokens_act_takes_bf16(int64_t T, int64_t K, int64_t N, int num_sms);
 cudaError_t tokens_act_launch(void* out, void* pre, const void* inp, const void* weight, const void* bias,
-                              const void* residual, int64_t T, int64_t K, int64_t N, int act, int dtype,
+                              const void* residual, int64_t T, int64_t K, int64_t N, int act, int dtype, int num_sms,
                               cudaStream_t stream);
 // dpre = dout * act'(pre), n values
 cudaError_t act_backward_launch(void* dpre, const void* dout, const void* pre, int64_t n, int act, int dtype,

@@ -5,7 +5,7 @@
 // bytes a lane with the next loads always in flight, and multiplies it there. Where the
 // rows alone give too few warps to keep HBM busy, several warps of a block share K and
 // add their sums in warp order through shared memory. One launch, no workspace, the same
-// bits on every call.
+// bits on every call. Prompts of more tokens whose tiles of 32 x 32 run all at once go the same way.
 //
 // bf16: mma.sync with the tokens as its 16 rows and 8 rows of the weight as its columns.
 // Which of a product's 16 values of k a lane holds does not matter as long as both
@@ -92,8 +92,8 @@ __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uin
 }
 
 // MT tiles of 16 tokens, NR groups of 8 weight rows to a warp, AHEAD chunks in flight.
-template <int MT, int NR, int AHEAD>
-__global__ void __launch_bounds__(32 * MAX_WARPS) tokens_bf16_kernel(const __grid_constant__ Params p) {
+template <int MT, int NR, int AHEAD, int WARPS = MAX_WARPS>
+__global__ void __launch_bounds__(32 * WARPS) tokens_bf16_kernel(const __grid_constant__ Params p) {
     constexpr int ROWS = 8 * NR, TOKENS = 16 * MT;
     extern __shared__ __align__(16) float red[];  // [warp][TOKENS][ROWS]
     const int warp = static_cast<int>(threadIdx.x >> 5), lane = static_cast<int>(threadIdx.x & 31), g = lane >> 2, t = lane & 3;
@@ -101,6 +101,7 @@ __global__ void __launch_bounds__(32 * MAX_WARPS) tokens_bf16_kernel(const __gri
     const int64_t block0 = static_cast<int64_t>(blockIdx.x) * (groups * ROWS), n0 = block0 + group * ROWS;
     ptx::grid_launch_dependents();
     ptx::grid_dependency_wait();
+    const int t0 = static_cast<int>(blockIdx.y) * TOKENS, tokens = min(p.T - t0, TOKENS);
     // Rows beyond the last, and tokens, read the last one's: what they give is not stored.
     const __nv_bfloat16* w[NR];
 #pragma unroll
@@ -108,7 +109,7 @@ __global__ void __launch_bounds__(32 * MAX_WARPS) tokens_bf16_kernel(const __gri
         w[i] = static_cast<const __nv_bfloat16*>(p.weight) + min(n0 + 8 * i + g, p.N - 1) * p.K + 8 * t;
     const __nv_bfloat16* x[2 * MT];
 #pragma unroll
-    for (int i = 0; i < 2 * MT; ++i) x[i] = static_cast<const __nv_bfloat16*>(p.inp) + static_cast<int64_t>(min(8 * i + g, p.T - 1)) * p.K + 8 * t;
+    for (int i = 0; i < 2 * MT; ++i) x[i] = static_cast<const __nv_bfloat16*>(p.inp) + static_cast<int64_t>(t0 + min(8 * i + g, tokens - 1)) * p.K + 8 * t;
     float c[MT][NR][4];
 #pragma unroll
     for (int m = 0; m < MT; ++m)
@@ -126,7 +127,7 @@ __global__ void __launch_bounds__(32 * MAX_WARPS) tokens_bf16_kernel(const __gri
         for (int i = 0; i < NR; ++i) wv[u][i] = in ? stream16(w[i] + at) : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
         for (int i = 0; i < 2 * MT; ++i)
-            xv[u][i] = in && (i == 0 || 8 * i < p.T) ? __ldg(reinterpret_cast<const uint4*>(x[i] + at)) : make_uint4(0u, 0u, 0u, 0u);
+            xv[u][i] = in && (i == 0 || 8 * i < tokens) ? __ldg(reinterpret_cast<const uint4*>(x[i] + at)) : make_uint4(0u, 0u, 0u, 0u);
     };
 #pragma unroll
     for (int u = 0; u < AHEAD; ++u) fetch(u, lo + u);
@@ -154,7 +155,7 @@ __global__ void __launch_bounds__(32 * MAX_WARPS) tokens_bf16_kernel(const __gri
                 for (int h = 0; h < 2; ++h) {
                     const int token = 16 * m + 8 * h + g;
                     const int64_t n = n0 + 8 * i + 2 * t;
-                    if (token < p.T && n < p.N) finish<__nv_bfloat16>(p, token, n, c[m][i][2 * h], c[m][i][2 * h + 1]);
+                    if (token < tokens && n < p.N) finish<__nv_bfloat16>(p, t0 + token, n, c[m][i][2 * h], c[m][i][2 * h + 1]);
                 }
         return;
     }
@@ -164,10 +165,10 @@ __global__ void __launch_bounds__(32 * MAX_WARPS) tokens_bf16_kernel(const __gri
         for (int i = 0; i < NR; ++i)
 #pragma unroll
             for (int h = 0; h < 2; ++h)
-                if (16 * m + 8 * h + g < p.T)
+                if (16 * m + 8 * h + g < tokens)
                     *reinterpret_cast<float2*>(red + (warp * TOKENS + 16 * m + 8 * h + g) * ROWS + 8 * i + 2 * t) =
                         make_float2(c[m][i][2 * h], c[m][i][2 * h + 1]);
-    join<__nv_bfloat16, TOKENS, ROWS>(p, red, block0, 0, p.T);
+    join<__nv_bfloat16, TOKENS, ROWS>(p, red, block0, t0, tokens);
 }
 
 // TOKENS tokens from blockIdx.y on (those beyond T read the last one's), four weight rows to
@@ -231,7 +232,7 @@ __global__ void __launch_bounds__(32 * MAX_WARPS) tokens_f32_kernel(const __grid
     join<float, TOKENS, ROWS>(p, red, block0, t0, tokens);
 }
 
-template <auto kernel>
+template <auto kernel, int MOST = MAX_WARPS>
 cudaError_t launch(Params p, int tokens, int rows, int share, cudaStream_t stream) {
     const int warps = std::max(share, 8), smem = warps * tokens * rows * 4;
     if (smem > 48 * 1024) {
@@ -240,7 +241,7 @@ cudaError_t launch(Params p, int tokens, int rows, int share, cudaStream_t strea
         cudaError_t e = cudaGetDevice(&dev);
         if (e != cudaSuccess) return e;
         if (dev < 0 || dev >= 64 || !done[dev]) {
-            e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, MAX_WARPS * tokens * rows * 4);
+            e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, MOST * tokens * rows * 4);
             if (e != cudaSuccess) return e;
             if (dev >= 0 && dev < 64) done[dev] = true;
         }
@@ -261,18 +262,31 @@ cudaError_t launch(Params p, int tokens, int rows, int share, cudaStream_t strea
     return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
+// More than 32 tokens: how many of a block's eight warps share the K of 32 tokens by 32 rows,
+// so that all blocks run at once; 0 where they do not.
+int prompt_share(int64_t T, int64_t N, int num_sms) {
+    const int64_t tiles = (T + 31) / 32 * ((N + 31) / 32);
+    int share = 8;
+    while (share > 0 && tiles * share > 8 * num_sms) share /= 2;
+    return share;
+}
+
 }  // namespace
 
-// Up to 32 tokens, and up to 64 by the time of either kernel (us, fitted to the sizes
-// below): this one goes by the weight's bytes, the tensor-core kernel by the k-blocks
-// of its rounds of tiles. Measured, this / that: 64 tokens 1600 -> 6400 16.9 / 13.9, 6400 ->
-// 1600 16.3 / 36.2, 768 -> 768 5.0 / 8.7; 32 tokens 1600 -> 6400 10.1 / 14.0, 6400 -> 1600 10.5 / 36.1; 16
+// Up to 32 tokens, and more by the time of either kernel (us, fitted to the sizes below): this one
+// goes by the chunks of K that a warp has, the tensor-core kernel by the k-blocks
+// of its rounds of tiles. Measured, this / that: 65 tokens 600 -> 600 4.5 / 7.8, 119 tokens 1720 -> 536 6.2 /
+// 12.7, 133 tokens 168 -> 240 3.8 / 5.7, 128 tokens 768 -> 768 4.5 / 8.4, 768 -> 2304 6.6 / 8.5, 1600 -> 6400 28
+// / 12.8, 256 tokens 3000 -> 504 8.5 / 18.1, 512 tokens 768 -> 768 12.0 / 8.4, 4000 -> 400 16.2 / 21.7;
+// 32 tokens 1600 -> 6400 10.1 / 14.0, 6400 -> 1600 10.5 / 36.1; 16
 // tokens 768 -> 50304 16.6 / 29.3; one token 1600 -> 6400 5.6 / 14.7.
 bool tokens_act_takes_bf16(int64_t T, int64_t K, int64_t N, int num_sms) {
-    if (T <= 32 || T > ACT_TOKENS) return T <= 32;
-    const double bytes = 2.0 * static_cast<double>(N) * static_cast<double>(K), tiles = static_cast<double>((N + 255) / 256);
-    const double rounds = static_cast<double>(static_cast<int64_t>((tiles + num_sms / 2 - 1) / (num_sms / 2)));
-    return 3.0 + bytes / 1.4e6 < 5.5 + rounds * 0.33 * static_cast<double>((K + 63) / 64);
+    if (T <= 32) return true;
+    const int share = prompt_share(T, N, num_sms);
+    if (share == 0) return false;
+    const int64_t chunks = ((K + 31) / 32 + share - 1) / share, tiles = (T + 255) / 256 * ((N + 255) / 256), pairs = num_sms / 2;
+    const double a_chunk = share == 8 ? 0.45 : share == 4 ? 0.55 : share == 2 ? 0.7 : 1.0;
+    return 3.2 + a_chunk * static_cast<double>(chunks) < 5.0 + 0.28 * static_cast<double>((tiles + pairs - 1) / pairs * ((K + 63) / 64));
 }
 
 // How many warps share K: as many as give the device `want` warps or more, with two chunks
@@ -280,7 +294,7 @@ bool tokens_act_takes_bf16(int64_t T, int64_t K, int64_t N, int num_sms) {
 // 6400 -> 1600 by 16 7.0, by 8 9.3; 16 tokens 768 -> 50304 by 1 16.6, by 4 18.5; one token
 // 6400 -> 1600 fp32 by 8 8.6, by 4 9.4; 8 tokens by 4 17.5, by 8 20.4.
 cudaError_t tokens_act_launch(void* out, void* pre, const void* inp, const void* weight, const void* bias,
-                              const void* residual, int64_t T, int64_t K, int64_t N, int act, int dtype,
+                              const void* residual, int64_t T, int64_t K, int64_t N, int act, int dtype, int num_sms,
                               cudaStream_t stream) {
     if (take_injected_launch_failure()) return cudaErrorLaunchFailure;
     const Params p{out, pre, inp, weight, bias, residual, N, K, static_cast<int>(T), act, 1};
@@ -295,12 +309,12 @@ cudaError_t tokens_act_launch(void* out, void* pre, const void* inp, const void*
         if (T <= 4) return launch<tokens_f32_kernel<4, 2>>(p, 4, 4, share, stream);
         return launch<tokens_f32_kernel<8, 1>>(p, 8, 4, share, stream);
     }
+    if (T > 32) return launch<tokens_bf16_kernel<2, 4, 2, 8>, 8>(p, 32, 32, prompt_share(T, N, num_sms), stream);
     const int share = shared_by((N + 15) / 16, (K + 31) / 32 / 2, T <= 16 ? 2400 : 1600);
     if (T <= 16)  // (fewer loads in flight to a warp leave the registers for more of them)
         return share < MAX_WARPS ? launch<tokens_bf16_kernel<1, 2, 2>>(p, 16, 16, share, stream)
                                  : launch<tokens_bf16_kernel<1, 2, 4>>(p, 16, 16, share, stream);
-    if (T <= 32) return launch<tokens_bf16_kernel<2, 2, 3>>(p, 32, 16, share, stream);
-    return launch<tokens_bf16_kernel<4, 2, 1>>(p, 64, 16, share, stream);
+    return launch<tokens_bf16_kernel<2, 2, 3>>(p, 32, 16, share, stream);
 }
 
 }  // namespace mmbwd

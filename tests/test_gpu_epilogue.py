@@ -472,3 +472,28 @@ def test_rows_that_start_between_32_byte_boundaries(T, shift):
     ok(mm.mmbwd_forward_act(res, None, d["inp"], d["weight"], d["bias"], res, 1, T, C, OC, mm.ACT_SILU, mm.BF16))
     assert torch.equal(out, want[0]) and torch.equal(pre, want[1]) and torch.equal(res, want[0])
     assert (room[:, :shift] == 3).all() and (room[:, shift + T * OC:] == 3).all()
+
+
+@pytest.mark.parametrize("path", ["32", "64"])
+@pytest.mark.parametrize("size", [(2000, 64, 40), (1300, 36, 20), (40, 68, 3000), (130, 1028, 68), (3, 4000, 100), (700, 500, 36)],
+                         ids=lambda s: "x".join(map(str, s)))
+def test_fp32_sums_shared_by_blocks(monkeypatch, size, path):
+    """Few tiles and long sums, of either product: forward, both gradients, dbias."""
+    monkeypatch.setenv("MMBWD_ACT_F32_PATH", path)
+    x = inputs(*size, "f32", 51)
+    first = check_forward(x, "gelu", "f32")
+    assert all(torch.equal(a, b) for a, b in zip(forward(x, "gelu", "f32"), first))
+    y = gradient_inputs(*size, "f32", "silu", 52)
+    first = check_run(y, "silu", "f32")
+    for got in (run(y, "silu", "f32"), run(y, "silu", "f32", in_place=True)):
+        assert all(torch.equal(a, b) for a, b in zip(got, first))
+
+
+@pytest.mark.parametrize("T", [33, 65, 119, 256, 509])
+@pytest.mark.parametrize("size", [(8, 8), (1720, 536), (3000, 72), (264, 1000)], ids=lambda s: "x".join(map(str, s)))
+def test_forward_of_prompts(T, size):
+    """Few tiles: K shared by the warps of a block, tokens in several rows of blocks."""
+    x = inputs(T, *size, "bf16", 61)
+    first = check_forward(x, "gelu", "bf16")
+    for got in (forward(x, "gelu", "bf16"), forward(x, "gelu", "bf16", pre=False, in_place=True)):
+        assert torch.equal(got[0], first[0])
