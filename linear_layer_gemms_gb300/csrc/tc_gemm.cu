@@ -141,8 +141,8 @@ struct Smem {
 constexpr int SMEM_TOTAL = Smem<0>::SMEM_TOTAL > Smem<2>::SMEM_TOTAL ? Smem<0>::SMEM_TOTAL : Smem<2>::SMEM_TOTAL;
 
 // MODE 6: k-blocks (of 32) that a pair of accumulators takes before they are read back.
-// Relative error (2-norm) of the sums at any length: 6e-7 with 4, 9e-7 with 8, in the same time
-// (2048 x 1600 -> 2400 110 us with either); without, 1.2e-5 at 1600 values.
+// Relative error (2-norm) of the sums at any length: 6e-7 with 4, 9e-7 with 8, in the same
+// time; without, 1.2e-5 at 1600 values.
 constexpr int X3_SPAN = 4;
 
 constexpr unsigned long long DEFAULT_TIMEOUT_NS = 2000000000ull;  // 2 s per wait
