@@ -1656,6 +1656,15 @@ double assign_lpt(TcPlan& pl, int pairs) {
     static thread_local ItemCost cost[TC_MAX_SCHED_ITEMS];
     const int n = pl.n_items;
     for (int w = 0; w < n; ++w) order[w] = w, cost[w] = item_cost(pl, w);
+    // dweight tiles along the dimension that has fewer, so that the pairs that run together read
+    // few panels of the larger operand, at the same k: GPT-2 XL projection (7 x 25 tiles)
+    // 211 -> 205 us, its DRAM reads 521 -> 358 MB
+    if (pl.dw_tiles_m < pl.dw_tiles_n) {
+        for (int k = 0; k < pl.n_dw_items; ++k) {
+            const int m = k % pl.dw_tiles_m, rest = k / pl.dw_tiles_m;
+            order[k] = (rest / pl.dw_tiles_n * pl.dw_tiles_m + m) * pl.dw_tiles_n + rest % pl.dw_tiles_n;
+        }
+    }
     std::stable_sort(order, order + n, [&](int a, int b) { return cost[a].run > cost[b].run; });
     for (int c = 0; c < pairs; ++c) load[c] = last_epi[c] = 0.0, cnt[c] = 0;
     for (int k = 0; k < n; ++k) {
