@@ -329,15 +329,17 @@ Product product(float* D, const float* A, const float* B, int64_t M, int64_t N, 
 namespace {
 
 // Blocks of a cluster that share the K of a product's tiles, a power of two: as many as have
-// an SM each, with a K-tile at least for every warp. Of two products the one that wants more is
-// shared, or both. (Up to two blocks an SM: 100 x 768 -> 768 16.4 -> 12.5 us, but 200 x 264 -> 388's gradients 8.2
-// -> 11.5, 40 x 600 -> 600 7.3 -> 10.1.)
+// an SM each, with a K-tile at least for every warp; of tiles of 32 half an SM each where K is long (18 x
+// 3732 -> 4032 70 -> 40 us, 100 x 768 -> 768 16.4 -> 12.5, but of shorter ones 200 x 264 -> 388's
+// gradients 8.2 -> 11.5, 40 x 600 -> 600 7.3 -> 10.1). Of two products the one that wants more is
+// shared, or both.
 int share_products(Product* q, int n, int tile, int num_sms) {
     int cluster = 1;
     for (int i = 0; i < n; ++i) {
         const int64_t tiles = tiles_of(q[i].M, q[i].N, tile);
         q[i].share = 1;
-        while (q[i].share < 8 && 2 * q[i].share * tiles <= num_sms && 2 * q[i].share * 64 <= q[i].K) q[i].share *= 2;
+        auto room = [&](int share) { return tile == 32 && q[i].K >= 384 * share ? 2 * num_sms : num_sms; };
+        while (q[i].share < 8 && 2 * q[i].share * tiles <= room(2 * q[i].share) && 2 * q[i].share * 64 <= q[i].K) q[i].share *= 2;
         cluster = std::max(cluster, q[i].share);
     }
     for (int i = 0; i < n; ++i)
@@ -348,12 +350,13 @@ int share_products(Product* q, int n, int tile, int num_sms) {
 // Time models (us), fitted to the measurements below; times (us) on one GB300:
 //                         tokens  32 x 32  64 x 64  spans (forward | backward 32, 64, spans)
 //     6 x   92 -> 2072         3.6      3.5      5.8   11.7 |  7.4 12.2 53.6
-//    16 x 6400 -> 1600        29.0     61.6     55.7    148 |  108  127 59.7
+//    16 x 6400 -> 1600        28.9     38.2     55.5    148 |  108  127 58.7
+//    18 x 3732 -> 4032                 39.8     56.2   94.4 |  156  195  105
 //    40 x  600 ->  600         7.6      7.4      8.6   23.6 |  8.9 14.3 22.3
 //    40 x 1600 -> 6400                 63.5     51.2   46.9 |  127  148  154
 //    64 x 4000 ->   64         5.8      9.6     18.7   95.4 |  7.2  7.7 13.0
-//   100 x  768 ->  768                 16.4     10.6   27.2 | 13.5 17.6 26.4
-//   100 x  768 -> 2304                 19.4     15.9   27.4 | 36.7 34.6 61.3
+//   100 x  768 ->  768                 12.5     10.7   27.2 | 14.9 17.6 26.4
+//   100 x  768 -> 2304                 19.4     16.0   27.4 | 33.9 34.8 61.2
 //   200 x  264 ->  388                  7.4      7.7   17.6 |  8.2 10.3 19.1
 //   333 x  772 -> 1300                 27.2     24.4   28.6 | 46.5 44.9 39.1
 //   407 x 1120 ->  408                 26.5     20.8   35.8 | 26.2 28.0 21.2
@@ -374,7 +377,8 @@ double small_us(int tile, const Product* q, int n, int num_sms) {
         const int share = shared[i].share;
         const double K = static_cast<double>(q[i].K) / share, blocks = static_cast<double>(tiles_of(q[i].M, q[i].N, tile) * share);
         work += blocks * (tile == 32 ? (std::max(K, 64.0) + 60.0) * 0.0107 : (std::max(K, 64.0) + 120.0) * 0.0298);
-        longest = std::max(longest, K * (tile == 32 ? 0.0148 : 0.0265) + (share > 1 ? 1.5 : 0.0));
+        const double beside = share > 1 ? std::max(1.0, blocks / num_sms) : 1.0;  // shared tiles: blocks of one SM
+        longest = std::max(longest, K * beside * (tile == 32 ? 0.0148 : 0.0265) + (share > 1 ? 1.5 : 0.0));
     }
     return 3.0 + std::max(work / num_sms, longest);
 }
