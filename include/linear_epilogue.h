@@ -26,7 +26,8 @@
  * infinite fp32 operand may give NaN where the sum is infinite (infinity has no remainder
  * to split off), in the outputs that it belongs to.
  * MMBWD_ACT_F32_PATH in the environment forces the fp32 kernel: "32", "64" (tiles of
- * fused multiply-adds) or "spans".
+ * fused multiply-adds) or "spans"; MMBWD_ACT_BF16_PATH that of the bf16 forward: "tokens" (the
+ * kernel for few tokens) or "tiles" (the tensor cores').
  */
 #ifndef LINEAR_EPILOGUE_H
 #define LINEAR_EPILOGUE_H

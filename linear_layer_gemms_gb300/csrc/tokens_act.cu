@@ -20,6 +20,8 @@
 
 #include <algorithm>
 #include <cstdint>
+#include <cstdlib>
+#include <cstring>
 
 namespace mmbwd {
 namespace {
@@ -280,7 +282,13 @@ int prompt_share(int64_t T, int64_t N, int num_sms) {
 // / 12.8, 256 tokens 3000 -> 504 8.5 / 18.1, 512 tokens 768 -> 768 12.0 / 8.4, 4000 -> 400 16.2 / 21.7;
 // 32 tokens 1600 -> 6400 10.1 / 14.0, 6400 -> 1600 10.5 / 36.1; 16
 // tokens 768 -> 50304 16.6 / 29.3; one token 1600 -> 6400 5.6 / 14.7.
+// MMBWD_ACT_BF16_PATH = "tokens" or "tiles" forces this kernel (up to the tokens that a grid
+// holds) or the tensor-core one (tests, tuning).
 bool tokens_act_takes_bf16(int64_t T, int64_t K, int64_t N, int num_sms) {
+    if (const char* e = std::getenv("MMBWD_ACT_BF16_PATH")) {
+        if (std::strcmp(e, "tokens") == 0) return T <= 32 * 65535;
+        if (std::strcmp(e, "tiles") == 0) return false;
+    }
     if (T <= 32) return true;
     const int share = prompt_share(T, N, num_sms);
     if (share == 0) return false;
@@ -309,7 +317,7 @@ cudaError_t tokens_act_launch(void* out, void* pre, const void* inp, const void*
         if (T <= 4) return launch<tokens_f32_kernel<4, 2>>(p, 4, 4, share, stream);
         return launch<tokens_f32_kernel<8, 1>>(p, 8, 4, share, stream);
     }
-    if (T > 32) return launch<tokens_bf16_kernel<2, 4, 2, 8>, 8>(p, 32, 32, prompt_share(T, N, num_sms), stream);
+    if (T > 32) return launch<tokens_bf16_kernel<2, 4, 2, 8>, 8>(p, 32, 32, std::max(1, prompt_share(T, N, num_sms)), stream);
     const int share = shared_by((N + 15) / 16, (K + 31) / 32 / 2, T <= 16 ? 2400 : 1600);
     if (T <= 16)  // (fewer loads in flight to a warp leave the registers for more of them)
         return share < MAX_WARPS ? launch<tokens_bf16_kernel<1, 2, 2>>(p, 16, 16, share, stream)
