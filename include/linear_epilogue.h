@@ -81,7 +81,8 @@ int mmbwd_forward_act(void* out, void* pre_or_null, const void* inp, const void*
  *   dout          device, (BT, OC), read only
  *   inp           device, (BT, C),  read only: act(pre), the layer's input
  *   weight        device, (OC, C),  read only
- *   pre           device, (BT, C),  read only (unless dpre is it)
+ *   pre           device, (BT, C),  read only (unless dpre is it); not used with
+ *                 MMBWD_ACT_NONE (may be NULL)
  *   workspace     device, 256-byte aligned, mmbwd_run_act_workspace_bytes() bytes (NULL
  *                 where that is 0): the caller's, so that calls with workspaces of their own
  *                 may overlap. Nothing in it is kept from call to call.
@@ -105,7 +106,8 @@ size_t mmbwd_run_act_workspace_bytes(int64_t B, int64_t T, int64_t C, int64_t OC
  *
  *   dpre   device, n values, written; may be dout or pre itself
  *   dout   device, n values, read only
- *   pre    device, n values, read only
+ *   pre    device, n values, read only; not used with MMBWD_ACT_NONE (may be NULL), which
+ *          copies dout
  *
  * n >= 0, any; pointers 16-byte aligned.
  */

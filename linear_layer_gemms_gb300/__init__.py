@@ -290,8 +290,8 @@ def mmbwd_forward_act(out, pre, inp, weight, bias, residual, B: int, T: int, C: 
 def mmbwd_run_act(dpre, dweight, dbias, dout, inp, weight, pre, workspace, workspace_bytes: int, B: int, T: int, C: int,
                   OC: int, act: int, dtype: int, stream=None) -> int:
     """Enqueue the backward of a layer whose inp is act(pre): dpre = (dout . weight) *
-    act'(pre) (overwritten; may be pre), dweight += dout^T . inp and dbias (None
-    skips it). Returns the C status code."""
+    act'(pre) (overwritten; may be pre; pre may be None with ACT_NONE), dweight +=
+    dout^T . inp and dbias (None skips it). Returns the C status code."""
     return load().mmbwd_run_act(_ptr(dpre), _ptr(dweight), _ptr(dbias), _ptr(dout), _ptr(inp), _ptr(weight), _ptr(pre),
                                 _ptr(workspace), workspace_bytes, B, T, C, OC, act, dtype, _stream(stream))
 
@@ -301,8 +301,8 @@ def mmbwd_run_act_workspace_bytes(B: int, T: int, C: int, OC: int, dtype: int) -
 
 
 def mmbwd_act_backward(dpre, dout, pre, n: int, act: int, dtype: int, stream=None) -> int:
-    """Enqueue dpre = dout * act'(pre) over n values; dpre may be dout or pre.
-    Returns the C status code."""
+    """Enqueue dpre = dout * act'(pre) over n values; dpre may be dout or pre, pre may
+    be None with ACT_NONE. Returns the C status code."""
     return load().mmbwd_act_backward(_ptr(dpre), _ptr(dout), _ptr(pre), n, act, dtype, _stream(stream))
 
 

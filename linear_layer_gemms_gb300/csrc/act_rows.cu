@@ -31,7 +31,7 @@ __device__ __forceinline__ uint4 slope_product(const uint4& d, const uint4& x) {
 }
 
 // dpre = dout * act'(pre): bound by HBM, two reads and a write of each value. dpre may be
-// dout or pre: a thread has read what it writes.
+// dout or pre: a thread has read what it writes. No activation: no pre, a copy of dout.
 template <typename T>
 __global__ void __launch_bounds__(THREADS) act_backward_kernel(T* dpre, const T* dout, const T* pre, int64_t n, int act) {
     ptx::grid_launch_dependents();
@@ -44,7 +44,10 @@ __global__ void __launch_bounds__(THREADS) act_backward_kernel(T* dpre, const T*
     uint4 d[VECS], x[VECS];
 #pragma unroll
     for (int j = 0; j < VECS; ++j)
-        if (at + j * THREADS < vecs) d[j] = d4[at + j * THREADS], x[j] = x4[at + j * THREADS];
+        if (at + j * THREADS < vecs) {
+            d[j] = d4[at + j * THREADS];
+            x[j] = pre ? x4[at + j * THREADS] : make_uint4(0u, 0u, 0u, 0u);
+        }
     act::with(act, [&](auto a) {
 #pragma unroll
         for (int j = 0; j < VECS; ++j)
@@ -52,7 +55,7 @@ __global__ void __launch_bounds__(THREADS) act_backward_kernel(T* dpre, const T*
         const int64_t i = vecs * PER + at;  // the loose values at the end: the first threads'
         if (i < n) {
             float v = static_cast<float>(dout[i]), unused = 0.f;
-            const float x = static_cast<float>(pre[i]);
+            const float x = pre ? static_cast<float>(pre[i]) : 0.f;
             if constexpr (sizeof(T) == 2) act::slope_fast<decltype(a)::value>(v, unused, x, 0.f);
             else v *= act::slope<decltype(a)::value>(x);
             dpre[i] = static_cast<T>(v);

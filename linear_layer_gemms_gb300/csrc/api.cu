@@ -1236,9 +1236,11 @@ int mmbwd_run_act(void* dpre, void* dweight, void* dbias, const void* dout, cons
     int rc = check_shape(B, T, C, OC, dtype, &s);
     if (rc != MMBWD_OK) return rc;
     if (!act_ok(act)) return MMBWD_ERR_SHAPE;
+    const bool has_act = act != MMBWD_ACT_NONE;
+    if (!has_act) pre = nullptr;  // not looked at
     const size_t b_inp = static_cast<size_t>(s.n_dinp) * s.es, b_w = static_cast<size_t>(s.n_dw) * s.es,
                  b_col = static_cast<size_t>(OC) * s.es, b_dout = static_cast<size_t>(s.n_dout) * s.es;
-    if ((b_inp && (!dpre || !inp || !pre)) || (b_w && (!dweight || !weight)) || (b_dout && !dout)) return MMBWD_ERR_NULL;
+    if ((b_inp && (!dpre || !inp || (has_act && !pre))) || (b_w && (!dweight || !weight)) || (b_dout && !dout)) return MMBWD_ERR_NULL;
     if ((static_cast<size_t>(C) * s.es) % 16 != 0 || b_col % 16 != 0) return MMBWD_ERR_ALIGN;
     if (reinterpret_cast<uintptr_t>(workspace) & 255u) return MMBWD_ERR_ALIGN;
 
@@ -1286,7 +1288,9 @@ int mmbwd_act_backward(void* dpre, const void* dout, const void* pre, int64_t n,
     NvtxRange nvtx("mmbwd_act_backward");
     if (dtype != MMBWD_F32 && dtype != MMBWD_BF16) return MMBWD_ERR_DTYPE;
     if (!act_ok(act) || n < 0 || n > (int64_t(1) << 42)) return MMBWD_ERR_SHAPE;
-    if (n && (!dpre || !dout || !pre)) return MMBWD_ERR_NULL;
+    const bool has_act = act != MMBWD_ACT_NONE;
+    if (!has_act) pre = nullptr;  // not looked at
+    if (n && (!dpre || !dout || (has_act && !pre))) return MMBWD_ERR_NULL;
     const size_t bytes = static_cast<size_t>(n) * (dtype == MMBWD_F32 ? 4 : 2);
     const Arg args[3] = {{dpre, bytes, true},
                          {dout == dpre ? nullptr : dout, bytes, false},

@@ -119,7 +119,7 @@ struct TcParams {
     int wide_rows;                  // MODE 4: the outputs' and the residual's rows start at multiples of 32 bytes
     const __nv_bfloat16* residual;  // MODE 4; may be null, may be the output
     // MODE 6: the forward (bias and pre may be null; x3_aux: the residual or null) or the
-    // backward (x3_aux: pre). x3_aux may be the output.
+    // backward (x3_aux: pre, null without an activation). x3_aux may be the output.
     int x3_forward;
     const float* x3_bias;
     float* x3_pre;
@@ -173,7 +173,7 @@ cudaError_t tc_launch_x3_pair(const TcPlan& plan, float* dinp, float* dweight, f
 // The same three products with the accumulators added up in registers (MODE 6), for the
 // epilogues with an activation: out = act(inp . weight^T + bias) + residual (pre, bias and
 // residual may be null, residual may be out); dpre = (dout . weight) * act'(pre) (dpre may
-// be pre), dweight += dout^T . inp, dbias = column sums of dout (may be null). Plans: of a
+// be pre, which is null without an activation), dweight += dout^T . inp, dbias = column sums of dout (may be null). Plans: of a
 // product M x N over K, and of one dw_rows x N over M (0: none).
 TcPlan tc_make_plan_span(int64_t M, int64_t N, int64_t K, int64_t dw_rows, int num_sms);
 cudaError_t tc_launch_span_forward(const TcPlan& plan, float* out, float* pre, const float* inp, const float* weight,
@@ -193,12 +193,13 @@ cudaError_t tc_launch_forward_act(const TcPlan& plan, void* out, void* pre, cons
 // Launch the tensor-core kernel (and, with split dweight, the fixed-order
 // split reduction after it on the same stream). `ws` must hold plan.ws_bytes()
 // bytes. `sr`: stochastic rounding of the outputs with `sr_seed` (sr.cuh).
-// With `pre` (not with sr): dinp = product * act'(pre), overwritten; pre may be dinp.
+// With `act` >= 0 (not with sr): dinp = product * act'(pre), overwritten; pre may be dinp, and
+// is null without an activation.
 // Returns a cudaError_t.
 cudaError_t tc_launch(const TcPlan& plan, void* dinp, void* dweight, void* dbias, const void* dout,
                       const void* inp, const void* weight, int64_t BT, int64_t C, int64_t OC,
                       void* ws, cudaStream_t stream, bool sr = false, uint64_t sr_seed = 0,
-                      const void* pre = nullptr, int act = 0);
+                      const void* pre = nullptr, int act = -1);
 
 size_t tc_smem_bytes();
 

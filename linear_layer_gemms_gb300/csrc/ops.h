@@ -111,7 +111,7 @@ bool tokens_act_takes_bf16(int64_t T, int64_t K, int64_t N, int num_sms);
 cudaError_t tokens_act_launch(void* out, void* pre, const void* inp, const void* weight, const void* bias,
                               const void* residual, int64_t T, int64_t K, int64_t N, int act, int dtype, int num_sms,
                               cudaStream_t stream);
-// dpre = dout * act'(pre), n values
+// dpre = dout * act'(pre), n values; pre is null without an activation
 cudaError_t act_backward_launch(void* dpre, const void* dout, const void* pre, int64_t n, int act, int dtype,
                                 cudaStream_t stream);
 // the forward without a product (C == 0): pre = bias, out = act(bias) + residual

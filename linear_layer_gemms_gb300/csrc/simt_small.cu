@@ -43,7 +43,7 @@ struct Params {
     Product first, second;
     const float* bias;         // forward
     const float* residual;     // forward; may be D
-    float* pre;                // forward: stored; backward: read, may be D
+    float* pre;                // forward: stored, may be null; backward: read, may be D, null without an activation
     float* dbias;              // second product
     int act;
     int cluster;               // blocks of a cluster; a product is shared by all of them or by none
@@ -230,7 +230,7 @@ __device__ __forceinline__ void tile_product(const Params& p, const Product& q, 
             const float4 r = *reinterpret_cast<const float4*>(add + at);
             o.x += r.x, o.y += r.y, o.z += r.z, o.w += r.w;
         }
-        if constexpr (EPI == DPRE) {
+        if (EPI == DPRE && p.pre) {
             const float4 x = *reinterpret_cast<const float4*>(p.pre + at);
             act::with(p.act, [&](auto kind) {
                 constexpr int ACT = decltype(kind)::value;

@@ -1027,6 +1027,7 @@ __global__ void __launch_bounds__(Smem<MODE>::THREADS, 1)
             // goes back out with one bulk store. Rows and columns outside the
             // tensor read as zero and are not stored.
             const bool tma_rmw = !FWD && !X3 && !split_mode;
+            const bool load_old = tma_rmw && !(DACT && !it.is_dw && p.act == MMBWD_ACT_NONE);  // (no pre to load)
             constexpr bool TMA_FWD = FWD && !X3 && !EPI;  // the forward's stores through TMA as well
             const void* tmo = it.is_dw ? static_cast<const void*>(&tm_dw_rmw) : static_cast<const void*>(&tm_dinp_rmw);
             const void* tml = DACT && !it.is_dw ? static_cast<const void*>(&tm_pre) : tmo;  // a chunk is loaded through
@@ -1040,7 +1041,7 @@ __global__ void __launch_bounds__(Smem<MODE>::THREADS, 1)
                 if (lane == 0) ptx::bulk_wait_read_all();
                 __syncwarp();
             }
-            if (tma_rmw && qvalid && lane == 0) {
+            if (load_old && qvalid && lane == 0) {
                 for (int k = 0; k < OLD_SLOTS && k < nloc; ++k) {
                     const uint32_t b = oldbar0 + 8u * k;
                     ptx::mbar_arrive_expect_tx(b, OLD_CHUNK_BYTES);
@@ -1266,12 +1267,14 @@ __global__ void __launch_bounds__(Smem<MODE>::THREADS, 1)
                     ptx::tmem_ld32(tbase + c * 32, v);
                     const int slot = k & (OLD_SLOTS - 1);
                     const uint32_t b = oldbar0 + 8u * slot;
-                    if (!wt.wait_warp(b, (oldpar >> slot) & 1u, SITE_EPI_OLD, w)) {
-                        ok = false;
-                        break;
+                    if (load_old) {
+                        if (!wt.wait_warp(b, (oldpar >> slot) & 1u, SITE_EPI_OLD, w)) {
+                            ok = false;
+                            break;
+                        }
+                        oldpar ^= 1u << slot;
+                        oldpend &= ~(1u << slot);
                     }
-                    oldpar ^= 1u << slot;
-                    oldpend &= ~(1u << slot);
                     const uint32_t rowaddr = oldbuf + slot * OLD_CHUNK_BYTES + lane * 64;
                     // the row's 32 columns start at element e_row (a multiple of 8:
                     // C is), so their eight words have consecutive counters
@@ -1322,10 +1325,12 @@ __global__ void __launch_bounds__(Smem<MODE>::THREADS, 1)
                         const int kn = k + OLD_SLOTS;
                         if (kn < nloc) {
                             ptx::bulk_wait_read_all();
-                            ptx::mbar_arrive_expect_tx(b, OLD_CHUNK_BYTES);
-                            ptx::tma_load_2d(oldbuf + slot * OLD_CHUNK_BYTES, tml, b, col0 + (h + NH * kn) * 32,
-                                             static_cast<int32_t>(qrow0));
-                            oldpend |= 1u << slot;
+                            if (load_old) {
+                                ptx::mbar_arrive_expect_tx(b, OLD_CHUNK_BYTES);
+                                ptx::tma_load_2d(oldbuf + slot * OLD_CHUNK_BYTES, tml, b, col0 + (h + NH * kn) * 32,
+                                                 static_cast<int32_t>(qrow0));
+                                oldpend |= 1u << slot;
+                            }
                         }
                     }
                     __syncwarp();
@@ -1924,7 +1929,7 @@ struct MapSpec {
 // Encodes the six tensor maps, completes the parameters from the plan, and
 // launches the kernel (and the split fixup when the plan splits dweight). `aux`: what
 // the dinp-type items read in place of their output's old values (MODE 4: the residual,
-// MODE 5: pre).
+// MODE 5: pre; may be null).
 cudaError_t launch_common(const TcPlan& plan, const MapSpec (&specs)[6], TcParams& p, int mode, cudaStream_t stream,
                           const MapSpec* pair_specs = nullptr, const MapSpec* aux = nullptr) {
     const bool bwd = mode == 0 || mode == 3 || mode == 5;  // bf16 backward
@@ -2144,7 +2149,7 @@ cudaError_t tc_launch(const TcPlan& plan, void* dinp, void* dweight, void* dbias
     p.bias_mma = (dbias && db && std::strcmp(db, "ones") == 0) ? 1 : 0;
     p.act = act;
     const MapSpec aux{pre, c, bt, 128, TC_BM, CU_TENSOR_MAP_SWIZZLE_NONE};
-    return launch_common(plan, specs, p, pre ? 5 : sr ? 3 : 0, stream, nullptr, pre ? &aux : nullptr);
+    return launch_common(plan, specs, p, act >= 0 ? 5 : sr ? 3 : 0, stream, nullptr, pre ? &aux : nullptr);
 }
 
 cudaError_t tc_launch_forward(const TcPlan& plan, void* out, const void* inp, const void* weight, const void* bias,
@@ -2367,7 +2372,7 @@ cudaError_t tc_launch_span_run(const TcPlan& plan, float* dpre, float* dweight, 
     p.dweight = reinterpret_cast<__nv_bfloat16*>(dweight);
     p.x3_aux = pre;
     p.act = act;
-    return launch_common(plan, specs, p, 6, stream, pair, &aux);
+    return launch_common(plan, specs, p, 6, stream, pair, pre ? &aux : nullptr);
 }
 
 cudaError_t tc_read_status(int* code, int* info3, bool reset) {

@@ -97,6 +97,15 @@ def test_act_backward_refusals():
     assert alone(dpre=2 * A + 16) == mm.ERR_ALIAS
 
 
+def test_no_activation_has_no_argument():
+    """ACT_NONE does not look at pre: none at all, unaligned, inside an output."""
+    for pre in (None, 7 * A + 8, 2 * A, A + 64):
+        refused = (mm.ERR_NULL, mm.ERR_ALIGN, mm.ERR_ALIAS)
+        assert run(pre=pre) in refused and run(pre=pre, act=mm.ACT_NONE) not in refused
+        assert alone(pre=pre, act=mm.ACT_NONE) not in refused
+    assert alone(pre=None) == mm.ERR_NULL
+
+
 def norms(**kw):
     a = dict(out=A, residual_out=2 * A, mean_post=3 * A, rstd_post=4 * A, mean=5 * A, rstd=6 * A, x=7 * A, branch=8 * A,
              gate=9 * A, weight_post=10 * A, bias_post=11 * A, weight=12 * A, bias=13 * A, B=2, T=8, C=64, scale=0.5,
