@@ -1661,10 +1661,16 @@ double assign_lpt(TcPlan& pl, int pairs) {
     static thread_local ItemCost cost[TC_MAX_SCHED_ITEMS];
     const int n = pl.n_items;
     for (int w = 0; w < n; ++w) order[w] = w, cost[w] = item_cost(pl, w);
-    // dweight tiles along the dimension that has fewer, so that the pairs that run together read
-    // few panels of the larger operand, at the same k: GPT-2 XL projection (7 x 25 tiles)
-    // 211 -> 205 us, its DRAM reads 521 -> 358 MB
-    if (pl.dw_tiles_m < pl.dw_tiles_n) {
+    // bf16: dweight tiles along the dimension that has fewer, so that the pairs that run together
+    // read few panels of the larger operand, at the same k. Measured row by row and so, us:
+    // 8192 tokens 6400 -> 1600 (7 x 25 tiles, DRAM reads 521 -> 358 MB) 206 -> 202, 16384 tokens
+    // 452 -> 446, 4096 tokens 105 -> 102; 8192 tokens 12800 -> 520 213 -> 207; 4096 tokens 8192 ->
+    // 2048 through the GELU 176 -> 172; the same where L2 holds the operands (8192 tokens 3200 ->
+    // 800 66.2 -> 66.1) and for 16384 tokens 4096 -> 1024 (190 -> 191). fp32 stays row by row: three
+    // tf32 products take the same time either way (4096 tokens 6400 -> 1600 703), in spans it costs
+    // more than it gives (2048 tokens 6400 -> 1600 519 -> 537, 4096 tokens 1033 -> 1057; 8192
+    // tokens 1600 -> 520 283 -> 276).
+    if (!pl.x3 && pl.dw_tiles_m < pl.dw_tiles_n) {
         for (int k = 0; k < pl.n_dw_items; ++k) {
             const int m = k % pl.dw_tiles_m, rest = k / pl.dw_tiles_m;
             order[k] = (rest / pl.dw_tiles_n * pl.dw_tiles_m + m) * pl.dw_tiles_n + rest % pl.dw_tiles_n;
