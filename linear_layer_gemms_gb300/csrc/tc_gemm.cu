@@ -494,8 +494,10 @@ __global__ void __launch_bounds__(Smem<MODE>::THREADS, 1)
                 ptx::prefetch_tmap(&tm_weight_w);
                 ptx::prefetch_tmap(&tm_dout_mn_w);
             }
-            ptx::prefetch_tmap(&tm_dinp_out);
-            ptx::prefetch_tmap(&tm_dw_out);
+            if constexpr (!EPI && !DACT) {
+                ptx::prefetch_tmap(&tm_dinp_out);
+                ptx::prefetch_tmap(&tm_dw_out);
+            }
             uint32_t stage = 0, phase = 0, issued = 0, last_parity = 0;
             bool ok = true, waited = false;
             for (int r = 0; ok; ++r) {
@@ -1932,10 +1934,10 @@ struct MapSpec {
     uint64_t pitch = 0;     // bytes between rows (0: inner x element size)
 };
 
-// Encodes the six tensor maps, completes the parameters from the plan, and
+// Encodes the tensor maps, completes the parameters from the plan, and
 // launches the kernel (and the split fixup when the plan splits dweight). `aux`: what
-// the dinp-type items read in place of their output's old values (MODE 4: the residual,
-// MODE 5: pre; may be null).
+// the dinp-type items read in place of their output's old values (MODE 5: pre; MODE 6: the
+// residual or pre, prefetched into L2; may be null).
 cudaError_t launch_common(const TcPlan& plan, const MapSpec (&specs)[6], TcParams& p, int mode, cudaStream_t stream,
                           const MapSpec* pair_specs = nullptr, const MapSpec* aux = nullptr) {
     const bool bwd = mode == 0 || mode == 3 || mode == 5;  // bf16 backward
@@ -1967,6 +1969,10 @@ cudaError_t launch_common(const TcPlan& plan, const MapSpec (&specs)[6], TcParam
     if (!encode) return cudaErrorNotSupported;
     CUtensorMap maps[13];
     for (int i = 0; i < 6; ++i) {
+        if (i >= 4 && (mode == 4 || mode == 5)) {  // nothing is prefetched into L2
+            maps[i] = maps[0];
+            continue;
+        }
         const MapSpec& m = i == 4 && aux ? *aux : specs[i];
         const cuuint64_t dims[2] = {m.inner, m.outer};
         const uint64_t es = x3 ? 4 : 2;
@@ -2190,10 +2196,9 @@ cudaError_t tc_launch_forward_act(const TcPlan& plan, void* out, void* pre, cons
         {weight, c, oc, TC_BK, 64, CU_TENSOR_MAP_SWIZZLE_128B},      // weight rows, K-major B (64 rows per box)
         {inp, c, bt, TC_BK, TC_BM, CU_TENSOR_MAP_SWIZZLE_128B},      // unused by forward items
         {weight, c, oc, TC_BK, 64, CU_TENSOR_MAP_SWIZZLE_128B},      // unused
-        {out, oc, bt, 128, TC_BM, CU_TENSOR_MAP_SWIZZLE_NONE},       // out, or the residual: L2 prefetch
+        {out, oc, bt, 128, TC_BM, CU_TENSOR_MAP_SWIZZLE_NONE},       // unused (out and residual go by pointers)
         {out, oc, bt, 128, TC_BM, CU_TENSOR_MAP_SWIZZLE_NONE},       // unused
     };
-    const MapSpec aux{residual, oc, bt, 128, TC_BM, CU_TENSOR_MAP_SWIZZLE_NONE};
     TcParams p{};
     p.BT = BT;
     p.C = C;
@@ -2206,7 +2211,7 @@ cudaError_t tc_launch_forward_act(const TcPlan& plan, void* out, void* pre, cons
     p.wide_rows = OC % 16 == 0 && ((reinterpret_cast<uintptr_t>(out) | reinterpret_cast<uintptr_t>(pre) |
                                     reinterpret_cast<uintptr_t>(residual)) & 31u) == 0;
     p.act = act;
-    return launch_common(plan, specs, p, 4, stream, nullptr, residual ? &aux : nullptr);
+    return launch_common(plan, specs, p, 4, stream);
 }
 
 TcPlan tc_make_plan_x3_pair(int64_t BT, int64_t C, int64_t OC, int num_sms) {
