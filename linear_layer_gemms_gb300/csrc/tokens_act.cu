@@ -234,27 +234,19 @@ __global__ void __launch_bounds__(32 * MAX_WARPS) tokens_f32_kernel(const __grid
     join<float, TOKENS, ROWS>(p, red, block0, t0, tokens);
 }
 
-template <auto kernel, int MOST = MAX_WARPS>
-cudaError_t launch(Params p, int tokens, int rows, int share, cudaStream_t stream) {
-    const int warps = std::max(share, 8), smem = warps * tokens * rows * 4;
-    if (smem > 48 * 1024) {
-        static bool done[64];  // (calls hold the library's lock)
-        int dev = 0;
-        cudaError_t e = cudaGetDevice(&dev);
-        if (e != cudaSuccess) return e;
-        if (dev < 0 || dev >= 64 || !done[dev]) {
-            e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, MOST * tokens * rows * 4);
-            if (e != cudaSuccess) return e;
-            if (dev >= 0 && dev < 64) done[dev] = true;
-        }
-    }
+// A kernel of TOKENS tokens by ROWS rows to a warp, eight warps to a block or as many as share
+// K, MOST at most.
+template <auto kernel, int TOKENS, int ROWS, int MOST = MAX_WARPS>
+cudaError_t launch(Params p, int share, cudaStream_t stream) {
+    static_assert(MOST * TOKENS * ROWS * 4 <= 48 * 1024, "the warps' sums fit the shared memory that needs no allowance");
+    const int warps = std::max(share, 8);
     p.share = share;
-    const int64_t per_block = static_cast<int64_t>(warps / share) * rows, blocks = (p.N + per_block - 1) / per_block;
+    const int64_t per_block = static_cast<int64_t>(warps / share) * ROWS, blocks = (p.N + per_block - 1) / per_block;
     if (blocks > INT32_MAX) return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>(blocks), static_cast<unsigned>((p.T + tokens - 1) / tokens), 1);
+    cfg.gridDim = dim3(static_cast<unsigned>(blocks), static_cast<unsigned>((p.T + TOKENS - 1) / TOKENS), 1);
     cfg.blockDim = dim3(static_cast<unsigned>(32 * warps), 1, 1);
-    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+    cfg.dynamicSmemBytes = static_cast<size_t>(warps * TOKENS * ROWS * 4);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -313,16 +305,16 @@ cudaError_t tokens_act_launch(void* out, void* pre, const void* inp, const void*
     };
     if (dtype == MMBWD_F32) {
         const int share = shared_by(N / 4 * ((T + 7) / 8), (K + 127) / 128, T <= 4 ? 2400 : 1600);
-        if (T <= 1) return launch<tokens_f32_kernel<1, 2>>(p, 1, 4, share, stream);
-        if (T <= 4) return launch<tokens_f32_kernel<4, 2>>(p, 4, 4, share, stream);
-        return launch<tokens_f32_kernel<8, 1>>(p, 8, 4, share, stream);
+        if (T <= 1) return launch<tokens_f32_kernel<1, 2>, 1, 4>(p, share, stream);
+        if (T <= 4) return launch<tokens_f32_kernel<4, 2>, 4, 4>(p, share, stream);
+        return launch<tokens_f32_kernel<8, 1>, 8, 4>(p, share, stream);
     }
-    if (T > 32) return launch<tokens_bf16_kernel<2, 4, 2, 8>, 8>(p, 32, 32, std::max(1, prompt_share(T, N, num_sms)), stream);
+    if (T > 32) return launch<tokens_bf16_kernel<2, 4, 2, 8>, 32, 32, 8>(p, std::max(1, prompt_share(T, N, num_sms)), stream);
     const int share = shared_by((N + 15) / 16, (K + 31) / 32 / 2, T <= 16 ? 2400 : 1600);
     if (T <= 16)  // (fewer loads in flight to a warp leave the registers for more of them)
-        return share < MAX_WARPS ? launch<tokens_bf16_kernel<1, 2, 2>>(p, 16, 16, share, stream)
-                                 : launch<tokens_bf16_kernel<1, 2, 4>>(p, 16, 16, share, stream);
-    return launch<tokens_bf16_kernel<2, 2, 3>>(p, 32, 16, share, stream);
+        return share < MAX_WARPS ? launch<tokens_bf16_kernel<1, 2, 2>, 16, 16>(p, share, stream)
+                                 : launch<tokens_bf16_kernel<1, 2, 4>, 16, 16>(p, share, stream);
+    return launch<tokens_bf16_kernel<2, 2, 3>, 32, 16>(p, share, stream);
 }
 
 }  // namespace mmbwd
