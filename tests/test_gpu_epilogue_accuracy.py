@@ -47,3 +47,39 @@ def test_fp32_derivatives(monkeypatch, act, path):
         ok(mm.mmbwd_run_act(dpre, torch.zeros_like(weight), None, dout, torch.zeros_like(dpre), weight, pre.float(), None, 0, 1, T, C,
                             OC, ACT[act], mm.F32))
     ref.check(dpre, ref.act_slope(pre, act), narrow_slope_bound(pre, act), "derivative")
+
+
+def long_sum_bound(length, path):
+    """Relative error, in the 2-norm, of sums of `length` products of random operands, whose partial
+    sums grow with the square root of what is in them, so that roundings of U of each on a
+    chain of n additions are U sqrt(n / 2) of the last sum. Fused multiply-adds: chains of an
+    eighth of the length at most, one rounding each, and a few to join them. Three tf32 products:
+    32 U of each product (lo lo' and the bits of lo that are not read), the sixteen steps of
+    a span that are cut, by 2 U each at most, 2 U sum sqrt(j / 16) = 23 U, and two
+    roundings a span of 128 on the running sum."""
+    fma = (length / 16) ** 0.5 + 8
+    spans = 32 + 23 + (length / 128) ** 0.5
+    return {"32": fma, "64": fma, "spans": spans, None: max(fma, spans)}[path] * ref.U
+
+
+@pytest.mark.parametrize("path", [None, "32", "64", "spans"])
+def test_fp32_sums_of_many_values(monkeypatch, path):
+    """Reductions of 262,180 and 300,005 values: the forward's, dweight's and dbias'."""
+    if path:
+        monkeypatch.setenv("MMBWD_ACT_F32_PATH", path)
+
+    def near(got, want, length, path):
+        error = ((got.double() - want).norm() / want.norm()).item()
+        assert error <= long_sum_bound(length, path), (error, long_sum_bound(length, path))
+
+    T, K, OC = 130, 262_180, 68
+    x, w = ref.rounded(ref.normal(1, T, K), "f32"), ref.rounded(ref.normal(2, OC, K), "f32")
+    out = torch.empty(T, OC, device="cuda")
+    ok(mm.mmbwd_forward_act(out, None, x.float(), w.float(), None, None, 1, T, K, OC, mm.ACT_NONE, mm.F32))
+    near(out, x @ w.t(), K, path)
+    T, C, OC = 300_005, 68, 36
+    dout, inp, w = ref.rounded(ref.normal(3, T, OC), "f32"), ref.rounded(ref.normal(4, T, C), "f32"), ref.rounded(ref.normal(5, OC, C), "f32")
+    dpre, dweight, dbias = torch.empty(T, C, device="cuda"), torch.zeros(OC, C, device="cuda"), torch.empty(OC, device="cuda")
+    ok(mm.mmbwd_run_act(dpre, dweight, dbias, dout.float(), inp.float(), w.float(), None, None, 0, 1, T, C, OC, mm.ACT_NONE, mm.F32))
+    near(dweight, dout.t() @ inp, T, path)
+    near(dbias, dout.sum(0), T, "32")  # plain fp32 sums, in chains of an eighth at most
