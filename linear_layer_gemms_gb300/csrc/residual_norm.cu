@@ -611,7 +611,10 @@ struct TeamSums {
 // (16-byte vectors, 32 warps apart), their weights and their sums in registers. The next
 // rows are on their way into shared memory, each thread's vectors to places that only it
 // reads (no barrier). MEAN, MEAN_POST: norm, post subtracts a mean (LAYER); without, their sums
-// of g are not formed (8192 x 1600 bf16 with two RMS norms takes 4 us less so).
+// of g are not formed (8192 x 1600 bf16 with two RMS norms takes 4 us less so). The columns' sums are
+// fp32, a chain of a team's rows each: 777 x 1004 fp32 ends 1.5e-7 from the exact gradients
+// where sums in 64 bits end 0.9e-7 from them, but 64 bits would double the four sums a column
+// that fill the registers, and run at a small part of the fp32 rate.
 template <typename L, bool MEAN, bool MEAN_POST>
 __global__ void __launch_bounds__(L::THREADS, 1) residual_rows_kernel(const __grid_constant__ Backward b) {
     using T = typename L::T;
