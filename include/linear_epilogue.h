@@ -67,8 +67,8 @@ extern "C" {
  *   dtype             MMBWD_F32 or MMBWD_BF16 (all tensors)
  *
  * Alignment, sizes and status codes as mmbwd_forward (ERR_SHAPE also for an unknown
- * act and for more than 8,388,480 outputs a row, OC; ERR_ALIAS: out or pre overlaps another tensor, unless out == residual). No
- * workspace. C == 0 gives pre = bias (or 0).
+ * act and for OC > 8,388,480; ERR_ALIAS: out or pre overlaps another tensor, unless
+ * out == residual). No workspace. C == 0 gives pre = bias (or 0).
  */
 int mmbwd_forward_act(void* out, void* pre_or_null, const void* inp, const void* weight, const void* bias_or_null,
                       const void* residual_or_null, int64_t B, int64_t T, int64_t C, int64_t OC, int act, int dtype,

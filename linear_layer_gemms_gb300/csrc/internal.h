@@ -173,7 +173,8 @@ cudaError_t tc_launch_x3_pair(const TcPlan& plan, float* dinp, float* dweight, f
 // The same three products with the accumulators added up in registers (MODE 6), for the
 // epilogues with an activation: out = act(inp . weight^T + bias) + residual (pre, bias and
 // residual may be null, residual may be out); dpre = (dout . weight) * act'(pre) (dpre may
-// be pre, which is null without an activation), dweight += dout^T . inp, dbias = column sums of dout (may be null). Plans: of a
+// be pre, which is null without an activation), dweight += dout^T . inp, dbias = column sums
+// of dout (may be null). Plans: of a
 // product M x N over K, and of one dw_rows x N over M (0: none).
 TcPlan tc_make_plan_span(int64_t M, int64_t N, int64_t K, int64_t dw_rows, int num_sms);
 cudaError_t tc_launch_span_forward(const TcPlan& plan, float* out, float* pre, const float* inp, const float* weight,
